@@ -458,3 +458,8 @@ def empty_staggered(specs, device="cuda", step=4096):
     base = (-buf.data_ptr()) % STAGGER_PERIOD
     return [buf[base + o:base + o + nbytes].view(dt).view(tuple(int(d) for d in shape))
             for (shape, dt), o, nbytes in zip(specs, offsets, sizes)]
+
+
+# The serving operators (include/ecmd_serving.h) under this package's name.
+from .serving import (page_assign, page_assign_workspace, page_compact, page_compact_workspace,  # noqa: E402
+                      page_copy, paged_attention, paged_attention_workspace, rope, rope_append, rope_frequencies)

@@ -32,7 +32,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libecmd.so")
 
 SOURCES = ["ecmd_host.cpp", "ecmd_serial.cpp", "ecmd_jit.cpp", "kernels_linear.hip", "kernels_interp.hip",
-           "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip"]
+           "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip", "ecmd_serving.cpp", "kernels_rope.hip",
+           "kernels_attention_f16.hip", "kernels_attention_bf16.hip", "kernels_attention_f32.hip", "kernels_pages.hip"]
 # Device headers the run-time compiler needs: embedded into the library as text.
 JIT_HEADERS = ["ecmd_tape.h", "ecmd_eval.h", "ecmd_kern_linear.h", "ecmd_kern_rows.h", "ecmd_kern_tiled.h",
                "ecmd_kern_gather.h"]

@@ -1,0 +1,411 @@
+// kernels_pages.hip -- the page bookkeeping of a paged key-value cache: assign,
+// compact, copy.
+//
+// Assigning and compacting need the rank of a page among the free (or live)
+// ones, and the page of a given rank.  Both come from one bit per page: a ballot
+// makes a wave's 64 bits, each word keeps the count of set bits before it
+// within its tile, each tile its total.  A rank is then two prefixes and a
+// population count, a selection two binary searches and one within a word.
+// What is left is integer reads and writes of the tables, a few microseconds of
+// dependent accesses and launches at any size met in practice, so the number of
+// launches is kept small: two to assign, three to compact.
+//
+// Only integer atomics (reference counts) are used: results do not depend on
+// their order.
+#include <hip/hip_runtime.h>
+
+#include "ecmd_launch.h"
+#include "ecmd_serving.h"
+
+namespace ecmd {
+
+namespace {
+
+constexpr uint32_t kBlock = 256, kWaves = kBlock / 64;
+
+__device__ inline uint32_t popc(uint64_t x) { return (uint32_t)__popcll(x); }
+
+// Exclusive prefix of x over the work-group (all threads call it); total gets
+// the sum.  scratch: kWaves + 1 entries, reusable after the next barrier.
+__device__ inline uint32_t block_prefix(uint32_t x, uint32_t *scratch, uint32_t &total)
+{
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t inc = x;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const uint32_t y = __shfl_up(inc, o);
+        if (lane >= (uint32_t)o) inc += y;
+    }
+    if (lane == 63) scratch[wave] = inc;
+    __syncthreads();
+    uint32_t before = 0;
+    total = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) {
+        if (w < wave) before += scratch[w];
+        total += scratch[w];
+    }
+    __syncthreads();
+    return before + inc - x;
+}
+
+// The bits, word prefixes and count of tile `tile`: set where pick(id).
+template <class F>
+__device__ inline void mark_tile(const PageBits &B, uint32_t tile, uint32_t *scratch, F pick)
+{
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t run = 0;
+    // 256 words at a time: the waves make their words' bits, then one prefix
+    for (uint32_t w0 = 0; w0 < B.tile_words; w0 += kBlock) {
+        const uint32_t words = min(kBlock, B.tile_words - w0);
+        __shared__ uint32_t s_count[kBlock];
+        for (uint32_t w = wave; w < words; w += kWaves) {
+            const uint64_t word = (uint64_t)tile * B.tile_words + w0 + w, id = word * 64 + lane;
+            const uint64_t bits = __ballot(id < B.n && pick((uint32_t)id));
+            if (lane == 0) {
+                B.word[word] = bits;
+                s_count[w] = popc(bits);
+            }
+        }
+        __syncthreads();
+        const uint32_t mine = threadIdx.x < words ? s_count[threadIdx.x] : 0;
+        uint32_t total;
+        const uint32_t before = block_prefix(mine, scratch, total);
+        if (threadIdx.x < words) B.word_prefix[(uint64_t)tile * B.tile_words + w0 + threadIdx.x] = run + before;
+        run += total;
+    }
+    if (threadIdx.x == 0) B.tile_count[tile] = run;
+}
+
+// Prefixes of the tile counts into LDS: prefix[t] set bits before tile t,
+// prefix[tiles] all of them.  Ends with a barrier.
+__device__ inline void tile_prefixes(const PageBits &B, uint32_t *prefix, uint32_t *scratch)
+{
+    uint32_t run = 0;
+    for (uint32_t t0 = 0; t0 < B.tiles; t0 += kBlock) {
+        const uint32_t t = t0 + threadIdx.x;
+        uint32_t total;
+        const uint32_t before = block_prefix(t < B.tiles ? B.tile_count[t] : 0, scratch, total);
+        if (t < B.tiles) prefix[t] = run + before;
+        run += total;
+    }
+    if (threadIdx.x == 0) prefix[B.tiles] = run;
+    __syncthreads();
+}
+
+// The id of the set bit with this rank (rank < prefix[tiles]).
+__device__ inline uint32_t select_bit(const PageBits &B, const uint32_t *prefix, uint32_t rank)
+{
+    uint32_t lo = 0, hi = B.tiles;   // prefix[lo] <= rank < prefix[hi]
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (prefix[mid] <= rank) lo = mid;
+        else hi = mid;
+    }
+    const uint64_t w0 = (uint64_t)lo * B.tile_words;
+    rank -= prefix[lo];
+    uint32_t a = 0, b = B.tile_words;
+    while (b - a > 1) {
+        const uint32_t mid = (a + b) / 2;
+        if (B.word_prefix[w0 + mid] <= rank) a = mid;
+        else b = mid;
+    }
+    rank -= B.word_prefix[w0 + a];
+    const uint64_t word = B.word[w0 + a];
+    uint32_t at = 0;
+#pragma unroll
+    for (uint32_t half = 32; half; half /= 2) {
+        const uint32_t low = popc((word >> at) & ((uint64_t(1) << half) - 1));
+        if (rank >= low) {
+            rank -= low;
+            at += half;
+        }
+    }
+    return (uint32_t)(w0 + a) * 64 + at;
+}
+
+// ---------------------------------------------------------------------------
+// Assign.
+
+struct RowPlan {
+    bool has;
+    uint32_t parent, old, length, len_new, keep, total;
+};
+__device__ inline RowPlan plan_row(const AssignArgs &A, uint32_t r)
+{
+    RowPlan p;
+    const uint32_t most = A.cols * A.page;
+    const int32_t parent = A.parent[r * A.parent_s];
+    p.has = parent >= 0 && (uint32_t)parent < A.rows;
+    p.parent = p.has ? (uint32_t)parent : r;
+    p.old = min((uint32_t)max(A.lens[r * A.lens_s], 0), most);
+    p.length = !p.has ? 0 : min((uint32_t)max(A.lens[p.parent * A.lens_s], 0), most);
+    p.len_new = min(p.length + (uint32_t)max(A.add[r * A.add_s], 0), most);   // both below 2^31
+    p.keep = p.has && p.parent == r ? A.by_page.div(p.length + A.page - 1) : A.by_page.div(p.length);
+    p.total = A.by_page.div(p.len_new + A.page - 1);
+    return p;
+}
+
+// First launch: a work-group per tile of pages (the free ones' bits, the copy of
+// the counts), then one per 256 rows (pages wanted).
+__global__ __launch_bounds__(kBlock) void k_assign_count(const AssignArgs A)
+{
+    __shared__ uint32_t scratch[kWaves];
+    if (blockIdx.x < A.bits.tiles) {
+        mark_tile(A.bits, blockIdx.x, scratch, [&](uint32_t id) {
+            const int32_t c = A.refs[id * A.refs_s];
+            A.refs_out[id * A.refs_out_s] = c;
+            return c == 0;
+        });
+        return;
+    }
+    const uint32_t g = blockIdx.x - A.bits.tiles, r = g * kBlock + threadIdx.x;
+    uint32_t want = 0, total;
+    if (r < A.rows) {
+        const RowPlan p = plan_row(A, r);
+        want = p.total - p.keep;
+    }
+    const uint32_t before = block_prefix(want, scratch, total);
+    if (r < A.rows) A.want[r] = before;
+    if (threadIdx.x == 0) A.want_group[g] = total;
+}
+
+// Second launch: a work-group per row.
+__global__ __launch_bounds__(kBlock) void k_assign(const AssignArgs A)
+{
+    __shared__ uint32_t prefix[kMaxPageTiles + 1], scratch[kWaves];
+    const uint32_t r = blockIdx.x;
+    RowPlan p{};
+    if (r < A.rows) p = plan_row(A, r);
+    const uint32_t fresh = p.total - p.keep;
+    uint32_t have = 0, base = 0;
+    if (fresh || r == 0) {   // the same for the whole work-group
+        tile_prefixes(A.bits, prefix, scratch);
+        have = prefix[A.bits.tiles];
+        uint32_t mine = 0, all = 0;
+        for (uint32_t g = threadIdx.x; g < A.row_groups; g += kBlock) {
+            const uint32_t w = A.want_group[g];
+            all += w;
+            if (g < r / kBlock) mine += w;
+        }
+        uint32_t wanted;
+        block_prefix(mine, scratch, base);
+        block_prefix(all, scratch, wanted);
+        if (r < A.rows) base += A.want[r];
+        if (r == 0 && threadIdx.x == 0) {
+            A.stats[0] = (int32_t)wanted;
+            A.stats[A.stats_s] = (int32_t)min(wanted, have);
+        }
+    }
+    if (r >= A.rows) return;   // no rows at all
+    const uint32_t held = A.by_page.div(p.old + A.page - 1), last = A.by_page.div(p.length);
+    const bool partial = p.has && p.parent != r && p.length != last * A.page;
+    const int32_t *own = A.pages + (int64_t)r * A.pages_s[0], *from = A.pages + (int64_t)p.parent * A.pages_s[0];
+    if (threadIdx.x == 0) {
+        A.lens_out[r * A.lens_out_s] = (int32_t)p.len_new;
+        if (!partial) A.src[r * A.src_s] = A.dst[r * A.dst_s] = -1;
+    }
+    for (uint32_t c = threadIdx.x; c < A.cols; c += kBlock) {
+        int32_t was = -1, now = -1;
+        if (c < held) was = own[c * A.pages_s[1]];
+        if (was < 0 || (uint32_t)was >= A.bits.n) was = -1;
+        if (c < p.keep) {
+            now = from[c * A.pages_s[1]];
+            if (now < 0 || (uint32_t)now >= A.bits.n) now = -1;
+        } else if (c < p.total) {
+            const uint32_t rank = base + (c - p.keep);
+            if (rank < have) now = (int32_t)select_bit(A.bits, prefix, rank);
+        }
+        A.pages_out[(int64_t)r * A.pages_out_s[0] + c * A.pages_out_s[1]] = now;
+        if (was != now) {
+            if (was >= 0) atomicSub(&A.refs_out[was * A.refs_out_s], 1);
+            if (now >= 0) atomicAdd(&A.refs_out[now * A.refs_out_s], 1);
+        }
+        if (partial && c == last) {
+            const int32_t a = from[c * A.pages_s[1]];
+            const bool copy = a >= 0 && (uint32_t)a < A.bits.n && now >= 0;
+            A.src[r * A.src_s] = copy ? a : -1;
+            A.dst[r * A.dst_s] = copy ? now : -1;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Compact.
+
+__global__ __launch_bounds__(kBlock) void k_compact_mark(const CompactArgs A)
+{
+    __shared__ uint32_t scratch[kWaves];
+    mark_tile(A.bits, blockIdx.x, scratch, [&](uint32_t id) { return A.refs[id * A.refs_s] > 0; });
+}
+
+// Set bits before id (id <= n).
+__device__ inline uint32_t rank_bit(const PageBits &B, const uint32_t *prefix, uint32_t id)
+{
+    const uint32_t w = id / 64, tile = w >> B.tile_shift;
+    if (tile >= B.tiles) return prefix[B.tiles];
+    return prefix[tile] + B.word_prefix[w] + popc(B.word[w] & ((uint64_t(1) << (id % 64)) - 1));
+}
+
+// Second launch: a work-group per tile.  With live = all set bits, the pages at
+// or past live are counted from the first of those (its rank: `kept`), the free
+// ids below live are id - rank(id)-th of their kind.
+__global__ __launch_bounds__(kBlock) void k_compact_plan(const CompactArgs A)
+{
+    __shared__ uint32_t prefix[kMaxPageTiles + 1], scratch[kWaves];
+    tile_prefixes(A.bits, prefix, scratch);
+    const uint32_t live = prefix[A.bits.tiles], kept = rank_bit(A.bits, prefix, live), moves = live - kept;
+    const uint64_t w0 = (uint64_t)blockIdx.x * A.bits.tile_words;
+    for (uint64_t i = threadIdx.x; i < (uint64_t)A.bits.tile_words * 64; i += kBlock) {
+        const uint64_t word = w0 + i / 64, id = word * 64 + i % 64;
+        const uint32_t before = prefix[blockIdx.x] + A.bits.word_prefix[word];
+        if (i % 64 == 0) A.rank[word] = before;
+        if (id >= A.bits.n) continue;
+        const uint64_t bits = A.bits.word[word];
+        const bool set = bits >> (i % 64) & 1;
+        const uint32_t rank = before + popc(bits & ((uint64_t(1) << (i % 64)) - 1));
+        if (set && id >= live) A.src[(rank - kept) * A.src_s] = (int32_t)id;
+        if (!set && id < live) A.dst[((uint32_t)id - rank) * A.dst_s] = (int32_t)id;
+        if (set && id < live) A.refs_out[id * A.refs_out_s] = A.refs[id * A.refs_s];
+        if (id >= live) A.refs_out[id * A.refs_out_s] = 0;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        uint32_t *head = A.rank + (uint64_t)A.bits.tiles * A.bits.tile_words;
+        head[0] = live;
+        head[1] = kept;
+        A.stats[0] = (int32_t)live;
+        A.stats[A.stats_s] = (int32_t)moves;
+    }
+}
+
+// Third launch: the table, the moved pages' counts and the unused pairs.
+__global__ __launch_bounds__(kBlock) void k_compact_apply(const CompactArgs A, uint32_t entry_groups)
+{
+    const uint32_t *head = A.rank + (uint64_t)A.bits.tiles * A.bits.tile_words;
+    const uint32_t live = head[0], kept = head[1], moves = live - kept;
+    if (blockIdx.x >= entry_groups) {
+        const uint32_t i = (blockIdx.x - entry_groups) * kBlock + threadIdx.x;
+        if (i < moves) {
+            A.refs_out[A.dst[i * A.dst_s] * A.refs_out_s] = A.refs[A.src[i * A.src_s] * A.refs_s];
+        } else if (i < A.capacity) {
+            A.src[i * A.src_s] = -1;
+            A.dst[i * A.dst_s] = -1;
+        }
+        return;
+    }
+    const uint32_t i = blockIdx.x * kBlock + threadIdx.x;
+    if (i >= A.rows * A.cols) return;
+    const uint32_t r = A.by_cols.div(i), c = i - r * A.cols;
+    const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
+    int32_t now = -1;
+    if (id >= 0 && (uint32_t)id < A.bits.n) {
+        const uint64_t bits = A.bits.word[id / 64];
+        if (bits >> (id % 64) & 1) {
+            now = id;
+            if ((uint32_t)id >= live)
+                now = A.dst[(A.rank[id / 64] + popc(bits & ((uint64_t(1) << (id % 64)) - 1)) - kept) * A.dst_s];
+        }
+    }
+    A.pages_out[(int64_t)r * A.pages_out_s[0] + (int64_t)c * A.pages_out_s[1]] = now;
+}
+
+// ---------------------------------------------------------------------------
+// Copy: a work-group takes one piece of one page (four vectors per work-item,
+// all loaded before the first store), or several whole small pages.  HBM bounds
+// it.
+
+template <int W>
+struct CopyVec;
+template <>
+struct CopyVec<16> {
+    typedef uint32_t V __attribute__((ext_vector_type(4)));
+};
+template <>
+struct CopyVec<8> {
+    typedef uint32_t V __attribute__((ext_vector_type(2)));
+};
+template <>
+struct CopyVec<4> {
+    typedef uint32_t V;
+};
+template <>
+struct CopyVec<2> {
+    typedef uint16_t V;
+};
+
+template <int W>
+__global__ __launch_bounds__(kBlock) void k_copy(const CopyArgs A)
+{
+    typedef typename CopyVec<W>::V V;
+    const CopyPool &P = A.pool[blockIdx.y];
+    uint32_t pair, first, step;
+    if (A.per_group > 1) {
+        const uint32_t in = A.by_vecs.div(threadIdx.x);
+        if (in >= A.per_group) return;
+        pair = blockIdx.x * A.per_group + in;
+        first = threadIdx.x - in * A.by_vecs.d;
+        step = A.by_vecs.d;
+        if (pair >= A.count) return;
+    } else {
+        pair = A.by_pieces.div(blockIdx.x);
+        first = (blockIdx.x - pair * A.pieces) * (4 * kBlock) + threadIdx.x;
+        step = kBlock;
+    }
+    const int32_t a = A.src[pair * A.src_s], b = A.dst[pair * A.dst_s];
+    if (a < 0 || b < 0 || (uint32_t)a >= P.n || (uint32_t)b >= P.n) return;
+    const char *from = P.base + a * P.page_stride;
+    char *to = P.base + b * P.page_stride;
+    auto at = [&](uint32_t v) {
+        const uint32_t row = P.by_row.div(v);
+        return (int64_t)row * P.row_stride + (int64_t)(v - row * P.row_vecs) * W;
+    };
+    V x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (first + k * step < P.vecs) x[k] = *(const V *)(from + at(first + k * step));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (first + k * step < P.vecs) *(V *)(to + at(first + k * step)) = x[k];
+}
+
+}  // namespace
+
+int launch_assign(const AssignArgs &A, void *stream)
+{
+    const uint32_t first = A.bits.tiles + A.row_groups;
+    if (first) {
+        const int rc = launch_kernel(reinterpret_cast<const void *>(&k_assign_count), dim3(first), dim3(kBlock), 0,
+                                     stream, A);
+        if (rc) return rc;
+    }
+    return launch_kernel(reinterpret_cast<const void *>(&k_assign), dim3(A.rows ? A.rows : 1), dim3(kBlock), 0, stream,
+                         A);
+}
+
+int launch_compact(const CompactArgs &A, void *stream)
+{
+    int rc = 0;
+    if (A.bits.tiles)
+        rc = launch_kernel(reinterpret_cast<const void *>(&k_compact_mark), dim3(A.bits.tiles), dim3(kBlock), 0, stream,
+                           A);
+    if (!rc)
+        rc = launch_kernel(reinterpret_cast<const void *>(&k_compact_plan), dim3(A.bits.tiles ? A.bits.tiles : 1),
+                           dim3(kBlock), 0, stream, A);
+    if (rc) return rc;
+    const uint32_t entries = (uint32_t)(((uint64_t)A.rows * A.cols + kBlock - 1) / kBlock);
+    const uint32_t moved = (uint32_t)(((uint64_t)A.capacity + kBlock - 1) / kBlock);
+    if (entries + moved == 0) return 0;
+    return launch_kernel(reinterpret_cast<const void *>(&k_compact_apply), dim3(entries + moved), dim3(kBlock), 0,
+                         stream, A, entries);
+}
+
+int launch_copy(int width, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream)
+{
+    const void *fn = width == 16  ? reinterpret_cast<const void *>(&k_copy<16>)
+                     : width == 8 ? reinterpret_cast<const void *>(&k_copy<8>)
+                     : width == 4 ? reinterpret_cast<const void *>(&k_copy<4>)
+                                  : reinterpret_cast<const void *>(&k_copy<2>);
+    return launch_kernel(fn, dim3(grid, pools), dim3(kBlock), 0, stream, A);
+}
+
+}  // namespace ecmd

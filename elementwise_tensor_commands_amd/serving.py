@@ -1,0 +1,265 @@
+"""Serving operators beside Commands: rotary positions, a paged key-value
+cache, attention of one new token over it, and the bookkeeping of its pages.
+
+A thin ctypes layer over ``include/ecmd_serving.h``, which defines every
+operator; outputs are the caller's tensors, work goes to torch's current stream
+or ``stream``, errors are ``Error`` with the library's status and message, and
+nothing is launched after a failed check.  Scratch memory is the caller's
+``workspace`` (a contiguous GPU tensor of at least the matching
+``*_workspace`` bytes) or, without one, taken from torch's allocator on the
+launch's stream.
+
+A decode step of a model's attention:
+
+    ecmd.page_assign(pages, lens, refs, parent, add, page, pages2, lens2, refs2, src, dst, stats)
+    ecmd.page_copy([k_cache, v_cache], src, dst)                  # forked rows get their own last page
+    ecmd.rope_append(q, k, v, pos, row, pages2, freq, q, k_cache, v_cache)
+    ecmd.paged_attention(q, k_cache, v_cache, pages2, lens2, out)
+
+``decode.py`` in this package runs it end to end.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+import struct
+
+from . import ARG_TENSOR, BF16, F16, F32, I32, Error, cmd_arg, lib
+
+F64 = 5
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+CHECK_ONLY = 1
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_args = ctypes.c_char_p      # packed cmd_arg structures
+for _name, _res, _sig in [
+        ("cmd_rope", ctypes.c_int, [_args, _i32, ctypes.c_double, _i32, _i32, _vp]),
+        ("cmd_rope_append", ctypes.c_int, [_args, _i32, ctypes.c_double, _i32, _vp]),
+        ("cmd_paged_attention", ctypes.c_int, [_args, ctypes.c_float, _i32, _vp, _i64, _i32, _vp]),
+        ("cmd_paged_attention_workspace", _i64, [_args, _i32]),
+        ("cmd_page_assign", ctypes.c_int, [_args, _i32, _vp, _i64, _i32, _vp]),
+        ("cmd_page_assign_workspace", _i64, [_args, _i32]),
+        ("cmd_page_compact", ctypes.c_int, [_args, _vp, _i64, _i32, _vp]),
+        ("cmd_page_compact_workspace", _i64, [_args]),
+        ("cmd_page_copy", ctypes.c_int, [_args, _i32, _args, _args, _i32, _vp])]:
+    getattr(lib, _name).restype = _res
+    getattr(lib, _name).argtypes = _sig
+
+# One cmd_arg: kind, dtype, ptr, size[4], stride[4], bits, reserved.
+_ARG = struct.Struct("iiQ4q4qII")
+assert _ARG.size == ctypes.sizeof(cmd_arg)
+_ABSENT = bytes(_ARG.size)
+_codes: dict = {}
+
+
+def _code(dtype) -> int:
+    if not _codes:
+        import torch
+        _codes.update({torch.float16: F16, torch.float32: F32, torch.int32: I32, torch.bfloat16: BF16,
+                       torch.float64: F64})
+    return _codes.get(dtype, 0)
+
+
+def _pack(t, rank: int) -> bytes:
+    """The tensor as a cmd_arg of this rank; another rank is packed with sizes
+    that the library refuses."""
+    code = _codes.get(t.dtype) or _code(t.dtype)
+    size = t.shape
+    if len(size) != rank:
+        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), -1, -1, -1, -1, 0, 0, 0, 0, 0, 0)
+    st = t.stride()
+    if rank == 4:
+        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), *size, *st, 0, 0)
+    if rank == 3:
+        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), *size, 0, *st, 0, 0, 0)
+    if rank == 2:
+        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), *size, 0, 0, *st, 0, 0, 0, 0)
+    return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), size[0], 0, 0, 0, st[0], 0, 0, 0, 0, 0)
+
+
+def _check(rc: int):
+    if rc < 0:
+        raise Error(int(rc), lib.cmd_last_error(None).decode())
+
+
+def _run(call, tensors, stream, workspace=None, need=None):
+    """call(workspace pointer, bytes, flags, stream handle) on the tensors'
+    device.  Tensors that are not all on the current GPU are an error, after
+    the errors that the library finds in them."""
+    import torch
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            dev = -2
+    if dev < 0 or dev != torch.cuda.current_device():
+        _check(call(None, 0, CHECK_ONLY, None))
+        raise Error(-1, "every tensor must be on the current GPU")
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, int):
+        handle = stream
+    else:
+        handle = getattr(stream, "cuda_stream", stream)
+        at = getattr(stream, "device", None)
+        if at is not None and at.index != dev:
+            raise Error(-1, "the stream belongs to another GPU")
+    ptr, size = None, 0
+    if need is not None:
+        size = need()
+        _check(size)
+        if workspace is not None:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise Error(-1, "the workspace must be contiguous and on the current GPU")
+            ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif size:
+            # from the allocator of the launch's stream: it may hand the memory on once that stream is done with it
+            on = contextlib.nullcontext()
+            if stream is not None:
+                on = torch.cuda.stream(torch.cuda.ExternalStream(handle) if isinstance(stream, int) else stream)
+            with on:
+                workspace = torch.empty(size, dtype=torch.uint8, device=tensors[0].device)
+            ptr = workspace.data_ptr()
+    _check(call(ptr, size, 0, handle))
+
+
+def _layout(layout) -> int:
+    return ROPE_LAYOUTS.get(layout, -1)
+
+
+def rope(x, pos, freq, out, *, layout="half", mscale=1.0, inverse=False, stream=None):
+    """Rotary positions (cmd_rope): x [b, t, h, d] turned by pos [b, t] (int32)
+    into out, pair i by pos * freq[i] (freq: float64, on the GPU).  out may be
+    x.  ``inverse`` is the transposed map: applied to the gradient of out it
+    gives the gradient of x."""
+    args = b"".join((_pack(x, 4), _pack(pos, 2), _pack(freq, 1), _pack(out, 4)))
+    _run(lambda w, n, flags, s: lib.cmd_rope(args, _layout(layout), mscale, bool(inverse), flags, s),
+         (x, pos, freq, out), stream)
+
+
+def rope_append(q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache, *, layout="half", mscale=1.0, stream=None):
+    """Rotary positions of packed tokens and the write into the cache
+    (cmd_rope_append): q [T, hq, d] turned into q_out (which may be q), k [T,
+    hk, d] turned and v [T, hk, dv] as it is into the slots of positions pos [T]
+    of sequences row [T].  Tokens whose row, position or page is out of range
+    are padding."""
+    args = b"".join((_pack(q, 3), _pack(k, 3), _pack(v, 3), _pack(pos, 1), _pack(row, 1), _pack(pages, 2),
+                     _pack(freq, 1), _pack(q_out, 3), _pack(k_cache, 4), _pack(v_cache, 4)))
+    _run(lambda w, n, flags, s: lib.cmd_rope_append(args, _layout(layout), mscale, flags, s),
+         (q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache), stream)
+
+
+def _attention_args(q, k_cache, v_cache, pages, lens, out, lse):
+    return b"".join((_pack(q, 3), _pack(k_cache, 4), _pack(v_cache, 4), _pack(pages, 2), _pack(lens, 1),
+                     _pack(out, 3), _ABSENT if lse is None else _pack(lse, 2)))
+
+
+def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=None, window=0, workspace=None,
+                    stream=None):
+    """Attention of one new token per sequence over the paged cache
+    (cmd_paged_attention): q [B, hq, d] over the first lens[r] positions of row
+    r -- the last ``window`` of them if that is not 0 -- into out [B, hq, dv],
+    the log of the softmax's sum into lse [B, hq] (float32) if given.  scale:
+    1 / sqrt(d) by default."""
+    args = _attention_args(q, k_cache, v_cache, pages, lens, out, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(max(1, q.shape[-1])) if q.dim() else 1.0
+    tensors = (q, k_cache, v_cache, pages, lens, out) + (() if lse is None else (lse,))
+    _run(lambda w, n, flags, s: lib.cmd_paged_attention(args, scale, window, w, n, flags, s), tensors, stream,
+         workspace, lambda: lib.cmd_paged_attention_workspace(args, window))
+
+
+def paged_attention_workspace(q, k_cache, v_cache, pages, lens, out, *, window=0) -> int:
+    """Bytes of workspace that paged_attention needs for these tensors."""
+    n = lib.cmd_paged_attention_workspace(_attention_args(q, k_cache, v_cache, pages, lens, out, None), window)
+    _check(n)
+    return n
+
+
+def _assign_args(pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats):
+    return b"".join((_pack(pages, 2), _pack(lens, 1), _pack(refs, 1), _pack(parent, 1), _pack(add, 1),
+                     _pack(pages_out, 2), _pack(lens_out, 1), _pack(refs_out, 1), _pack(src, 1), _pack(dst, 1),
+                     _pack(stats, 1)))
+
+
+def page_assign(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_out, src, dst, stats, *,
+                workspace=None, stream=None):
+    """One step in the page tables (cmd_page_assign): every sequence takes over
+    the state of sequence parent[r] (its own, another's: a fork, or -1: none)
+    and grows by add[r] positions.  Fills pages_out, lens_out, refs_out, the
+    page copies src -> dst that forks need (-1: none) and stats = (pages wanted,
+    pages given).  refs_out may be refs."""
+    tensors = (pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats)
+    args = _assign_args(*tensors)
+    _run(lambda w, n, flags, s: lib.cmd_page_assign(args, page, w, n, flags, s), tensors, stream, workspace,
+         lambda: lib.cmd_page_assign_workspace(args, page))
+
+
+def page_assign_workspace(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_out, src, dst, stats) -> int:
+    """Bytes of workspace that page_assign needs for these tensors."""
+    n = lib.cmd_page_assign_workspace(_assign_args(pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src,
+                                                   dst, stats), page)
+    _check(n)
+    return n
+
+
+def _compact_args(pages, refs, pages_out, refs_out, src, dst, stats):
+    return b"".join((_pack(pages, 2), _pack(refs, 1), _pack(pages_out, 2), _pack(refs_out, 1), _pack(src, 1),
+                     _pack(dst, 1), _pack(stats, 1)))
+
+
+def page_compact(pages, refs, pages_out, refs_out, src, dst, stats, *, workspace=None, stream=None):
+    """Pack the live pages (refs > 0) into the lowest ids (cmd_page_compact):
+    the table and counts after it, the copies src -> dst it takes (then -1) and
+    stats = (live pages, moves).  src and dst hold refs.numel() // 2 entries or
+    more; pages_out may be pages."""
+    tensors = (pages, refs, pages_out, refs_out, src, dst, stats)
+    args = _compact_args(*tensors)
+    _run(lambda w, n, flags, s: lib.cmd_page_compact(args, w, n, flags, s), tensors, stream, workspace,
+         lambda: lib.cmd_page_compact_workspace(args))
+
+
+def page_compact_workspace(pages, refs, pages_out, refs_out, src, dst, stats) -> int:
+    """Bytes of workspace that page_compact needs for these tensors."""
+    n = lib.cmd_page_compact_workspace(_compact_args(pages, refs, pages_out, refs_out, src, dst, stats))
+    _check(n)
+    return n
+
+
+def page_copy(pools, src, dst, *, stream=None):
+    """Copy page src[i] to page dst[i] in every pool [N, page, heads, d]
+    (cmd_page_copy); pairs with an id outside the pool are skipped."""
+    pools = list(pools)
+    args, a, b = b"".join([_pack(p, 4) for p in pools]), _pack(src, 1), _pack(dst, 1)
+    _run(lambda w, n, flags, s: lib.cmd_page_copy(args, len(pools), a, b, flags, s), (src, dst, *pools), stream)
+
+
+def rope_frequencies(width, *, base=10000.0, factor=1.0, scaling="linear", trained=0, slow=1.0, fast=32.0):
+    """The frequency table of a rotary part of this (even) width, float64 on the
+    CPU: base ** (-2 i / width), for contexts ``factor`` times as long as the
+    trained ones changed by ``scaling``:
+
+      "linear"  every frequency divided by factor (positions interpolated);
+      "base"    the base raised so that the slowest pair is divided by factor
+                and the fastest keeps its frequency;
+      "parts"   by how often a pair turns within ``trained`` positions: pairs
+                that turn more than ``fast`` times keep their frequency, those
+                that turn less than ``slow`` times are divided by factor, a
+                linear ramp between (usually with mscale = 0.1 ln factor + 1).
+    """
+    import torch
+    if width < 0 or width % 2:
+        raise ValueError("width must be even, got %d" % width)
+    if factor < 1.0 or scaling not in ("linear", "base", "parts"):
+        raise ValueError("factor must be at least 1 and scaling one of linear, base, parts")
+    if scaling == "base" and width > 2:
+        base = base * factor ** (width / (width - 2.0))
+    f = torch.tensor([base ** (-2.0 * i / width) for i in range(width // 2)], dtype=torch.float64)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if trained <= 0 or fast <= slow:
+            raise ValueError("scaling by parts needs the trained length and slow < fast")
+        keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    return f

@@ -1,0 +1,315 @@
+"""The serving operators on the host: argument checks (every refusal comes
+before any HIP call, so CPU tensors do), workspace sizes, frequency tables, and
+the oracle against hand-worked cases."""
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import elementwise_tensor_commands_amd as E
+import serving_oracle as O
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+I32 = torch.int32
+
+
+def _refused(name, fn, *args, **kw):
+    with pytest.raises(E.Error) as e:
+        fn(*args, **kw)
+    assert e.value.name == name, str(e.value)
+    assert len(str(e.value)) > len(name) + 8      # a message that says what is wrong
+    return str(e.value)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=I32)
+
+
+def test_library_exports_every_declared_function():
+    text = open(os.path.join(ROOT, "include", "ecmd_serving.h")).read()
+    declared = set(re.findall(r"^\s*(?:int|int64_t)\s+(cmd_\w+)\s*\(", text, re.M))
+    assert declared >= {"cmd_rope", "cmd_rope_append", "cmd_paged_attention", "cmd_page_assign", "cmd_page_compact",
+                        "cmd_page_copy"}
+    for name in declared:
+        assert hasattr(E.lib, name), name
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions.
+
+def rope_args(**kw):
+    a = dict(x=torch.zeros(2, 3, 4, 10), pos=i32(2, 3), freq=torch.zeros(4, dtype=torch.float64),
+             out=torch.zeros(2, 3, 4, 10))
+    a.update(kw)
+    return [a[k] for k in ("x", "pos", "freq", "out")]
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("CMD_E_DTYPE", dict(x=torch.zeros(2, 3, 4, 10, dtype=torch.float64))),
+    ("CMD_E_DTYPE", dict(out=torch.zeros(2, 3, 4, 10, dtype=torch.float16))),
+    ("CMD_E_DTYPE", dict(pos=torch.zeros(2, 3, dtype=torch.int64))),
+    ("CMD_E_DTYPE", dict(freq=torch.zeros(4))),
+    ("CMD_E_SHAPE", dict(x=torch.zeros(2, 3, 40))),
+    ("CMD_E_SHAPE", dict(out=torch.zeros(2, 3, 4, 9))),
+    ("CMD_E_SHAPE", dict(pos=i32(3, 2))),
+    ("CMD_E_SHAPE", dict(freq=torch.zeros(6, dtype=torch.float64))),
+    ("CMD_E_STRIDE", dict(out=torch.zeros(2, 3, 10, 4).transpose(2, 3))),
+    ("CMD_E_STRIDE", dict(out=torch.zeros(2, 1, 4, 10).expand(2, 3, 4, 10))),
+])
+def test_rope_refusals(name, kw):
+    _refused(name, E.rope, *rope_args(**kw))
+
+
+def test_rope_refusals_of_options_and_aliases():
+    _refused("CMD_E_ARG", E.rope, *rope_args(), layout="thirds")
+    _refused("CMD_E_ARG", E.rope, *rope_args(), mscale=math.inf)
+    big = torch.zeros(2, 3, 4, 20)
+    _refused("CMD_E_ALIAS", E.rope, *rope_args(x=big[..., :10], out=big[..., 5:15]))
+    _refused("CMD_E_LIMIT", E.rope, *rope_args(x=torch.zeros(1, 1, 1, 5000), out=torch.zeros(1, 1, 1, 5000), pos=i32(1, 1),
+                                               freq=torch.zeros(2049, dtype=torch.float64)))
+    # what is right but on the CPU is refused last, with in-place and packed views
+    x = torch.zeros(2, 3, 4, 10)
+    for args in (rope_args(), rope_args(x=x, out=x), rope_args(x=big[..., :10], out=big[..., 10:])):
+        assert "GPU" in _refused("CMD_E_ARG", E.rope, *args)
+
+
+# ---------------------------------------------------------------------------
+# The append.
+
+def append_args(**kw):
+    kc = torch.zeros(7, 16, 2, 8)
+    a = dict(q=torch.zeros(5, 4, 8), k=torch.zeros(5, 2, 8), v=torch.zeros(5, 2, 6), pos=i32(5), row=i32(5),
+             pages=i32(3, 2), freq=torch.zeros(4, dtype=torch.float64), q_out=torch.zeros(5, 4, 8), k_cache=kc,
+             v_cache=torch.zeros(7, 16, 2, 6))
+    a.update(kw)
+    return [a[k] for k in ("q", "k", "v", "pos", "row", "pages", "freq", "q_out", "k_cache", "v_cache")]
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("CMD_E_DTYPE", dict(k=torch.zeros(5, 2, 8, dtype=torch.bfloat16))),
+    ("CMD_E_DTYPE", dict(row=torch.zeros(5))),
+    ("CMD_E_SHAPE", dict(k=torch.zeros(4, 2, 8))),
+    ("CMD_E_SHAPE", dict(v=torch.zeros(5, 3, 6))),
+    ("CMD_E_SHAPE", dict(pos=i32(4))),
+    ("CMD_E_SHAPE", dict(k_cache=torch.zeros(7, 16, 3, 8))),
+    ("CMD_E_SHAPE", dict(v_cache=torch.zeros(6, 16, 2, 6))),
+    ("CMD_E_SHAPE", dict(v_cache=torch.zeros(7, 8, 2, 6))),
+    ("CMD_E_SHAPE", dict(freq=torch.zeros(5, dtype=torch.float64))),
+    ("CMD_E_STRIDE", dict(k_cache=torch.zeros(7, 16, 8, 2).transpose(2, 3))),
+    ("CMD_E_STRIDE", dict(v_cache=torch.zeros(1, 16, 2, 6).expand(7, 16, 2, 6))),
+])
+def test_append_refusals(name, kw):
+    _refused(name, E.rope_append, *append_args(**kw))
+
+
+def test_append_accepts_packed_and_refuses_overlapping():
+    qkv = torch.zeros(5, 8, 8)
+    packed = dict(q=qkv[:, :4], k=qkv[:, 4:6], v=qkv[:, 6:8], q_out=qkv[:, :4], v_cache=torch.zeros(7, 16, 2, 8))
+    assert "GPU" in _refused("CMD_E_ARG", E.rope_append, *append_args(**packed))       # q turned in place
+    kv = torch.zeros(7, 2, 16, 2, 8)
+    both = dict(v=torch.zeros(5, 2, 8), k_cache=kv[:, 0], v_cache=kv[:, 1])
+    assert "GPU" in _refused("CMD_E_ARG", E.rope_append, *append_args(**both))
+    kv = torch.zeros(7, 16, 2, 2, 8)
+    both.update(k_cache=kv[:, :, 0], v_cache=kv[:, :, 1])
+    assert "GPU" in _refused("CMD_E_ARG", E.rope_append, *append_args(**both))
+    both.update(v_cache=kv[:, :, 0])
+    _refused("CMD_E_ALIAS", E.rope_append, *append_args(**both))
+    packed["q_out"] = qkv[:, 1:5]
+    _refused("CMD_E_ALIAS", E.rope_append, *append_args(**packed))
+
+
+# ---------------------------------------------------------------------------
+# Attention.
+
+def attention_args(**kw):
+    a = dict(q=torch.zeros(3, 4, 8), k=torch.zeros(7, 16, 2, 8), v=torch.zeros(7, 16, 2, 6), pages=i32(3, 2),
+             lens=i32(3), out=torch.zeros(3, 4, 6))
+    a.update(kw)
+    return [a[k] for k in ("q", "k", "v", "pages", "lens", "out")]
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("CMD_E_DTYPE", dict(k=torch.zeros(7, 16, 2, 8, dtype=torch.float16))),
+    ("CMD_E_DTYPE", dict(lens=torch.zeros(3, dtype=torch.int64))),
+    ("CMD_E_SHAPE", dict(q=torch.zeros(3, 4, 9))),
+    ("CMD_E_SHAPE", dict(q=torch.zeros(3, 5, 8), out=torch.zeros(3, 5, 6))),
+    ("CMD_E_SHAPE", dict(v=torch.zeros(7, 15, 2, 6))),
+    ("CMD_E_SHAPE", dict(pages=i32(2, 2))),
+    ("CMD_E_SHAPE", dict(lens=i32(4))),
+    ("CMD_E_SHAPE", dict(out=torch.zeros(3, 4, 8))),
+    ("CMD_E_LIMIT", dict(q=torch.zeros(3, 4, 257), k=torch.zeros(7, 16, 2, 257))),
+    ("CMD_E_LIMIT", dict(pages=torch.zeros(3, 1, dtype=I32).expand(3, 1 << 27))),
+    ("CMD_E_STRIDE", dict(q=torch.zeros(3, 8, 4).transpose(1, 2))),
+    ("CMD_E_STRIDE", dict(out=torch.zeros(3, 1, 6).expand(3, 4, 6))),
+])
+def test_attention_refusals(name, kw):
+    _refused(name, E.paged_attention, *attention_args(**kw))
+    _refused(name, E.paged_attention_workspace, *attention_args(**kw))
+
+
+def test_attention_refusals_of_options():
+    _refused("CMD_E_ARG", E.paged_attention, *attention_args(), window=-1)
+    _refused("CMD_E_ARG", E.paged_attention, *attention_args(), scale=math.nan)
+    _refused("CMD_E_SHAPE", E.paged_attention, *attention_args(), lse=torch.zeros(3, 5))
+    _refused("CMD_E_DTYPE", E.paged_attention, *attention_args(), lse=torch.zeros(3, 4, dtype=torch.float64))
+    a = attention_args(q=torch.zeros(3, 4, 6), k=torch.zeros(7, 16, 2, 6))
+    a[5] = a[0]
+    _refused("CMD_E_ALIAS", E.paged_attention, *a)
+    assert "GPU" in _refused("CMD_E_ARG", E.paged_attention, *attention_args(), lse=torch.zeros(3, 4))
+
+
+def test_attention_workspace():
+    assert E.paged_attention_workspace(*attention_args(pages=i32(3, 1))) == 0           # one step of keys: nothing to join
+    a = attention_args(pages=i32(3, 4096))
+    need = E.paged_attention_workspace(*a)
+    assert need > 0 and E.paged_attention_workspace(*a, window=100) == 0
+    # a workspace too small is refused without a HIP call (from C, as a caller would)
+    from elementwise_tensor_commands_amd import serving as S
+    args = S._attention_args(*a, None)
+    buf = torch.zeros(need, dtype=torch.uint8)
+    assert E.lib.cmd_paged_attention(args, 1.0, 0, None, 0, 0, None) == -1
+    assert E.lib.cmd_paged_attention(args, 1.0, 0, buf.data_ptr(), need - 1, 0, None) == -1
+    assert b"workspace" in E.lib.cmd_last_error(None)
+    assert E.lib.cmd_paged_attention(None, 1.0, 0, None, 0, 0, None) == -1
+    assert E.lib.cmd_paged_attention(args, 1.0, 0, None, 0, 2, None) == -1              # unknown flag
+    assert E.lib.cmd_paged_attention(args, 1.0, 0, None, 0, S.CHECK_ONLY, None) == 0
+
+
+# ---------------------------------------------------------------------------
+# Pages.
+
+def assign_args(**kw):
+    a = dict(pages=i32(3, 4), lens=i32(3), refs=i32(9), parent=i32(3), add=i32(3), page=16, pages_out=i32(3, 4),
+             lens_out=i32(3), refs_out=i32(9), src=i32(3), dst=i32(3), stats=i32(2))
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("CMD_E_DTYPE", dict(pages=torch.zeros(3, 4, dtype=torch.int64))),
+    ("CMD_E_SHAPE", dict(lens=i32(4))),
+    ("CMD_E_SHAPE", dict(pages_out=i32(3, 5))),
+    ("CMD_E_SHAPE", dict(refs_out=i32(8))),
+    ("CMD_E_SHAPE", dict(src=i32(2))),
+    ("CMD_E_SHAPE", dict(stats=i32(3))),
+    ("CMD_E_ARG", dict(page=0)),
+    ("CMD_E_LIMIT", dict(page=1 << 30)),
+    ("CMD_E_STRIDE", dict(lens_out=i32(1).expand(3))),
+])
+def test_assign_refusals(name, kw):
+    _refused(name, E.page_assign, *assign_args(**kw))
+
+
+def test_assign_aliases():
+    p, l, r = i32(3, 4), i32(3), i32(9)
+    _refused("CMD_E_ALIAS", E.page_assign, *assign_args(pages=p, pages_out=p))
+    _refused("CMD_E_ALIAS", E.page_assign, *assign_args(lens=l, lens_out=l))
+    _refused("CMD_E_ALIAS", E.page_assign, *assign_args(src=l, dst=l))
+    assert "GPU" in _refused("CMD_E_ARG", E.page_assign, *assign_args(refs=r, refs_out=r))
+
+
+def compact_args(**kw):
+    a = dict(pages=i32(3, 4), refs=i32(9), pages_out=i32(3, 4), refs_out=i32(9), src=i32(4), dst=i32(4), stats=i32(2))
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("CMD_E_DTYPE", dict(refs=torch.zeros(9))),
+    ("CMD_E_SHAPE", dict(src=i32(3), dst=i32(3))),
+    ("CMD_E_SHAPE", dict(dst=i32(5))),
+    ("CMD_E_SHAPE", dict(pages_out=i32(4, 3))),
+    ("CMD_E_STRIDE", dict(refs_out=i32(1).expand(9))),
+])
+def test_compact_refusals(name, kw):
+    _refused(name, E.page_compact, *compact_args(**kw))
+
+
+def test_compact_aliases():
+    p, r = i32(3, 4), i32(9)
+    _refused("CMD_E_ALIAS", E.page_compact, *compact_args(refs=r, refs_out=r))
+    assert "GPU" in _refused("CMD_E_ARG", E.page_compact, *compact_args(pages=p, pages_out=p))
+
+
+def test_copy_refusals():
+    pool, s, d = torch.zeros(5, 4, 2, 8), i32(3), i32(3)
+    _refused("CMD_E_SHAPE", E.page_copy, [pool], s, i32(4))
+    _refused("CMD_E_SHAPE", E.page_copy, [pool[0]], s, d)
+    _refused("CMD_E_DTYPE", E.page_copy, [pool.to(torch.int8)], s, d)
+    _refused("CMD_E_STRIDE", E.page_copy, [pool[:1].expand(5, 4, 2, 8)], s, d)
+    _refused("CMD_E_STRIDE", E.page_copy, [torch.zeros(5, 8, 4, 16)[:, ::2, ::2, ::2]], s, d)
+    _refused("CMD_E_ALIAS", E.page_copy, [s.view(3, 1, 1, 1)], s, d)
+    assert "GPU" in _refused("CMD_E_ARG", E.page_copy, [pool, pool.transpose(1, 2)], s, d)
+
+
+# ---------------------------------------------------------------------------
+# The oracle and the tables of frequencies.
+
+def test_oracle_by_hand():
+    x = torch.tensor([[[1.0, 2.0, 3.0, 4.0, 5.0]]])
+    quarter = torch.tensor([math.pi / 2, 0.0], dtype=torch.float64)
+    y, _ = O.rope(x, torch.tensor([1]), quarter, "half")           # pairs (1, 3) and (2, 4), the first a quarter turn
+    assert torch.allclose(y, torch.tensor([[[-3.0, 2.0, 1.0, 4.0, 5.0]]]).double(), atol=1e-15)
+    y, _ = O.rope(x, torch.tensor([1]), quarter, "interleaved", mscale=2.0, inverse=True)
+    assert torch.allclose(y, torch.tensor([[[4.0, -2.0, 6.0, 8.0, 5.0]]]).double(), atol=1e-15)
+
+    k = torch.zeros(2, 2, 1, 1)
+    v = torch.tensor([1.0, 2.0, 4.0, 8.0]).view(2, 2, 1, 1)
+    k[1, 0] = math.log(3.0)
+    q = torch.ones(1, 1, 1)
+    pages = torch.tensor([[1, 0, -1]])
+    out, lse, _, _ = O.attention(q, k, v, pages, [3], 1.0)         # keys: 1.0 -> 4 (weight 3), 8, then 1
+    assert abs(out.item() - (3 * 4 + 8 + 1) / 5) < 1e-6 and abs(lse.item() - math.log(5)) < 1e-6
+    out, lse, _, _ = O.attention(q, k, v, pages, [3], 1.0, window=1)
+    assert out.item() == 1.0
+    out, lse, _, _ = O.attention(q, k, v, pages, [0], 1.0)
+    assert out.item() == 0.0 and lse.item() == -math.inf
+    out, lse, _, _ = O.attention(q, k, v, pages, [6], 1.0, window=2)   # only the hole's positions
+    assert out.item() == 0.0 and lse.item() == -math.inf
+
+    # rows: 0 goes on, 1 forks from 0 (shares page 3, copies page 1), 2 ends and starts anew with 5
+    out = O.assign([[3, 1, -1], [4, -1, -1], [0, -1, -1]], [6, 2, 4], [1, 1, 0, 1, 1, 0, 0], [0, 0, -1], [1, 3, 5], 4)
+    assert out[0] == [[3, 1, -1], [3, 2, 5], [6, -1, -1]]
+    assert out[1:] == ([7, 9, 5], [0, 1, 1, 2, 0, 1, 1], [-1, 1, -1], [-1, 2, -1], [4, 3])
+    assert O.compact([[5, 2], [3, 9]], [0, 0, 1, 1, 0, 2], 3) == (
+        [[1, 2], [0, -1]], [1, 2, 1, 0, 0, 0], [3, 5, -1], [0, 1, -1], [3, 2])
+
+
+def test_rope_gradient_is_the_inverse():
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(2, 3, 9, generator=g, dtype=torch.float64)
+    dy = torch.randn(2, 3, 9, generator=g, dtype=torch.float64)
+    pos, freq = torch.tensor([3, 7]), E.rope_frequencies(8)
+    for layout in ("half", "interleaved"):
+        dx, _ = O.rope(dy, pos, freq, layout, 1.3, inverse=True)
+        leaf = x.clone().requires_grad_()
+        u, v = O.pairs(leaf, 4, layout)
+        w = pos.double()[:, None, None] * freq
+        turned = torch.cat([u * w.cos() - v * w.sin(), v * w.cos() + u * w.sin()], -1) * 1.3
+        want = torch.cat([*O.pairs(dy, 4, layout)], -1)
+        ((turned * want).sum() + (leaf[..., 8:] * dy[..., 8:]).sum()).backward()
+        assert torch.allclose(leaf.grad, dx, atol=1e-12)
+        for i in (0, 4, 8):                                        # and against differences
+            h = 1e-4
+            e = torch.zeros_like(x)
+            e[1, 2, i] = h
+            d = ((O.rope(x + e, pos, freq, layout, 1.3)[0] - O.rope(x - e, pos, freq, layout, 1.3)[0]) * dy).sum() / (2 * h)
+            assert abs(float(d) - float(dx[1, 2, i])) < 1e-9
+
+
+def test_frequencies():
+    f = E.rope_frequencies(8)
+    assert f.dtype == torch.float64 and torch.allclose(f, 10000.0 ** (-torch.arange(4).double() / 4))
+    assert torch.allclose(E.rope_frequencies(8, factor=4.0), f / 4)
+    b = E.rope_frequencies(8, factor=4.0, scaling="base")
+    assert b[0] == 1 and abs(float(b[3] * 4 / f[3]) - 1) < 1e-12
+    p = E.rope_frequencies(128, factor=8.0, scaling="parts", trained=4096)
+    q = E.rope_frequencies(128)
+    assert p[0] == q[0] and abs(float(p[-1] * 8 / q[-1]) - 1) < 1e-12
+    assert bool(((p <= q) & (p >= q / 8 * (1 - 1e-12))).all())
+    assert E.rope_frequencies(0).numel() == 0 and E.rope_frequencies(2, factor=2.0, scaling="base").tolist() == [1.0]
+    for bad in (dict(width=7), dict(width=8, factor=0.5), dict(width=8, scaling="x"), dict(width=8, factor=2.0, scaling="parts")):
+        with pytest.raises(ValueError):
+            E.rope_frequencies(**bad)
