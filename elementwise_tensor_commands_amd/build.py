@@ -46,6 +46,10 @@ FLAGS = [
     "-Wall", "-Wno-unused-function", "-I", os.path.join(ROOT, "include"),
 ]
 
+# Further flags of single sources.  Attention: matrix results in the general
+# registers; with the accumulation registers, which the compiler otherwise gives
+# half of the file, the loop moved 32 values there and back in every turn.
+FILE_FLAGS = {"kernels_attention_%s.hip" % t: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for t in ("f16", "bf16", "f32")}
 
 # Options for run-time compilation: the device side of FLAGS.
 JIT_OPTIONS = ["--offload-arch=" + ARCH, "-O3", "-std=c++20", "-ffp-contract=off", "-fno-fast-math",
@@ -117,9 +121,10 @@ def build(asm: bool = True, verbose: bool = False) -> str:
         obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
         objs.append(obj)
         lang = ["-x", "hip"] if src.endswith(".hip") else []
-        cmds.append([HIPCC, *FLAGS, *lang, "-c", path, "-o", obj])
+        extra = FILE_FLAGS.get(src, [])
+        cmds.append([HIPCC, *FLAGS, *extra, *lang, "-c", path, "-o", obj])
         if asm and src.endswith(".hip"):
-            cmds.append([HIPCC, *FLAGS, "-x", "hip", "--offload-device-only", "-S",
+            cmds.append([HIPCC, *FLAGS, *extra, "-x", "hip", "--offload-device-only", "-S",
                          os.path.join(CSRC, src), "-o", os.path.join(BUILD, os.path.splitext(src)[0] + ".s")])
     if verbose:
         for c in cmds:

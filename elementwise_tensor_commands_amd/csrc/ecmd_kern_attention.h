@@ -28,6 +28,13 @@
 //            column VW h + c.
 //
 // A head's maximum and rescale factor belong to one lane column: no transposes.
+//
+// Rows differ in length (some are empty, the table says how long they could be,
+// not how long they are), so positions are dealt to work-groups by what the
+// lengths say on the device: the rows' positions in steps of 128, laid end to
+// end, are cut into equal runs, one for each work-group of a head.  A run may
+// span rows; each row in it is a segment with a start and an end of its own.
+// Segments of a row that is cut are joined by a second launch.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -72,25 +79,36 @@ __device__ inline f32x4 mma16(u32x4 a, u32x4 b, f32x4 c)
 
 __device__ inline float as_f(uint32_t x) { return __builtin_bit_cast(float, x); }
 
-// The first n elements (16-bit or 32-bit, `E` to a piece) of 16 bytes at p, the
-// rest 0; nothing past them is read.
-template <class T, int E, bool RAGGED>
-__device__ inline u32x4 load_piece(const char *p, int n)
+// x, computed here: what depends on it is not moved out of a loop into registers
+// that the loop needs.
+__device__ inline uint32_t fresh(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// 16 bytes at p, wherever that is.
+__device__ inline u32x4 load16(const char *p)
+{
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+// The first n of N elements at p, the rest 0; nothing past them is read.
+template <class T, int N>
+__device__ inline u32x4 load_some(const char *p, int n)
 {
     u32x4 v = {0, 0, 0, 0};
-    if (!RAGGED || n >= E) {
-        __builtin_memcpy(&v, p, 16);
-    } else if (n > 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (e < n) {
-                T x;
-                __builtin_memcpy(&x, p + e * sizeof(T), sizeof x);
-                if constexpr (E == 8)
-                    v[e / 2] |= (uint32_t)x << (16 * (e & 1));
-                else
-                    v[e] = __builtin_bit_cast(uint32_t, x);
-            }
+    for (int e = 0; e < N; ++e) {
+        if (e < n) {
+            T x;
+            __builtin_memcpy(&x, p + e * sizeof(T), sizeof x);
+            if constexpr (sizeof(T) == 2)
+                v[e / 2] |= (uint32_t)x << (16 * (e & 1));
+            else
+                v[e] = __builtin_bit_cast(uint32_t, x);
         }
     }
     return v;
@@ -110,11 +128,35 @@ __device__ inline Span row_span(const AttnArgs &A, uint32_t r)
     if (A.window && (uint32_t)len > A.window) s.lo = min((uint32_t)len - A.window, s.hi);
     return s;
 }
-// Each split's share of them: equal, in whole work-group steps.
-__device__ inline uint32_t split_share(const AttnArgs &A, uint32_t keys)
+__device__ inline uint32_t span_steps(Span s) { return (s.hi - s.lo + kAttnStep - 1) / kAttnStep; }
+
+// Steps before each row, and all of them, into prefix[0 .. b]; ends with a barrier.
+__device__ inline void row_prefixes(const AttnArgs &A, uint32_t *prefix, uint32_t *scratch)
 {
-    const uint32_t each = A.by_splits.div(keys + A.splits - 1);
-    return (each + kAttnShare - 1) / kAttnShare * kAttnShare;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t run = 0;
+    for (uint32_t r0 = 0; r0 < A.b; r0 += kAttnBlock) {
+        const uint32_t r = r0 + threadIdx.x;
+        const uint32_t x = r < A.b ? span_steps(row_span(A, r)) : 0;
+        uint32_t inc = x;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const uint32_t y = __shfl_up(inc, o);
+            if (lane >= (uint32_t)o) inc += y;
+        }
+        if (lane == 63) scratch[wave] = inc;
+        __syncthreads();
+        uint32_t before = run;
+#pragma unroll
+        for (uint32_t w = 0; w < kAttnWaves; ++w) {
+            if (w < wave) before += scratch[w];
+            run += scratch[w];
+        }
+        if (r < A.b) prefix[r] = before + inc - x;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) prefix[A.b] = run;
+    __syncthreads();
 }
 
 template <int TY>
@@ -137,17 +179,34 @@ constexpr float kSlack = 8.0f;
 template <int TY>
 constexpr float kBias = TY == S_F16 ? 6.0f : 0.0f;
 
+// How pieces that reach past the end of a row of d or dv elements are read.
+enum AttnEdge {
+    kExact,   // there are none: d = 4 E NK
+    kTail,    // moved back to end with the row; keys' elements read twice are masked off
+    kTiny,    // element by element: rows shorter than a piece
+};
+
+// Waves of a SIMD that an instance asks for: what its registers (keys, values,
+// query, sums and the rest, about) leave room for without spills in the loop.
+template <int TY, int NK, int VW, AttnEdge EDGE>
+constexpr int attn_waves()
+{
+    constexpr int KB = AttnType<TY>::KB, size = TY == S_F32 ? 4 : 2;
+    constexpr int regs = KB * NK * 4 + KB * VW * size + NK * 4 + VW * 4 + (TY == S_F32 ? 52 : 60) + (EDGE == kTail ? 10 : 0);
+    return regs > 268 ? 1 : regs > 172 ? 2 : regs > (TY == S_F32 ? 128 : 112) ? 3 : 4;
+}
+
 // VW: value columns of a lane (16 VW >= dv).  NK: 16-byte key pieces of a lane
-// (4 E NK >= d).  RAGGED: d is not 4 E NK, or dv no multiple of VW.
-template <int TY, int NK, int VW, bool RAGGED>
-__global__ __launch_bounds__(kAttnBlock) void k_attention(const AttnArgs A)
+// (4 E NK >= d).  DIRECT: a work-group takes one whole row, nothing is joined.
+template <int TY, int NK, int VW, AttnEdge EDGE, bool DIRECT>
+__global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void k_attention(const AttnArgs A)
 {
     typedef typename AttnType<TY>::T T;
     constexpr int E = AttnType<TY>::E, KB = AttnType<TY>::KB;
-    constexpr int VK = 4 * KB;                        // keys whose values a lane holds
-    constexpr int VP = VW * (int)sizeof(T) / 16 > 0 ? VW * (int)sizeof(T) / 16 : 1;   // 16-byte pieces of those
+    constexpr int VK = 4 * KB;                                  // keys whose values a lane holds
+    constexpr int PE = VW < E ? VW : E, VP = VW / PE;           // elements of a value piece; pieces
     constexpr uint32_t kTile = 16 * KB;
-    constexpr int kRow = 16 * VW + 4;                 // a head's row in the joining buffer (floats)
+    constexpr int kRow = 16 * VW + 4;                           // a head's row in the joining buffer (floats)
 
     __shared__ union {
         struct {
@@ -156,281 +215,356 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention(const AttnArgs A)
         } table;
         float join[kAttnWaves][8][kRow];
     } sh;
-    __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
+    __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16], s_ref[16], s_total[16];
+    extern __shared__ uint32_t s_prefix[];   // [b + 1], unless DIRECT
+    __shared__ uint32_t s_scratch[kAttnWaves];
 
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane >> 4, hh = lane & 15;
-    // heads of one row and split are neighbours: together they read whole slots
+    // heads of one run are neighbours: together they read whole slots
     const uint32_t heads = A.hk * A.head_tiles;
-    const uint32_t rs = A.by_heads.div(blockIdx.x), head = blockIdx.x - rs * heads;
-    const uint32_t r = A.by_splits.div(rs), split = rs - r * A.splits;
+    const uint32_t group = A.by_heads.div(blockIdx.x), head = blockIdx.x - group * heads;
     const uint32_t kvh = head / A.head_tiles, ht = head - kvh * A.head_tiles;
     const uint32_t q0 = kvh * A.group + ht * 16, q_n = min(16u, A.group - ht * 16);
 
-    const Span span = row_span(A, r);
-    const uint32_t share = split_share(A, span.hi - span.lo);
-    const uint32_t begin = span.lo + split * share;
-    // the first split of an empty row still writes its zeros
-    if (split > 0 && (split * (uint64_t)share >= span.hi - span.lo)) return;
-    const uint32_t end = min(begin + share, span.hi);
-    const uint32_t wshare = share / kAttnWaves;
-    const uint32_t wb = min(begin + wave * wshare, end), we = min(wb + wshare, end);
-
-    u32x4 q[NK];
-#pragma unroll
-    for (int c = 0; c < NK; ++c) {
-        const int at = (c * 4 + j) * E;
-        const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)(q0 + hh) * A.qs[1] + at) * sizeof(T);
-        q[c] = u32x4{0, 0, 0, 0};
-        if (hh < q_n) q[c] = load_piece<T, E, RAGGED>(p, (int)A.d - at);
+    // The run of this work-group: steps [step, stop) of all rows', from row r on.
+    uint32_t r = group, step = 0, stop = 0, share = 1;
+    if constexpr (!DIRECT) {
+        row_prefixes(A, s_prefix, s_scratch);
+        const uint32_t all = s_prefix[A.b];
+        share = max(1u, A.by_groups.div(all + A.groups - 1));
+        step = group * share;
+        stop = min(step + share, all);
+        if (step >= stop) return;
+        uint32_t lo = 0, hi = A.b;   // the row with prefix[r] <= step < prefix[r + 1]
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) / 2;
+            if (s_prefix[mid] <= step) lo = mid;
+            else hi = mid;
+        }
+        r = lo;
     }
 
-    f32x4 acc[VW];
+    // Where a lane's value pieces start; the last ones end with the row.
+    auto column = [&](uint32_t m, int piece) {
+        const uint32_t at = m * VW + piece * PE;
+        return EDGE == kTiny ? at : min(at, A.dv - PE);
+    };
+    // Piece c of a row of d elements at p.  One that would reach past the end is
+    // moved back to end with the row; masked() clears what earlier ones have, all
+    // of it where the piece lies past the end altogether.
+    auto load_row_piece = [&](const char *p, int c) {
+        const int at = (c * 4 + (int)j) * E;
+        if constexpr (EDGE == kTiny) return load_some<T, E>(p + at * sizeof(T), (int)A.d - at);
+        return load16(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
+    };
+    auto masked = [&](u32x4 x, int c) {
+        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {   // the same for the whole launch
+            const int at = (c * 4 + (int)j) * E, twice = at - min(at, (int)A.d - E);
 #pragma unroll
-    for (int c = 0; c < VW; ++c) acc[c] = f32x4{0, 0, 0, 0};
-    float m = -INFINITY, mref = 0.0f, l = 0.0f;
-
-    const char *kbase = (const char *)A.k + (int64_t)kvh * A.kcs[2] + j * 16;
-    const uint32_t vcol = RAGGED ? hh * VW : min(hh * VW, A.dv - VW);
-    const char *vbase = (const char *)A.v + (int64_t)kvh * A.vcs[2] + vcol * sizeof(T);
-    const int vleft = (int)A.dv - (int)vcol;
-
-    // Offsets of the wave's next kTableKeys positions; what is no position of
-    // this row's gets slot 0 of page 0, which exists, and a clear bit.
-    auto fill = [&](uint32_t at) {
-#pragma unroll
-        for (uint32_t g = 0; g < kTableKeys / 64; ++g) {
-            const uint32_t pos = at + g * 64 + lane;
-            int32_t id = -1;
-            uint32_t in = 0;
-            if (pos < we) {
-                const uint32_t col = A.by_page.div(pos);
-                in = pos - col * A.page;
-                id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
+            for (int w = 0; w < 4; ++w) {
+                if constexpr (E == 8)
+                    x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
+                else
+                    x[w] &= w >= twice ? ~0u : 0u;
             }
-            const bool ok = id >= 0 && (uint32_t)id < A.n;
-            if (!ok) id = 0, in = 0;
-            sh.table.k[wave][g * 64 + lane] = (uint64_t)((int64_t)id * A.kcs[0] + (int64_t)in * A.kcs[1]);
-            sh.table.v[wave][g * 64 + lane] = (uint64_t)((int64_t)id * A.vcs[0] + (int64_t)in * A.vcs[1]);
-            const uint64_t bits = __ballot(ok);
-            if (lane == 0) sh.table.valid[wave][g] = bits;
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        return x;
     };
 
-    u32x4 kr[KB][NK];
-    u32x4 vr[VK][VP];
-    uint32_t bits = 0;   // which of the tile's positions count
-    auto load_k = [&](uint32_t t) {   // t: offset of the tile in the table
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            const char *p = kbase + sh.table.k[wave][t + kb * 16 + hh];
-#pragma unroll
-            for (int c = 0; c < NK; ++c)
-                kr[kb][c] = load_piece<T, E, RAGGED>(p + c * 64, (int)A.d - (c * 4 + (int)j) * E);
+    const char *kbase = (const char *)A.k + (int64_t)kvh * A.kcs[2];
+    const char *vbase = (const char *)A.v + (int64_t)kvh * A.vcs[2];
+
+    for (;;) {   // one row of the run
+        const Span span = row_span(A, r);
+        uint32_t begin = span.lo, end = span.hi, steps = span_steps(span);
+        bool whole_row = true;
+        if constexpr (!DIRECT) {
+            const uint32_t first = s_prefix[r], last = s_prefix[r + 1];
+            const uint32_t here = min(stop, last);
+            whole_row = step == first && here == last;
+            begin += (step - first) * kAttnStep;
+            steps = here - step;
+            end = min(begin + steps * kAttnStep, span.hi);
         }
-        bits = (uint32_t)(sh.table.valid[wave][t / 64] >> (t % 64));
-        if constexpr (KB == 1) bits &= 0xFFFFu;
-        bits = __builtin_amdgcn_readfirstlane(bits);
-    };
-    auto load_v = [&](uint32_t t) {
+        const uint32_t wshare = steps * (kAttnStep / kAttnWaves);
+        const uint32_t wb = min(begin + wave * wshare, end), we = min(wb + wshare, end);
+
+        u32x4 q[NK];
 #pragma unroll
-        for (int x = 0; x < VK; ++x) {
-            const char *p = vbase + sh.table.v[wave][t + (x / 4) * 16 + j * 4 + x % 4];
+        for (int c = 0; c < NK; ++c) {
+            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)(q0 + (hh < q_n ? hh : 0)) * A.qs[1]) * sizeof(T);
+            q[c] = masked(load_row_piece(p, c), c);
+            if (hh >= q_n) q[c] = u32x4{0, 0, 0, 0};
+        }
+
+        f32x4 acc[VW];
 #pragma unroll
-            for (int c = 0; c < VP; ++c) {
-                if constexpr (VW * sizeof(T) >= 16) {
-                    vr[x][c] = load_piece<T, E, RAGGED>(p + c * 16, vleft - c * E);
-                } else {   // four 16-bit columns
-                    vr[x][c] = u32x4{0, 0, 0, 0};
-                    if (!RAGGED || vleft >= VW)
-                        __builtin_memcpy(&vr[x][c], p, VW * sizeof(T));
+        for (int c = 0; c < VW; ++c) acc[c] = f32x4{0, 0, 0, 0};
+        float m = -INFINITY, mref = 0.0f, l = 0.0f;
+
+        // Offsets of the wave's next kTableKeys positions; what is no position of
+        // this row's gets slot 0 of page 0, which exists, and a clear bit.
+        auto fill = [&](uint32_t at) {
+            constexpr int G = kTableKeys / 64;
+            int32_t id[G];
+            uint32_t in[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint32_t pos = min(at + g * 64 + lane, we - 1), col = A.by_page.div(pos);
+                in[g] = pos - col * A.page;
+                id[g] = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const bool ok = at + g * 64 + lane < we && id[g] >= 0 && (uint32_t)id[g] < A.n;
+                const int64_t page = ok ? id[g] : 0, slot = ok ? in[g] : 0;
+                sh.table.k[wave][g * 64 + lane] = (uint64_t)(page * A.kcs[0] + slot * A.kcs[1]);
+                sh.table.v[wave][g * 64 + lane] = (uint64_t)(page * A.vcs[0] + slot * A.vcs[1]);
+                const uint64_t bits = __ballot(ok);
+                if (lane == 0) sh.table.valid[wave][g] = bits;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+
+        u32x4 kr[KB][NK];
+        u32x4 vr[VK][VP];
+        uint32_t bits = 0;   // which of the tile's positions count
+        auto load_k = [&](uint32_t t) {   // t: offset of the tile in the table
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const char *p = kbase + sh.table.k[wave][t + kb * 16 + hh];
+#pragma unroll
+                for (int c = 0; c < NK; ++c) kr[kb][c] = load_row_piece(p, c);
+            }
+            bits = (uint32_t)(sh.table.valid[wave][t / 64] >> (t % 64));
+            if constexpr (KB == 1) bits &= 0xFFFFu;
+            bits = __builtin_amdgcn_readfirstlane(bits);
+        };
+        auto load_v = [&](uint32_t t) {
+#pragma unroll
+            for (int x = 0; x < VK; ++x) {
+                const char *p = vbase + sh.table.v[wave][t + (x / 4) * 16 + j * 4 + x % 4];
+#pragma unroll
+                for (int c = 0; c < VP; ++c) {
+                    const uint32_t at = column(hh, c);
+                    if constexpr (EDGE == kTiny)
+                        vr[x][c] = load_some<T, PE>(p + at * sizeof(T), (int)A.dv - (int)at);
                     else
-                        vr[x][c] = load_piece<T, E, true>(p, vleft);
+                        __builtin_memcpy(&vr[x][c], p + at * sizeof(T), PE * sizeof(T));
                 }
             }
-        }
-    };
+        };
 
-    uint32_t tile = wb, in_table = 0;
-    if (wb < we) {
-        fill(wb);
-        load_k(0);
-        load_v(0);
-    }
-    while (tile < we) {
-        // scores of head hh at the lane's keys
-        f32x4 s[KB];
+        uint32_t tile = wb, in_table = 0;
+        if (wb < we) {
+            fill(wb);
+            load_k(0);
+            load_v(0);
+        }
+        while (tile < we) {
+            // scores of head hh at the lane's keys
+            f32x4 s[KB];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            s[kb] = f32x4{0, 0, 0, 0};
+            for (int kb = 0; kb < KB; ++kb) {
+                s[kb] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int c = 0; c < NK; ++c) {
-                if constexpr (TY == S_F32) {
+                for (int c = 0; c < NK; ++c) {
+                    const u32x4 k = masked(kr[kb][c], c);
+                    if constexpr (TY == S_F32) {
 #pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        s[kb] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(kr[kb][c][f]), as_f(q[c][f]), s[kb], 0, 0, 0);
-                } else {
-                    s[kb] = mma16<TY>(kr[kb][c], q[c], s[kb]);
+                        for (int f = 0; f < 4; ++f)
+                            s[kb] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(k[f]), as_f(q[c][f]), s[kb], 0, 0, 0);
+                    } else {
+                        s[kb] = mma16<TY>(k, q[c], s[kb]);
+                    }
                 }
             }
-        }
-        const uint32_t now = bits;
-        const uint32_t v_at = in_table;
-        (void)v_at;
-        tile += kTile;
-        in_table += kTile;
-        if (tile < we) {
-            if (in_table == kTableKeys) {
-                fill(tile);
-                in_table = 0;
+            const uint32_t now = bits;
+            tile += kTile;
+            in_table += kTile;
+            if (tile < we) {
+                if (in_table == kTableKeys) {
+                    fill(tile);
+                    in_table = 0;
+                }
+                load_k(in_table);
             }
-            load_k(in_table);
-        }
 
-        float p[VK];
-        float top = -INFINITY;
-        const bool whole = now == (KB == 2 ? 0xFFFFFFFFu : 0xFFFFu);
+            float p[VK];
+            float top = -INFINITY;
+            const bool whole = now == (KB == 2 ? 0xFFFFFFFFu : 0xFFFFu);
 #pragma unroll
-        for (int x = 0; x < VK; ++x) {
-            p[x] = s[x / 4][x % 4] * A.scale_log2;
+            for (int x = 0; x < VK; ++x) p[x] = s[x / 4][x % 4] * A.scale_log2;
             if (!whole) {
-                const bool ok = now >> ((x / 4) * 16 + j * 4 + x % 4) & 1;
-                p[x] = ok ? p[x] : -INFINITY;
-                if (!ok) {   // whatever lies there may be NaN: it gets weight 0 and value 0
+                // whatever lies in other slots may be NaN: it gets weight 0 and value 0
 #pragma unroll
-                    for (int c = 0; c < VP; ++c) vr[x][c] = u32x4{0, 0, 0, 0};
-                }
-            }
-            top = fmaxf(top, p[x]);
-        }
-        if (__any(top > m + kSlack)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float mn = fmaxf(m, top);
-            mref = mn == -INFINITY ? 0.0f : mn;
-            const float a = __builtin_amdgcn_exp2f(m - mref);
-            m = mn;
-            l *= a;
+                for (int x = 0; x < VK; ++x) {
+                    const bool ok = now >> ((x / 4) * 16 + j * 4 + x % 4) & 1;
+                    p[x] = ok ? p[x] : -INFINITY;
+                    const uint32_t keep = ok ? ~0u : 0u;
 #pragma unroll
-            for (int c = 0; c < VW; ++c) acc[c] *= a;
-        }
-#pragma unroll
-        for (int x = 0; x < VK; ++x) {
-            p[x] = __builtin_amdgcn_exp2f(p[x] - (mref - kBias<TY>));
-            l += p[x];
-        }
-
-        if constexpr (TY == S_F32) {
-#pragma unroll
-            for (int x = 0; x < VK; ++x)
-#pragma unroll
-                for (int c = 0; c < VW; ++c)
-                    acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(vr[x][c / 4][c % 4]), p[x], acc[c], 0, 0, 0);
-        } else {
-            // A weight goes in as the sum of two 16-bit numbers, its leading bits
-            // and the rest: weights rounded to one would double the error of the
-            // output's own rounding, and the matrix units are idle enough.
-            u32x4 hi, lo;
-#pragma unroll
-            for (int x = 0; x < VK; x += 2) {
-                if constexpr (TY == S_BF16) {
-                    const uint32_t a = __builtin_bit_cast(uint32_t, p[x]), b = __builtin_bit_cast(uint32_t, p[x + 1]);
-                    hi[x / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);
-                    const f32x2 rest = {p[x] - as_f(a & 0xFFFF0000u), p[x + 1] - as_f(b & 0xFFFF0000u)};
-                    lo[x / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
-                } else {
-                    const auto h = __builtin_amdgcn_cvt_pkrtz(p[x], p[x + 1]);
-                    hi[x / 2] = __builtin_bit_cast(uint32_t, h);
-                    lo[x / 2] = __builtin_bit_cast(
-                        uint32_t, __builtin_amdgcn_cvt_pkrtz(p[x] - (float)h[0], p[x + 1] - (float)h[1]));
+                    for (int c = 0; c < VP; ++c) vr[x][c] = vr[x][c] & u32x4{keep, keep, keep, keep};
                 }
             }
 #pragma unroll
-            for (int c = 0; c < VW; ++c) {
-                u32x4 a;
+            for (int x = 0; x < VK; ++x) top = fmaxf(top, p[x]);
+            if (__any(top > m + kSlack)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float mn = fmaxf(m, top);
+                mref = mn == -INFINITY ? 0.0f : mn;
+                const float a = __builtin_amdgcn_exp2f(m - mref);
+                m = mn;
+                l *= a;
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    a[w] = __builtin_amdgcn_perm(vr[2 * w + 1][c / 8][c % 8 / 2], vr[2 * w][c / 8][c % 8 / 2],
-                                                 c & 1 ? 0x07060302 : 0x05040100);
-                acc[c] = mma16<TY>(a, hi, acc[c]);
-                acc[c] = mma16<TY>(a, lo, acc[c]);
+                for (int c = 0; c < VW; ++c) acc[c] *= a;
             }
-        }
-        if (tile < we) load_v(in_table);
-    }
+#pragma unroll
+            for (int x = 0; x < VK; ++x) {
+                p[x] = __builtin_amdgcn_exp2f(p[x] - (mref - kBias<TY>));
+                l += p[x];
+            }
 
-    // Join the waves: common maximum, then sums head by head through LDS, eight
-    // heads at a time.
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    __syncthreads();   // the tables are done with
-    if (lane < 16) {
-        s_m[wave][lane] = m;
-        s_l[wave][lane] = l;
-    }
-    __syncthreads();
-    float mj = -INFINITY;
+            if constexpr (TY == S_F32) {
 #pragma unroll
-    for (int w = 0; w < (int)kAttnWaves; ++w) mj = fmaxf(mj, s_m[w][hh]);
-    const float factor = __builtin_amdgcn_exp2f(m - (mj == -INFINITY ? 0.0f : mj));
+                for (int x = 0; x < VK; ++x)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        if (half * 8 >= (int)q_n) break;
-        if (half) __syncthreads();
-        if ((hh >> 3) == (uint32_t)half) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < VW; ++c) sh.join[wave][hh & 7][(j * 4 + i) * VW + c] = acc[c][i] * factor;
-        }
-        __syncthreads();
-        for (uint32_t x = threadIdx.x; x < 8 * 16 * VW; x += kAttnBlock) {
-            const uint32_t g = x / (16 * VW), c = x % (16 * VW), hx = half * 8 + g;
-            if (hx >= q_n || c >= A.dv) continue;
-            float sum = 0.0f, total = 0.0f, mm = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < (int)kAttnWaves; ++w) mm = fmaxf(mm, s_m[w][hx]);
-            const float ref = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-            for (int w = 0; w < (int)kAttnWaves; ++w) {
-                sum += sh.join[w][g][c];
-                total += s_l[w][hx] * __builtin_amdgcn_exp2f(s_m[w][hx] - ref);
-            }
-            const uint32_t h = q0 + hx;
-            if (A.splits == 1) {
-                store_out<TY>(A, r, h, c, total == 0.0f ? 0.0f : sum / total);
-                if (c == 0 && A.lse)
-                    A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] =
-                        total == 0.0f ? -INFINITY : (ref - kBias<TY> + log2f(total)) * 0.69314718055994530942f;
+                    for (int c = 0; c < VW; ++c)
+                        acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(vr[x][c / 4][c % 4]), p[x], acc[c], 0, 0, 0);
             } else {
-                const uint64_t at = ((uint64_t)r * A.hq + h) * A.splits + split;
-                A.acc[at * A.dv + c] = sum;
-                if (c == 0) {
-                    A.ml[2 * at] = mm;
-                    A.ml[2 * at + 1] = total;
+                // A weight goes in as the sum of two 16-bit numbers, its leading bits
+                // and the rest: weights rounded to one would double the error of the
+                // output's own rounding, and the matrix units are idle enough.
+                u32x4 hi, lo;
+#pragma unroll
+                for (int x = 0; x < VK; x += 2) {
+                    if constexpr (TY == S_BF16) {
+                        const uint32_t a = __builtin_bit_cast(uint32_t, p[x]), b = __builtin_bit_cast(uint32_t, p[x + 1]);
+                        hi[x / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);
+                        const f32x2 rest = {p[x] - as_f(a & 0xFFFF0000u), p[x + 1] - as_f(b & 0xFFFF0000u)};
+                        lo[x / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
+                    } else {
+                        const auto h = __builtin_amdgcn_cvt_pkrtz(p[x], p[x + 1]);
+                        hi[x / 2] = __builtin_bit_cast(uint32_t, h);
+                        lo[x / 2] = __builtin_bit_cast(
+                            uint32_t, __builtin_amdgcn_cvt_pkrtz(p[x] - (float)h[0], p[x + 1] - (float)h[1]));
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < VW; ++c) {
+                    u32x4 a;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        a[w] = __builtin_amdgcn_perm(vr[2 * w + 1][c / 8][c % 8 / 2], vr[2 * w][c / 8][c % 8 / 2],
+                                                     c & 1 ? 0x07060302 : 0x05040100);
+                    acc[c] = mma16<TY>(a, hi, acc[c]);
+                    acc[c] = mma16<TY>(a, lo, acc[c]);
                 }
             }
+            if (tile < we) load_v(in_table);
+        }
+
+        // Join the waves: common maximum, then sums head by head through LDS,
+        // eight heads at a time.
+        const uint32_t tid = fresh(threadIdx.x), eh = tid & 15, ej = tid >> 4 & 3;
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (ej == 0) {
+            s_m[wave][eh] = m;
+            s_l[wave][eh] = l;
+        }
+        __syncthreads();   // also: the tables are done with
+        float mj = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < (int)kAttnWaves; ++w) mj = fmaxf(mj, s_m[w][eh]);
+        const float ref = mj == -INFINITY ? 0.0f : mj;
+        if (tid < 16) {
+            float total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < (int)kAttnWaves; ++w) total += s_l[w][eh] * __builtin_amdgcn_exp2f(s_m[w][eh] - ref);
+            s_ref[eh] = mj;
+            s_total[eh] = total;
+        }
+        const float factor = __builtin_amdgcn_exp2f(m - ref);
+        const bool final = DIRECT || whole_row;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half * 8 >= (int)q_n) break;
+            if (half) __syncthreads();
+            if ((eh >> 3) == (uint32_t)half) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < VW; ++c)
+                        sh.join[wave][eh & 7][column(ej * 4 + i, c / PE) + c % PE] = acc[c][i] * factor;
+            }
+            __syncthreads();
+            for (uint32_t x = tid; x < 8 * 16 * VW; x += kAttnBlock) {
+                const uint32_t g = x / (16 * VW), c = x % (16 * VW), hx = half * 8 + g;
+                if (hx >= q_n || c >= A.dv) continue;
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < (int)kAttnWaves; ++w) sum += sh.join[w][g][c];
+                const float total = s_total[hx], top = s_ref[hx];
+                const uint32_t h = q0 + hx;
+                if (final) {
+                    store_out<TY>(A, r, h, c, total == 0.0f ? 0.0f : sum / total);
+                    if (c == 0 && A.lse)
+                        A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] =
+                            total == 0.0f ? -INFINITY
+                                          : ((top == -INFINITY ? 0.0f : top) - kBias<TY> + log2f(total)) *
+                                                0.69314718055994530942f;
+                } else {
+                    // the segment's place: work-groups and rows only go forward
+                    const uint64_t at = (uint64_t)(group + r) * A.hq + h;
+                    A.acc[at * A.dv + c] = sum;
+                    if (c == 0) {
+                        A.ml[2 * at] = top;
+                        A.ml[2 * at + 1] = total;
+                    }
+                }
+            }
+        }
+        if constexpr (DIRECT) {
+            return;
+        } else {
+            step += steps;
+            if (step >= stop) return;
+            do ++r;
+            while (s_prefix[r + 1] <= step);   // past empty rows
+            __syncthreads();
         }
     }
 }
 
-// Joins the splits of one row and query head (a work-group).
+// Joins the segments of one row and query head (a work-group), or writes an
+// empty row's zeros.  Lanes take columns, groups of lanes every so many
+// segments, four of them at a time.
 template <int TY>
 __global__ __launch_bounds__(kAttnBlock) void k_attention_join(const AttnArgs A)
 {
-    __shared__ float s_w[kAttnMaxSplits];
+    extern __shared__ uint32_t s_prefix[];
+    __shared__ uint32_t s_scratch[kAttnWaves];
+    __shared__ float s_w[kAttnMaxGroups];
     __shared__ float s_red[2][kAttnWaves];
     __shared__ float s_sum[kAttnBlock];
     const uint32_t r = A.by_heads.div(blockIdx.x), h = blockIdx.x - r * A.hq;   // by_heads: hq here
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Span span = row_span(A, r);
-    const uint32_t keys = span.hi - span.lo, share = split_share(A, keys);
-    const uint32_t parts = keys ? min(A.splits, (keys + share - 1) / share) : 1;
-    const uint64_t at = ((uint64_t)r * A.hq + h) * A.splits;
+    row_prefixes(A, s_prefix, s_scratch);
+    const uint32_t all = s_prefix[A.b], share = max(1u, A.by_groups.div(all + A.groups - 1));
+    const uint32_t from = s_prefix[r], to = s_prefix[r + 1];
+    if (from == to) {
+        for (uint32_t c = threadIdx.x; c < A.dv; c += kAttnBlock) store_out<TY>(A, r, h, c, 0.0f);
+        if (threadIdx.x == 0 && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = -INFINITY;
+        return;
+    }
+    const uint32_t first = from / share, parts = (to - 1) / share - first + 1;
+    if (parts == 1) return;   // written by its work-group
+    const uint64_t at = (uint64_t)(first + r) * A.hq + h;   // segment s: at + s * hq
 
     float m = -INFINITY;
-    for (uint32_t s = threadIdx.x; s < parts; s += kAttnBlock) m = fmaxf(m, A.ml[2 * (at + s)]);
+    for (uint32_t s = threadIdx.x; s < parts; s += kAttnBlock) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
     if (lane == 0) s_red[0][wave] = m;
@@ -440,9 +574,10 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join(const AttnArgs A)
     const float ref = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
     for (uint32_t s = threadIdx.x; s < parts; s += kAttnBlock) {
-        const float w = __builtin_amdgcn_exp2f(A.ml[2 * (at + s)] - ref);
+        const uint64_t x = 2 * (at + (uint64_t)s * A.hq);
+        const float w = __builtin_amdgcn_exp2f(A.ml[x] - ref);
         s_w[s] = w;
-        l += w * A.ml[2 * (at + s) + 1];
+        l += w * A.ml[x + 1];
     }
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) l += __shfl_xor(l, o);
@@ -452,13 +587,23 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join(const AttnArgs A)
 #pragma unroll
     for (int w = 0; w < (int)kAttnWaves; ++w) total += s_red[1][w];
 
-    // columns across lanes, the splits dealt to groups of lanes
     uint32_t width = 32;
     while (width < A.dv) width *= 2;   // dv <= 256
     const uint32_t c = threadIdx.x % width, g = threadIdx.x / width, groups = kAttnBlock / width;
     float sum = 0.0f;
-    if (c < A.dv)
-        for (uint32_t s = g; s < parts; s += groups) sum += A.acc[(at + s) * A.dv + c] * s_w[s];
+    if (c < A.dv) {
+        const float *p = A.acc + at * A.dv + c;
+        const uint64_t stride = (uint64_t)A.hq * A.dv;
+        uint32_t s = g;
+        for (; s + 7 * groups < parts; s += 8 * groups) {
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = p[(s + u * groups) * stride];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sum += x[u] * s_w[s + u * groups];
+        }
+        for (; s < parts; s += groups) sum += p[s * stride] * s_w[s];
+    }
     s_sum[threadIdx.x] = sum;
     __syncthreads();
     if (g == 0 && c < A.dv) {
@@ -470,36 +615,48 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join(const AttnArgs A)
             total == 0.0f ? -INFINITY : (ref - kBias<TY> + log2f(total)) * 0.69314718055994530942f;
 }
 
-template <int TY, int NK, int VW, bool RAGGED>
+template <int TY, int NK, int VW, AttnEdge EDGE>
 int launch_attn_one(const AttnArgs &A, void *stream)
 {
-    return launch_kernel(reinterpret_cast<const void *>(&k_attention<TY, NK, VW, RAGGED>),
-                         dim3(A.b * A.splits * A.hk * A.head_tiles), dim3(kAttnBlock), 0, stream, A);
+    const uint32_t heads = A.hk * A.head_tiles;
+    if (A.direct)
+        return launch_kernel(reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, true>), dim3(A.b * heads),
+                             dim3(kAttnBlock), 0, stream, A);
+    return launch_kernel(reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, false>), dim3(A.groups * heads),
+                         dim3(kAttnBlock), (A.b + 1) * 4, stream, A);
 }
 
-// The instance: whole pieces of keys and values where d and dv have them (the
-// common head widths), else the next larger one that checks each piece.
+// The instance: the smallest that holds d and dv; whole key pieces where d is one
+// of the common head widths.
 template <int TY>
 int launch_attn_type(const AttnArgs &A, void *stream)
 {
-    constexpr int E = AttnType<TY>::E, U = 8 / E;   // 16-byte pieces of 32 elements: 4 U
+    constexpr int E = AttnType<TY>::E, U = 8 / E;   // 4 U pieces of 16 bytes: 32 elements
     const uint32_t d = A.d, dv = A.dv;
-    if (dv % 8 == 0 && dv <= 64 && dv % 4 == 0) {
-        if (d == 64) return launch_attn_one<TY, 2 * U, 4, false>(A, stream);
-        if (d == 96) return launch_attn_one<TY, 3 * U, 4, false>(A, stream);
-        if (d == 128) return launch_attn_one<TY, 4 * U, 4, false>(A, stream);
-    } else if (dv % 8 == 0 && dv <= 128) {
-        if (d == 64) return launch_attn_one<TY, 2 * U, 8, false>(A, stream);
-        if (d == 96) return launch_attn_one<TY, 3 * U, 8, false>(A, stream);
-        if (d == 128) return launch_attn_one<TY, 4 * U, 8, false>(A, stream);
+    if (d < (uint32_t)E || dv < (uint32_t)E)
+        return d <= 64 && dv <= 64 ? launch_attn_one<TY, 2 * U, 4, kTiny>(A, stream)
+                                   : launch_attn_one<TY, 8 * U, 16, kTiny>(A, stream);
+    if (dv <= 64) {
+        if (d == 64) return launch_attn_one<TY, 2 * U, 4, kExact>(A, stream);
+        if (d == 96) return launch_attn_one<TY, 3 * U, 4, kExact>(A, stream);
+        if (d == 128) return launch_attn_one<TY, 4 * U, 4, kExact>(A, stream);
+        if (TY == S_F32 && d == 80) return launch_attn_one<TY, 5 * U / 2, 4, TY == S_F32 ? kExact : kTail>(A, stream);
+        if (d <= 64) return launch_attn_one<TY, 2 * U, 4, kTail>(A, stream);
+        if (d <= 96) return launch_attn_one<TY, 3 * U, 4, kTail>(A, stream);
     }
-    if (dv % 16 == 0) {
-        if (d == 192) return launch_attn_one<TY, 6 * U, 16, false>(A, stream);
-        if (d == 256) return launch_attn_one<TY, 8 * U, 16, false>(A, stream);
+    if (dv <= 128) {
+        if (d == 64) return launch_attn_one<TY, 2 * U, 8, kExact>(A, stream);
+        if (d == 96) return launch_attn_one<TY, 3 * U, 8, kExact>(A, stream);
+        if (d == 128) return launch_attn_one<TY, 4 * U, 8, kExact>(A, stream);
+        if (d == 192) return launch_attn_one<TY, 6 * U, 8, kExact>(A, stream);
+        if (TY == S_F32 && d == 80) return launch_attn_one<TY, 5 * U / 2, 8, TY == S_F32 ? kExact : kTail>(A, stream);
+        if (d <= 96) return launch_attn_one<TY, 3 * U, 8, kTail>(A, stream);
+        if (d <= 128) return launch_attn_one<TY, 4 * U, 8, kTail>(A, stream);
     }
-    if (d <= 64 && dv <= 64) return launch_attn_one<TY, 2 * U, 4, true>(A, stream);
-    if (d <= 128 && dv <= 128) return launch_attn_one<TY, 4 * U, 8, true>(A, stream);
-    return launch_attn_one<TY, 8 * U, 16, true>(A, stream);
+    if (d == 192) return launch_attn_one<TY, 6 * U, 16, kExact>(A, stream);
+    if (d == 256) return launch_attn_one<TY, 8 * U, 16, kExact>(A, stream);
+    if (d <= 192) return launch_attn_one<TY, 6 * U, 16, kTail>(A, stream);
+    return launch_attn_one<TY, 8 * U, 16, kTail>(A, stream);
 }
 
 template <int TY>
@@ -507,8 +664,8 @@ int launch_join_type(const AttnArgs &A, void *stream)
 {
     AttnArgs J = A;
     J.by_heads = Div31(A.hq);
-    return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY>), dim3(A.b * A.hq), dim3(kAttnBlock), 0,
-                         stream, J);
+    return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY>), dim3(A.b * A.hq), dim3(kAttnBlock),
+                         (A.b + 1) * 4, stream, J);
 }
 
 }  // namespace

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 #include "../../include/ecmd_serving.h"
@@ -487,19 +488,21 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.window = (uint32_t)window;
     A.by_page = Div31(A.page);
     A.by_heads = Div31(A.hk * A.head_tiles);
-    // Work-groups: enough for every compute unit several times over, whatever
-    // the rows; a split is no smaller than the step of its four waves.
-    const uint64_t base = (uint64_t)A.b * A.hk * A.head_tiles;
+    // Work-groups of a head: about 768 in all, what 256 compute units hold at
+    // three each, but no more than there can be steps.
+    const uint64_t heads = (uint64_t)A.hk * A.head_tiles;
     uint64_t keys = (uint64_t)A.cols * A.page;
     if (window) keys = std::min<uint64_t>(keys, (uint64_t)window);
-    uint64_t splits = (2048 + base - 1) / base;
-    splits = std::min<uint64_t>(splits, ceil_div(keys, kAttnShare));
-    splits = std::min<uint64_t>(std::max<uint64_t>(splits, 1), kAttnMaxSplits);
-    if (base * splits > (uint64_t)kMaxCount || (uint64_t)A.b * A.hq > (uint64_t)kMaxCount)
+    const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep;
+    if ((uint64_t)b * heads > (uint64_t)kMaxCount || (uint64_t)b * hq > (uint64_t)kMaxCount)
         return refuse(CMD_E_LIMIT, "too many sequences times heads");
-    A.splits = (uint32_t)splits;
-    A.by_splits = Div31(A.splits);
-    if (splits > 1) P.workspace = (int64_t)((uint64_t)b * hq * splits * (dv + 2) * 4 + 16);
+    A.direct = steps <= 1 || b > kAttnMaxRows;
+    static const int kTarget = getenv("ECMD_ATTN_GROUPS") ? atoi(getenv("ECMD_ATTN_GROUPS")) : 768;
+    uint64_t groups = std::max<uint64_t>(1, kTarget / heads);
+    groups = std::min<uint64_t>(std::min<uint64_t>(groups, steps * (uint64_t)b), kAttnMaxGroups);
+    A.groups = (uint32_t)std::max<uint64_t>(groups, 1);
+    A.by_groups = Div31(A.groups);
+    if (!A.direct) P.workspace = (int64_t)(((uint64_t)A.groups + b) * hq * (dv + 2) * 4 + 16);
     return CMD_OK;
 }
 
@@ -526,15 +529,15 @@ int cmd_paged_attention(const cmd_arg args[7], float scale, int32_t window, void
     TRY(check_workspace(workspace, workspace_bytes, P.workspace));
     AttnArgs &A = P.A;
     A.scale_log2 = (float)((double)scale * 1.44269504088896340736);
-    if (A.splits > 1) {
+    if (!A.direct) {
         A.ml = (float *)workspace;
-        A.acc = A.ml + (((uint64_t)A.b * A.hq * A.splits * 2 + 3) & ~uint64_t(3));
+        A.acc = A.ml + ((((uint64_t)A.groups + A.b) * A.hq * 2 + 3) & ~uint64_t(3));
     }
     const int rc = P.type == S_F16    ? launch_attention_f16(A, hip_stream)
                    : P.type == S_BF16 ? launch_attention_bf16(A, hip_stream)
                                       : launch_attention_f32(A, hip_stream);
     TRY(launched(rc, "paged_attention"));
-    if (A.splits == 1) return CMD_OK;
+    if (A.direct) return CMD_OK;
     return launched(P.type == S_F16    ? launch_attention_join_f16(A, hip_stream)
                     : P.type == S_BF16 ? launch_attention_join_bf16(A, hip_stream)
                                        : launch_attention_join_f32(A, hip_stream),

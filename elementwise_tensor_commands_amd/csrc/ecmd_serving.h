@@ -74,21 +74,24 @@ struct AttnArgs {
     const int32_t *pages, *lens;
     void *out;
     float *lse;                            // may be null
-    float *acc;                            // workspace: [b, hq, splits, dv] sums
-    float *ml;                             // workspace: [b, hq, splits] (maximum, sum) pairs
+    float *acc;                            // workspace: [groups + b, hq, dv] sums
+    float *ml;                             // workspace: [groups + b, hq] (maximum, sum) pairs
     int64_t qs[2], os[2], ls[2];           // batch, head
     int64_t kcs[3], vcs[3];                // BYTE strides of page, slot, head
     int64_t pages_s[2], lens_s;
     uint32_t b, hq, hk, d, dv, group, head_tiles;
     uint32_t n, page, cols;
-    uint32_t splits, window;
+    uint32_t groups, window;               // work-groups of one head
+    uint32_t direct;                       // 1: a work-group to a row and head, no join
     float scale_log2;                      // scale * log2(e)
-    Div31 by_page, by_heads, by_splits;
+    Div31 by_page, by_heads, by_groups;
 };
 
-// Positions a work-group's share of a row is rounded to: its four waves' tiles.
-constexpr uint32_t kAttnShare = 128;
-constexpr uint32_t kAttnMaxSplits = 1024;
+// Positions are dealt to work-groups in steps of this many: a tile for each of
+// four waves, at 16 bits.
+constexpr uint32_t kAttnStep = 128;
+constexpr uint32_t kAttnMaxGroups = 1024;
+constexpr uint32_t kAttnMaxRows = 2048;    // rows whose prefixes fit LDS; more go direct
 
 int launch_attention_f16(const AttnArgs &A, void *stream);
 int launch_attention_bf16(const AttnArgs &A, void *stream);
