@@ -1,4 +1,5 @@
-"""Build libecmd.so (the C ABI and its gfx950 kernels) in-tree with hipcc.
+"""Build libecmd.so (the C ABI and its gfx950 kernels) and _binding.so (the
+compiled part of the Python binding) in-tree.
 
     python elementwise_tensor_commands_amd/build.py [-v]
 
@@ -30,6 +31,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libecmd.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["ecmd_host.cpp", "ecmd_serial.cpp", "ecmd_jit.cpp", "kernels_linear.hip", "kernels_interp.hip",
            "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip", "ecmd_serving.cpp", "kernels_rope.hip",
@@ -109,6 +111,21 @@ def _run_all(cmds):
         raise RuntimeError("hipcc failed:\n" + "\n\n".join(errors))
 
 
+def binding_command(out: str):
+    """The command that builds the Python extension module _binding: host code
+    against torch's and Python's headers, with the host compiler."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
+    inc = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(rocm, "include")]
+    lib = os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+            "-DUSE_ROCM=1", *[x for i in inc for x in ("-isystem", i)], os.path.join(CSRC, "ecmd_binding.cpp"), "-o", out,
+            "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath," + lib]
+
+
 def build(asm: bool = True, verbose: bool = False) -> str:
     """Compile every source and link libecmd.so next to this file.  With asm,
     also write each kernel file's gfx950 assembly to _build/<name>.s (used by the
@@ -126,6 +143,8 @@ def build(asm: bool = True, verbose: bool = False) -> str:
         if asm and src.endswith(".hip"):
             cmds.append([HIPCC, *FLAGS, *extra, "-x", "hip", "--offload-device-only", "-S",
                          os.path.join(CSRC, src), "-o", os.path.join(BUILD, os.path.splitext(src)[0] + ".s")])
+    tmp_binding = BINDING + ".tmp%d" % os.getpid()
+    cmds.append(binding_command(tmp_binding))
     if verbose:
         for c in cmds:
             print(" ".join(c))
@@ -135,6 +154,7 @@ def build(asm: bool = True, verbose: bool = False) -> str:
     _run_all([[HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs,
                "-L" + rocm_lib, "-lhiprtc", "-Wl,-rpath," + rocm_lib]])
     os.replace(tmp, LIB)
+    os.replace(tmp_binding, BINDING)
     return LIB
 
 

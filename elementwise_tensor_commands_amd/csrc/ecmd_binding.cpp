@@ -1,0 +1,102 @@
+// ecmd_binding.cpp -- the part of the Python binding that is worth compiling:
+// torch tensors to cmd_arg structures (a Python extension module, _binding).
+//
+//   pack(ranks, *tensors) -> (cmd_args, device, stream)
+//
+// cmd_args holds one structure for each tensor, in order: the tensor of the
+// rank that its byte of `ranks` says; another rank is packed with sizes that the
+// library refuses; None gives kind 0.  device is the GPU that holds every tensor
+// if that is the current one, else -1; stream its current stream's handle (0
+// without one).  Reading four attributes of each tensor from Python takes
+// about 1 us a tensor, as long as the kernels of a small call; this takes 0.1.
+#include <Python.h>
+
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/ecmd_serving.h"
+
+namespace {
+
+int32_t code(at::ScalarType t)
+{
+    switch (t) {
+    case at::kHalf: return CMD_F16;
+    case at::kFloat: return CMD_F32;
+    case at::kInt: return CMD_I32;
+    case at::kBFloat16: return CMD_BF16;
+    case at::kDouble: return CMD_F64;
+    default: return 0;
+    }
+}
+
+PyObject *pack_tensors(PyObject *const *args, Py_ssize_t n)
+{
+    if (n < 1 || !PyBytes_Check(args[0]) || PyBytes_GET_SIZE(args[0]) != n - 1) {
+        PyErr_SetString(PyExc_TypeError, "pack(ranks, *tensors): one byte of ranks for each tensor");
+        return nullptr;
+    }
+    const char *ranks = PyBytes_AS_STRING(args[0]);
+    PyObject *out = PyBytes_FromStringAndSize(nullptr, (n - 1) * (Py_ssize_t)sizeof(cmd_arg));
+    if (!out) return nullptr;
+    cmd_arg *a = (cmd_arg *)PyBytes_AS_STRING(out);
+    memset(static_cast<void *>(a), 0, (n - 1) * sizeof(cmd_arg));
+    int64_t device = -2;   // none seen yet
+    for (Py_ssize_t i = 1; i < n; ++i, ++a, ++ranks) {
+        if (args[i] == Py_None) continue;
+        if (!THPVariable_Check(args[i])) {
+            Py_DECREF(out);
+            PyErr_Format(PyExc_TypeError, "a torch.Tensor expected, got %s", Py_TYPE(args[i])->tp_name);
+            return nullptr;
+        }
+        const at::Tensor &t = THPVariable_Unpack(args[i]);
+        if (t.layout() != at::kStrided) {
+            Py_DECREF(out);
+            PyErr_SetString(PyExc_TypeError, "a strided tensor expected");
+            return nullptr;
+        }
+        const int64_t on = t.is_cuda() ? t.get_device() : -1;
+        device = device == -2 || device == on ? on : -1;
+        a->kind = CMD_ARG_TENSOR;
+        a->dtype = code(t.scalar_type());
+        a->ptr = t.mutable_data_ptr();
+        if (t.dim() == *ranks) {
+            for (int k = 0; k < *ranks; ++k) {
+                a->size[k] = t.size(k);
+                a->stride[k] = t.stride(k);
+            }
+        } else {
+            for (int k = 0; k < 4; ++k) a->size[k] = -1;
+        }
+    }
+    void *stream = nullptr;
+    if (device >= 0) {
+        if (device == c10::hip::current_device()) stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
+        else device = -1;
+    } else {
+        device = -1;
+    }
+    return Py_BuildValue("(NLK)", out, (long long)device, (unsigned long long)(uintptr_t)stream);
+}
+
+PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    try {
+        return pack_tensors(args, n);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+PyMethodDef methods[] = {
+    {"pack", (PyCFunction)(void (*)(void))pack, METH_FASTCALL, "pack(ranks, *tensors) -> (cmd_args, device, stream)"},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "torch tensors to cmd_arg structures", -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }

@@ -22,21 +22,26 @@
 //            also run in any order of keys, so the same lane's weights are its
 //            operand as they are, with lane j loading the values of keys
 //            16 kb + 4 j + i.
-//   out      D[dv][head] += V^T P^T.  Lane h loads VW consecutive elements of
-//            its keys' values; product c takes element c of each (16-bit types:
-//            two keys' elements joined by one byte permute), so its row h is
-//            column VW h + c.
+//   out      D[dv][head] += V^T P^T.  Lane h loads the h-th 16 bytes of its keys'
+//            values (of each 256); product c takes element c of each (16-bit
+//            types: two keys' elements joined by one byte permute), so its row h
+//            is column 8 h + c (binary32: 4 h + c).
 //
 // A head's maximum and rescale factor belong to one lane column: no transposes.
 //
 // Rows differ in length (some are empty, the table says how long they could be,
-// not how long they are), so positions are dealt to work-groups by what the
-// lengths say on the device: the rows' positions in steps of 128, laid end to
-// end, are cut into equal runs, one for each work-group of a head.  A run may
-// span rows; each row in it is a segment with a start and an end of its own.
-// Segments of a row that is cut are joined by a second launch.
+// not how long they are), so positions are dealt out by what the lengths say on
+// the device: the rows' positions in steps, laid end to end, are cut into equal
+// runs.  A run may span rows; each row in it is a segment with a start and an
+// end of its own.  Segments of a row that is cut are joined by a second launch.
+//
+// The four waves of a work-group split its positions and join their sums through
+// LDS, or, where there is much to read and the heads allow it, take four kv heads
+// of the same positions: together they then read whole slots and exchange nothing.
 #pragma once
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "ecmd_launch.h"
 #include "ecmd_serving.h"
@@ -87,12 +92,13 @@ __device__ inline uint32_t fresh(uint32_t x)
     return x;
 }
 
-// 16 bytes at p, wherever that is.
+// 16 bytes at p, wherever that is.  STREAM: not to be kept in the caches.
+template <bool STREAM = false>
 __device__ inline u32x4 load16(const char *p)
 {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
+    typedef u32x4 U __attribute__((aligned(2)));
+    if constexpr (STREAM) return __builtin_nontemporal_load((const U *)p);
+    else return *(const U *)p;
 }
 
 // The first n of N elements at p, the rest 0; nothing past them is read.
@@ -128,35 +134,88 @@ __device__ inline Span row_span(const AttnArgs &A, uint32_t r)
     if (A.window && (uint32_t)len > A.window) s.lo = min((uint32_t)len - A.window, s.hi);
     return s;
 }
-__device__ inline uint32_t span_steps(Span s) { return (s.hi - s.lo + kAttnStep - 1) / kAttnStep; }
 
-// Steps before each row, and all of them, into prefix[0 .. b]; ends with a barrier.
-__device__ inline void row_prefixes(const AttnArgs &A, uint32_t *prefix, uint32_t *scratch)
+// The rows' spans and the steps before each row, in LDS.
+struct Rows {
+    uint32_t *prefix;    // [b + 1]
+    uint32_t *lo, *hi;   // [b]
+    uint32_t all, longest;
+};
+__host__ __device__ inline uint32_t rows_lds(uint32_t b) { return (3 * b + 1) * 4; }
+
+// Up to 64 rows every wave makes the whole of it, the same values in the same
+// places, and waits for nobody; more rows are the first kAttnBlock work-items'
+// and end with a barrier.
+__device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scratch)
 {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t run = 0;
+    Rows R{lds, lds + A.b + 1, lds + 2 * A.b + 1, 0, 0};
+    const bool alone = A.b <= 64;
+    uint32_t run = 0, most = 0;
     for (uint32_t r0 = 0; r0 < A.b; r0 += kAttnBlock) {
-        const uint32_t r = r0 + threadIdx.x;
-        const uint32_t x = r < A.b ? span_steps(row_span(A, r)) : 0;
+        const uint32_t r = alone ? lane : threadIdx.x < kAttnBlock ? r0 + threadIdx.x : A.b;
+        uint32_t x = 0;
+        if (r < A.b) {
+            const Span s = row_span(A, r);
+            R.lo[r] = s.lo;
+            R.hi[r] = s.hi;
+            x = (s.hi - s.lo + kAttnStep - 1) / kAttnStep;
+            most = max(most, x);
+        }
         uint32_t inc = x;
 #pragma unroll
         for (int o = 1; o < 64; o *= 2) {
             const uint32_t y = __shfl_up(inc, o);
             if (lane >= (uint32_t)o) inc += y;
         }
-        if (lane == 63) scratch[wave] = inc;
-        __syncthreads();
         uint32_t before = run;
+        if (alone) {
+            run = __shfl(inc, 63);
+        } else {
+            if (lane == 63 && wave < kAttnWaves) scratch[wave] = inc;
+            __syncthreads();
 #pragma unroll
-        for (uint32_t w = 0; w < kAttnWaves; ++w) {
-            if (w < wave) before += scratch[w];
-            run += scratch[w];
+            for (uint32_t w = 0; w < kAttnWaves; ++w) {
+                if (w < wave) before += scratch[w];
+                run += scratch[w];
+            }
+            __syncthreads();
         }
-        if (r < A.b) prefix[r] = before + inc - x;
-        __syncthreads();
+        if (r < A.b) R.prefix[r] = before + inc - x;
     }
-    if (threadIdx.x == 0) prefix[A.b] = run;
-    __syncthreads();
+    if (alone ? lane == 0 : threadIdx.x == 0) R.prefix[A.b] = run;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) most = max(most, (uint32_t)__shfl_xor((int)most, o));
+    if (alone) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    } else {
+        if (lane == 0 && wave < kAttnWaves) scratch[wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (uint32_t w = 0; w < kAttnWaves; ++w) most = max(most, scratch[w]);
+    }
+    R.all = __builtin_amdgcn_readfirstlane(run);
+    R.longest = __builtin_amdgcn_readfirstlane(most);
+    return R;
+}
+
+// How the steps are dealt out, the same in every work-group and in the join.
+struct Deal {
+    uint32_t head_shift;   // 2^head_shift waves of a work-group take a head each
+    uint32_t share;        // steps of a run; 0: a run is a row
+};
+__device__ inline Deal deal_steps(const AttnArgs &A, const Rows &R)
+{
+    Deal D;
+    const uint32_t heads = A.hk * A.head_tiles;
+    const bool much = (uint64_t)R.all * heads >= kAttnMuch;
+    D.head_shift = much ? A.head_shift : 0;
+    const uint32_t runs = much ? A.runs_much : A.runs;
+    D.share = (much ? A.by_runs_much : A.by_runs).div(R.all + runs - 1);
+    // Rows of about one run's length are not cut at all.
+    if (R.longest <= 2 * D.share && A.b <= runs) D.share = 0;
+    return D;
 }
 
 template <int TY>
@@ -179,6 +238,15 @@ constexpr float kSlack = 8.0f;
 template <int TY>
 constexpr float kBias = TY == S_F16 ? 6.0f : 0.0f;
 
+// The natural logarithm of the softmax's sum from a maximum (log2) and the sum
+// of the weights against it.
+template <int TY>
+__device__ inline float log_sum(float top, float total)
+{
+    if (total == 0.0f) return -INFINITY;
+    return ((top == -INFINITY ? 0.0f : top) - kBias<TY> + log2f(total)) * 0.69314718055994530942f;
+}
+
 // How pieces that reach past the end of a row of d or dv elements are read.
 enum AttnEdge {
     kExact,   // there are none: d = 4 E NK
@@ -197,16 +265,16 @@ constexpr int attn_waves()
 }
 
 // VW: value columns of a lane (16 VW >= dv).  NK: 16-byte key pieces of a lane
-// (4 E NK >= d).  DIRECT: a work-group takes one whole row, nothing is joined.
-template <int TY, int NK, int VW, AttnEdge EDGE, bool DIRECT>
+// (4 E NK >= d).  STREAM: the cache is larger than the last-level cache.
+template <int TY, int NK, int VW, AttnEdge EDGE, bool STREAM>
 __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void k_attention(const AttnArgs A)
 {
     typedef typename AttnType<TY>::T T;
     constexpr int E = AttnType<TY>::E, KB = AttnType<TY>::KB;
-    constexpr int VK = 4 * KB;                                  // keys whose values a lane holds
-    constexpr int PE = VW < E ? VW : E, VP = VW / PE;           // elements of a value piece; pieces
+    constexpr int VK = 4 * KB;                          // keys whose values a lane holds
+    constexpr int PE = VW < E ? VW : E, VP = VW / PE;   // elements of a value piece; pieces
     constexpr uint32_t kTile = 16 * KB;
-    constexpr int kRow = 16 * VW + 4;                           // a head's row in the joining buffer (floats)
+    constexpr int kRow = 16 * VW + 4;                   // a head's row in the joining buffer (floats)
 
     __shared__ union {
         struct {
@@ -215,47 +283,63 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         } table;
         float join[kAttnWaves][8][kRow];
     } sh;
-    __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16], s_ref[16], s_total[16];
-    extern __shared__ uint32_t s_prefix[];   // [b + 1], unless DIRECT
+    __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16], s_top[kAttnWaves][16], s_total[kAttnWaves][16];
+    extern __shared__ uint32_t s_rows[];   // unless A.direct
     __shared__ uint32_t s_scratch[kAttnWaves];
 
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane >> 4, hh = lane & 15;
-    // heads of one run are neighbours: together they read whole slots
-    const uint32_t heads = A.hk * A.head_tiles;
-    const uint32_t group = A.by_heads.div(blockIdx.x), head = blockIdx.x - group * heads;
-    const uint32_t kvh = head / A.head_tiles, ht = head - kvh * A.head_tiles;
+    const uint32_t lane = threadIdx.x & 63, j = lane >> 4, hh = lane & 15;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // The run of this work-group: steps [step, stop) of all rows', from row r on.
+    uint32_t head_shift = 0, group, r, step = 0, stop = 0, bh;
+    Rows R{};
+    if (A.direct) {
+        group = r = A.by_heads.div(blockIdx.x);
+        bh = blockIdx.x - group * A.by_heads.d;
+    } else {
+        R = make_rows(A, s_rows, s_scratch);
+        const Deal D = deal_steps(A, R);
+        head_shift = D.head_shift;
+        const Div31 by = head_shift ? A.by_heads_much : A.by_heads;
+        group = by.div(blockIdx.x);
+        bh = blockIdx.x - group * by.d;
+        if (D.share == 0) {
+            if (group >= A.b) return;
+            r = group;
+            step = __builtin_amdgcn_readfirstlane(R.prefix[r]);
+            stop = __builtin_amdgcn_readfirstlane(R.prefix[r + 1]);
+            if (step == stop) return;
+        } else {
+            step = group * D.share;
+            stop = min(step + D.share, R.all);
+            if (step >= stop) return;
+            uint32_t lo = 0, hi = A.b;   // the row with prefix[r] <= step < prefix[r + 1]
+            while (hi - lo > 1) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (__builtin_amdgcn_readfirstlane(R.prefix[mid]) <= step) lo = mid;
+                else hi = mid;
+            }
+            r = lo;
+        }
+    }
+    // hw waves side by side take a head each, the others a part of the positions
+    const uint32_t hw = 1u << head_shift, part = wave >> head_shift, parts = kAttnWaves >> head_shift;
+    const uint32_t sub = wave & (hw - 1), head = bh * hw + sub;
+    const uint32_t kvh = A.by_tiles.div(head), ht = head - kvh * A.head_tiles;
     const uint32_t q0 = kvh * A.group + ht * 16, q_n = min(16u, A.group - ht * 16);
 
-    // The run of this work-group: steps [step, stop) of all rows', from row r on.
-    uint32_t r = group, step = 0, stop = 0, share = 1;
-    if constexpr (!DIRECT) {
-        row_prefixes(A, s_prefix, s_scratch);
-        const uint32_t all = s_prefix[A.b];
-        share = max(1u, A.by_groups.div(all + A.groups - 1));
-        step = group * share;
-        stop = min(step + share, all);
-        if (step >= stop) return;
-        uint32_t lo = 0, hi = A.b;   // the row with prefix[r] <= step < prefix[r + 1]
-        while (hi - lo > 1) {
-            const uint32_t mid = (lo + hi) / 2;
-            if (s_prefix[mid] <= step) lo = mid;
-            else hi = mid;
-        }
-        r = lo;
-    }
-
-    // Where a lane's value pieces start; the last ones end with the row.
+    // Where a lane's value pieces start: neighbours to neighbours.  The last ones
+    // end with the row.
     auto column = [&](uint32_t m, int piece) {
-        const uint32_t at = m * VW + piece * PE;
+        const uint32_t at = (piece * 16 + m) * PE;
         return EDGE == kTiny ? at : min(at, A.dv - PE);
     };
     // Piece c of a row of d elements at p.  One that would reach past the end is
     // moved back to end with the row; masked() clears what earlier ones have, all
     // of it where the piece lies past the end altogether.
-    auto load_row_piece = [&](const char *p, int c) {
+    auto load_row_piece = [&](const char *p, int c, auto stream) {
         const int at = (c * 4 + (int)j) * E;
         if constexpr (EDGE == kTiny) return load_some<T, E>(p + at * sizeof(T), (int)A.d - at);
-        return load16(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
+        return load16<stream>(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
     };
     auto masked = [&](u32x4 x, int c) {
         if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {   // the same for the whole launch
@@ -275,25 +359,33 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
     const char *vbase = (const char *)A.v + (int64_t)kvh * A.vcs[2];
 
     for (;;) {   // one row of the run
-        const Span span = row_span(A, r);
-        uint32_t begin = span.lo, end = span.hi, steps = span_steps(span);
+        uint32_t begin, end, steps = 0;
         bool whole_row = true;
-        if constexpr (!DIRECT) {
-            const uint32_t first = s_prefix[r], last = s_prefix[r + 1];
-            const uint32_t here = min(stop, last);
+        if (A.direct) {
+            const Span span = row_span(A, r);
+            begin = span.lo;
+            end = span.hi;
+        } else {
+            const uint32_t first = __builtin_amdgcn_readfirstlane(R.prefix[r]);
+            const uint32_t last = __builtin_amdgcn_readfirstlane(R.prefix[r + 1]);
+            const uint32_t here = min(stop, last), hi = __builtin_amdgcn_readfirstlane(R.hi[r]);
             whole_row = step == first && here == last;
-            begin += (step - first) * kAttnStep;
             steps = here - step;
-            end = min(begin + steps * kAttnStep, span.hi);
+            begin = __builtin_amdgcn_readfirstlane(R.lo[r]) + (step - first) * kAttnStep;
+            end = min(begin + steps * kAttnStep, hi);
         }
-        const uint32_t wshare = steps * (kAttnStep / kAttnWaves);
-        const uint32_t wb = min(begin + wave * wshare, end), we = min(wb + wshare, end);
+        uint32_t wb = begin, we = end;
+        if (parts > 1) {
+            const uint32_t each = (end - begin + parts * 32 - 1) >> (7 - head_shift) << 5;
+            wb = min(begin + part * each, end);
+            we = min(wb + each, end);
+        }
 
         u32x4 q[NK];
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
             const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)(q0 + (hh < q_n ? hh : 0)) * A.qs[1]) * sizeof(T);
-            q[c] = masked(load_row_piece(p, c), c);
+            q[c] = masked(load_row_piece(p, c, std::false_type()), c);
             if (hh >= q_n) q[c] = u32x4{0, 0, 0, 0};
         }
 
@@ -335,7 +427,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             for (int kb = 0; kb < KB; ++kb) {
                 const char *p = kbase + sh.table.k[wave][t + kb * 16 + hh];
 #pragma unroll
-                for (int c = 0; c < NK; ++c) kr[kb][c] = load_row_piece(p, c);
+                for (int c = 0; c < NK; ++c) kr[kb][c] = load_row_piece(p, c, std::bool_constant<STREAM>());
             }
             bits = (uint32_t)(sh.table.valid[wave][t / 64] >> (t % 64));
             if constexpr (KB == 1) bits &= 0xFFFFu;
@@ -350,6 +442,8 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                     const uint32_t at = column(hh, c);
                     if constexpr (EDGE == kTiny)
                         vr[x][c] = load_some<T, PE>(p + at * sizeof(T), (int)A.dv - (int)at);
+                    else if constexpr (PE * sizeof(T) == 16)
+                        vr[x][c] = load16<STREAM>(p + at * sizeof(T));
                     else
                         __builtin_memcpy(&vr[x][c], p + at * sizeof(T), PE * sizeof(T));
                 }
@@ -465,115 +559,194 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             if (tile < we) load_v(in_table);
         }
 
-        // Join the waves: common maximum, then sums head by head through LDS,
-        // eight heads at a time.
+        // The segment's sums: final, or for the second launch at a place of its
+        // own (work-groups and rows only go forward).
         const uint32_t tid = fresh(threadIdx.x), eh = tid & 15, ej = tid >> 4 & 3;
+        const uint64_t place = (uint64_t)(group + r) * A.hq + q0;
+        auto put = [&](uint32_t hx, uint32_t c, float sum, float total) {
+            if (whole_row) store_out<TY>(A, r, q0 + hx, c, total == 0.0f ? 0.0f : sum / total);
+            else A.acc[(place + hx) * A.dv + c] = sum;
+        };
+        auto put_statistics = [&](uint32_t hx, float top, float total) {
+            if (!whole_row) {
+                A.ml[2 * (place + hx)] = top;
+                A.ml[2 * (place + hx) + 1] = total;
+            } else if (A.lse) {
+                A.lse[(int64_t)r * A.ls[0] + (int64_t)(q0 + hx) * A.ls[1]] = log_sum<TY>(top, total);
+            }
+        };
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
-        if (ej == 0) {
-            s_m[wave][eh] = m;
-            s_l[wave][eh] = l;
-        }
-        __syncthreads();   // also: the tables are done with
-        float mj = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < (int)kAttnWaves; ++w) mj = fmaxf(mj, s_m[w][eh]);
-        const float ref = mj == -INFINITY ? 0.0f : mj;
-        if (tid < 16) {
-            float total = 0.0f;
-#pragma unroll
-            for (int w = 0; w < (int)kAttnWaves; ++w) total += s_l[w][eh] * __builtin_amdgcn_exp2f(s_m[w][eh] - ref);
-            s_ref[eh] = mj;
-            s_total[eh] = total;
-        }
-        const float factor = __builtin_amdgcn_exp2f(m - ref);
-        const bool final = DIRECT || whole_row;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half * 8 >= (int)q_n) break;
-            if (half) __syncthreads();
-            if ((eh >> 3) == (uint32_t)half) {
+        if (parts == 1) {
+            if (eh < q_n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < VW; ++c)
-                        sh.join[wave][eh & 7][column(ej * 4 + i, c / PE) + c % PE] = acc[c][i] * factor;
-            }
-            __syncthreads();
-            for (uint32_t x = tid; x < 8 * 16 * VW; x += kAttnBlock) {
-                const uint32_t g = x / (16 * VW), c = x % (16 * VW), hx = half * 8 + g;
-                if (hx >= q_n || c >= A.dv) continue;
-                float sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < (int)kAttnWaves; ++w) sum += sh.join[w][g][c];
-                const float total = s_total[hx], top = s_ref[hx];
-                const uint32_t h = q0 + hx;
-                if (final) {
-                    store_out<TY>(A, r, h, c, total == 0.0f ? 0.0f : sum / total);
-                    if (c == 0 && A.lse)
-                        A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] =
-                            total == 0.0f ? -INFINITY
-                                          : ((top == -INFINITY ? 0.0f : top) - kBias<TY> + log2f(total)) *
-                                                0.69314718055994530942f;
-                } else {
-                    // the segment's place: work-groups and rows only go forward
-                    const uint64_t at = (uint64_t)(group + r) * A.hq + h;
-                    A.acc[at * A.dv + c] = sum;
-                    if (c == 0) {
-                        A.ml[2 * at] = top;
-                        A.ml[2 * at + 1] = total;
+                    for (int c = 0; c < VW; ++c) {
+                        const uint32_t at = column(ej * 4 + i, c / PE) + c % PE;
+                        if (EDGE != kTiny || at < A.dv) put(eh, at, acc[c][i], l);
                     }
+                if (ej == 0) put_statistics(eh, m, l);
+            }
+        } else {
+            // common maximum, then sums head by head through LDS, eight at a time
+            if (ej == 0) {
+                s_m[wave][eh] = m;
+                s_l[wave][eh] = l;
+            }
+            __syncthreads();   // also: the tables are done with
+            float top = -INFINITY, total = 0.0f;
+            for (uint32_t w = sub; w < kAttnWaves; w += hw) top = fmaxf(top, s_m[w][eh]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            for (uint32_t w = sub; w < kAttnWaves; w += hw)
+                total += s_l[w][eh] * __builtin_amdgcn_exp2f(s_m[w][eh] - ref);
+            if (ej == 0) {   // read after the next barrier
+                s_top[wave][eh] = top;
+                s_total[wave][eh] = total;
+            }
+            const float factor = __builtin_amdgcn_exp2f(m - ref);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (half * 8 >= (int)min(16u, A.group)) break;   // the same for all waves: barriers follow
+                if (half) __syncthreads();
+                if ((eh >> 3) == (uint32_t)half) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < VW; ++c)
+                            sh.join[wave][eh & 7][column(ej * 4 + i, c / PE) + c % PE] = acc[c][i] * factor;
+                }
+                __syncthreads();
+                // the `parts` waves of a head share its rows
+                for (uint32_t x = part * 64 + (tid & 63); x < 8 * 16 * VW; x += parts * 64) {
+                    const uint32_t g = x / (16 * VW), c = x % (16 * VW), hx = half * 8 + g;
+                    if (hx >= q_n || c >= A.dv) continue;
+                    float sum = 0.0f;
+                    for (uint32_t w = sub; w < kAttnWaves; w += hw) sum += sh.join[w][g][c];
+                    put(hx, c, sum, s_total[wave][hx]);
+                    if (c == 0) put_statistics(hx, s_top[wave][hx], s_total[wave][hx]);
                 }
             }
         }
-        if constexpr (DIRECT) {
-            return;
-        } else {
-            step += steps;
-            if (step >= stop) return;
-            do ++r;
-            while (s_prefix[r + 1] <= step);   // past empty rows
-            __syncthreads();
-        }
+        if (A.direct) return;
+        step += steps;
+        if (step >= stop) return;
+        do ++r;
+        while (__builtin_amdgcn_readfirstlane(R.prefix[r + 1]) <= step);   // past empty rows
+        if (parts > 1) __syncthreads();
     }
 }
 
-// Joins the segments of one row and query head (a work-group), or writes an
-// empty row's zeros.  Lanes take columns, groups of lanes every so many
-// segments, four of them at a time.
-template <int TY>
-__global__ __launch_bounds__(kAttnBlock) void k_attention_join(const AttnArgs A)
+// The segments of row r, from the work-group `first` on; none: the row is empty.
+struct Segments {
+    uint32_t first, count;
+};
+__device__ inline Segments row_segments(const AttnArgs &A, const Rows &R, uint32_t r)
 {
-    extern __shared__ uint32_t s_prefix[];
+    const uint32_t from = R.prefix[r], to = R.prefix[r + 1], share = deal_steps(A, R).share;
+    if (from == to) return Segments{0, 0};
+    if (share == 0) return Segments{r, 1};
+    return Segments{from / share, (to - 1) / share - from / share + 1};
+}
+
+// Joins the segments of rows that were cut into few, or writes an empty row's
+// zeros: a wave to a row and query head, a segment to a lane and then columns.
+template <int TY>
+__global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArgs A)
+{
+    extern __shared__ uint32_t s_rows[];
     __shared__ uint32_t s_scratch[kAttnWaves];
-    __shared__ float s_w[kAttnMaxGroups];
-    __shared__ float s_red[2][kAttnWaves];
-    __shared__ float s_sum[kAttnBlock];
-    const uint32_t r = A.by_heads.div(blockIdx.x), h = blockIdx.x - r * A.hq;   // by_heads: hq here
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    row_prefixes(A, s_prefix, s_scratch);
-    const uint32_t all = s_prefix[A.b], share = max(1u, A.by_groups.div(all + A.groups - 1));
-    const uint32_t from = s_prefix[r], to = s_prefix[r + 1];
-    if (from == to) {
-        for (uint32_t c = threadIdx.x; c < A.dv; c += kAttnBlock) store_out<TY>(A, r, h, c, 0.0f);
-        if (threadIdx.x == 0 && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = -INFINITY;
+    const uint32_t lane = threadIdx.x & 63;
+    const Rows R = make_rows(A, s_rows, s_scratch);
+    const uint32_t x = __builtin_amdgcn_readfirstlane(blockIdx.x * kAttnWaves + threadIdx.x / 64);
+    if (x >= A.b * A.hq) return;
+    const uint32_t r = A.by_heads.div(x), h = x - r * A.hq;   // by_heads: hq here
+    const Segments S = row_segments(A, R, r);
+    if (S.count == 0) {
+        for (uint32_t c = lane; c < A.dv; c += 64) store_out<TY>(A, r, h, c, 0.0f);
+        if (lane == 0 && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = -INFINITY;
         return;
     }
-    const uint32_t first = from / share, parts = (to - 1) / share - first + 1;
+    if (S.count == 1) return;   // written by its work-group
+    const uint64_t at = (uint64_t)(S.first + r) * A.hq + h;   // segment s: at + s * hq
+    float m = -INFINITY;
+    for (uint32_t s = lane; s < S.count; s += 64) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float total = 0.0f, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t s0 = 0; s0 < S.count; s0 += 64) {
+        const uint32_t s = s0 + lane;
+        float w = 0.0f;
+        if (s < S.count) {
+            const uint64_t y = 2 * (at + (uint64_t)s * A.hq);
+            w = __builtin_amdgcn_exp2f(A.ml[y] - ref);
+            total += w * A.ml[y + 1];
+        }
+        const uint32_t n = min(64u, S.count - s0);
+        for (uint32_t k = 0; k < n; k += 4) {
+            float v[4][4];
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                const float *p = A.acc + (at + (uint64_t)(s0 + min(k + u, n - 1)) * A.hq) * A.dv;
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) v[u][c] = p[min(c * 64 + lane, A.dv - 1)];
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+                if (k + u < n) {
+                    const float wu = __shfl(w, (int)(k + u));
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c) sum[c] += v[u][c] * wu;
+                }
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+        if (c * 64 + lane < A.dv) store_out<TY>(A, r, h, c * 64 + lane, total == 0.0f ? 0.0f : sum[c] / total);
+    if (lane == 0 && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = log_sum<TY>(m, total);
+}
+
+// The same for rows cut into many.
+// A work-group takes COLS columns: groups of COLS work-items take every so many
+// segments, eight loads in flight each.
+template <int TY, int THREADS, int COLS>
+__global__ __launch_bounds__(THREADS) void k_attention_join(const AttnArgs A)
+{
+    constexpr uint32_t kGroups = THREADS / COLS, kW = THREADS / 64;
+    extern __shared__ uint32_t s_rows[];
+    __shared__ uint32_t s_scratch[kAttnWaves];
+    __shared__ float s_w[kAttnMaxRuns];
+    __shared__ float s_red[2][kW];
+    __shared__ float s_sum[THREADS];
+    const uint32_t r = A.by_heads.div(blockIdx.x), h = blockIdx.x - r * A.hq;   // by_heads: hq here
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t c0 = blockIdx.y * COLS, c = c0 + threadIdx.x % COLS, g = threadIdx.x / COLS;
+    const Rows R = make_rows(A, s_rows, s_scratch);
+    const Segments S = row_segments(A, R, r);
+    const bool first_cols = blockIdx.y == 0 && threadIdx.x == 0;
+    if (S.count == 0) {
+        if (g == 0 && c < A.dv) store_out<TY>(A, r, h, c, 0.0f);
+        if (first_cols && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = -INFINITY;
+        return;
+    }
+    const uint32_t first = S.first, parts = S.count;
     if (parts == 1) return;   // written by its work-group
     const uint64_t at = (uint64_t)(first + r) * A.hq + h;   // segment s: at + s * hq
 
     float m = -INFINITY;
-    for (uint32_t s = threadIdx.x; s < parts; s += kAttnBlock) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
+    for (uint32_t s = threadIdx.x; s < parts; s += THREADS) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
     if (lane == 0) s_red[0][wave] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < (int)kAttnWaves; ++w) m = fmaxf(m, s_red[0][w]);
+    for (uint32_t w = 0; w < kW; ++w) m = fmaxf(m, s_red[0][w]);
     const float ref = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
-    for (uint32_t s = threadIdx.x; s < parts; s += kAttnBlock) {
+    for (uint32_t s = threadIdx.x; s < parts; s += THREADS) {
         const uint64_t x = 2 * (at + (uint64_t)s * A.hq);
         const float w = __builtin_amdgcn_exp2f(A.ml[x] - ref);
         s_w[s] = w;
@@ -585,45 +758,37 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join(const AttnArgs A)
     __syncthreads();
     float total = 0.0f;
 #pragma unroll
-    for (int w = 0; w < (int)kAttnWaves; ++w) total += s_red[1][w];
+    for (uint32_t w = 0; w < kW; ++w) total += s_red[1][w];
 
-    uint32_t width = 32;
-    while (width < A.dv) width *= 2;   // dv <= 256
-    const uint32_t c = threadIdx.x % width, g = threadIdx.x / width, groups = kAttnBlock / width;
     float sum = 0.0f;
     if (c < A.dv) {
         const float *p = A.acc + at * A.dv + c;
         const uint64_t stride = (uint64_t)A.hq * A.dv;
-        uint32_t s = g;
-        for (; s + 7 * groups < parts; s += 8 * groups) {
+        for (uint32_t s = g; s < parts; s += 8 * kGroups) {
             float x[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = p[(s + u * groups) * stride];
+            for (uint32_t u = 0; u < 8; ++u) x[u] = s + u * kGroups < parts ? p[(s + u * kGroups) * stride] : 0.0f;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) sum += x[u] * s_w[s + u * groups];
+            for (uint32_t u = 0; u < 8; ++u)
+                if (s + u * kGroups < parts) sum += x[u] * s_w[s + u * kGroups];
         }
-        for (; s < parts; s += groups) sum += p[s * stride] * s_w[s];
     }
     s_sum[threadIdx.x] = sum;
     __syncthreads();
     if (g == 0 && c < A.dv) {
-        for (uint32_t x = 1; x < groups; ++x) sum += s_sum[x * width + c];
+        for (uint32_t x = 1; x < kGroups; ++x) sum += s_sum[x * COLS + c - c0];
         store_out<TY>(A, r, h, c, total == 0.0f ? 0.0f : sum / total);
     }
-    if (threadIdx.x == 0 && A.lse)
-        A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] =
-            total == 0.0f ? -INFINITY : (ref - kBias<TY> + log2f(total)) * 0.69314718055994530942f;
+    if (first_cols && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = log_sum<TY>(m, total);
 }
 
 template <int TY, int NK, int VW, AttnEdge EDGE>
 int launch_attn_one(const AttnArgs &A, void *stream)
 {
-    const uint32_t heads = A.hk * A.head_tiles;
-    if (A.direct)
-        return launch_kernel(reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, true>), dim3(A.b * heads),
-                             dim3(kAttnBlock), 0, stream, A);
-    return launch_kernel(reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, false>), dim3(A.groups * heads),
-                         dim3(kAttnBlock), (A.b + 1) * 4, stream, A);
+    const void *fn = EDGE != kTiny && A.stream
+                         ? reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, EDGE != kTiny>)
+                         : reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, false>);
+    return launch_kernel(fn, dim3(A.grid), dim3(kAttnBlock), A.direct ? 0 : rows_lds(A.b), stream, A);
 }
 
 // The instance: the smallest that holds d and dv; whole key pieces where d is one
@@ -664,8 +829,11 @@ int launch_join_type(const AttnArgs &A, void *stream)
 {
     AttnArgs J = A;
     J.by_heads = Div31(A.hq);
-    return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY>), dim3(A.b * A.hq), dim3(kAttnBlock),
-                         (A.b + 1) * 4, stream, J);
+    if (A.join_many)
+        return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY, 1024, 32>),
+                             dim3(A.b * A.hq, (A.dv + 31) / 32), dim3(1024), rows_lds(A.b), stream, J);
+    return launch_kernel(reinterpret_cast<const void *>(&k_attention_join_few<TY>),
+                         dim3((A.b * A.hq + kAttnWaves - 1) / kAttnWaves), dim3(kAttnBlock), rows_lds(A.b), stream, J);
 }
 
 }  // namespace

@@ -7,7 +7,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 
 #include "../../include/ecmd_serving.h"
@@ -487,22 +486,35 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.cols = n > 0 && page > 0 ? (uint32_t)cols : 0;   // a cache without slots: every row is empty
     A.window = (uint32_t)window;
     A.by_page = Div31(A.page);
-    A.by_heads = Div31(A.hk * A.head_tiles);
-    // Work-groups of a head: about 768 in all, what 256 compute units hold at
-    // three each, but no more than there can be steps.
     const uint64_t heads = (uint64_t)A.hk * A.head_tiles;
-    uint64_t keys = (uint64_t)A.cols * A.page;
-    if (window) keys = std::min<uint64_t>(keys, (uint64_t)window);
-    const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep;
     if ((uint64_t)b * heads > (uint64_t)kMaxCount || (uint64_t)b * hq > (uint64_t)kMaxCount)
         return refuse(CMD_E_LIMIT, "too many sequences times heads");
-    A.direct = steps <= 1 || b > kAttnMaxRows;
-    static const int kTarget = getenv("ECMD_ATTN_GROUPS") ? atoi(getenv("ECMD_ATTN_GROUPS")) : 768;
-    uint64_t groups = std::max<uint64_t>(1, kTarget / heads);
-    groups = std::min<uint64_t>(std::min<uint64_t>(groups, steps * (uint64_t)b), kAttnMaxGroups);
-    A.groups = (uint32_t)std::max<uint64_t>(groups, 1);
-    A.by_groups = Div31(A.groups);
-    if (!A.direct) P.workspace = (int64_t)(((uint64_t)A.groups + b) * hq * (dv + 2) * 4 + 16);
+    uint64_t keys = (uint64_t)A.cols * A.page;
+    if (window) keys = std::min<uint64_t>(keys, (uint64_t)window);
+    const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep, most = std::max<uint64_t>(1, steps * (uint64_t)b);
+    // One work-group to a row and head, without a join, where cutting rows would
+    // gain less than the second launch costs.
+    A.direct = steps <= 6 || (steps <= 8 && (uint64_t)b * heads >= 512) || b > kAttnMaxRows || most > (uint64_t(1) << 30);
+    // Runs for three work-groups on each of 256 compute units (what registers
+    // allow at the common widths), but no more than there can be steps.
+    A.head_shift = heads % 4 == 0 ? 2 : heads % 2 == 0 ? 1 : 0;
+    const uint64_t much = heads >> A.head_shift;
+    auto runs = [&](uint64_t work_groups, uint64_t per_run) {
+        return (uint32_t)std::min(std::max<uint64_t>(1, work_groups / per_run), std::min<uint64_t>(most, kAttnMaxRuns));
+    };
+    A.runs = runs(768, heads);
+    A.runs_much = runs(768, much);
+    A.runs_most = std::max(A.runs, A.runs_much);
+    A.by_heads = Div31((uint32_t)heads);
+    A.by_heads_much = Div31((uint32_t)much);
+    A.by_tiles = Div31(A.head_tiles);
+    A.by_runs = Div31(A.runs);
+    A.by_runs_much = Div31(A.runs_much);
+    A.grid = (uint32_t)(A.direct ? b * heads : std::max(A.runs * heads, A.runs_much * much));
+    // Reads that nothing can find in a 256 MiB cache again pass it by.
+    A.stream = (t[1].span() + t[2].span()) > (int64_t(1) << 28);
+    A.join_many = std::min<uint64_t>(A.runs_most, steps) > 16 && (uint64_t)b * hq * ((dv + 31) / 32) <= 512;
+    if (!A.direct) P.workspace = (int64_t)(((uint64_t)A.runs_most + b) * hq * (dv + 2) * 4 + 16);
     return CMD_OK;
 }
 
@@ -531,7 +543,7 @@ int cmd_paged_attention(const cmd_arg args[7], float scale, int32_t window, void
     A.scale_log2 = (float)((double)scale * 1.44269504088896340736);
     if (!A.direct) {
         A.ml = (float *)workspace;
-        A.acc = A.ml + ((((uint64_t)A.groups + A.b) * A.hq * 2 + 3) & ~uint64_t(3));
+        A.acc = A.ml + ((((uint64_t)A.runs_most + A.b) * A.hq * 2 + 3) & ~uint64_t(3));
     }
     const int rc = P.type == S_F16    ? launch_attention_f16(A, hip_stream)
                    : P.type == S_BF16 ? launch_attention_bf16(A, hip_stream)

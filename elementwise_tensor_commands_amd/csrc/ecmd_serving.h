@@ -74,23 +74,33 @@ struct AttnArgs {
     const int32_t *pages, *lens;
     void *out;
     float *lse;                            // may be null
-    float *acc;                            // workspace: [groups + b, hq, dv] sums
-    float *ml;                             // workspace: [groups + b, hq] (maximum, sum) pairs
+    float *acc;                            // workspace: [runs + b, hq, dv] sums
+    float *ml;                             // workspace: [runs + b, hq] (maximum, sum) pairs
     int64_t qs[2], os[2], ls[2];           // batch, head
     int64_t kcs[3], vcs[3];                // BYTE strides of page, slot, head
     int64_t pages_s[2], lens_s;
     uint32_t b, hq, hk, d, dv, group, head_tiles;
     uint32_t n, page, cols;
-    uint32_t groups, window;               // work-groups of one head
+    uint32_t window;
     uint32_t direct;                       // 1: a work-group to a row and head, no join
+    uint32_t head_shift;                   // with much to read, 2^this waves of a work-group take a head each
+    uint32_t runs, runs_much, runs_most;   // runs of positions for each head; the larger one
+    uint32_t grid;
+    uint32_t stream, join_many;            // larger than the last-level cache; rows may have many segments
     float scale_log2;                      // scale * log2(e)
-    Div31 by_page, by_heads, by_groups;
+    Div31 by_page;
+    Div31 by_heads, by_heads_much;         // work-groups of one run: heads, heads / head_waves
+    Div31 by_tiles;                        // head_tiles
+    Div31 by_runs, by_runs_much;
 };
 
 // Positions are dealt to work-groups in steps of this many: a tile for each of
 // four waves, at 16 bits.
 constexpr uint32_t kAttnStep = 128;
-constexpr uint32_t kAttnMaxGroups = 1024;
+// Steps of all heads that count as much to read.
+constexpr uint32_t kAttnMuch = 6144;
+
+constexpr uint32_t kAttnMaxRuns = 1024;
 constexpr uint32_t kAttnMaxRows = 2048;    // rows whose prefixes fit LDS; more go direct
 
 int launch_attention_f16(const AttnArgs &A, void *stream);

@@ -78,14 +78,15 @@ __device__ inline void mark_tile(const PageBits &B, uint32_t tile, uint32_t *scr
 }
 
 // Prefixes of the tile counts into LDS: prefix[t] set bits before tile t,
-// prefix[tiles] all of them.  Ends with a barrier.
-__device__ inline void tile_prefixes(const PageBits &B, uint32_t *prefix, uint32_t *scratch)
+// prefix[tiles] all of them.  mine: the count of tile threadIdx.x (or 0), read
+// early.  Ends with a barrier.
+__device__ inline void tile_prefixes(const PageBits &B, uint32_t *prefix, uint32_t *scratch, uint32_t mine)
 {
     uint32_t run = 0;
     for (uint32_t t0 = 0; t0 < B.tiles; t0 += kBlock) {
         const uint32_t t = t0 + threadIdx.x;
         uint32_t total;
-        const uint32_t before = block_prefix(t < B.tiles ? B.tile_count[t] : 0, scratch, total);
+        const uint32_t before = block_prefix(t0 == 0 ? mine : t < B.tiles ? B.tile_count[t] : 0, scratch, total);
         if (t < B.tiles) prefix[t] = run + before;
         run += total;
     }
@@ -93,7 +94,8 @@ __device__ inline void tile_prefixes(const PageBits &B, uint32_t *prefix, uint32
     __syncthreads();
 }
 
-// The id of the set bit with this rank (rank < prefix[tiles]).
+// The id of the set bit with this rank (rank < prefix[tiles]).  Sixteen word
+// prefixes are read at once: one wait instead of four.
 __device__ inline uint32_t select_bit(const PageBits &B, const uint32_t *prefix, uint32_t rank)
 {
     uint32_t lo = 0, hi = B.tiles;   // prefix[lo] <= rank < prefix[hi]
@@ -104,13 +106,25 @@ __device__ inline uint32_t select_bit(const PageBits &B, const uint32_t *prefix,
     }
     const uint64_t w0 = (uint64_t)lo * B.tile_words;
     rank -= prefix[lo];
-    uint32_t a = 0, b = B.tile_words;
-    while (b - a > 1) {
+    uint32_t a = 0, b = B.tile_words;   // tile_words: 16 times a power of two
+    while (b - a > 16) {
         const uint32_t mid = (a + b) / 2;
         if (B.word_prefix[w0 + mid] <= rank) a = mid;
         else b = mid;
     }
-    rank -= B.word_prefix[w0 + a];
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = ((const u32x4 *)(B.word_prefix + w0 + a))[k];
+    uint32_t in = 0, before = 0;
+#pragma unroll
+    for (int k = 1; k < 16; ++k)
+        if (p[k / 4][k % 4] <= rank) {
+            in = k;
+            before = p[k / 4][k % 4];
+        }
+    a += in;
+    rank -= in ? before : p[0][0];
     const uint64_t word = B.word[w0 + a];
     uint32_t at = 0;
 #pragma unroll
@@ -170,31 +184,57 @@ __global__ __launch_bounds__(kBlock) void k_assign_count(const AssignArgs A)
     if (threadIdx.x == 0) A.want_group[g] = total;
 }
 
-// Second launch: a work-group per row.
+// Sums over the work-group; scratch: 2 kWaves entries.
+__device__ inline void block_sums(uint32_t &x, uint32_t &y, uint32_t *scratch)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        x += __shfl_xor((int)x, o);
+        y += __shfl_xor((int)y, o);
+    }
+    if ((threadIdx.x & 63) == 0) {
+        scratch[threadIdx.x >> 6] = x;
+        scratch[kWaves + (threadIdx.x >> 6)] = y;
+    }
+    __syncthreads();
+    x = y = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) {
+        x += scratch[w];
+        y += scratch[kWaves + w];
+    }
+}
+
+// Second launch: a work-group per row.  What it waits for is the chain of
+// loads, so the first launch's counts are asked for before the row's own plan is
+// made of three dependent loads.
 __global__ __launch_bounds__(kBlock) void k_assign(const AssignArgs A)
 {
-    __shared__ uint32_t prefix[kMaxPageTiles + 1], scratch[kWaves];
+    __shared__ uint32_t prefix[kMaxPageTiles + 1], scratch[kWaves], scratch2[2 * kWaves];
     const uint32_t r = blockIdx.x;
+    uint32_t count = threadIdx.x < A.bits.tiles ? A.bits.tile_count[threadIdx.x] : 0;
+    uint32_t mine = 0, all = 0;
+    for (uint32_t g = threadIdx.x; g < A.row_groups; g += kBlock) {
+        const uint32_t w = A.want_group[g];
+        all += w;
+        if (g < r / kBlock) mine += w;
+    }
     RowPlan p{};
-    if (r < A.rows) p = plan_row(A, r);
+    uint32_t base = 0;
+    if (r < A.rows) {
+        base = A.want[r];
+        p = plan_row(A, r);
+    }
     const uint32_t fresh = p.total - p.keep;
-    uint32_t have = 0, base = 0;
+    uint32_t have = 0;
     if (fresh || r == 0) {   // the same for the whole work-group
-        tile_prefixes(A.bits, prefix, scratch);
+        tile_prefixes(A.bits, prefix, scratch, count);
         have = prefix[A.bits.tiles];
-        uint32_t mine = 0, all = 0;
-        for (uint32_t g = threadIdx.x; g < A.row_groups; g += kBlock) {
-            const uint32_t w = A.want_group[g];
-            all += w;
-            if (g < r / kBlock) mine += w;
-        }
-        uint32_t wanted;
-        block_prefix(mine, scratch, base);
-        block_prefix(all, scratch, wanted);
-        if (r < A.rows) base += A.want[r];
+        block_sums(mine, all, scratch2);
+        base += mine;
         if (r == 0 && threadIdx.x == 0) {
-            A.stats[0] = (int32_t)wanted;
-            A.stats[A.stats_s] = (int32_t)min(wanted, have);
+            A.stats[0] = (int32_t)all;
+            A.stats[A.stats_s] = (int32_t)min(all, have);
         }
     }
     if (r >= A.rows) return;   // no rows at all
@@ -253,7 +293,7 @@ __device__ inline uint32_t rank_bit(const PageBits &B, const uint32_t *prefix, u
 __global__ __launch_bounds__(kBlock) void k_compact_plan(const CompactArgs A)
 {
     __shared__ uint32_t prefix[kMaxPageTiles + 1], scratch[kWaves];
-    tile_prefixes(A.bits, prefix, scratch);
+    tile_prefixes(A.bits, prefix, scratch, threadIdx.x < A.bits.tiles ? A.bits.tile_count[threadIdx.x] : 0);
     const uint32_t live = prefix[A.bits.tiles], kept = rank_bit(A.bits, prefix, live), moves = live - kept;
     const uint64_t w0 = (uint64_t)blockIdx.x * A.bits.tile_words;
     for (uint64_t i = threadIdx.x; i < (uint64_t)A.bits.tile_words * 64; i += kBlock) {

@@ -1,7 +1,7 @@
 """Serving operators beside Commands: rotary positions, a paged key-value
 cache, attention of one new token over it, and the bookkeeping of its pages.
 
-A thin ctypes layer over ``include/ecmd_serving.h``, which defines every
+A thin layer over ``include/ecmd_serving.h``, which defines every
 operator; outputs are the caller's tensors, work goes to torch's current stream
 or ``stream``, errors are ``Error`` with the library's status and message, and
 nothing is launched after a failed check.  Scratch memory is the caller's
@@ -20,14 +20,11 @@ A decode step of a model's attention:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
-import struct
 
-from . import ARG_TENSOR, BF16, F16, F32, I32, Error, cmd_arg, lib
+from . import Error, cmd_arg, lib
 
-F64 = 5
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 CHECK_ONLY = 1
 
@@ -46,36 +43,20 @@ for _name, _res, _sig in [
     getattr(lib, _name).restype = _res
     getattr(lib, _name).argtypes = _sig
 
-# One cmd_arg: kind, dtype, ptr, size[4], stride[4], bits, reserved.
-_ARG = struct.Struct("iiQ4q4qII")
-assert _ARG.size == ctypes.sizeof(cmd_arg)
-_ABSENT = bytes(_ARG.size)
-_codes: dict = {}
+_SIZE = ctypes.sizeof(cmd_arg)
+_binding = None
 
 
-def _code(dtype) -> int:
-    if not _codes:
-        import torch
-        _codes.update({torch.float16: F16, torch.float32: F32, torch.int32: I32, torch.bfloat16: BF16,
-                       torch.float64: F64})
-    return _codes.get(dtype, 0)
+def _pack(ranks: bytes, *tensors):
+    """(cmd_arg structures of the tensors, their GPU if it is the current one or
+    -1, its current stream's handle); see ecmd_binding.cpp."""
+    global _binding
+    if _binding is None:
+        import torch  # noqa: F401  (first: the module links against its libraries)
 
-
-def _pack(t, rank: int) -> bytes:
-    """The tensor as a cmd_arg of this rank; another rank is packed with sizes
-    that the library refuses."""
-    code = _codes.get(t.dtype) or _code(t.dtype)
-    size = t.shape
-    if len(size) != rank:
-        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), -1, -1, -1, -1, 0, 0, 0, 0, 0, 0)
-    st = t.stride()
-    if rank == 4:
-        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), *size, *st, 0, 0)
-    if rank == 3:
-        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), *size, 0, *st, 0, 0, 0)
-    if rank == 2:
-        return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), *size, 0, 0, *st, 0, 0, 0, 0)
-    return _ARG.pack(ARG_TENSOR, code, t.data_ptr(), size[0], 0, 0, 0, st[0], 0, 0, 0, 0, 0)
+        from . import _binding as module
+        _binding = module
+    return _binding.pack(ranks, *tensors)
 
 
 def _check(rc: int):
@@ -83,44 +64,40 @@ def _check(rc: int):
         raise Error(int(rc), lib.cmd_last_error(None).decode())
 
 
-def _run(call, tensors, stream, workspace=None, need=None):
-    """call(workspace pointer, bytes, flags, stream handle) on the tensors'
-    device.  Tensors that are not all on the current GPU are an error, after
-    the errors that the library finds in them."""
+def _refuse(rc: int):
+    """Tensors that are not all on the current GPU are an error, after the errors
+    that the library found in them (its status rc with CHECK_ONLY)."""
+    _check(rc)
+    raise Error(-1, "every tensor must be on the current GPU")
+
+
+def _handle(stream, device: int) -> int:
+    if isinstance(stream, int):
+        return stream
+    at = getattr(stream, "device", None)
+    if at is not None and at.index != device:
+        raise Error(-1, "the stream belongs to another GPU")
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _scratch(workspace, size: int, stream, device: int):
+    """(pointer, bytes, owner) of the workspace: the caller's, or from the
+    allocator of the launch's stream, which may hand the memory on once that
+    stream is done with it."""
+    _check(size)
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise Error(-1, "the workspace must be contiguous and on the current GPU")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if size == 0:
+        return None, 0, None
     import torch
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            dev = -2
-    if dev < 0 or dev != torch.cuda.current_device():
-        _check(call(None, 0, CHECK_ONLY, None))
-        raise Error(-1, "every tensor must be on the current GPU")
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, int):
-        handle = stream
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
-        handle = getattr(stream, "cuda_stream", stream)
-        at = getattr(stream, "device", None)
-        if at is not None and at.index != dev:
-            raise Error(-1, "the stream belongs to another GPU")
-    ptr, size = None, 0
-    if need is not None:
-        size = need()
-        _check(size)
-        if workspace is not None:
-            if workspace.get_device() != dev or not workspace.is_contiguous():
-                raise Error(-1, "the workspace must be contiguous and on the current GPU")
-            ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        elif size:
-            # from the allocator of the launch's stream: it may hand the memory on once that stream is done with it
-            on = contextlib.nullcontext()
-            if stream is not None:
-                on = torch.cuda.stream(torch.cuda.ExternalStream(handle) if isinstance(stream, int) else stream)
-            with on:
-                workspace = torch.empty(size, dtype=torch.uint8, device=tensors[0].device)
-            ptr = workspace.data_ptr()
-    _check(call(ptr, size, 0, handle))
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    return workspace.data_ptr(), size, workspace
 
 
 def _layout(layout) -> int:
@@ -132,9 +109,11 @@ def rope(x, pos, freq, out, *, layout="half", mscale=1.0, inverse=False, stream=
     into out, pair i by pos * freq[i] (freq: float64, on the GPU).  out may be
     x.  ``inverse`` is the transposed map: applied to the gradient of out it
     gives the gradient of x."""
-    args = b"".join((_pack(x, 4), _pack(pos, 2), _pack(freq, 1), _pack(out, 4)))
-    _run(lambda w, n, flags, s: lib.cmd_rope(args, _layout(layout), mscale, bool(inverse), flags, s),
-         (x, pos, freq, out), stream)
+    args, dev, current = _pack(b"\4\2\1\4", x, pos, freq, out)
+    if dev < 0:
+        _refuse(lib.cmd_rope(args, _layout(layout), mscale, bool(inverse), CHECK_ONLY, None))
+    _check(lib.cmd_rope(args, _layout(layout), mscale, bool(inverse), 0,
+                        current if stream is None else _handle(stream, dev)))
 
 
 def rope_append(q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache, *, layout="half", mscale=1.0, stream=None):
@@ -143,15 +122,13 @@ def rope_append(q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache, *, layo
     hk, d] turned and v [T, hk, dv] as it is into the slots of positions pos [T]
     of sequences row [T].  Tokens whose row, position or page is out of range
     are padding."""
-    args = b"".join((_pack(q, 3), _pack(k, 3), _pack(v, 3), _pack(pos, 1), _pack(row, 1), _pack(pages, 2),
-                     _pack(freq, 1), _pack(q_out, 3), _pack(k_cache, 4), _pack(v_cache, 4)))
-    _run(lambda w, n, flags, s: lib.cmd_rope_append(args, _layout(layout), mscale, flags, s),
-         (q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache), stream)
+    args, dev, current = _pack(b"\3\3\3\1\1\2\1\3\4\4", q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache)
+    if dev < 0:
+        _refuse(lib.cmd_rope_append(args, _layout(layout), mscale, CHECK_ONLY, None))
+    _check(lib.cmd_rope_append(args, _layout(layout), mscale, 0, current if stream is None else _handle(stream, dev)))
 
 
-def _attention_args(q, k_cache, v_cache, pages, lens, out, lse):
-    return b"".join((_pack(q, 3), _pack(k_cache, 4), _pack(v_cache, 4), _pack(pages, 2), _pack(lens, 1),
-                     _pack(out, 3), _ABSENT if lse is None else _pack(lse, 2)))
+_ATTENTION = b"\3\4\4\2\1\3\2"
 
 
 def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=None, window=0, workspace=None,
@@ -161,25 +138,24 @@ def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=No
     r -- the last ``window`` of them if that is not 0 -- into out [B, hq, dv],
     the log of the softmax's sum into lse [B, hq] (float32) if given.  scale:
     1 / sqrt(d) by default."""
-    args = _attention_args(q, k_cache, v_cache, pages, lens, out, lse)
+    args, dev, current = _pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(max(1, q.shape[-1])) if q.dim() else 1.0
-    tensors = (q, k_cache, v_cache, pages, lens, out) + (() if lse is None else (lse,))
-    _run(lambda w, n, flags, s: lib.cmd_paged_attention(args, scale, window, w, n, flags, s), tensors, stream,
-         workspace, lambda: lib.cmd_paged_attention_workspace(args, window))
+    if dev < 0:
+        _refuse(lib.cmd_paged_attention(args, scale, window, None, 0, CHECK_ONLY, None))
+    ptr, size, _owner = _scratch(workspace, lib.cmd_paged_attention_workspace(args, window), stream, dev)
+    _check(lib.cmd_paged_attention(args, scale, window, ptr, size, 0,
+                                   current if stream is None else _handle(stream, dev)))
 
 
 def paged_attention_workspace(q, k_cache, v_cache, pages, lens, out, *, window=0) -> int:
     """Bytes of workspace that paged_attention needs for these tensors."""
-    n = lib.cmd_paged_attention_workspace(_attention_args(q, k_cache, v_cache, pages, lens, out, None), window)
+    n = lib.cmd_paged_attention_workspace(_pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, None)[0], window)
     _check(n)
     return n
 
 
-def _assign_args(pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats):
-    return b"".join((_pack(pages, 2), _pack(lens, 1), _pack(refs, 1), _pack(parent, 1), _pack(add, 1),
-                     _pack(pages_out, 2), _pack(lens_out, 1), _pack(refs_out, 1), _pack(src, 1), _pack(dst, 1),
-                     _pack(stats, 1)))
+_ASSIGN = b"\2\1\1\1\1\2\1\1\1\1\1"
 
 
 def page_assign(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_out, src, dst, stats, *,
@@ -189,23 +165,22 @@ def page_assign(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_
     and grows by add[r] positions.  Fills pages_out, lens_out, refs_out, the
     page copies src -> dst that forks need (-1: none) and stats = (pages wanted,
     pages given).  refs_out may be refs."""
-    tensors = (pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats)
-    args = _assign_args(*tensors)
-    _run(lambda w, n, flags, s: lib.cmd_page_assign(args, page, w, n, flags, s), tensors, stream, workspace,
-         lambda: lib.cmd_page_assign_workspace(args, page))
+    args, dev, current = _pack(_ASSIGN, pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats)
+    if dev < 0:
+        _refuse(lib.cmd_page_assign(args, page, None, 0, CHECK_ONLY, None))
+    ptr, size, _owner = _scratch(workspace, lib.cmd_page_assign_workspace(args, page), stream, dev)
+    _check(lib.cmd_page_assign(args, page, ptr, size, 0, current if stream is None else _handle(stream, dev)))
 
 
 def page_assign_workspace(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_out, src, dst, stats) -> int:
     """Bytes of workspace that page_assign needs for these tensors."""
-    n = lib.cmd_page_assign_workspace(_assign_args(pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src,
-                                                   dst, stats), page)
+    args = _pack(_ASSIGN, pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats)[0]
+    n = lib.cmd_page_assign_workspace(args, page)
     _check(n)
     return n
 
 
-def _compact_args(pages, refs, pages_out, refs_out, src, dst, stats):
-    return b"".join((_pack(pages, 2), _pack(refs, 1), _pack(pages_out, 2), _pack(refs_out, 1), _pack(src, 1),
-                     _pack(dst, 1), _pack(stats, 1)))
+_COMPACT = b"\2\1\2\1\1\1\1"
 
 
 def page_compact(pages, refs, pages_out, refs_out, src, dst, stats, *, workspace=None, stream=None):
@@ -213,15 +188,16 @@ def page_compact(pages, refs, pages_out, refs_out, src, dst, stats, *, workspace
     the table and counts after it, the copies src -> dst it takes (then -1) and
     stats = (live pages, moves).  src and dst hold refs.numel() // 2 entries or
     more; pages_out may be pages."""
-    tensors = (pages, refs, pages_out, refs_out, src, dst, stats)
-    args = _compact_args(*tensors)
-    _run(lambda w, n, flags, s: lib.cmd_page_compact(args, w, n, flags, s), tensors, stream, workspace,
-         lambda: lib.cmd_page_compact_workspace(args))
+    args, dev, current = _pack(_COMPACT, pages, refs, pages_out, refs_out, src, dst, stats)
+    if dev < 0:
+        _refuse(lib.cmd_page_compact(args, None, 0, CHECK_ONLY, None))
+    ptr, size, _owner = _scratch(workspace, lib.cmd_page_compact_workspace(args), stream, dev)
+    _check(lib.cmd_page_compact(args, ptr, size, 0, current if stream is None else _handle(stream, dev)))
 
 
 def page_compact_workspace(pages, refs, pages_out, refs_out, src, dst, stats) -> int:
     """Bytes of workspace that page_compact needs for these tensors."""
-    n = lib.cmd_page_compact_workspace(_compact_args(pages, refs, pages_out, refs_out, src, dst, stats))
+    n = lib.cmd_page_compact_workspace(_pack(_COMPACT, pages, refs, pages_out, refs_out, src, dst, stats)[0])
     _check(n)
     return n
 
@@ -230,8 +206,12 @@ def page_copy(pools, src, dst, *, stream=None):
     """Copy page src[i] to page dst[i] in every pool [N, page, heads, d]
     (cmd_page_copy); pairs with an id outside the pool are skipped."""
     pools = list(pools)
-    args, a, b = b"".join([_pack(p, 4) for p in pools]), _pack(src, 1), _pack(dst, 1)
-    _run(lambda w, n, flags, s: lib.cmd_page_copy(args, len(pools), a, b, flags, s), (src, dst, *pools), stream)
+    n = len(pools)
+    args, dev, current = _pack(b"\1\1" + b"\4" * n, src, dst, *pools)
+    pairs = (args[2 * _SIZE:], n, args[:_SIZE], args[_SIZE:2 * _SIZE])
+    if dev < 0:
+        _refuse(lib.cmd_page_copy(*pairs, CHECK_ONLY, None))
+    _check(lib.cmd_page_copy(*pairs, 0, current if stream is None else _handle(stream, dev)))
 
 
 def rope_frequencies(width, *, base=10000.0, factor=1.0, scaling="linear", trained=0, slow=1.0, fast=32.0):

@@ -506,3 +506,20 @@ def test_captured_step():
         torch.cuda.synchronize()
         for key in eager:
             assert torch.equal(eager[key], captured[key]), (i, key)
+
+
+@pytest.mark.parametrize("b", [64, 65, 100, 300])
+def test_attention_many_rows(b):
+    """Row prefixes of one wave, of a work-group, and over several turns; few and many runs to a row."""
+    rng = random.Random(b)
+    lens = [rng.choice([0, 0, 1, 40, 200, 700]) for _ in range(b)]
+    check_attention(*attention_case(b, torch.float16, b, 2, 1, 32, 32, 16, lens), what=b)
+    lens = [0] * (b - 1) + [3000]
+    check_attention(*attention_case(b, torch.bfloat16, b, 4, 4, 64, 64, 16, lens), what=("last", b))
+    assert not bool(check_attention(*attention_case(b, torch.float32, b, 2, 2, 32, 32, 16, [0] * b, cols=20)).any())
+
+
+def test_attention_more_rows_than_prefixes():
+    b = 2100
+    lens = [(i * 37) % 90 for i in range(b)]
+    check_attention(*attention_case(1, torch.bfloat16, b, 2, 1, 32, 32, 16, lens), what=b)

@@ -161,13 +161,13 @@ def test_attention_refusals_of_options():
 
 
 def test_attention_workspace():
-    assert E.paged_attention_workspace(*attention_args(pages=i32(3, 1))) == 0           # one step of keys: nothing to join
+    assert E.paged_attention_workspace(*attention_args(pages=i32(3, 1))) == 0           # too few keys to cut
     a = attention_args(pages=i32(3, 4096))
     need = E.paged_attention_workspace(*a)
     assert need > 0 and E.paged_attention_workspace(*a, window=100) == 0
     # a workspace too small is refused without a HIP call (from C, as a caller would)
     from elementwise_tensor_commands_amd import serving as S
-    args = S._attention_args(*a, None)
+    args = S._pack(S._ATTENTION, *a, None)[0]
     buf = torch.zeros(need, dtype=torch.uint8)
     assert E.lib.cmd_paged_attention(args, 1.0, 0, None, 0, 0, None) == -1
     assert E.lib.cmd_paged_attention(args, 1.0, 0, buf.data_ptr(), need - 1, 0, None) == -1
