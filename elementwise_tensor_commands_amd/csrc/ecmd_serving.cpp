@@ -246,12 +246,20 @@ uint32_t head_items(int type, int layout, uint32_t pairs, uint32_t width)
     return rot + ceil_div(width - 2 * pairs, e);
 }
 
-// Tokens of a work-group: about 2048 items (eight for each work-item), while
+// No vector of a head is cut short.
+bool whole_items(int type, int layout, uint32_t pairs, uint32_t width)
+{
+    const uint32_t e = type == S_F32 ? 4 : 8;
+    return (layout == CMD_ROPE_HALF ? pairs : 2 * pairs) % e == 0 && (width - 2 * pairs) % e == 0;
+}
+
+// Tokens of a work-group: about 1024 items (the four that each work-item loads at
+// once), while
 // there remain enough groups for 256 compute units four times over and the
 // cosines stay within 16 KiB of LDS.
 uint32_t tokens_per_group(uint64_t tokens, uint64_t items, uint64_t pairs)
 {
-    uint64_t tb = std::max<uint64_t>(1, 2048 / std::max<uint64_t>(1, items));
+    uint64_t tb = std::max<uint64_t>(1, 1024 / std::max<uint64_t>(1, items));
     tb = std::min(tb, std::max<uint64_t>(1, tokens / 1024));
     tb = std::min(tb, std::max<uint64_t>(1, 16384 / (8 * ((pairs + 7) / 8 * 8) + 16)));
     return (uint32_t)tb;
@@ -310,7 +318,9 @@ int cmd_rope(const cmd_arg args[4], int32_t layout, double mscale, int32_t inver
     A.by_t = Div31((uint32_t)n);
     A.by_head_items = Div31((uint32_t)per_head);
     A.by_token_items = Div31(A.items);
-    return launched(launch_rope(type, layout, A, ceil_div(A.tokens, A.tb), turn_lds(A.tb, A.pairs), hip_stream), "rope");
+    return launched(launch_rope(type, layout, whole_items(type, layout, A.pairs, A.width), A, ceil_div(A.tokens, A.tb),
+                                turn_lds(A.tb, A.pairs), hip_stream),
+                    "rope");
 }
 
 int cmd_rope_append(const cmd_arg args[10], int32_t layout, double mscale, int32_t flags, void *hip_stream)
@@ -382,20 +392,21 @@ int cmd_rope_append(const cmd_arg args[10], int32_t layout, double mscale, int32
     A.page = (uint32_t)std::max<int64_t>(1, page);
     A.rows = (uint32_t)t[5].size(0);
     A.cols = (uint32_t)t[5].size(1);
-    A.q_items = (uint32_t)(per_qk * hq);
-    A.qk_items = (uint32_t)(per_qk * (hq + hk));
-    A.items = (uint32_t)items;
     A.mscale = mscale;
     A.tb = tokens_per_group(A.tokens, items, m);
     // few tokens: several work-groups to a token
     A.parts = A.tb > 1 ? 1 : std::max(1u, std::min(ceil_div(items, 256), 1024 / A.tokens));
     A.by_page = Div31(A.page);
-    A.by_qk = Div31((uint32_t)std::max<uint64_t>(1, per_qk));
-    A.by_v = Div31((uint32_t)std::max<uint64_t>(1, per_v));
-    A.by_token_items = Div31(A.items);
+    auto div = [](uint64_t n) { return Div31((uint32_t)n); };
+    A.by_q = div(per_qk * hq);
+    A.by_k = div(per_qk * hk);
+    A.by_v = div(per_v * hk);
+    A.by_qk_head = div(per_qk);
+    A.by_v_head = div(per_v);
     A.by_parts = Div31(A.parts);
     const uint64_t grid = (uint64_t)ceil_div(A.tokens, A.tb) * A.parts;
-    return launched(launch_append(type, layout, A, (uint32_t)grid, turn_lds(A.tb, A.pairs) + A.tb * 16, hip_stream),
+    const bool exact = whole_items(type, layout, A.pairs, A.d) && A.dv % e == 0;
+    return launched(launch_append(type, layout, exact, A, (uint32_t)grid, turn_lds(A.tb, A.pairs) + A.tb * 16, hip_stream),
                     "rope_append");
 }
 

@@ -60,12 +60,14 @@ struct AppendArgs {
     uint32_t rows, cols, n, page;
     uint32_t tb, parts;                    // tokens per work-group; work-groups per token group
     double mscale;
-    Div31 by_page, by_qk, by_v, by_token_items, by_parts;
-    uint32_t q_items, qk_items, items;     // per token: q; q and k; q, k and v
+    Div31 by_page, by_parts;
+    Div31 by_q, by_k, by_v;                // items of a token
+    Div31 by_qk_head, by_v_head;           // items of a head
 };
 
-int launch_rope(int type, int layout, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream);
-int launch_append(int type, int layout, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream);
+// exact: pairs, tails and value rows are whole 16-byte vectors
+int launch_rope(int type, int layout, bool exact, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream);
+int launch_append(int type, int layout, bool exact, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream);
 
 // --- paged attention -------------------------------------------------------
 

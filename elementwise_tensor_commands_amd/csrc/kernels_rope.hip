@@ -106,7 +106,9 @@ __host__ __device__ constexpr uint32_t rot_items(uint32_t pairs)
     return LAYOUT == 0 ? (pairs + E - 1) / E : (2 * pairs + E - 1) / E;
 }
 
-template <int TY, int LAYOUT>
+// EXACT: pairs and tail are whole vectors, so that loads need no branch (those
+// of a half layout's tail read one vector twice).
+template <int TY, int LAYOUT, bool EXACT>
 struct Item {
     typedef typename Elem<TY>::T T;
     static constexpr int E = Elem<TY>::E;
@@ -115,6 +117,12 @@ struct Item {
     __device__ void load(const T *head, uint32_t item, uint32_t pairs, uint32_t width)
     {
         const uint32_t rot = rot_items<LAYOUT, E>(pairs);
+        if constexpr (EXACT) {
+            const uint32_t at = LAYOUT == 0 && item >= rot ? 2 * pairs + (item - rot) * E : item * E;
+            a = load_vec<T, E>(head + at, E);
+            if constexpr (LAYOUT == 0) b = load_vec<T, E>(head + (item < rot ? pairs + at : at), E);
+            return;
+        }
         if (item >= rot) {
             const int at = 2 * pairs + (item - rot) * E;
             a = load_vec<T, E>(head + at, (int)width - at);
@@ -135,7 +143,7 @@ struct Item {
         const uint32_t rot = rot_items<LAYOUT, E>(pairs);
         if (item >= rot) {
             const int at = 2 * pairs + (item - rot) * E;
-            store_vec<T, E>(head + at, a, (int)width - at);
+            store_vec<T, E>(head + at, a, EXACT ? E : (int)width - at);
             return;
         }
         const int at = item * E;
@@ -146,8 +154,8 @@ struct Item {
                 a[i] = (T)(u * c - v * s);
                 b[i] = (T)(v * c + u * s);
             }
-            store_vec<T, E>(head + at, a, (int)pairs - at);
-            store_vec<T, E>(head + pairs + at, b, (int)pairs - at);
+            store_vec<T, E>(head + at, a, EXACT ? E : (int)pairs - at);
+            store_vec<T, E>(head + pairs + at, b, EXACT ? E : (int)pairs - at);
         } else {
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
@@ -156,7 +164,7 @@ struct Item {
                 a[i] = (T)(u * c - v * s);
                 a[i + 1] = (T)(v * c + u * s);
             }
-            store_vec<T, E>(head + at, a, (int)(2 * pairs) - at);
+            store_vec<T, E>(head + at, a, EXACT ? E : (int)(2 * pairs) - at);
         }
     }
 };
@@ -167,7 +175,7 @@ __host__ __device__ inline uint32_t lds_row(uint32_t pairs) { return (pairs + 7)
 extern __shared__ __attribute__((aligned(16))) float s_turn[];
 
 // A work-group: A.tb tokens, all their heads.
-template <int TY, int LAYOUT>
+template <int TY, int LAYOUT, bool EXACT>
 __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
 {
     typedef typename Elem<TY>::T T;
@@ -178,25 +186,32 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
     const uint32_t total = count * A.items;
     const uint32_t head_items = A.by_head_items.d;
 
-    uint32_t tok, head, item;
-    auto split = [&](uint32_t i) {
-        tok = A.by_token_items.div(i);
-        const uint32_t r = i - tok * A.items;
-        head = A.by_head_items.div(r);
-        item = r - head * head_items;
+    struct Place {
+        uint32_t tok, head, item;
     };
-    auto offset = [&](const int64_t *s) {
-        const uint32_t g = first + tok, bb = A.by_t.div(g);
-        return (int64_t)bb * s[0] + (int64_t)(g - bb * A.by_t.d) * s[1] + (int64_t)head * s[2];
+    auto split = [&](uint32_t i) {
+        const uint32_t tok = A.by_token_items.div(i), r = i - tok * A.items, head = A.by_head_items.div(r);
+        return Place{tok, head, r - head * head_items};
+    };
+    auto offset = [&](const Place &p, const int64_t *s) {
+        const uint32_t g = first + p.tok, bb = A.by_t.div(g);
+        return (int64_t)bb * s[0] + (int64_t)(g - bb * A.by_t.d) * s[1] + (int64_t)p.head * s[2];
     };
 
-    // The first item's loads are on their way while the angles are computed.
-    Item<TY, LAYOUT> it;
+    // Several items' loads are on their way before the first is stored, the first
+    // ones' while the angles are computed.
+    constexpr int U = 4;
+    Item<TY, LAYOUT, EXACT> it[U];
+    auto load = [&](uint32_t i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (EXACT || i0 + u * kBlock < total) {   // EXACT: the last item again instead of a branch
+                const Place p = split(EXACT ? min(i0 + u * kBlock, total - 1) : i0 + u * kBlock);
+                it[u].load((const T *)A.x + offset(p, A.xs), p.item, A.pairs, A.width);
+            }
+    };
     uint32_t i = threadIdx.x;
-    if (i < total) {
-        split(i);
-        it.load((const T *)A.x + offset(A.xs), item, A.pairs, A.width);
-    }
+    load(i);
     for (uint32_t j = threadIdx.x; j < count * A.pairs; j += kBlock) {
         const uint32_t t = j / A.pairs, p = j - t * A.pairs;
         const uint32_t g = first + t, bb = A.by_t.div(g);
@@ -208,62 +223,69 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
     }
     __syncthreads();
     while (i < total) {
-        it.finish((T *)A.out + offset(A.os), item, A.pairs, A.width, cs + tok * row, sn + tok * row);
-        i += kBlock;
-        if (i < total) {
-            split(i);
-            it.load((const T *)A.x + offset(A.xs), item, A.pairs, A.width);
-        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * kBlock < total) {
+                const Place p = split(i + u * kBlock);
+                it[u].finish((T *)A.out + offset(p, A.os), p.item, A.pairs, A.width, cs + p.tok * row, sn + p.tok * row);
+            }
+        i += U * kBlock;
+        load(i);
     }
 }
 
-// A work-group: A.tb tokens, or (A.parts > 1) a part of one token's items.
-// Items of a token: q's, k's, then v's (copied).
-template <int TY, int LAYOUT>
+// A work-group: A.tb tokens, or (A.parts > 1) a part of one token's items.  The
+// items are q's, k's, then v's (copied: a head without pairs), each kind's number
+// rounded up to whole waves: a wave's pointers and strides are then scalars.
+template <int TY, int LAYOUT, bool EXACT>
 __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
 {
     typedef typename Elem<TY>::T T;
-    constexpr int E = Elem<TY>::E;
     const uint32_t group = A.by_parts.div(blockIdx.x), part = blockIdx.x - group * A.parts;
     const uint32_t first = group * A.tb;
     const uint32_t count = min(A.tb, A.tokens - first);
     const uint32_t row = lds_row(A.pairs);
     float *cs = s_turn, *sn = s_turn + A.tb * row;
     int64_t *slot = (int64_t *)(sn + A.tb * row);   // [tb][2]: element offsets into the caches, -1: padding
-    const uint32_t total = count * A.items, step = kBlock * A.parts;
+    auto waves = [](uint32_t n) { return (n + 63) / 64 * 64; };
+    const uint32_t k_from = waves(count * A.by_q.d), v_from = k_from + waves(count * A.by_k.d);
+    const uint32_t total = v_from + waves(count * A.by_v.d), step = kBlock * A.parts;
 
-    uint32_t tok, head, item;
-    int kind;   // 0 q, 1 k, 2 v
+    struct Place {
+        uint32_t kind, tok, head, item;   // kind: 0 q, 1 k, 2 v; the same for the wave
+        bool real;
+    };
     auto split = [&](uint32_t i) {
-        tok = A.by_token_items.div(i);
-        uint32_t r = i - tok * A.items;
-        if (r >= A.qk_items) {
-            kind = 2;
-            r -= A.qk_items;
-            head = A.by_v.div(r);
-            item = r - head * A.by_v.d;
-        } else {
-            kind = r >= A.q_items;
-            if (kind) r -= A.q_items;
-            head = A.by_qk.div(r);
-            item = r - head * A.by_qk.d;
-        }
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(i & ~63u);
+        Place p;
+        p.kind = wave >= v_from ? 2 : wave >= k_from ? 1 : 0;
+        const Div31 by_token = p.kind == 2 ? A.by_v : p.kind ? A.by_k : A.by_q;
+        const Div31 by_head = p.kind == 2 ? A.by_v_head : A.by_qk_head;
+        uint32_t r = i - (p.kind == 2 ? v_from : p.kind ? k_from : 0);
+        p.real = r < count * by_token.d;
+        if (!p.real) r = 0;
+        p.tok = by_token.div(r);
+        r -= p.tok * by_token.d;
+        p.head = by_head.div(r);
+        p.item = r - p.head * by_head.d;
+        return p;
     };
-    Item<TY, LAYOUT> it;
-    auto load = [&]() {
-        const int64_t t = first + tok;
-        if (kind == 2)
-            it.a = load_vec<T, E>((const T *)A.v + t * A.vs[0] + head * A.vs[1] + item * E, (int)A.dv - (int)item * E);
-        else
-            it.load(kind ? (const T *)A.k + t * A.ks[0] + head * A.ks[1] : (const T *)A.q + t * A.qs[0] + head * A.qs[1],
-                    item, A.pairs, A.d);
+    constexpr int U = 4;   // as above
+    Item<TY, LAYOUT, EXACT> it[U];
+    auto load = [&](uint32_t i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * step < total) {
+                const Place p = split(i0 + u * step);
+                const T *from = (const T *)(p.kind == 2 ? A.v : p.kind ? A.k : A.q);
+                const int64_t ts = p.kind == 2 ? A.vs[0] : p.kind ? A.ks[0] : A.qs[0];
+                const int64_t hs = p.kind == 2 ? A.vs[1] : p.kind ? A.ks[1] : A.qs[1];
+                it[u].load(from + (int64_t)(first + p.tok) * ts + p.head * hs, p.item, p.kind == 2 ? 0 : A.pairs,
+                           p.kind == 2 ? A.dv : A.d);
+            }
     };
-
     uint32_t i = part * kBlock + threadIdx.x;
-    if (i < total) {
-        split(i);
-        load();
-    }
+    load(i);
     for (uint32_t t = threadIdx.x; t < count; t += kBlock) {
         const int32_t r = A.row[(first + t) * A.row_s], pos = A.pos[(first + t) * A.pos_s];
         int64_t ko = -1, vo = -1;
@@ -289,47 +311,43 @@ __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
     }
     __syncthreads();
     while (i < total) {
-        if (kind == 2) {
-            const int64_t at = slot[2 * tok + 1];
-            if (at >= 0)
-                store_vec<T, E>((T *)A.v_cache + at + head * A.vcs[2] + item * E, it.a, (int)A.dv - (int)item * E);
-        } else if (kind == 1) {
-            const int64_t at = slot[2 * tok];
-            if (at >= 0)
-                it.finish((T *)A.k_cache + at + head * A.kcs[2], item, A.pairs, A.d, cs + tok * row, sn + tok * row);
-        } else {
-            it.finish((T *)A.q_out + (first + tok) * A.qos[0] + head * A.qos[1], item, A.pairs, A.d, cs + tok * row,
-                      sn + tok * row);
-        }
-        i += step;
-        if (i < total) {
-            split(i);
-            load();
-        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * step < total) {
+                const Place p = split(i + u * step);
+                T *to = (T *)(p.kind == 2 ? A.v_cache : p.kind ? A.k_cache : A.q_out);
+                const int64_t hs = p.kind == 2 ? A.vcs[2] : p.kind ? A.kcs[2] : A.qos[1];
+                const int64_t at = p.kind ? slot[2 * p.tok + p.kind - 1] : (int64_t)(first + p.tok) * A.qos[0];
+                if (p.real && at >= 0)
+                    it[u].finish(to + at + p.head * hs, p.item, p.kind == 2 ? 0 : A.pairs, p.kind == 2 ? A.dv : A.d,
+                                 cs + p.tok * row, sn + p.tok * row);
+            }
+        i += U * step;
+        load(i);
     }
 }
 
 }  // namespace
 
-int launch_rope(int type, int layout, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
+int launch_rope(int type, int layout, bool exact, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-#define ECMD_CASE(TY, L)              \
-    if (type == TY && layout == L)    \
-        return launch_kernel(reinterpret_cast<const void *>(&k_rope<TY, L>), dim3(grid), dim3(kBlock), lds, stream, A);
-    ECMD_CASE(S_F16, 0) ECMD_CASE(S_F16, 1) ECMD_CASE(S_BF16, 0) ECMD_CASE(S_BF16, 1) ECMD_CASE(S_F32, 0)
-    ECMD_CASE(S_F32, 1)
+#define ECMD_CASE(TY, L, X)                                                                                      \
+    if (type == TY && layout == L && exact == X)                                                                 \
+        return launch_kernel(reinterpret_cast<const void *>(&k_rope<TY, L, X>), dim3(grid), dim3(kBlock), lds, stream, A);
+#define ECMD_CASES(TY) ECMD_CASE(TY, 0, false) ECMD_CASE(TY, 1, false) ECMD_CASE(TY, 0, true) ECMD_CASE(TY, 1, true)
+    ECMD_CASES(S_F16) ECMD_CASES(S_BF16) ECMD_CASES(S_F32)
 #undef ECMD_CASE
     return (int)hipErrorInvalidValue;
 }
 
-int launch_append(int type, int layout, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream)
+int launch_append(int type, int layout, bool exact, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-#define ECMD_CASE(TY, L)              \
-    if (type == TY && layout == L)    \
-        return launch_kernel(reinterpret_cast<const void *>(&k_append<TY, L>), dim3(grid), dim3(kBlock), lds, stream, A);
-    ECMD_CASE(S_F16, 0) ECMD_CASE(S_F16, 1) ECMD_CASE(S_BF16, 0) ECMD_CASE(S_BF16, 1) ECMD_CASE(S_F32, 0)
-    ECMD_CASE(S_F32, 1)
+#define ECMD_CASE(TY, L, X)                                                                                        \
+    if (type == TY && layout == L && exact == X)                                                                   \
+        return launch_kernel(reinterpret_cast<const void *>(&k_append<TY, L, X>), dim3(grid), dim3(kBlock), lds, stream, A);
+    ECMD_CASES(S_F16) ECMD_CASES(S_BF16) ECMD_CASES(S_F32)
 #undef ECMD_CASE
+#undef ECMD_CASES
     return (int)hipErrorInvalidValue;
 }
 
