@@ -65,9 +65,9 @@ struct AppendArgs {
     Div31 by_qk_head, by_v_head;           // items of a head
 };
 
-// exact: pairs, tails and value rows are whole 16-byte vectors
-int launch_rope(int type, int layout, bool exact, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream);
-int launch_append(int type, int layout, bool exact, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream);
+// exact: pairs, tails and value rows are whole 16-byte vectors; past: go past the caches
+int launch_rope(int type, int layout, bool exact, bool past, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream);
+int launch_append(int type, int layout, bool exact, bool past, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream);
 
 // --- paged attention -------------------------------------------------------
 
@@ -168,7 +168,7 @@ struct CopyArgs {
 
 int launch_assign(const AssignArgs &A, void *stream);
 int launch_compact(const CompactArgs &A, void *stream);
-// width: bytes of one vector (16, 8, 4 or 2)
-int launch_copy(int width, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream);
+// width: bytes of one vector (16, 8, 4 or 2); past: go past the caches
+int launch_copy(int width, bool past, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream);
 
 }  // namespace ecmd

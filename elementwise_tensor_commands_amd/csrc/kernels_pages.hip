@@ -373,7 +373,7 @@ struct CopyVec<2> {
     typedef uint16_t V;
 };
 
-template <int W>
+template <int W, bool STREAM>
 __global__ __launch_bounds__(kBlock) void k_copy(const CopyArgs A)
 {
     typedef typename CopyVec<W>::V V;
@@ -402,10 +402,18 @@ __global__ __launch_bounds__(kBlock) void k_copy(const CopyArgs A)
     V x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        if (first + k * step < P.vecs) x[k] = *(const V *)(from + at(first + k * step));
+        if (first + k * step < P.vecs) {
+            const V *p = (const V *)(from + at(first + k * step));
+            if constexpr (STREAM) x[k] = __builtin_nontemporal_load(p);
+            else x[k] = *p;
+        }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        if (first + k * step < P.vecs) *(V *)(to + at(first + k * step)) = x[k];
+        if (first + k * step < P.vecs) {
+            V *p = (V *)(to + at(first + k * step));
+            if constexpr (STREAM) __builtin_nontemporal_store(x[k], p);
+            else *p = x[k];
+        }
 }
 
 }  // namespace
@@ -439,12 +447,13 @@ int launch_compact(const CompactArgs &A, void *stream)
                          stream, A, entries);
 }
 
-int launch_copy(int width, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream)
+int launch_copy(int width, bool past, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream)
 {
-    const void *fn = width == 16  ? reinterpret_cast<const void *>(&k_copy<16>)
-                     : width == 8 ? reinterpret_cast<const void *>(&k_copy<8>)
-                     : width == 4 ? reinterpret_cast<const void *>(&k_copy<4>)
-                                  : reinterpret_cast<const void *>(&k_copy<2>);
+    const void *fn = width == 16  ? past ? reinterpret_cast<const void *>(&k_copy<16, true>)
+                                         : reinterpret_cast<const void *>(&k_copy<16, false>)
+                     : width == 8 ? reinterpret_cast<const void *>(&k_copy<8, false>)
+                     : width == 4 ? reinterpret_cast<const void *>(&k_copy<4, false>)
+                                  : reinterpret_cast<const void *>(&k_copy<2, false>);
     return launch_kernel(fn, dim3(grid, pools), dim3(kBlock), 0, stream, A);
 }
 

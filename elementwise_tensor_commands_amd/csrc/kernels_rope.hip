@@ -70,26 +70,30 @@ __device__ inline void turn(double w, double mscale, float &c, float &s)
 
 // E elements from p, of which the first n exist (the others are left alone).
 // Rows may start at any element: the 16-byte accesses need no alignment.
+// STREAM: past the caches, where a launch moves more than they hold.
 template <class T, int E>
 using Vec = T __attribute__((ext_vector_type(E)));
-template <class T, int E>
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 Any16 __attribute__((aligned(2)));
+template <class T, int E, bool STREAM>
 __device__ inline Vec<T, E> load_vec(const T *p, int n)
 {
-    Vec<T, E> v = (T)0.0f;
     if (n >= E) {
-        __builtin_memcpy(&v, p, sizeof v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (i < n) v[i] = p[i];
+        if constexpr (STREAM) return __builtin_bit_cast(Vec<T, E>, __builtin_nontemporal_load((const Any16 *)p));
+        else return __builtin_bit_cast(Vec<T, E>, *(const Any16 *)p);
     }
+    Vec<T, E> v = (T)0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if (i < n) v[i] = p[i];
     return v;
 }
-template <class T, int E>
+template <class T, int E, bool STREAM>
 __device__ inline void store_vec(T *p, Vec<T, E> v, int n)
 {
     if (n >= E) {
-        __builtin_memcpy(p, &v, sizeof v);
+        if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (Any16 *)p);
+        else *(Any16 *)p = __builtin_bit_cast(u32x4, v);
     } else {
 #pragma unroll
         for (int i = 0; i < E; ++i)
@@ -108,7 +112,7 @@ __host__ __device__ constexpr uint32_t rot_items(uint32_t pairs)
 
 // EXACT: pairs and tail are whole vectors, so that loads need no branch (those
 // of a half layout's tail read one vector twice).
-template <int TY, int LAYOUT, bool EXACT>
+template <int TY, int LAYOUT, bool EXACT, bool STREAM>
 struct Item {
     typedef typename Elem<TY>::T T;
     static constexpr int E = Elem<TY>::E;
@@ -119,20 +123,20 @@ struct Item {
         const uint32_t rot = rot_items<LAYOUT, E>(pairs);
         if constexpr (EXACT) {
             const uint32_t at = LAYOUT == 0 && item >= rot ? 2 * pairs + (item - rot) * E : item * E;
-            a = load_vec<T, E>(head + at, E);
-            if constexpr (LAYOUT == 0) b = load_vec<T, E>(head + (item < rot ? pairs + at : at), E);
+            a = load_vec<T, E, STREAM>(head + at, E);
+            if constexpr (LAYOUT == 0) b = load_vec<T, E, STREAM>(head + (item < rot ? pairs + at : at), E);
             return;
         }
         if (item >= rot) {
             const int at = 2 * pairs + (item - rot) * E;
-            a = load_vec<T, E>(head + at, (int)width - at);
+            a = load_vec<T, E, STREAM>(head + at, (int)width - at);
         } else if (LAYOUT == 0) {
             const int at = item * E;
-            a = load_vec<T, E>(head + at, (int)pairs - at);
-            b = load_vec<T, E>(head + pairs + at, (int)pairs - at);
+            a = load_vec<T, E, STREAM>(head + at, (int)pairs - at);
+            b = load_vec<T, E, STREAM>(head + pairs + at, (int)pairs - at);
         } else {
             const int at = item * E;
-            a = load_vec<T, E>(head + at, (int)(2 * pairs) - at);
+            a = load_vec<T, E, STREAM>(head + at, (int)(2 * pairs) - at);
         }
     }
 
@@ -143,7 +147,7 @@ struct Item {
         const uint32_t rot = rot_items<LAYOUT, E>(pairs);
         if (item >= rot) {
             const int at = 2 * pairs + (item - rot) * E;
-            store_vec<T, E>(head + at, a, EXACT ? E : (int)width - at);
+            store_vec<T, E, STREAM>(head + at, a, EXACT ? E : (int)width - at);
             return;
         }
         const int at = item * E;
@@ -154,8 +158,8 @@ struct Item {
                 a[i] = (T)(u * c - v * s);
                 b[i] = (T)(v * c + u * s);
             }
-            store_vec<T, E>(head + at, a, EXACT ? E : (int)pairs - at);
-            store_vec<T, E>(head + pairs + at, b, EXACT ? E : (int)pairs - at);
+            store_vec<T, E, STREAM>(head + at, a, EXACT ? E : (int)pairs - at);
+            store_vec<T, E, STREAM>(head + pairs + at, b, EXACT ? E : (int)pairs - at);
         } else {
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
@@ -164,7 +168,7 @@ struct Item {
                 a[i] = (T)(u * c - v * s);
                 a[i + 1] = (T)(v * c + u * s);
             }
-            store_vec<T, E>(head + at, a, EXACT ? E : (int)(2 * pairs) - at);
+            store_vec<T, E, STREAM>(head + at, a, EXACT ? E : (int)(2 * pairs) - at);
         }
     }
 };
@@ -175,7 +179,7 @@ __host__ __device__ inline uint32_t lds_row(uint32_t pairs) { return (pairs + 7)
 extern __shared__ __attribute__((aligned(16))) float s_turn[];
 
 // A work-group: A.tb tokens, all their heads.
-template <int TY, int LAYOUT, bool EXACT>
+template <int TY, int LAYOUT, bool EXACT, bool STREAM>
 __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
 {
     typedef typename Elem<TY>::T T;
@@ -201,7 +205,7 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
     // Several items' loads are on their way before the first is stored, the first
     // ones' while the angles are computed.
     constexpr int U = 4;
-    Item<TY, LAYOUT, EXACT> it[U];
+    Item<TY, LAYOUT, EXACT, STREAM> it[U];
     auto load = [&](uint32_t i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -237,7 +241,7 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
 // A work-group: A.tb tokens, or (A.parts > 1) a part of one token's items.  The
 // items are q's, k's, then v's (copied: a head without pairs), each kind's number
 // rounded up to whole waves: a wave's pointers and strides are then scalars.
-template <int TY, int LAYOUT, bool EXACT>
+template <int TY, int LAYOUT, bool EXACT, bool STREAM>
 __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
 {
     typedef typename Elem<TY>::T T;
@@ -271,7 +275,7 @@ __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
         return p;
     };
     constexpr int U = 4;   // as above
-    Item<TY, LAYOUT, EXACT> it[U];
+    Item<TY, LAYOUT, EXACT, STREAM> it[U];
     auto load = [&](uint32_t i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -329,26 +333,51 @@ __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
 
 }  // namespace
 
-int launch_rope(int type, int layout, bool exact, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
+template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+static int launch_one(const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-#define ECMD_CASE(TY, L, X)                                                                                      \
-    if (type == TY && layout == L && exact == X)                                                                 \
-        return launch_kernel(reinterpret_cast<const void *>(&k_rope<TY, L, X>), dim3(grid), dim3(kBlock), lds, stream, A);
-#define ECMD_CASES(TY) ECMD_CASE(TY, 0, false) ECMD_CASE(TY, 1, false) ECMD_CASE(TY, 0, true) ECMD_CASE(TY, 1, true)
-    ECMD_CASES(S_F16) ECMD_CASES(S_BF16) ECMD_CASES(S_F32)
-#undef ECMD_CASE
+    return launch_kernel(reinterpret_cast<const void *>(&k_rope<TY, LAYOUT, EXACT, STREAM>), dim3(grid), dim3(kBlock),
+                         lds, stream, A);
+}
+template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+static int launch_one(const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream)
+{
+    return launch_kernel(reinterpret_cast<const void *>(&k_append<TY, LAYOUT, EXACT, STREAM>), dim3(grid), dim3(kBlock),
+                         lds, stream, A);
+}
+template <int TY, int LAYOUT, class Args>
+static int launch_layout(bool exact, bool past, const Args &A, uint32_t grid, uint32_t lds, void *stream)
+{
+    if (exact)
+        return past ? launch_one<TY, LAYOUT, true, true>(A, grid, lds, stream)
+                    : launch_one<TY, LAYOUT, true, false>(A, grid, lds, stream);
+    return past ? launch_one<TY, LAYOUT, false, true>(A, grid, lds, stream)
+                : launch_one<TY, LAYOUT, false, false>(A, grid, lds, stream);
+}
+template <class Args>
+static int launch_any(int type, int layout, bool exact, bool past, const Args &A, uint32_t grid, uint32_t lds,
+                      void *stream)
+{
+    switch (2 * type + layout) {
+    case 2 * S_F16: return launch_layout<S_F16, 0>(exact, past, A, grid, lds, stream);
+    case 2 * S_F16 + 1: return launch_layout<S_F16, 1>(exact, past, A, grid, lds, stream);
+    case 2 * S_BF16: return launch_layout<S_BF16, 0>(exact, past, A, grid, lds, stream);
+    case 2 * S_BF16 + 1: return launch_layout<S_BF16, 1>(exact, past, A, grid, lds, stream);
+    case 2 * S_F32: return launch_layout<S_F32, 0>(exact, past, A, grid, lds, stream);
+    case 2 * S_F32 + 1: return launch_layout<S_F32, 1>(exact, past, A, grid, lds, stream);
+    }
     return (int)hipErrorInvalidValue;
 }
 
-int launch_append(int type, int layout, bool exact, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream)
+int launch_rope(int type, int layout, bool exact, bool past, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-#define ECMD_CASE(TY, L, X)                                                                                        \
-    if (type == TY && layout == L && exact == X)                                                                   \
-        return launch_kernel(reinterpret_cast<const void *>(&k_append<TY, L, X>), dim3(grid), dim3(kBlock), lds, stream, A);
-    ECMD_CASES(S_F16) ECMD_CASES(S_BF16) ECMD_CASES(S_F32)
-#undef ECMD_CASE
-#undef ECMD_CASES
-    return (int)hipErrorInvalidValue;
+    return launch_any(type, layout, exact, past, A, grid, lds, stream);
+}
+
+int launch_append(int type, int layout, bool exact, bool past, const AppendArgs &A, uint32_t grid, uint32_t lds,
+                  void *stream)
+{
+    return launch_any(type, layout, exact, past, A, grid, lds, stream);
 }
 
 }  // namespace ecmd
