@@ -700,7 +700,7 @@ int plan_compact(const cmd_arg *args, CompactPlan &P)
     A.cols = (uint32_t)cols;
     A.capacity = (uint32_t)t[4].size(0);
     A.by_cols = Div31(std::max(1u, A.cols));
-    P.workspace = plan_bits(A.bits, n) + ((int64_t)A.bits.tiles * A.bits.tile_words + 2) * 4;
+    P.workspace = plan_bits(A.bits, n);
     return CMD_OK;
 }
 
@@ -773,7 +773,7 @@ int cmd_page_compact(const cmd_arg args[7], void *workspace, int64_t workspace_b
     TRY(plan_compact(args, P));
     if (flags & CMD_CHECK_ONLY) return CMD_OK;
     TRY(check_workspace(workspace, workspace_bytes, P.workspace));
-    P.A.rank = (uint32_t *)place_bits(P.A.bits, (char *)workspace);
+    place_bits(P.A.bits, (char *)workspace);
     return launched(launch_compact(P.A, hip_stream), "page_compact");
 }
 

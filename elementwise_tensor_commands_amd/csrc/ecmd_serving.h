@@ -145,7 +145,6 @@ struct CompactArgs {
     int64_t refs_s, refs_out_s, src_s, dst_s, stats_s;
     uint32_t rows, cols, capacity;
     PageBits bits;
-    uint32_t *rank;          // workspace: [tiles * tile_words + 2] set bits before the word; then live, rank(live)
     Div31 by_cols;
 };
 

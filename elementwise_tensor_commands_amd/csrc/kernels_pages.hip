@@ -94,38 +94,43 @@ __device__ inline void tile_prefixes(const PageBits &B, uint32_t *prefix, uint32
     __syncthreads();
 }
 
-// The id of the set bit with this rank (rank < prefix[tiles]).  Sixteen word
-// prefixes are read at once: one wait instead of four.
+// The id of the set (SET) or clear bit with this rank, which has to exist.
+// Sixteen word prefixes are read at once: one wait instead of four.
+template <bool SET>
 __device__ inline uint32_t select_bit(const PageBits &B, const uint32_t *prefix, uint32_t rank)
 {
-    uint32_t lo = 0, hi = B.tiles;   // prefix[lo] <= rank < prefix[hi]
+    // bits of the kind before a place, from the set ones before it
+    auto kind = [](uint32_t set, uint64_t places) { return SET ? set : (uint32_t)places - set; };
+    uint32_t lo = 0, hi = B.tiles;
     while (hi - lo > 1) {
         const uint32_t mid = (lo + hi) / 2;
-        if (prefix[mid] <= rank) lo = mid;
+        if (kind(prefix[mid], (uint64_t)mid * B.tile_words * 64) <= rank) lo = mid;
         else hi = mid;
     }
     const uint64_t w0 = (uint64_t)lo * B.tile_words;
-    rank -= prefix[lo];
+    rank -= kind(prefix[lo], w0 * 64);
     uint32_t a = 0, b = B.tile_words;   // tile_words: 16 times a power of two
     while (b - a > 16) {
         const uint32_t mid = (a + b) / 2;
-        if (B.word_prefix[w0 + mid] <= rank) a = mid;
+        if (kind(B.word_prefix[w0 + mid], mid * 64) <= rank) a = mid;
         else b = mid;
     }
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     u32x4 p[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) p[k] = ((const u32x4 *)(B.word_prefix + w0 + a))[k];
-    uint32_t in = 0, before = 0;
+    uint32_t in = 0, before = kind(p[0][0], a * 64);
 #pragma unroll
-    for (int k = 1; k < 16; ++k)
-        if (p[k / 4][k % 4] <= rank) {
+    for (int k = 1; k < 16; ++k) {
+        const uint32_t x = kind(p[k / 4][k % 4], (a + k) * 64);
+        if (x <= rank) {
             in = k;
-            before = p[k / 4][k % 4];
+            before = x;
         }
+    }
+    rank -= before;
     a += in;
-    rank -= in ? before : p[0][0];
-    const uint64_t word = B.word[w0 + a];
+    const uint64_t word = SET ? B.word[w0 + a] : ~B.word[w0 + a];
     uint32_t at = 0;
 #pragma unroll
     for (uint32_t half = 32; half; half /= 2) {
@@ -254,7 +259,7 @@ __global__ __launch_bounds__(kBlock) void k_assign(const AssignArgs A)
             if (now < 0 || (uint32_t)now >= A.bits.n) now = -1;
         } else if (c < p.total) {
             const uint32_t rank = base + (c - p.keep);
-            if (rank < have) now = (int32_t)select_bit(A.bits, prefix, rank);
+            if (rank < have) now = (int32_t)select_bit<true>(A.bits, prefix, rank);
         }
         A.pages_out[(int64_t)r * A.pages_out_s[0] + c * A.pages_out_s[1]] = now;
         if (was != now) {
@@ -287,66 +292,55 @@ __device__ inline uint32_t rank_bit(const PageBits &B, const uint32_t *prefix, u
     return prefix[tile] + B.word_prefix[w] + popc(B.word[w] & ((uint64_t(1) << (id % 64)) - 1));
 }
 
-// Second launch: a work-group per tile.  With live = all set bits, the pages at
-// or past live are counted from the first of those (its rank: `kept`), the free
-// ids below live are id - rank(id)-th of their kind.
-__global__ __launch_bounds__(kBlock) void k_compact_plan(const CompactArgs A)
+// Second launch, all of the rest from the bits: work-groups for the ids, then for
+// the table's entries.  With `live` set bits in all, `kept` of them before id live,
+// the i-th move goes from the set bit of rank kept + i to the clear bit of rank i.
+__global__ __launch_bounds__(kBlock) void k_compact(const CompactArgs A, uint32_t id_groups)
 {
     __shared__ uint32_t prefix[kMaxPageTiles + 1], scratch[kWaves];
-    tile_prefixes(A.bits, prefix, scratch, threadIdx.x < A.bits.tiles ? A.bits.tile_count[threadIdx.x] : 0);
+    const uint32_t count = threadIdx.x < A.bits.tiles ? A.bits.tile_count[threadIdx.x] : 0;
+    const bool entries = blockIdx.x >= id_groups;
+    const uint32_t i = (blockIdx.x - (entries ? id_groups : 0)) * kBlock + threadIdx.x;
+    // what the bits are asked for, read before they are
+    const bool here = entries ? i < A.rows * A.cols : i < A.bits.n;
+    const uint32_t r = entries ? A.by_cols.div(i) : 0, c = i - r * A.cols;
+    int32_t id = (int32_t)i, refs = 0;
+    if (entries && here) id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
+    if (!entries && here) refs = A.refs[i * A.refs_s];
+    const bool valid = here && id >= 0 && (uint32_t)id < A.bits.n;
+    const uint64_t word = valid ? A.bits.word[id / 64] : 0;
+    const uint32_t word_prefix = valid ? A.bits.word_prefix[id / 64] : 0;
+    tile_prefixes(A.bits, prefix, scratch, count);
     const uint32_t live = prefix[A.bits.tiles], kept = rank_bit(A.bits, prefix, live), moves = live - kept;
-    const uint64_t w0 = (uint64_t)blockIdx.x * A.bits.tile_words;
-    for (uint64_t i = threadIdx.x; i < (uint64_t)A.bits.tile_words * 64; i += kBlock) {
-        const uint64_t word = w0 + i / 64, id = word * 64 + i % 64;
-        const uint32_t before = prefix[blockIdx.x] + A.bits.word_prefix[word];
-        if (i % 64 == 0) A.rank[word] = before;
-        if (id >= A.bits.n) continue;
-        const uint64_t bits = A.bits.word[word];
-        const bool set = bits >> (i % 64) & 1;
-        const uint32_t rank = before + popc(bits & ((uint64_t(1) << (i % 64)) - 1));
-        if (set && id >= live) A.src[(rank - kept) * A.src_s] = (int32_t)id;
-        if (!set && id < live) A.dst[((uint32_t)id - rank) * A.dst_s] = (int32_t)id;
-        if (set && id < live) A.refs_out[id * A.refs_out_s] = A.refs[id * A.refs_s];
-        if (id >= live) A.refs_out[id * A.refs_out_s] = 0;
+    const bool set = valid && (word >> (id % 64) & 1);
+    const uint32_t rank = valid ? prefix[id / 64 >> A.bits.tile_shift] + word_prefix +
+                                      popc(word & ((uint64_t(1) << (id % 64)) - 1))
+                                : 0;
+    if (entries) {
+        if (!here) return;
+        int32_t now = -1;
+        if (set) now = (uint32_t)id < live ? id : (int32_t)select_bit<false>(A.bits, prefix, rank - kept);
+        A.pages_out[(int64_t)r * A.pages_out_s[0] + (int64_t)c * A.pages_out_s[1]] = now;
+        return;
+    }
+    if (i >= moves && i < A.capacity) {
+        A.src[i * A.src_s] = -1;
+        A.dst[i * A.dst_s] = -1;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        uint32_t *head = A.rank + (uint64_t)A.bits.tiles * A.bits.tile_words;
-        head[0] = live;
-        head[1] = kept;
         A.stats[0] = (int32_t)live;
         A.stats[A.stats_s] = (int32_t)moves;
     }
-}
-
-// Third launch: the table, the moved pages' counts and the unused pairs.
-__global__ __launch_bounds__(kBlock) void k_compact_apply(const CompactArgs A, uint32_t entry_groups)
-{
-    const uint32_t *head = A.rank + (uint64_t)A.bits.tiles * A.bits.tile_words;
-    const uint32_t live = head[0], kept = head[1], moves = live - kept;
-    if (blockIdx.x >= entry_groups) {
-        const uint32_t i = (blockIdx.x - entry_groups) * kBlock + threadIdx.x;
-        if (i < moves) {
-            A.refs_out[A.dst[i * A.dst_s] * A.refs_out_s] = A.refs[A.src[i * A.src_s] * A.refs_s];
-        } else if (i < A.capacity) {
-            A.src[i * A.src_s] = -1;
-            A.dst[i * A.dst_s] = -1;
-        }
-        return;
+    if (!here) return;
+    if (i >= live) {
+        refs = 0;
+    } else if (!set) {   // a page comes here
+        const uint32_t move = i - rank, from = select_bit<true>(A.bits, prefix, kept + move);
+        A.src[move * A.src_s] = (int32_t)from;
+        A.dst[move * A.dst_s] = (int32_t)i;
+        refs = A.refs[from * A.refs_s];
     }
-    const uint32_t i = blockIdx.x * kBlock + threadIdx.x;
-    if (i >= A.rows * A.cols) return;
-    const uint32_t r = A.by_cols.div(i), c = i - r * A.cols;
-    const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
-    int32_t now = -1;
-    if (id >= 0 && (uint32_t)id < A.bits.n) {
-        const uint64_t bits = A.bits.word[id / 64];
-        if (bits >> (id % 64) & 1) {
-            now = id;
-            if ((uint32_t)id >= live)
-                now = A.dst[(A.rank[id / 64] + popc(bits & ((uint64_t(1) << (id % 64)) - 1)) - kept) * A.dst_s];
-        }
-    }
-    A.pages_out[(int64_t)r * A.pages_out_s[0] + (int64_t)c * A.pages_out_s[1]] = now;
+    A.refs_out[i * A.refs_out_s] = refs;
 }
 
 // ---------------------------------------------------------------------------
@@ -436,15 +430,12 @@ int launch_compact(const CompactArgs &A, void *stream)
     if (A.bits.tiles)
         rc = launch_kernel(reinterpret_cast<const void *>(&k_compact_mark), dim3(A.bits.tiles), dim3(kBlock), 0, stream,
                            A);
-    if (!rc)
-        rc = launch_kernel(reinterpret_cast<const void *>(&k_compact_plan), dim3(A.bits.tiles ? A.bits.tiles : 1),
-                           dim3(kBlock), 0, stream, A);
     if (rc) return rc;
     const uint32_t entries = (uint32_t)(((uint64_t)A.rows * A.cols + kBlock - 1) / kBlock);
-    const uint32_t moved = (uint32_t)(((uint64_t)A.capacity + kBlock - 1) / kBlock);
-    if (entries + moved == 0) return 0;
-    return launch_kernel(reinterpret_cast<const void *>(&k_compact_apply), dim3(entries + moved), dim3(kBlock), 0,
-                         stream, A, entries);
+    const uint64_t ids = A.bits.n > A.capacity ? A.bits.n : A.capacity;
+    const uint32_t id_groups = ids ? (uint32_t)((ids + kBlock - 1) / kBlock) : 1;   // one at least, for the counts
+    return launch_kernel(reinterpret_cast<const void *>(&k_compact), dim3(id_groups + entries), dim3(kBlock), 0, stream,
+                         A, id_groups);
 }
 
 int launch_copy(int width, bool past, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream)
