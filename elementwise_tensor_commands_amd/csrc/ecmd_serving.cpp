@@ -654,8 +654,11 @@ int plan_assign(const cmd_arg *args, int32_t page, AssignPlan &P)
     A.cols = (uint32_t)cols;
     A.page = (uint32_t)page;
     A.by_page = Div31(A.page);
+    A.by_cols = Div31(std::max(1u, A.cols));
     A.row_groups = ceil_div(A.rows, 256);
     P.workspace = plan_bits(A.bits, n) + (int64_t)A.rows * 4 + (int64_t)A.row_groups * 4;
+    A.small = n <= kSmallPages && rows <= kSmallRows && rows * cols <= kSmallEntries;
+    if (A.small) P.workspace = 0;
     return CMD_OK;
 }
 
@@ -701,6 +704,8 @@ int plan_compact(const cmd_arg *args, CompactPlan &P)
     A.capacity = (uint32_t)t[4].size(0);
     A.by_cols = Div31(std::max(1u, A.cols));
     P.workspace = plan_bits(A.bits, n);
+    A.small = n <= kSmallPages && A.capacity <= kSmallPages && rows * cols <= kSmallEntries;
+    if (A.small) P.workspace = 0;
     return CMD_OK;
 }
 

@@ -125,6 +125,9 @@ struct PageBits {
     uint32_t n, tiles, tile_words, tile_shift;   // tile_words = 1 << tile_shift
 };
 
+// What one work-group does alone, in one launch and without a workspace.
+constexpr uint32_t kSmallPages = 4096, kSmallRows = 1024, kSmallEntries = 2048;
+
 struct AssignArgs {
     const int32_t *pages, *lens, *refs, *parent, *add;
     int32_t *pages_out, *lens_out, *refs_out, *src, *dst, *stats;
@@ -134,8 +137,8 @@ struct AssignArgs {
     PageBits bits;
     uint32_t *want;          // workspace: [rows] pages wanted before the row within its group of 256
     uint32_t *want_group;    // workspace: [groups] pages wanted by the group
-    uint32_t row_groups;
-    Div31 by_page;
+    uint32_t row_groups, small;
+    Div31 by_page, by_cols;
 };
 
 struct CompactArgs {
@@ -143,7 +146,7 @@ struct CompactArgs {
     int32_t *pages_out, *refs_out, *src, *dst, *stats;
     int64_t pages_s[2], pages_out_s[2];
     int64_t refs_s, refs_out_s, src_s, dst_s, stats_s;
-    uint32_t rows, cols, capacity;
+    uint32_t rows, cols, capacity, small;
     PageBits bits;
     Div31 by_cols;
 };

@@ -25,8 +25,9 @@ constexpr uint32_t kBlock = 256, kWaves = kBlock / 64;
 
 __device__ inline uint32_t popc(uint64_t x) { return (uint32_t)__popcll(x); }
 
-// Exclusive prefix of x over the work-group (all threads call it); total gets
-// the sum.  scratch: kWaves + 1 entries, reusable after the next barrier.
+// Exclusive prefix of x over the work-group of NW waves (all threads call it);
+// total gets the sum.  scratch: NW entries, free again when it returns.
+template <uint32_t NW = kWaves>
 __device__ inline uint32_t block_prefix(uint32_t x, uint32_t *scratch, uint32_t &total)
 {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -41,7 +42,7 @@ __device__ inline uint32_t block_prefix(uint32_t x, uint32_t *scratch, uint32_t 
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (uint32_t w = 0; w < kWaves; ++w) {
+    for (uint32_t w = 0; w < NW; ++w) {
         if (w < wave) before += scratch[w];
         total += scratch[w];
     }
@@ -189,6 +190,38 @@ __global__ __launch_bounds__(kBlock) void k_assign_count(const AssignArgs A)
     if (threadIdx.x == 0) A.want_group[g] = total;
 }
 
+// Column c of row r: its page, what that changes in the counts (add(id, by)), and
+// the copy of a parent's partial page.
+template <class F>
+__device__ inline void assign_entry(const AssignArgs &A, const PageBits &B, const uint32_t *prefix, const RowPlan &p,
+                                    uint32_t r, uint32_t c, uint32_t base, uint32_t have, F add)
+{
+    const uint32_t held = A.by_page.div(p.old + A.page - 1), last = A.by_page.div(p.length);
+    const int32_t *own = A.pages + (int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1];
+    const int32_t *from = A.pages + (int64_t)p.parent * A.pages_s[0] + (int64_t)c * A.pages_s[1];
+    int32_t was = -1, now = -1;
+    if (c < held) was = *own;
+    if (was < 0 || (uint32_t)was >= B.n) was = -1;
+    if (c < p.keep) {
+        now = *from;
+        if (now < 0 || (uint32_t)now >= B.n) now = -1;
+    } else if (c < p.total) {
+        const uint32_t rank = base + (c - p.keep);
+        if (rank < have) now = (int32_t)select_bit<true>(B, prefix, rank);
+    }
+    A.pages_out[(int64_t)r * A.pages_out_s[0] + (int64_t)c * A.pages_out_s[1]] = now;
+    if (was != now) {
+        if (was >= 0) add(was, -1);
+        if (now >= 0) add(now, 1);
+    }
+    if (c == last && p.has && p.parent != r && p.length != last * A.page) {
+        const int32_t a = *from;
+        const bool copy = a >= 0 && (uint32_t)a < B.n && now >= 0;
+        A.src[r * A.src_s] = copy ? a : -1;
+        A.dst[r * A.dst_s] = copy ? now : -1;
+    }
+}
+
 // Sums over the work-group; scratch: 2 kWaves entries.
 __device__ inline void block_sums(uint32_t &x, uint32_t &y, uint32_t *scratch)
 {
@@ -243,36 +276,14 @@ __global__ __launch_bounds__(kBlock) void k_assign(const AssignArgs A)
         }
     }
     if (r >= A.rows) return;   // no rows at all
-    const uint32_t held = A.by_page.div(p.old + A.page - 1), last = A.by_page.div(p.length);
-    const bool partial = p.has && p.parent != r && p.length != last * A.page;
-    const int32_t *own = A.pages + (int64_t)r * A.pages_s[0], *from = A.pages + (int64_t)p.parent * A.pages_s[0];
+    const bool partial = p.has && p.parent != r && p.length != A.by_page.div(p.length) * A.page;
     if (threadIdx.x == 0) {
         A.lens_out[r * A.lens_out_s] = (int32_t)p.len_new;
         if (!partial) A.src[r * A.src_s] = A.dst[r * A.dst_s] = -1;
     }
-    for (uint32_t c = threadIdx.x; c < A.cols; c += kBlock) {
-        int32_t was = -1, now = -1;
-        if (c < held) was = own[c * A.pages_s[1]];
-        if (was < 0 || (uint32_t)was >= A.bits.n) was = -1;
-        if (c < p.keep) {
-            now = from[c * A.pages_s[1]];
-            if (now < 0 || (uint32_t)now >= A.bits.n) now = -1;
-        } else if (c < p.total) {
-            const uint32_t rank = base + (c - p.keep);
-            if (rank < have) now = (int32_t)select_bit<true>(A.bits, prefix, rank);
-        }
-        A.pages_out[(int64_t)r * A.pages_out_s[0] + c * A.pages_out_s[1]] = now;
-        if (was != now) {
-            if (was >= 0) atomicSub(&A.refs_out[was * A.refs_out_s], 1);
-            if (now >= 0) atomicAdd(&A.refs_out[now * A.refs_out_s], 1);
-        }
-        if (partial && c == last) {
-            const int32_t a = from[c * A.pages_s[1]];
-            const bool copy = a >= 0 && (uint32_t)a < A.bits.n && now >= 0;
-            A.src[r * A.src_s] = copy ? a : -1;
-            A.dst[r * A.dst_s] = copy ? now : -1;
-        }
-    }
+    for (uint32_t c = threadIdx.x; c < A.cols; c += kBlock)
+        assign_entry(A, A.bits, prefix, p, r, c, base, have,
+                     [&](int32_t id, int32_t by) { atomicAdd(&A.refs_out[id * A.refs_out_s], by); });
 }
 
 // ---------------------------------------------------------------------------
@@ -341,6 +352,125 @@ __global__ __launch_bounds__(kBlock) void k_compact(const CompactArgs A, uint32_
         refs = A.refs[from * A.refs_s];
     }
     A.refs_out[i * A.refs_out_s] = refs;
+}
+
+// ---------------------------------------------------------------------------
+// Small problems in one launch: one work-group, bits and counts in LDS.  On the
+// stream that is no faster (2000 pages, 32 rows of 64 entries: assigning 9.4 us
+// against 7.4 in two launches, compacting 7.4 against 6.3), but a caller's time is
+// mostly launches, 2.5 us each, and the workspace, 1.5 us: page_assign and
+// page_copy together 11.9 us a step against 15.7.  With four times the entries one
+// compute unit takes twice the two launches' time (16.7 us against 7.7), so the
+// limit is two entries to a work-item.
+
+constexpr uint32_t kSmallBlock = kSmallRows, kSmallWords = kSmallPages / 64;
+
+struct SmallBits {
+    uint64_t word[kSmallWords];
+    __attribute__((aligned(16))) uint32_t word_prefix[kSmallWords];
+    uint32_t prefix[2], scratch[kSmallBlock / 64];
+};
+
+// The counts into LDS and the bits of those that pick(count) says.
+template <class F>
+__device__ inline PageBits small_bits(SmallBits &S, int32_t *counts, const int32_t *refs, int64_t stride, uint32_t n, F pick)
+{
+    for (uint32_t id = threadIdx.x; id < kSmallPages; id += kSmallBlock) {   // whole waves
+        int32_t c = 0;
+        if (id < n) counts[id] = c = refs[id * stride];
+        const uint64_t bits = __ballot(id < n && pick(c));
+        if (threadIdx.x % 64 == 0) S.word[id / 64] = bits;
+    }
+    __syncthreads();
+    const uint32_t w = threadIdx.x;
+    uint32_t total;
+    const uint32_t before = block_prefix<kSmallBlock / 64>(w < kSmallWords ? popc(S.word[w]) : 0, S.scratch, total);
+    if (w < kSmallWords) S.word_prefix[w] = before;
+    if (w == 0) {
+        S.prefix[0] = 0;
+        S.prefix[1] = total;
+    }
+    __syncthreads();
+    PageBits B{};
+    B.word = S.word;
+    B.word_prefix = S.word_prefix;
+    B.n = n;
+    B.tiles = 1;
+    B.tile_words = kSmallWords;
+    while ((1u << B.tile_shift) < kSmallWords) ++B.tile_shift;
+    return B;
+}
+
+__global__ __launch_bounds__(kSmallBlock) void k_assign_small(const AssignArgs A)
+{
+    __shared__ SmallBits S;
+    __shared__ int32_t counts[kSmallPages];
+    __shared__ uint32_t s_base[kSmallBlock];
+    __shared__ RowPlan s_plan[kSmallBlock];
+    const uint32_t n = A.bits.n, tid = threadIdx.x;
+    RowPlan p{};
+    if (tid < A.rows) p = plan_row(A, tid);
+    const PageBits B = small_bits(S, counts, A.refs, A.refs_s, n, [](int32_t c) { return c == 0; });
+    const uint32_t have = S.prefix[1];
+    uint32_t wanted;
+    const uint32_t base = block_prefix<kSmallBlock / 64>(p.total - p.keep, S.scratch, wanted);
+    if (tid < A.rows) {
+        s_plan[tid] = p;
+        s_base[tid] = base;
+        A.lens_out[tid * A.lens_out_s] = (int32_t)p.len_new;
+        const bool partial = p.has && p.parent != tid && p.length != A.by_page.div(p.length) * A.page;
+        if (!partial) A.src[tid * A.src_s] = A.dst[tid * A.dst_s] = -1;
+    }
+    if (tid == 0) {
+        A.stats[0] = (int32_t)wanted;
+        A.stats[A.stats_s] = (int32_t)min(wanted, have);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = tid; i < A.rows * A.cols; i += kSmallBlock) {
+        const uint32_t r = A.by_cols.div(i), c = i - r * A.cols;
+        const RowPlan &P = s_plan[r];
+        assign_entry(A, B, S.prefix, P, r, c, s_base[r], have, [&](int32_t id, int32_t by) { atomicAdd(&counts[id], by); });
+    }
+    __syncthreads();
+    for (uint32_t id = tid; id < n; id += kSmallBlock) A.refs_out[id * A.refs_out_s] = counts[id];
+}
+
+__global__ __launch_bounds__(kSmallBlock) void k_compact_small(const CompactArgs A)
+{
+    __shared__ SmallBits S;
+    __shared__ int32_t counts[kSmallPages];
+    const uint32_t n = A.bits.n, tid = threadIdx.x;
+    const PageBits B = small_bits(S, counts, A.refs, A.refs_s, n, [](int32_t c) { return c > 0; });
+    const uint32_t live = S.prefix[1], kept = rank_bit(B, S.prefix, live), moves = live - kept;
+    if (tid == 0) {
+        A.stats[0] = (int32_t)live;
+        A.stats[A.stats_s] = (int32_t)moves;
+    }
+    for (uint32_t i = tid; i < max(n, A.capacity); i += kSmallBlock) {
+        if (i >= moves && i < A.capacity) {
+            A.src[i * A.src_s] = -1;
+            A.dst[i * A.dst_s] = -1;
+        }
+        if (i >= n) continue;
+        int32_t refs = i < live ? counts[i] : 0;
+        if (i < live && !(B.word[i / 64] >> (i % 64) & 1)) {   // a page comes here
+            const uint32_t move = i - rank_bit(B, S.prefix, i), from = select_bit<true>(B, S.prefix, kept + move);
+            A.src[move * A.src_s] = (int32_t)from;
+            A.dst[move * A.dst_s] = (int32_t)i;
+            refs = counts[from];
+        }
+        A.refs_out[i * A.refs_out_s] = refs;
+    }
+#pragma unroll 4
+    for (uint32_t i = tid; i < A.rows * A.cols; i += kSmallBlock) {
+        const uint32_t r = A.by_cols.div(i), c = i - r * A.cols;
+        const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
+        int32_t now = -1;
+        if (id >= 0 && (uint32_t)id < n && (B.word[id / 64] >> (id % 64) & 1))
+            now = (uint32_t)id < live ? id : (int32_t)select_bit<false>(B, S.prefix, rank_bit(B, S.prefix, id) - kept);
+        A.pages_out[(int64_t)r * A.pages_out_s[0] + (int64_t)c * A.pages_out_s[1]] = now;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -414,6 +544,8 @@ __global__ __launch_bounds__(kBlock) void k_copy(const CopyArgs A)
 
 int launch_assign(const AssignArgs &A, void *stream)
 {
+    if (A.small)
+        return launch_kernel(reinterpret_cast<const void *>(&k_assign_small), dim3(1), dim3(kSmallBlock), 0, stream, A);
     const uint32_t first = A.bits.tiles + A.row_groups;
     if (first) {
         const int rc = launch_kernel(reinterpret_cast<const void *>(&k_assign_count), dim3(first), dim3(kBlock), 0,
@@ -426,6 +558,8 @@ int launch_assign(const AssignArgs &A, void *stream)
 
 int launch_compact(const CompactArgs &A, void *stream)
 {
+    if (A.small)
+        return launch_kernel(reinterpret_cast<const void *>(&k_compact_small), dim3(1), dim3(kSmallBlock), 0, stream, A);
     int rc = 0;
     if (A.bits.tiles)
         rc = launch_kernel(reinterpret_cast<const void *>(&k_compact_mark), dim3(A.bits.tiles), dim3(kBlock), 0, stream,
