@@ -163,14 +163,13 @@ __device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scr
             most = max(most, x);
         }
         uint32_t inc = x;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
+        for (uint32_t o = 1; o < 64 && o < A.b; o *= 2) {
             const uint32_t y = __shfl_up(inc, o);
-            if (lane >= (uint32_t)o) inc += y;
+            if (lane >= o) inc += y;
         }
         uint32_t before = run;
         if (alone) {
-            run = __shfl(inc, 63);
+            run = __builtin_amdgcn_readlane(inc, A.b - 1);
         } else {
             if (lane == 63 && wave < kAttnWaves) scratch[wave] = inc;
             __syncthreads();
@@ -184,8 +183,7 @@ __device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scr
         if (r < A.b) R.prefix[r] = before + inc - x;
     }
     if (alone ? lane == 0 : threadIdx.x == 0) R.prefix[A.b] = run;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) most = max(most, (uint32_t)__shfl_xor((int)most, o));
+    for (uint32_t o = 1; o < 64 && o < A.b; o *= 2) most = max(most, (uint32_t)__shfl_xor((int)most, (int)o));
     if (alone) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -281,7 +279,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             uint64_t k[kAttnWaves][kTableKeys], v[kAttnWaves][kTableKeys];
             uint64_t valid[kAttnWaves][kTableKeys / 64];
         } table;
-        float join[kAttnWaves][8][kRow];
+        __attribute__((aligned(16))) float join[kAttnWaves][8][kRow];
     } sh;
     __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16], s_top[kAttnWaves][16], s_total[kAttnWaves][16];
     extern __shared__ uint32_t s_rows[];   // unless A.direct
@@ -575,31 +573,24 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                 A.lse[(int64_t)r * A.ls[0] + (int64_t)(q0 + hx) * A.ls[1]] = log_sum<TY>(top, total);
             }
         };
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
-        if (parts == 1) {
-            if (eh < q_n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < VW; ++c) {
-                        const uint32_t at = column(ej * 4 + i, c / PE) + c % PE;
-                        if (EDGE != kTiny || at < A.dv) put(eh, at, acc[c][i], l);
-                    }
-                if (ej == 0) put_statistics(eh, m, l);
-            }
-        } else {
-            // common maximum, then sums head by head through LDS, eight at a time
+        // Of `PARTS` waves with the same heads: common maximum, then sums through
+        // LDS, eight heads at a time and four columns to a work-item.
+        auto join_waves = [&](auto PARTS) {
+            constexpr uint32_t P = decltype(PARTS)::value, HW = kAttnWaves / P;
             if (ej == 0) {
                 s_m[wave][eh] = m;
                 s_l[wave][eh] = l;
             }
             __syncthreads();   // also: the tables are done with
-            float top = -INFINITY, total = 0.0f;
-            for (uint32_t w = sub; w < kAttnWaves; w += hw) top = fmaxf(top, s_m[w][eh]);
+            float top = -INFINITY, total = 0.0f, ms[P];
+#pragma unroll
+            for (uint32_t w = 0; w < P; ++w) {
+                ms[w] = s_m[sub + w * HW][eh];
+                top = fmaxf(top, ms[w]);
+            }
             const float ref = top == -INFINITY ? 0.0f : top;
-            for (uint32_t w = sub; w < kAttnWaves; w += hw)
-                total += s_l[w][eh] * __builtin_amdgcn_exp2f(s_m[w][eh] - ref);
+#pragma unroll
+            for (uint32_t w = 0; w < P; ++w) total += s_l[sub + w * HW][eh] * __builtin_amdgcn_exp2f(ms[w] - ref);
             if (ej == 0) {   // read after the next barrier
                 s_top[wave][eh] = top;
                 s_total[wave][eh] = total;
@@ -617,16 +608,37 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                             sh.join[wave][eh & 7][column(ej * 4 + i, c / PE) + c % PE] = acc[c][i] * factor;
                 }
                 __syncthreads();
-                // the `parts` waves of a head share its rows
-                for (uint32_t x = part * 64 + (tid & 63); x < 8 * 16 * VW; x += parts * 64) {
-                    const uint32_t g = x / (16 * VW), c = x % (16 * VW), hx = half * 8 + g;
-                    if (hx >= q_n || c >= A.dv) continue;
-                    float sum = 0.0f;
-                    for (uint32_t w = sub; w < kAttnWaves; w += hw) sum += sh.join[w][g][c];
-                    put(hx, c, sum, s_total[wave][hx]);
-                    if (c == 0) put_statistics(hx, s_top[wave][hx], s_total[wave][hx]);
+                const uint32_t heads_here = min(8u, q_n > half * 8u ? q_n - half * 8u : 0u);
+                for (uint32_t x = part * 64 + (tid & 63); x < heads_here * 4 * VW; x += P * 64) {
+                    const uint32_t g = x / (4 * VW), c = x % (4 * VW) * 4, hx = half * 8 + g;
+                    f32x4 sum = *(const f32x4 *)&sh.join[sub][g][c];
+#pragma unroll
+                    for (uint32_t w = 1; w < P; ++w) sum += *(const f32x4 *)&sh.join[sub + w * HW][g][c];
+                    const float all = s_total[wave][hx];
+#pragma unroll
+                    for (uint32_t k = 0; k < 4; ++k)
+                        if (c + k < A.dv) put(hx, c + k, sum[k], all);
+                    if (c == 0) put_statistics(hx, s_top[wave][hx], all);
                 }
             }
+        };
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (parts == 1) {
+            if (eh < q_n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < VW; ++c) {
+                        const uint32_t at = column(ej * 4 + i, c / PE) + c % PE;
+                        if (EDGE != kTiny || at < A.dv) put(eh, at, acc[c][i], l);
+                    }
+                if (ej == 0) put_statistics(eh, m, l);
+            }
+        } else if (parts == 4) {
+            join_waves(std::integral_constant<uint32_t, 4>());
+        } else {
+            join_waves(std::integral_constant<uint32_t, 2>());
         }
         if (A.direct) return;
         step += steps;
@@ -669,6 +681,17 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArg
     }
     if (S.count == 1) return;   // written by its work-group
     const uint64_t at = (uint64_t)(S.first + r) * A.hq + h;   // segment s: at + s * hq
+    float v[4][4];   // columns lane, lane + 64, ... of four segments
+    auto load = [&](uint32_t s) {
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+            const float *p = A.acc + (at + (uint64_t)min(s + u, S.count - 1) * A.hq) * A.dv;
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c)
+                if (c == 0 || c * 64 < A.dv) v[u][c] = p[min(c * 64 + lane, A.dv - 1)];
+        }
+    };
+    load(0);   // on their way while the weights are made
     float m = -INFINITY;
     for (uint32_t s = lane; s < S.count; s += 64) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
 #pragma unroll
@@ -685,19 +708,14 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArg
         }
         const uint32_t n = min(64u, S.count - s0);
         for (uint32_t k = 0; k < n; k += 4) {
-            float v[4][4];
-#pragma unroll
-            for (uint32_t u = 0; u < 4; ++u) {
-                const float *p = A.acc + (at + (uint64_t)(s0 + min(k + u, n - 1)) * A.hq) * A.dv;
-#pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) v[u][c] = p[min(c * 64 + lane, A.dv - 1)];
-            }
+            if (s0 + k) load(s0 + k);
 #pragma unroll
             for (uint32_t u = 0; u < 4; ++u)
                 if (k + u < n) {
                     const float wu = __shfl(w, (int)(k + u));
 #pragma unroll
-                    for (uint32_t c = 0; c < 4; ++c) sum[c] += v[u][c] * wu;
+                    for (uint32_t c = 0; c < 4; ++c)
+                        if (c == 0 || c * 64 < A.dv) sum[c] += v[u][c] * wu;
                 }
         }
     }
