@@ -290,16 +290,22 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
     // The run of this work-group: steps [step, stop) of all rows', from row r on.
     uint32_t head_shift = 0, group, r, step = 0, stop = 0, bh;
     Rows R{};
+    // Work-groups go to the eight dies in turn: the heads of a run follow each other
+    // on one, a slot's heads together use all of its cache's channels.
+    auto place = [&](const Div31 &by) {   // by: eight runs' work-groups
+        const uint32_t u = by.div(blockIdx.x), x = blockIdx.x - u * by.d;
+        group = u * 8 + x % 8;
+        bh = x / 8;
+    };
     if (A.direct) {
-        group = r = A.by_heads.div(blockIdx.x);
-        bh = blockIdx.x - group * A.by_heads.d;
+        place(A.by_heads);
+        if (group >= A.b) return;
+        r = group;
     } else {
         R = make_rows(A, s_rows, s_scratch);
         const Deal D = deal_steps(A, R);
         head_shift = D.head_shift;
-        const Div31 by = head_shift ? A.by_heads_much : A.by_heads;
-        group = by.div(blockIdx.x);
-        bh = blockIdx.x - group * by.d;
+        place(head_shift ? A.by_heads_much : A.by_heads);
         if (D.share == 0) {
             if (group >= A.b) return;
             r = group;

@@ -505,7 +505,7 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.window = (uint32_t)window;
     A.by_page = Div31(A.page);
     const uint64_t heads = (uint64_t)A.hk * A.head_tiles;
-    if ((uint64_t)b * heads > (uint64_t)kMaxCount || (uint64_t)b * hq > (uint64_t)kMaxCount)
+    if ((uint64_t)(b + 8) * heads > (uint64_t)kMaxCount / 8 || (uint64_t)b * hq > (uint64_t)kMaxCount)
         return refuse(CMD_E_LIMIT, "too many sequences times heads");
     uint64_t keys = (uint64_t)A.cols * A.page;
     if (window) keys = std::min<uint64_t>(keys, (uint64_t)window);
@@ -523,12 +523,13 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.runs = runs(768, heads);
     A.runs_much = runs(768, much);
     A.runs_most = std::max(A.runs, A.runs_much);
-    A.by_heads = Div31((uint32_t)heads);
-    A.by_heads_much = Div31((uint32_t)much);
+    A.by_heads = Div31((uint32_t)(8 * heads));
+    A.by_heads_much = Div31((uint32_t)(8 * much));
     A.by_tiles = Div31(A.head_tiles);
     A.by_runs = Div31(A.runs);
     A.by_runs_much = Div31(A.runs_much);
-    A.grid = (uint32_t)(A.direct ? b * heads : std::max(A.runs * heads, A.runs_much * much));
+    auto eight = [](uint64_t n) { return (n + 7) / 8 * 8; };
+    A.grid = (uint32_t)(A.direct ? eight(b) * heads : std::max(eight(A.runs) * heads, eight(A.runs_much) * much));
     // Reads that nothing can find in a 256 MiB cache again pass it by.
     A.stream = (t[1].span() + t[2].span()) > (int64_t(1) << 28);
     A.join_many = std::min<uint64_t>(A.runs_most, steps) > 16 && (uint64_t)b * hq * ((dv + 31) / 32) <= 512;

@@ -91,7 +91,7 @@ struct AttnArgs {
     uint32_t stream, join_many;            // larger than the last-level cache; rows may have many segments
     float scale_log2;                      // scale * log2(e)
     Div31 by_page;
-    Div31 by_heads, by_heads_much;         // work-groups of one run: heads, heads / head_waves
+    Div31 by_heads, by_heads_much;         // work-groups of eight runs: 8 heads; 8 heads >> head_shift
     Div31 by_tiles;                        // head_tiles
     Div31 by_runs, by_runs_much;
 };
