@@ -207,6 +207,9 @@ __device__ inline Deal deal_steps(const AttnArgs &A, const Rows &R)
 {
     Deal D;
     const uint32_t heads = A.hk * A.head_tiles;
+    // Rows of nearly one length (none a quarter above the mean), enough of them to
+    // use the whole memory: cutting them would only add segments.
+    if (A.b <= A.runs_whole && (uint64_t)R.all * 5 >= (uint64_t)R.longest * A.b * 4) return Deal{0, 0};
     const bool much = (uint64_t)R.all * heads >= kAttnMuch;
     D.head_shift = much ? A.head_shift : 0;
     const uint32_t runs = much ? A.runs_much : A.runs;

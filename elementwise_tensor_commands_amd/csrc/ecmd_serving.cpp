@@ -510,9 +510,14 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     uint64_t keys = (uint64_t)A.cols * A.page;
     if (window) keys = std::min<uint64_t>(keys, (uint64_t)window);
     const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep, most = std::max<uint64_t>(1, steps * (uint64_t)b);
-    // One work-group to a row and head, without a join, where cutting rows would
-    // gain less than the second launch costs.
-    A.direct = steps <= 6 || (steps <= 8 && (uint64_t)b * heads >= 512) || b > kAttnMaxRows || most > (uint64_t(1) << 30);
+    // One work-group to a row and head, without a join, where the longest row that
+    // the table can hold takes one no longer than cutting it does with the second
+    // launch: 600 positions of 512 bytes 10.2 us against 11.0, 777 12.8 against
+    // 12.0, binary32's 300 of 1024 bytes 12.7 against 13.2; with many rows twice that.
+    const uint64_t row_bytes = keys * (uint64_t)((d + dv) * esize);
+    A.direct = (steps <= 6 && row_bytes <= (256 << 10)) ||
+               (steps <= 8 && row_bytes <= (512 << 10) && (uint64_t)b * heads >= 512) || b > kAttnMaxRows ||
+               most > (uint64_t(1) << 30);
     // Runs for three work-groups on each of 256 compute units (what registers
     // allow at the common widths), but no more than there can be steps.
     A.head_shift = heads % 4 == 0 ? 2 : heads % 2 == 0 ? 1 : 0;
@@ -528,8 +533,11 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.by_tiles = Div31(A.head_tiles);
     A.by_runs = Div31(A.runs);
     A.by_runs_much = Div31(A.runs_much);
+    // With 128 work-groups or more (a compute unit alone reads 55 to 70 GB/s of 6
+    // TB/s) rows may be taken whole; many more than needed would only start and end.
+    A.runs_whole = (uint64_t)b * heads >= 128 && (uint64_t)b * heads <= 2048 ? (uint32_t)b : 0;
     auto eight = [](uint64_t n) { return (n + 7) / 8 * 8; };
-    A.grid = (uint32_t)(A.direct ? eight(b) * heads : std::max(eight(A.runs) * heads, eight(A.runs_much) * much));
+    A.grid = (uint32_t)(A.direct ? eight(b) * heads : std::max(eight(std::max(A.runs, A.runs_whole)) * heads, eight(A.runs_much) * much));
     // Reads that nothing can find in a 256 MiB cache again pass it by.
     A.stream = (t[1].span() + t[2].span()) > (int64_t(1) << 28);
     A.join_many = std::min<uint64_t>(A.runs_most, steps) > 16 && (uint64_t)b * hq * ((dv + 31) / 32) <= 512;

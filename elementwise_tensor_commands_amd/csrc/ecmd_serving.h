@@ -87,6 +87,7 @@ struct AttnArgs {
     uint32_t direct;                       // 1: a work-group to a row and head, no join
     uint32_t head_shift;                   // with much to read, 2^this waves of a work-group take a head each
     uint32_t runs, runs_much, runs_most;   // runs of positions for each head; the larger one
+    uint32_t runs_whole;                   // rows up to which they may all be runs (0: too few work-groups)
     uint32_t grid;
     uint32_t stream, join_many;            // larger than the last-level cache; rows may have many segments
     float scale_log2;                      // scale * log2(e)
