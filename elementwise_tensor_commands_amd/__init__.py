@@ -69,6 +69,12 @@ def _load_library():
         raise ImportError(
             "libecmd.so is not built (%s); build it with "
             "`python elementwise_tensor_commands_amd/build.py`" % LIB_PATH)
+    # torch first: it brings a HIP runtime of its own, and a library loaded
+    # before it would bind to another one, which then sees no device.
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     L = ctypes.CDLL(LIB_PATH)
     vp, i32p = ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)
     sig = {

@@ -1,0 +1,84 @@
+"""The decoder of decode.py (every serving operator and a Command, together)
+against a dense recomputation of each sequence in 64 bits without a cache."""
+import math
+
+import pytest
+import torch
+
+from elementwise_tensor_commands_amd.decode import Decoder
+import serving_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+
+def dense_logits(m, tokens):
+    """Logits of every position of one sequence, from the definition."""
+    x = m.embedding.cpu().double()[torch.tensor(tokens)]
+    n, hq, hk, d = len(tokens), m.hq, m.hk, m.d
+    pos = torch.arange(n)
+    mask = torch.triu(torch.full((n, n), -math.inf, dtype=torch.float64), 1)
+    for qkv, o in zip(m.qkv, m.o):
+        h = (x @ qkv.cpu().double()).view(n, hq + 2 * hk, d)
+        q, _ = O.rope(h[:, :hq].float(), pos, m.freq.cpu(), "half")
+        k, _ = O.rope(h[:, hq:hq + hk].float(), pos, m.freq.cpu(), "half")
+        v = h[:, hq + hk:]
+        out = []
+        for a in range(hq):
+            g = a // (hq // hk)
+            out.append(torch.softmax(q[:, a] @ k[:, g].t() / math.sqrt(d) + mask, -1) @ v[:, g])
+        x = x + torch.stack(out, 1).reshape(n, hq * d) @ o.cpu().double()
+    return x @ m.embedding.cpu().double().t()
+
+
+def test_decode_with_forks_ends_and_compaction():
+    m = Decoder(layers=2, vocab=211, hq=4, hk=2, d=32, rows=6, n=40, page=4, cols=12, dtype=torch.float32)
+    width = 128
+    g = torch.Generator().manual_seed(3)
+    pick = lambda k: torch.randint(0, m.vocab, (k,), generator=g).tolist()
+    seqs = [pick(9), pick(1), [], pick(14), pick(5), []]
+    got = m.prefill(seqs[:5]).cpu().double()
+
+    # Every sum has at most `terms` products of binary32 numbers, whose sizes the
+    # layers at most square-root-of-terms-fold: an error of terms half steps a sum,
+    # carried through two layers' sums and the last product.
+    def close(got, want):
+        terms = width + 32 + 64
+        bound = 5 * terms * 2.0 ** -24 * float(want.abs().max())
+        assert float((got - want).abs().max()) <= bound
+
+    for at, r in enumerate((0, 1, 3, 4)):                          # row 2 has no token yet
+        close(got[at], dense_logits(m, seqs[r])[-1])
+    plans = [[0, 1, 2, 3, 0, 3], [0, 0, 2, 4, 4, 5], [1, 0, -1, 3, 4, 5], [0, 1, 2, 3, 4, 5], [5, 5, -1, 3, 3, 0]]
+    for i, plan in enumerate(plans):
+        new = pick(6)
+        alive = torch.tensor([p >= 0 for p in plan], dtype=torch.int32).cuda()
+        out = m.decode(torch.tensor(new).cuda(), torch.tensor(plan, dtype=torch.int32).cuda(), alive).cpu().double()
+        seqs = [seqs[p] + [new[r]] if p >= 0 else [] for r, p in enumerate(plan)]
+        assert m.cache.lens.tolist() == [len(s) for s in seqs]
+        for r in range(6):
+            if seqs[r]:
+                close(out[r], dense_logits(m, seqs[r])[-1])
+        want, given = m.cache.stats.tolist()
+        assert want == given
+        # the counts are those of the table
+        refs = [0] * 40
+        for row in m.cache.pages.tolist():
+            for p in row:
+                if p >= 0:
+                    refs[p] += 1
+        assert m.cache.refs.tolist() == refs
+        if i == 2:
+            m.cache.compact()
+            live, moved = m.cache.stats.tolist()
+            assert live == sum(x > 0 for x in refs) and max(max(r) for r in m.cache.pages.tolist()) == live - 1
+
+
+def test_the_command_runs_and_finds_the_gpu():
+    """In a process where the package is imported before torch."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "elementwise_tensor_commands_amd.decode", "--steps", "4", "--beams", "2"],
+                       cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stdout + r.stderr
