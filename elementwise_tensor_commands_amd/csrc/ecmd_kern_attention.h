@@ -45,6 +45,7 @@
 
 #include "ecmd_launch.h"
 #include "ecmd_serving.h"
+#include "ecmd_wave.h"
 
 namespace ecmd {
 
@@ -162,14 +163,10 @@ __device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scr
             x = (s.hi - s.lo + kAttnStep - 1) / kAttnStep;
             most = max(most, x);
         }
-        uint32_t inc = x;
-        for (uint32_t o = 1; o < 64 && o < A.b; o *= 2) {
-            const uint32_t y = __shfl_up(inc, o);
-            if (lane >= o) inc += y;
-        }
+        const uint32_t inc = wave_prefix(x);
         uint32_t before = run;
         if (alone) {
-            run = __builtin_amdgcn_readlane(inc, A.b - 1);
+            run = last_lane(inc);
         } else {
             if (lane == 63 && wave < kAttnWaves) scratch[wave] = inc;
             __syncthreads();
@@ -183,7 +180,7 @@ __device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scr
         if (r < A.b) R.prefix[r] = before + inc - x;
     }
     if (alone ? lane == 0 : threadIdx.x == 0) R.prefix[A.b] = run;
-    for (uint32_t o = 1; o < 64 && o < A.b; o *= 2) most = max(most, (uint32_t)__shfl_xor((int)most, (int)o));
+    most = wave_max(most);
     if (alone) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -703,8 +700,7 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArg
     load(0);   // on their way while the weights are made
     float m = -INFINITY;
     for (uint32_t s = lane; s < S.count; s += 64) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
+    m = wave_max(m);
     const float ref = m == -INFINITY ? 0.0f : m;
     float total = 0.0f, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (uint32_t s0 = 0; s0 < S.count; s0 += 64) {
@@ -721,15 +717,14 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArg
 #pragma unroll
             for (uint32_t u = 0; u < 4; ++u)
                 if (k + u < n) {
-                    const float wu = __shfl(w, (int)(k + u));
+                    const float wu = as_f(__builtin_amdgcn_readlane(__builtin_bit_cast(uint32_t, w), k + u));
 #pragma unroll
                     for (uint32_t c = 0; c < 4; ++c)
                         if (c == 0 || c * 64 < A.dv) sum[c] += v[u][c] * wu;
                 }
         }
     }
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) total += __shfl_xor(total, o);
+    total = wave_sum(total);
 #pragma unroll
     for (uint32_t c = 0; c < 4; ++c)
         if (c * 64 + lane < A.dv) store_out<TY>(A, r, h, c * 64 + lane, total == 0.0f ? 0.0f : sum[c] / total);
@@ -765,8 +760,7 @@ __global__ __launch_bounds__(THREADS) void k_attention_join(const AttnArgs A)
 
     float m = -INFINITY;
     for (uint32_t s = threadIdx.x; s < parts; s += THREADS) m = fmaxf(m, A.ml[2 * (at + (uint64_t)s * A.hq)]);
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
+    m = wave_max(m);
     if (lane == 0) s_red[0][wave] = m;
     __syncthreads();
 #pragma unroll
@@ -779,8 +773,7 @@ __global__ __launch_bounds__(THREADS) void k_attention_join(const AttnArgs A)
         s_w[s] = w;
         l += w * A.ml[x + 1];
     }
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) l += __shfl_xor(l, o);
+    l = wave_sum(l);
     if (lane == 0) s_red[1][wave] = l;
     __syncthreads();
     float total = 0.0f;

@@ -16,6 +16,7 @@
 
 #include "ecmd_launch.h"
 #include "ecmd_serving.h"
+#include "ecmd_wave.h"
 
 namespace ecmd {
 
@@ -31,12 +32,7 @@ template <uint32_t NW = kWaves>
 __device__ inline uint32_t block_prefix(uint32_t x, uint32_t *scratch, uint32_t &total)
 {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t inc = x;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const uint32_t y = __shfl_up(inc, o);
-        if (lane >= (uint32_t)o) inc += y;
-    }
+    const uint32_t inc = wave_prefix(x);
     if (lane == 63) scratch[wave] = inc;
     __syncthreads();
     uint32_t before = 0;
@@ -225,11 +221,8 @@ __device__ inline void assign_entry(const AssignArgs &A, const PageBits &B, cons
 // Sums over the work-group; scratch: 2 kWaves entries.
 __device__ inline void block_sums(uint32_t &x, uint32_t &y, uint32_t *scratch)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        x += __shfl_xor((int)x, o);
-        y += __shfl_xor((int)y, o);
-    }
+    x = wave_sum(x);
+    y = wave_sum(y);
     if ((threadIdx.x & 63) == 0) {
         scratch[threadIdx.x >> 6] = x;
         scratch[kWaves + (threadIdx.x >> 6)] = y;
