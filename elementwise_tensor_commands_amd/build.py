@@ -34,8 +34,9 @@ LIB = os.path.join(PKG, "libecmd.so")
 BINDING = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["ecmd_host.cpp", "ecmd_serial.cpp", "ecmd_jit.cpp", "kernels_linear.hip", "kernels_interp.hip",
-           "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip", "ecmd_serving.cpp", "kernels_rope.hip",
-           "kernels_attention_f16.hip", "kernels_attention_bf16.hip", "kernels_attention_f32.hip", "kernels_pages.hip"]
+           "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip", "serving/ecmd_serving.cpp",
+           "serving/kernels_rope.hip", "serving/kernels_attention_f16.hip", "serving/kernels_attention_bf16.hip",
+           "serving/kernels_attention_f32.hip", "serving/kernels_pages.hip"]
 # Device headers the run-time compiler needs: embedded into the library as text.
 JIT_HEADERS = ["ecmd_tape.h", "ecmd_eval.h", "ecmd_kern_linear.h", "ecmd_kern_rows.h", "ecmd_kern_tiled.h",
                "ecmd_kern_gather.h"]
@@ -51,7 +52,7 @@ FLAGS = [
 # Further flags of single sources.  Attention: matrix results in the general
 # registers; with the accumulation registers, which the compiler otherwise gives
 # half of the file, the loop moved 32 values there and back in every turn.
-FILE_FLAGS = {"kernels_attention_%s.hip" % t: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for t in ("f16", "bf16", "f32")}
+FILE_FLAGS = {"serving/kernels_attention_%s.hip" % t: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for t in ("f16", "bf16", "f32")}
 
 # Options for run-time compilation: the device side of FLAGS.
 JIT_OPTIONS = ["--offload-arch=" + ARCH, "-O3", "-std=c++20", "-ffp-contract=off", "-fno-fast-math",
@@ -142,7 +143,7 @@ def build(asm: bool = True, verbose: bool = False) -> str:
         cmds.append([HIPCC, *FLAGS, *extra, *lang, "-c", path, "-o", obj])
         if asm and src.endswith(".hip"):
             cmds.append([HIPCC, *FLAGS, *extra, "-x", "hip", "--offload-device-only", "-S",
-                         os.path.join(CSRC, src), "-o", os.path.join(BUILD, os.path.splitext(src)[0] + ".s")])
+                         os.path.join(CSRC, src), "-o", os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".s")])
     tmp_binding = BINDING + ".tmp%d" % os.getpid()
     cmds.append(binding_command(tmp_binding))
     if verbose:

@@ -43,7 +43,7 @@
 
 #include <type_traits>
 
-#include "ecmd_launch.h"
+#include "../ecmd_launch.h"
 #include "ecmd_serving.h"
 #include "ecmd_wave.h"
 

@@ -9,9 +9,9 @@
 #include <cstdio>
 #include <cstring>
 
-#include "../../include/ecmd_serving.h"
-#include "ecmd_command.h"
-#include "ecmd_launch.h"
+#include "../../../include/ecmd_serving.h"
+#include "../ecmd_command.h"
+#include "../ecmd_launch.h"
 
 using namespace ecmd;
 

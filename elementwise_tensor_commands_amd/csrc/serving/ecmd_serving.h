@@ -17,6 +17,7 @@ struct Div31 {
     Div31() = default;
     explicit Div31(uint32_t div) : d(div)
     {
+        if (div == 0) return;   // the size of something empty: nothing asks for a quotient
         while ((uint64_t(1) << shift) < div) ++shift;
         mul = (uint32_t)((((uint64_t(1) << shift) - div) << 32) / div + 1);
     }

@@ -14,7 +14,7 @@
 // their order.
 #include <hip/hip_runtime.h>
 
-#include "ecmd_launch.h"
+#include "../ecmd_launch.h"
 #include "ecmd_serving.h"
 #include "ecmd_wave.h"
 

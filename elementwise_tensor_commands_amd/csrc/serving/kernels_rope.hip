@@ -9,7 +9,7 @@
 // streams the heads past them in 16-byte vectors.
 #include <hip/hip_runtime.h>
 
-#include "ecmd_launch.h"
+#include "../ecmd_launch.h"
 #include "ecmd_serving.h"
 
 namespace ecmd {

@@ -104,6 +104,12 @@ def _layout(layout) -> int:
     return ROPE_LAYOUTS.get(layout, -1)
 
 
+def _int32(x) -> int:
+    """x for a C int32 argument; what does not fit becomes the nearest number that
+    does, which the library refuses or which means the same."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 def rope(x, pos, freq, out, *, layout="half", mscale=1.0, inverse=False, stream=None):
     """Rotary positions (cmd_rope): x [b, t, h, d] turned by pos [b, t] (int32)
     into out, pair i by pos * freq[i] (freq: float64, on the GPU).  out may be
@@ -141,6 +147,7 @@ def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=No
     args, dev, current = _pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(max(1, q.shape[-1])) if q.dim() else 1.0
+    window = _int32(window)
     if dev < 0:
         _refuse(lib.cmd_paged_attention(args, scale, window, None, 0, CHECK_ONLY, None))
     ptr, size, _owner = _scratch(workspace, lib.cmd_paged_attention_workspace(args, window), stream, dev)
@@ -150,7 +157,8 @@ def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=No
 
 def paged_attention_workspace(q, k_cache, v_cache, pages, lens, out, *, window=0) -> int:
     """Bytes of workspace that paged_attention needs for these tensors."""
-    n = lib.cmd_paged_attention_workspace(_pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, None)[0], window)
+    n = lib.cmd_paged_attention_workspace(_pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, None)[0],
+                                          _int32(window))
     _check(n)
     return n
 
@@ -165,6 +173,7 @@ def page_assign(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_
     and grows by add[r] positions.  Fills pages_out, lens_out, refs_out, the
     page copies src -> dst that forks need (-1: none) and stats = (pages wanted,
     pages given).  refs_out may be refs."""
+    page = _int32(page)
     args, dev, current = _pack(_ASSIGN, pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats)
     if dev < 0:
         _refuse(lib.cmd_page_assign(args, page, None, 0, CHECK_ONLY, None))
@@ -175,7 +184,7 @@ def page_assign(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_
 def page_assign_workspace(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_out, src, dst, stats) -> int:
     """Bytes of workspace that page_assign needs for these tensors."""
     args = _pack(_ASSIGN, pages, lens, refs, parent, add, pages_out, lens_out, refs_out, src, dst, stats)[0]
-    n = lib.cmd_page_assign_workspace(args, page)
+    n = lib.cmd_page_assign_workspace(args, _int32(page))
     _check(n)
     return n
 

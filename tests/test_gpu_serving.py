@@ -157,6 +157,19 @@ def test_append(dtype, layout):
         assert bool((qkv_g[:, :hq] == out).all()), case              # q in place
 
 
+@pytest.mark.parametrize("hq,hk,d,dv", [(0, 2, 8, 8), (2, 1, 8, 0), (0, 0, 8, 8), (3, 0, 8, 8), (2, 1, 0, 8)])
+def test_append_of_nothing(hq, hk, d, dv):
+    """No query heads, no kv heads, or heads without elements: the rest is done."""
+    z = lambda *s: torch.ones(*s, device="cuda")
+    kc, vc, out = z(4, 2, hk, d) * 0, z(4, 2, hk, dv) * 0, z(3, hq, d) * 0
+    m = torch.zeros(0, dtype=torch.float64, device="cuda")
+    E.rope_append(z(3, hq, d), z(3, hk, d), z(3, hk, dv), ints([0, 1, 3]).cuda(), ints([0, 0, -1]).cuda(),
+                  ints([[2, 1]]).cuda(), m, out, kc, vc)
+    assert bool((out == 1).all())
+    for c in (kc, vc):
+        assert bool((c[2] == 1).all()) and not bool(c[[0, 1, 3]].any())
+
+
 # ---------------------------------------------------------------------------
 # Attention.
 

@@ -151,6 +151,7 @@ def test_attention_refusals(name, kw):
 
 def test_attention_refusals_of_options():
     _refused("CMD_E_ARG", E.paged_attention, *attention_args(), window=-1)
+    _refused("CMD_E_ARG", E.paged_attention, *attention_args(), window=5 - (1 << 32))
     _refused("CMD_E_ARG", E.paged_attention, *attention_args(), scale=math.nan)
     _refused("CMD_E_SHAPE", E.paged_attention, *attention_args(), lse=torch.zeros(3, 5))
     _refused("CMD_E_DTYPE", E.paged_attention, *attention_args(), lse=torch.zeros(3, 4, dtype=torch.float64))
@@ -196,6 +197,8 @@ def assign_args(**kw):
     ("CMD_E_SHAPE", dict(stats=i32(3))),
     ("CMD_E_ARG", dict(page=0)),
     ("CMD_E_LIMIT", dict(page=1 << 30)),
+    ("CMD_E_LIMIT", dict(page=(1 << 32) + 16)),                      # not 16, as 32 bits would have it
+    ("CMD_E_ARG", dict(page=16 - (1 << 32))),
     ("CMD_E_STRIDE", dict(lens_out=i32(1).expand(3))),
 ])
 def test_assign_refusals(name, kw):
@@ -313,3 +316,31 @@ def test_frequencies():
     for bad in (dict(width=7), dict(width=8, factor=0.5), dict(width=8, scaling="x"), dict(width=8, factor=2.0, scaling="parts")):
         with pytest.raises(ValueError):
             E.rope_frequencies(**bad)
+
+
+# ---------------------------------------------------------------------------
+# The kernels' own assembly.
+
+@pytest.mark.parametrize("name", ["kernels_rope", "kernels_pages", "kernels_attention_f16", "kernels_attention_bf16",
+                                  "kernels_attention_f32"])
+def test_own_assembly(name):
+    """No scratch memory, no packed binary32 arithmetic; attention on matrix instructions."""
+    import importlib.util
+    import subprocess
+    spec = importlib.util.spec_from_file_location("ecmd_build", os.path.join(ROOT, "elementwise_tensor_commands_amd", "build.py"))
+    B = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(B)
+    src, path = "serving/%s.hip" % name, os.path.join(B.BUILD, name + ".s")
+    folder = os.path.join(B.CSRC, "serving")
+    newest = max(os.path.getmtime(os.path.join(folder, f)) for f in os.listdir(folder))
+    if not os.path.exists(path) or os.path.getmtime(path) < newest:
+        os.makedirs(B.BUILD, exist_ok=True)
+        subprocess.run([B.HIPCC, *B.FLAGS, *B.FILE_FLAGS.get(src, []), "-x", "hip", "--offload-device-only", "-S",
+                        os.path.join(B.CSRC, src), "-o", path], check=True, capture_output=True)
+    text = open(path).read()
+    sizes = re.findall(r"\.private_segment_fixed_size:\s+(\d+)", text)
+    assert sizes and all(s == "0" for s in sizes)
+    assert not re.search(r"v_pk_(add|mul|fma)_f32", text)
+    if "attention" in name:
+        kind = {"f16": "16x16x32_f16", "bf16": "16x16x32_bf16", "f32": "16x16x4_f32"}[name.rsplit("_", 1)[1]]
+        assert text.count("v_mfma_f32_" + kind) > 100
