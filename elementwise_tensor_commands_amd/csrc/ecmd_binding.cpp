@@ -2,6 +2,7 @@
 // torch tensors to cmd_arg structures (a Python extension module, _binding).
 //
 //   pack(ranks, *tensors) -> (cmd_args, device, stream)
+//   scratch(bytes, device) -> (pointer, owner)
 //
 // cmd_args holds one structure for each tensor, in order: the tensor of the
 // rank that its byte of `ranks` says; another rank is packed with sizes that the
@@ -9,9 +10,11 @@
 // if that is the current one, else -1; stream its current stream's handle (0
 // without one).  Reading four attributes of each tensor from Python takes
 // about 1 us a tensor, as long as the kernels of a small call; this takes 0.1.
+// scratch is an uninitialised tensor of that many bytes on that GPU and its address.
 #include <Python.h>
 
 #include <c10/hip/HIPFunctions.h>
+#include <ATen/ATen.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -90,7 +93,27 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n)
     }
 }
 
+PyObject *scratch(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    try {
+        if (n != 2) {
+            PyErr_SetString(PyExc_TypeError, "scratch(bytes, device)");
+            return nullptr;
+        }
+        const long long size = PyLong_AsLongLong(args[0]), device = PyLong_AsLongLong(args[1]);
+        if (PyErr_Occurred()) return nullptr;
+        at::Tensor t = at::empty({(int64_t)size},
+                                 at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)device));
+        const unsigned long long at = (unsigned long long)(uintptr_t)t.mutable_data_ptr();
+        return Py_BuildValue("(KN)", at, THPVariable_Wrap(std::move(t)));
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 PyMethodDef methods[] = {
+    {"scratch", (PyCFunction)(void (*)(void))scratch, METH_FASTCALL, "scratch(bytes, device) -> (pointer, owner)"},
     {"pack", (PyCFunction)(void (*)(void))pack, METH_FASTCALL, "pack(ranks, *tensors) -> (cmd_args, device, stream)"},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -38,6 +38,16 @@
 // The four waves of a work-group split its positions and join their sums through
 // LDS, or, where there is much to read and the heads allow it, take four kv heads
 // of the same positions: together they then read whole slots and exchange nothing.
+//
+// Measured on one MI355X (a stream of independent reads reaches 6.2 TB/s there, a
+// copy 4.9): 64 rows of up to 8192 positions, 8 kv heads of 128, bfloat16, 987 MB:
+// 166 us, 5.9 TB/s, the join 6.5 us; two rows of up to 262143, 289 MB: 50 and 5.7
+// us.  One row of 777: 7.2 and 4.6 us, all of it the chain of dependent loads
+// (length, page, key) and of barriers.  Tried and dropped: as many splits for every
+// row (205 us on the first; equal runs 199), half of the registers as accumulation
+// registers, which the compiler prefers (32 moves there and back in every tile),
+// eight waves to a work-group (a compute unit alone reads no more than 55 to 70
+// GB/s either way).
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -196,6 +206,10 @@ __device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scr
 }
 
 // How the steps are dealt out, the same in every work-group and in the join.
+// Waves by heads or by positions: 1138 MB in 64 ragged rows take 209 us by heads
+// and 228 by positions (streaming loads), 262 MB in 64 rows of 1000 (4096 steps of
+// 8 heads) 55 and 45.  Rows whole or cut: 16 rows of 2500, 16 heads, 33 us whole
+// and 43 cut; 64 ragged rows of up to 8192, 295 whole and 204 cut.
 struct Deal {
     uint32_t head_shift;   // 2^head_shift waves of a work-group take a head each
     uint32_t share;        // steps of a run; 0: a run is a row
@@ -231,7 +245,8 @@ __device__ inline void store_out(const AttnArgs &A, uint32_t r, uint32_t h, uint
 // Weights are held as 2^kBias exp2(score - m).  m is raised only where a score
 // passes it by more than kSlack (log2), which spares most tiles the exchange
 // between lanes and the rescale; a weight stays below 2^(kBias + kSlack).  The
-// bias keeps small binary16 weights out of its subnormals.
+// bias keeps small binary16 weights out of its subnormals (their sum, the score and
+// every statistic are binary32).
 constexpr float kSlack = 8.0f;
 template <int TY>
 constexpr float kBias = TY == S_F16 ? 6.0f : 0.0f;

@@ -6,7 +6,14 @@
 // (the inverse turns by -w).  Both kernels read and write each element once, so
 // HBM bounds them; the angles are shared by all heads of a token.  A work-group
 // takes a few tokens, computes their cosines and sines once into LDS, then
-// streams the heads past them in 16-byte vectors.
+// streams the heads past them in 16-byte vectors, four to a work-item at once.
+//
+// Measured on one MI355X: 4 x 4096 tokens of 40 heads of 128, bfloat16, 336 MB: 60
+// us, 5.6 TB/s (one vector at a time 71, four 66, past the caches 60).  The append
+// of 16 ragged prompts, 36 + 4 heads, binary16, 212 MB: 45 us, 4.7 TB/s, its writes
+// scattered over pages (65 with one vector at a time; 52 with four).  One token of
+// each of 64 sequences: 4.3 us, of which the angles' chain of binary64 operations
+// overlaps the loads.
 #include <hip/hip_runtime.h>
 
 #include "../ecmd_launch.h"

@@ -91,13 +91,13 @@ def _scratch(workspace, size: int, stream, device: int):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if size == 0:
         return None, 0, None
-    import torch
     if stream is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+        ptr, owner = _binding.scratch(size, device)
     else:
+        import torch
         with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
-            workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    return workspace.data_ptr(), size, workspace
+            ptr, owner = _binding.scratch(size, device)
+    return ptr, size, owner
 
 
 def _layout(layout) -> int:

@@ -347,7 +347,8 @@ int32_t cmd_arg_info(cmd_t h, int32_t index, int32_t *kind, int32_t *dtype, int3
 
 /* Message describing the last failure on this handle ("" if none).  Never
  * NULL; valid until the next call on the handle.  For a NULL handle it
- * describes the last failure of cmd_create or cmd_from_yaml on this thread. */
+ * describes the last failure of cmd_create, cmd_from_yaml or an operator of
+ * ecmd_serving.h on this thread. */
 const char *cmd_last_error(cmd_t h);
 
 /* Library version as 10000*major + 100*minor + patch. */
