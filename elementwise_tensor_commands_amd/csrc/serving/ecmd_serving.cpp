@@ -251,11 +251,13 @@ uint32_t head_items(int type, int layout, uint32_t pairs, uint32_t width)
 // 45 us; smaller ones leave their output where the next kernel finds it.
 constexpr uint64_t kPastCaches = 64 << 20;
 
-// No vector of a head is cut short.
-bool whole_items(int type, int layout, uint32_t pairs, uint32_t width)
+// The kernels' edge for heads of this kind: 0, no vector is cut short; 1, none is
+// longer than what it is cut from; 2.
+int head_edge(int type, int layout, uint32_t pairs, uint32_t width)
 {
-    const uint32_t e = type == S_F32 ? 4 : 8;
-    return (layout == CMD_ROPE_HALF ? pairs : 2 * pairs) % e == 0 && (width - 2 * pairs) % e == 0;
+    const uint32_t e = type == S_F32 ? 4 : 8, part = layout == CMD_ROPE_HALF ? pairs : 2 * pairs;
+    if (part % e == 0 && (width - 2 * pairs) % e == 0) return 0;
+    return (part == 0 || part >= e) && width >= e ? 1 : 2;
 }
 
 // Tokens of a work-group: about 1024 items (the four that each work-item loads at
@@ -322,7 +324,7 @@ int cmd_rope(const cmd_arg args[4], int32_t layout, double mscale, int32_t inver
     A.by_t = Div31((uint32_t)n);
     A.by_head_items = Div31((uint32_t)per_head);
     A.by_token_items = Div31(A.items);
-    return launched(launch_rope(type, layout, whole_items(type, layout, A.pairs, A.width),
+    return launched(launch_rope(type, layout, head_edge(type, layout, A.pairs, A.width),
                                 (uint64_t)A.tokens * 2 * (h * d) * type_size(dt) > kPastCaches, A,
                                 ceil_div(A.tokens, A.tb), turn_lds(A.tb, A.pairs), hip_stream),
                     "rope");
@@ -410,9 +412,9 @@ int cmd_rope_append(const cmd_arg args[10], int32_t layout, double mscale, int32
     A.by_v_head = div(per_v);
     A.by_parts = Div31(A.parts);
     const uint64_t grid = (uint64_t)ceil_div(A.tokens, A.tb) * A.parts;
-    const bool exact = whole_items(type, layout, A.pairs, A.d) && A.dv % e == 0;
+    const int edge = std::max(head_edge(type, layout, A.pairs, A.d), A.dv % e == 0 ? 0 : A.dv >= e ? 1 : 2);
     const bool past = (uint64_t)A.tokens * 2 * ((hq + hk) * d + hk * dv) * type_size(dt) > kPastCaches;
-    return launched(launch_append(type, layout, exact, past, A, (uint32_t)grid, turn_lds(A.tb, A.pairs) + A.tb * 16,
+    return launched(launch_append(type, layout, edge, past, A, (uint32_t)grid, turn_lds(A.tb, A.pairs) + A.tb * 16,
                                   hip_stream),
                     "rope_append");
 }

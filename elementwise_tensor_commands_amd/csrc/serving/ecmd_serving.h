@@ -66,9 +66,10 @@ struct AppendArgs {
     Div31 by_qk_head, by_v_head;           // items of a head
 };
 
-// exact: pairs, tails and value rows are whole 16-byte vectors; past: go past the caches
-int launch_rope(int type, int layout, bool exact, bool past, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream);
-int launch_append(int type, int layout, bool exact, bool past, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream);
+// edge: 0 pairs, tails and value rows are whole 16-byte vectors, 1 they are no shorter
+// than one, 2 some are; past: go past the caches
+int launch_rope(int type, int layout, int edge, bool past, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream);
+int launch_append(int type, int layout, int edge, bool past, const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream);
 
 // --- paged attention -------------------------------------------------------
 

@@ -108,6 +108,15 @@ __device__ inline void store_vec(T *p, Vec<T, E> v, int n)
     }
 }
 
+// Elements from `skip` on.
+template <class T, int E>
+__device__ inline void store_own(T *p, Vec<T, E> v, uint32_t skip)
+{
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+        if ((uint32_t)i >= skip) p[i] = v[i];
+}
+
 // One item: a 16-byte vector of pairs of one head (half layout: E pairs, from
 // both halves; interleaved: E / 2 pairs), or of the copied tail.  Items of a
 // head: rot_items(pairs) of pairs, then the tail's.
@@ -117,19 +126,38 @@ __host__ __device__ constexpr uint32_t rot_items(uint32_t pairs)
     return LAYOUT == 0 ? (pairs + E - 1) / E : (2 * pairs + E - 1) / E;
 }
 
-// EXACT: pairs and tail are whole vectors, so that loads need no branch (those
-// of a half layout's tail read one vector twice).
-template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+// How vectors that would reach past their part of a head (the pairs of a half, the
+// pairs, the tail) are read and written.
+enum RopeEdge {
+    kWhole,    // there are none: loads need no branch (those of a half layout's tail read one vector twice)
+    kMoved,    // moved back to end with the part: what an earlier item has is read and turned twice, and
+               // written twice, the same, unless it could be read in between (in place) or is no tail
+    kGuarded,  // element by element: parts shorter than a vector
+};
+
+template <int TY, int LAYOUT, RopeEdge EDGE, bool STREAM>
 struct Item {
     typedef typename Elem<TY>::T T;
     static constexpr int E = Elem<TY>::E;
     Vec<T, E> a, b;
 
+    // kMoved: where an item's vector starts (from the head, or from the half), and how
+    // many of its first elements are an earlier item's.
+    __device__ static uint32_t start(uint32_t item, uint32_t rot, uint32_t pairs, uint32_t width, uint32_t &skip)
+    {
+        const uint32_t from = item < rot ? item * E : 2 * pairs + (item - rot) * E;
+        const uint32_t at = min(from, (item >= rot ? width : LAYOUT == 0 ? pairs : 2 * pairs) - E);
+        skip = from - at;
+        return at;
+    }
+
     __device__ void load(const T *head, uint32_t item, uint32_t pairs, uint32_t width)
     {
         const uint32_t rot = rot_items<LAYOUT, E>(pairs);
-        if constexpr (EXACT) {
-            const uint32_t at = LAYOUT == 0 && item >= rot ? 2 * pairs + (item - rot) * E : item * E;
+        if constexpr (EDGE != kGuarded) {
+            uint32_t at, skip;
+            if constexpr (EDGE == kMoved) at = start(item, rot, pairs, width, skip);
+            else at = LAYOUT == 0 && item >= rot ? 2 * pairs + (item - rot) * E : item * E;
             a = load_vec<T, E, STREAM>(head + at, E);
             if constexpr (LAYOUT == 0) b = load_vec<T, E, STREAM>(head + (item < rot ? pairs + at : at), E);
             return;
@@ -149,15 +177,21 @@ struct Item {
 
     // cs and sn: the token's rows in LDS, 16-byte aligned, readable up to a
     // multiple of 8 entries.
-    __device__ void finish(T *head, uint32_t item, uint32_t pairs, uint32_t width, const float *cs, const float *sn)
+    __device__ void finish(T *head, uint32_t item, uint32_t pairs, uint32_t width, const float *cs, const float *sn,
+                           bool in_place)
     {
         const uint32_t rot = rot_items<LAYOUT, E>(pairs);
+        uint32_t skip = 0, at = item < rot ? item * E : 2 * pairs + (item - rot) * E;
+        if constexpr (EDGE == kMoved) at = start(item, rot, pairs, width, skip);
+        // elements there are (kGuarded)
+        const int n = EDGE != kGuarded ? E : (int)((item >= rot ? width : LAYOUT == 0 ? pairs : 2 * pairs) - at);
+        const bool part = EDGE == kMoved && skip && (in_place || at < 2 * pairs);
         if (item >= rot) {
-            const int at = 2 * pairs + (item - rot) * E;
-            store_vec<T, E, STREAM>(head + at, a, EXACT ? E : (int)width - at);
+            if (part) store_own<T, E>(head + at, a, skip);
+            else store_vec<T, E, STREAM>(head + at, a, n);
             return;
         }
-        const int at = item * E;
+        const bool own = EDGE == kMoved && skip && in_place;
         if (LAYOUT == 0) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
@@ -165,8 +199,13 @@ struct Item {
                 a[i] = (T)(u * c - v * s);
                 b[i] = (T)(v * c + u * s);
             }
-            store_vec<T, E, STREAM>(head + at, a, EXACT ? E : (int)pairs - at);
-            store_vec<T, E, STREAM>(head + pairs + at, b, EXACT ? E : (int)pairs - at);
+            if (own) {
+                store_own<T, E>(head + at, a, skip);
+                store_own<T, E>(head + pairs + at, b, skip);
+            } else {
+                store_vec<T, E, STREAM>(head + at, a, n);
+                store_vec<T, E, STREAM>(head + pairs + at, b, n);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < E; i += 2) {
@@ -175,7 +214,8 @@ struct Item {
                 a[i] = (T)(u * c - v * s);
                 a[i + 1] = (T)(v * c + u * s);
             }
-            store_vec<T, E, STREAM>(head + at, a, EXACT ? E : (int)(2 * pairs) - at);
+            if (own) store_own<T, E>(head + at, a, skip);
+            else store_vec<T, E, STREAM>(head + at, a, n);
         }
     }
 };
@@ -186,7 +226,7 @@ __host__ __device__ inline uint32_t lds_row(uint32_t pairs) { return (pairs + 7)
 extern __shared__ __attribute__((aligned(16))) float s_turn[];
 
 // A work-group: A.tb tokens, all their heads.
-template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+template <int TY, int LAYOUT, RopeEdge EDGE, bool STREAM>
 __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
 {
     typedef typename Elem<TY>::T T;
@@ -212,12 +252,12 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
     // Several items' loads are on their way before the first is stored, the first
     // ones' while the angles are computed.
     constexpr int U = 4;
-    Item<TY, LAYOUT, EXACT, STREAM> it[U];
+    Item<TY, LAYOUT, EDGE, STREAM> it[U];
     auto load = [&](uint32_t i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (EXACT || i0 + u * kBlock < total) {   // EXACT: the last item again instead of a branch
-                const Place p = split(EXACT ? min(i0 + u * kBlock, total - 1) : i0 + u * kBlock);
+            if (EDGE != kGuarded || i0 + u * kBlock < total) {   // the last item again instead of a branch
+                const Place p = split(EDGE != kGuarded ? min(i0 + u * kBlock, total - 1) : i0 + u * kBlock);
                 it[u].load((const T *)A.x + offset(p, A.xs), p.item, A.pairs, A.width);
             }
     };
@@ -238,7 +278,8 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
         for (int u = 0; u < U; ++u)
             if (i + u * kBlock < total) {
                 const Place p = split(i + u * kBlock);
-                it[u].finish((T *)A.out + offset(p, A.os), p.item, A.pairs, A.width, cs + p.tok * row, sn + p.tok * row);
+                it[u].finish((T *)A.out + offset(p, A.os), p.item, A.pairs, A.width, cs + p.tok * row, sn + p.tok * row,
+                             A.x == A.out);
             }
         i += U * kBlock;
         load(i);
@@ -248,7 +289,7 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
 // A work-group: A.tb tokens, or (A.parts > 1) a part of one token's items.  The
 // items are q's, k's, then v's (copied: a head without pairs), each kind's number
 // rounded up to whole waves: a wave's pointers and strides are then scalars.
-template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+template <int TY, int LAYOUT, RopeEdge EDGE, bool STREAM>
 __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
 {
     typedef typename Elem<TY>::T T;
@@ -282,7 +323,7 @@ __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
         return p;
     };
     constexpr int U = 4;   // as above
-    Item<TY, LAYOUT, EXACT, STREAM> it[U];
+    Item<TY, LAYOUT, EDGE, STREAM> it[U];
     auto load = [&](uint32_t i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -331,7 +372,7 @@ __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
                 const int64_t at = p.kind ? slot[2 * p.tok + p.kind - 1] : (int64_t)(first + p.tok) * A.qos[0];
                 if (p.real && at >= 0)
                     it[u].finish(to + at + p.head * hs, p.item, p.kind == 2 ? 0 : A.pairs, p.kind == 2 ? A.dv : A.d,
-                                 cs + p.tok * row, sn + p.tok * row);
+                                 cs + p.tok * row, sn + p.tok * row, p.kind == 0 && A.q == A.q_out);
             }
         i += U * step;
         load(i);
@@ -340,51 +381,55 @@ __global__ __launch_bounds__(kBlock) void k_append(const AppendArgs A)
 
 }  // namespace
 
-template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+template <int TY, int LAYOUT, RopeEdge EDGE, bool STREAM>
 static int launch_one(const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-    return launch_kernel(reinterpret_cast<const void *>(&k_rope<TY, LAYOUT, EXACT, STREAM>), dim3(grid), dim3(kBlock),
+    return launch_kernel(reinterpret_cast<const void *>(&k_rope<TY, LAYOUT, EDGE, STREAM>), dim3(grid), dim3(kBlock),
                          lds, stream, A);
 }
-template <int TY, int LAYOUT, bool EXACT, bool STREAM>
+template <int TY, int LAYOUT, RopeEdge EDGE, bool STREAM>
 static int launch_one(const AppendArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-    return launch_kernel(reinterpret_cast<const void *>(&k_append<TY, LAYOUT, EXACT, STREAM>), dim3(grid), dim3(kBlock),
+    return launch_kernel(reinterpret_cast<const void *>(&k_append<TY, LAYOUT, EDGE, STREAM>), dim3(grid), dim3(kBlock),
                          lds, stream, A);
 }
 template <int TY, int LAYOUT, class Args>
-static int launch_layout(bool exact, bool past, const Args &A, uint32_t grid, uint32_t lds, void *stream)
+static int launch_layout(int edge, bool past, const Args &A, uint32_t grid, uint32_t lds, void *stream)
 {
-    if (exact)
-        return past ? launch_one<TY, LAYOUT, true, true>(A, grid, lds, stream)
-                    : launch_one<TY, LAYOUT, true, false>(A, grid, lds, stream);
-    return past ? launch_one<TY, LAYOUT, false, true>(A, grid, lds, stream)
-                : launch_one<TY, LAYOUT, false, false>(A, grid, lds, stream);
+    switch (edge) {
+    case kWhole:
+        return past ? launch_one<TY, LAYOUT, kWhole, true>(A, grid, lds, stream)
+                    : launch_one<TY, LAYOUT, kWhole, false>(A, grid, lds, stream);
+    case kMoved:
+        return past ? launch_one<TY, LAYOUT, kMoved, true>(A, grid, lds, stream)
+                    : launch_one<TY, LAYOUT, kMoved, false>(A, grid, lds, stream);
+    default: return launch_one<TY, LAYOUT, kGuarded, false>(A, grid, lds, stream);
+    }
 }
 template <class Args>
-static int launch_any(int type, int layout, bool exact, bool past, const Args &A, uint32_t grid, uint32_t lds,
+static int launch_any(int type, int layout, int edge, bool past, const Args &A, uint32_t grid, uint32_t lds,
                       void *stream)
 {
     switch (2 * type + layout) {
-    case 2 * S_F16: return launch_layout<S_F16, 0>(exact, past, A, grid, lds, stream);
-    case 2 * S_F16 + 1: return launch_layout<S_F16, 1>(exact, past, A, grid, lds, stream);
-    case 2 * S_BF16: return launch_layout<S_BF16, 0>(exact, past, A, grid, lds, stream);
-    case 2 * S_BF16 + 1: return launch_layout<S_BF16, 1>(exact, past, A, grid, lds, stream);
-    case 2 * S_F32: return launch_layout<S_F32, 0>(exact, past, A, grid, lds, stream);
-    case 2 * S_F32 + 1: return launch_layout<S_F32, 1>(exact, past, A, grid, lds, stream);
+    case 2 * S_F16: return launch_layout<S_F16, 0>(edge, past, A, grid, lds, stream);
+    case 2 * S_F16 + 1: return launch_layout<S_F16, 1>(edge, past, A, grid, lds, stream);
+    case 2 * S_BF16: return launch_layout<S_BF16, 0>(edge, past, A, grid, lds, stream);
+    case 2 * S_BF16 + 1: return launch_layout<S_BF16, 1>(edge, past, A, grid, lds, stream);
+    case 2 * S_F32: return launch_layout<S_F32, 0>(edge, past, A, grid, lds, stream);
+    case 2 * S_F32 + 1: return launch_layout<S_F32, 1>(edge, past, A, grid, lds, stream);
     }
     return (int)hipErrorInvalidValue;
 }
 
-int launch_rope(int type, int layout, bool exact, bool past, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
+int launch_rope(int type, int layout, int edge, bool past, const RopeArgs &A, uint32_t grid, uint32_t lds, void *stream)
 {
-    return launch_any(type, layout, exact, past, A, grid, lds, stream);
+    return launch_any(type, layout, edge, past, A, grid, lds, stream);
 }
 
-int launch_append(int type, int layout, bool exact, bool past, const AppendArgs &A, uint32_t grid, uint32_t lds,
+int launch_append(int type, int layout, int edge, bool past, const AppendArgs &A, uint32_t grid, uint32_t lds,
                   void *stream)
 {
-    return launch_any(type, layout, exact, past, A, grid, lds, stream);
+    return launch_any(type, layout, edge, past, A, grid, lds, stream);
 }
 
 }  // namespace ecmd
