@@ -395,7 +395,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         }
         uint32_t wb = begin, we = end;
         if (parts > 1) {
-            const uint32_t each = (end - begin + parts * 32 - 1) >> (7 - head_shift) << 5;
+            const uint32_t each = (end - begin + parts * kTile - 1) / kTile >> (2 - head_shift) << (KB == 2 ? 5 : 4);
             wb = min(begin + part * each, end);
             we = min(wb + each, end);
         }
@@ -864,9 +864,13 @@ int launch_join_type(const AttnArgs &A, void *stream)
 {
     AttnArgs J = A;
     J.by_heads = Div31(A.hq);
-    if (A.join_many)
-        return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY, 1024, 32>),
-                             dim3(A.b * A.hq, (A.dv + 31) / 32), dim3(1024), rows_lds(A.b), stream, J);
+    const dim3 grid(A.b * A.hq, (A.dv + 31) / 32);
+    if (A.join == 2)
+        return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY, 1024, 32>), grid, dim3(1024),
+                             rows_lds(A.b), stream, J);
+    if (A.join == 1)
+        return launch_kernel(reinterpret_cast<const void *>(&k_attention_join<TY, 256, 32>), grid, dim3(256),
+                             rows_lds(A.b), stream, J);
     return launch_kernel(reinterpret_cast<const void *>(&k_attention_join_few<TY>),
                          dim3((A.b * A.hq + kAttnWaves - 1) / kAttnWaves), dim3(kAttnBlock), rows_lds(A.b), stream, J);
 }

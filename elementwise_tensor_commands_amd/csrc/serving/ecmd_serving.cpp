@@ -546,8 +546,11 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.stream = (t[1].span() + t[2].span()) > (int64_t(1) << 28);
     // Many segments to few rows: two rows of 262143 positions are joined by 1024
     // work-items to 32 columns in 5.7 us, by 256 to a row in 14.8; 8 rows of 2000 take
-    // 28.7 us with the former and 21.3 with a wave to a row.
-    A.join_many = std::min<uint64_t>(A.runs_most, steps) > 16 && (uint64_t)b * hq * ((dv + 31) / 32) <= 512;
+    // 28.7 us with the former and 21.3 with a wave to a row; 8 ragged rows of up to
+    // 6263, 3 kv heads, 22 us with a wave to a row and 16 with 256 work-items
+    // to 32 columns.
+    const uint64_t segments = std::min<uint64_t>(A.runs_most, steps);   // of a row, at most
+    A.join = segments <= 16 ? 0 : (uint64_t)b * hq * ((dv + 31) / 32) <= 512 ? 2 : A.runs_most > 12 * (uint64_t)b ? 1 : 0;
     if (!A.direct) P.workspace = (int64_t)(((uint64_t)A.runs_most + b) * hq * (dv + 2) * 4 + 16);
     return CMD_OK;
 }

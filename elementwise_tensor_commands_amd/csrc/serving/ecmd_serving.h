@@ -91,7 +91,8 @@ struct AttnArgs {
     uint32_t runs, runs_much, runs_most;   // runs of positions for each head; the larger one
     uint32_t runs_whole;                   // rows up to which they may all be runs (0: too few work-groups)
     uint32_t grid;
-    uint32_t stream, join_many;            // larger than the last-level cache; rows may have many segments
+    uint32_t stream;                       // 1: larger than the last-level cache
+    uint32_t join;                         // 0, 1, 2: few, many, very many segments to a row
     float scale_log2;                      // scale * log2(e)
     Div31 by_page;
     Div31 by_heads, by_heads_much;         // work-groups of eight runs: 8 heads; 8 heads >> head_shift
@@ -100,7 +101,9 @@ struct AttnArgs {
 };
 
 // Positions are dealt to work-groups in steps of this many: a tile for each of
-// four waves, at 16 bits.
+// four waves, at 16 bits.  (Half of it for binary32: one row of 19296 positions 26
+// us instead of 29, nine rows of up to 1000 20 instead of 18, as runs then end
+// within rows.)
 constexpr uint32_t kAttnStep = 128;
 // Steps of all heads that count as much to read (see deal_steps).
 constexpr uint32_t kAttnMuch = 6144;

@@ -253,16 +253,17 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
     // ones' while the angles are computed.
     constexpr int U = 4;
     Item<TY, LAYOUT, EDGE, STREAM> it[U];
-    auto load = [&](uint32_t i0) {
+    auto load = [&](uint32_t from) {   // from: the work-group's
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (EDGE != kGuarded || i0 + u * kBlock < total) {   // the last item again instead of a branch
-                const Place p = split(EDGE != kGuarded ? min(i0 + u * kBlock, total - 1) : i0 + u * kBlock);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = from + u * kBlock + threadIdx.x;
+            if (EDGE != kGuarded ? from + u * kBlock < total : i < total) {   // the last item again, not a branch
+                const Place p = split(EDGE != kGuarded ? min(i, total - 1) : i);
                 it[u].load((const T *)A.x + offset(p, A.xs), p.item, A.pairs, A.width);
             }
+        }
     };
-    uint32_t i = threadIdx.x;
-    load(i);
+    load(0);
     for (uint32_t j = threadIdx.x; j < count * A.pairs; j += kBlock) {
         const uint32_t t = j / A.pairs, p = j - t * A.pairs;
         const uint32_t g = first + t, bb = A.by_t.div(g);
@@ -273,16 +274,18 @@ __global__ __launch_bounds__(kBlock) void k_rope(const RopeArgs A)
         sn[t * row + p] = A.inverse ? -s : s;
     }
     __syncthreads();
-    while (i < total) {
+    for (uint32_t from = 0; from < total;) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u * kBlock < total) {
-                const Place p = split(i + u * kBlock);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = from + u * kBlock + threadIdx.x;
+            if (i < total) {
+                const Place p = split(i);
                 it[u].finish((T *)A.out + offset(p, A.os), p.item, A.pairs, A.width, cs + p.tok * row, sn + p.tok * row,
                              A.x == A.out);
             }
-        i += U * kBlock;
-        load(i);
+        }
+        from += U * kBlock;
+        if (from < total) load(from);
     }
 }
 
