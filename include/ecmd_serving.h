@@ -13,8 +13,9 @@
  *     be one-to-one; an output overlaps no other argument unless the call says
  *     so (then: the identical view);
  *   - the library allocates no device memory: calls that need scratch memory
- *     take a workspace (16-byte aligned, its contents need no preparation and
- *     mean nothing afterwards), sized by the matching *_workspace call;
+ *     take a workspace (16-byte aligned, apart from every argument; its contents
+ *     need no preparation and mean nothing afterwards), sized by the matching
+ *     *_workspace call;
  *   - cmd_last_error(NULL) describes the last failure on this thread.
  *
  * What the data say -- positions, row numbers, page ids, lengths, reference
@@ -67,8 +68,8 @@ int cmd_rope(const cmd_arg args[4], int32_t layout, double mscale, int32_t inver
  * the identical view as q.  Every token's q is rotated into q_out; k rotated
  * and v as it is go to position pos[t] of sequence row[t].  A token whose row
  * or position is outside the table, or whose page is a hole, is padding: its
- * q_out is written, the cache is not.  Two tokens of one call at one slot leave
- * either one's values there. */
+ * q_out is written, the cache is not.  After two tokens of one call at one slot
+ * each element there is one or the other's. */
 int cmd_rope_append(const cmd_arg args[10], int32_t layout, double mscale, int32_t flags, void *hip_stream);
 
 /* Attention of one new token per sequence over the paged cache.  args:
