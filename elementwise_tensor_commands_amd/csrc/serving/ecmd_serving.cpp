@@ -465,7 +465,7 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     if (d < 1 || dv < 1) return refuse(CMD_E_SHAPE, "heads of width 0");
     if (d > 256 || dv > 256) return refuse(CMD_E_LIMIT, "heads wider than 256");
     if (window < 0) return refuse(CMD_E_ARG, "negative window");
-    for (int i : {0, 1, 2}) TRY(check_unit(t[i]));
+    for (int i : {0, 1, 2, 5}) TRY(check_unit(t[i]));
     TRY(check_outputs(t, 7, 5, nullptr));
     if (cols * std::max<int64_t>(page, 1) > (int64_t(1) << 30))
         return refuse(CMD_E_LIMIT, "the table holds more than 2^30 positions");

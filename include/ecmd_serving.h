@@ -12,6 +12,10 @@
  *   - strides are >= 0; an input may have stride 0 (broadcast); an output must
  *     be one-to-one; an output overlaps no other argument unless the call says
  *     so (then: the identical view);
+ *   - the elements of a head (the last dimension of x, q, k, v, the caches and
+ *     their outputs, where it has more than one) are neighbours: stride 1, else
+ *     CMD_E_STRIDE.  Every other dimension, and all of the tables, lse and the
+ *     pools of cmd_page_copy, may have any strides that the call does not exclude;
  *   - the library allocates no device memory: calls that need scratch memory
  *     take a workspace (16-byte aligned, apart from every argument; its contents
  *     need no preparation and mean nothing afterwards), sized by the matching
@@ -26,8 +30,8 @@
  * The cache: k_cache [N, page, kv heads, d] and v_cache [N, page, kv heads, dv]
  * are N pages of `page` slots.  A page table row pages[r, 0..P) names the pages
  * of sequence r: position p lies in slot p % page of page pages[r, p / page].
- * An id outside 0 .. N - 1 is a hole.  Any strides: a cache laid out [N, kv
- * heads, page, d] is passed as its permuted view.
+ * An id outside 0 .. N - 1 is a hole.  Any strides but the last: a cache laid
+ * out [N, kv heads, page, d] is passed as its permuted view.
  */
 #ifndef ECMD_SERVING_H
 #define ECMD_SERVING_H

@@ -149,6 +149,18 @@ def test_attention_refusals(name, kw):
     _refused(name, E.paged_attention_workspace, *attention_args(**kw))
 
 
+def test_attention_out_has_neighbouring_columns():
+    """An out whose last dimension has another stride is refused, as the inputs are."""
+    for out in (torch.zeros(3, 6, 4).transpose(1, 2), torch.zeros(3, 4, 12)[..., ::2]):
+        assert tuple(out.shape) == (3, 4, 6)
+        for fn in (E.paged_attention, E.paged_attention_workspace):
+            assert "last dimension" in _refused("CMD_E_STRIDE", fn, *attention_args(out=out))
+    # any strides of the other dimensions, a last dimension of one element, and lse of any strides
+    for kw in (dict(out=torch.zeros(4, 3, 9)[..., 2:8].transpose(0, 1)),
+               dict(v=torch.zeros(7, 16, 2, 1), out=torch.zeros(3, 4, 5)[..., 3:4])):
+        assert "GPU" in _refused("CMD_E_ARG", E.paged_attention, *attention_args(**kw), lse=torch.zeros(4, 6).t()[::2])
+
+
 def test_attention_refusals_of_options():
     _refused("CMD_E_ARG", E.paged_attention, *attention_args(), window=-1)
     _refused("CMD_E_ARG", E.paged_attention, *attention_args(), window=5 - (1 << 32))
