@@ -95,7 +95,9 @@ def _scratch(workspace, size: int, stream, device: int):
         ptr, owner = _binding.scratch(size, device)
     else:
         import torch
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        if isinstance(stream, int):   # of handle 0 ExternalStream would make a new stream
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
             ptr, owner = _binding.scratch(size, device)
     return ptr, size, owner
 

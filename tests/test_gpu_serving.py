@@ -476,6 +476,36 @@ def test_streams_and_workspace():
         E.paged_attention(args[0].cpu(), *args[1:], out)
 
 
+def test_default_stream_by_its_handle(monkeypatch):
+    """stream=0: the scratch memory is of the default stream too, and the results are the same."""
+    import types
+
+    from elementwise_tensor_commands_amd import serving as S
+    args, out = step_state()
+    E.paged_attention(*args, out)
+    allocated_on = []
+
+    def scratch(size, device):
+        allocated_on.append(torch.cuda.current_stream().cuda_stream)
+        return binding.scratch(size, device)
+
+    binding = S._binding
+    monkeypatch.setattr(S, "_binding", types.SimpleNamespace(pack=binding.pack, scratch=scratch))
+    rng, pages, lens, refs = tables(3, 300, 7, 8, 5000, 1000)
+    new = lambda *s: torch.full(s, 77, dtype=I32, device="cuda")
+    ins = [pages.cuda(), ints(lens).cuda(), ints(refs).cuda(), torch.arange(300, dtype=I32).cuda(), torch.ones(300, dtype=I32).cuda()]
+    want, got = ([new(300, 7), new(300), new(5000), new(300), new(300), new(2)] for _ in range(2))
+    E.page_assign(*ins, 8, *want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        other = torch.empty_like(out)
+        E.paged_attention(*args, other, stream=0)
+        E.page_assign(*ins, 8, *got, stream=0)
+    torch.cuda.synchronize()
+    assert len(allocated_on) == 3 and allocated_on[1:] == [0, 0]
+    assert torch.equal(other, out) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_captured_step():
     """A whole decode step in one graph, replayed with other lengths and inputs."""
     def build():

@@ -190,6 +190,30 @@ def test_attention_workspace():
     assert E.lib.cmd_paged_attention(args, 1.0, 0, None, 0, S.CHECK_ONLY, None) == 0
 
 
+def test_scratch_memory_is_the_launch_stream_s(monkeypatch):
+    """Of a handle, its stream's; of handle 0, the default stream's (which torch wraps in no ExternalStream)."""
+    import contextlib
+    import types
+
+    from elementwise_tensor_commands_amd import serving as S
+    entered = []
+
+    @contextlib.contextmanager
+    def enter(stream):
+        entered.append(stream)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", device))
+    monkeypatch.setattr(S, "_binding", types.SimpleNamespace(scratch=lambda size, device: (4096, "owner")))
+    other = object()
+    for stream, want in ((0, ("default", 3)), (77, ("external", 77)), (other, other)):
+        assert S._scratch(None, 64, stream, 3) == (4096, 64, "owner")
+        assert entered.pop() == want
+    assert S._scratch(None, 64, None, 3) == (4096, 64, "owner") and not entered      # torch's current stream
+
+
 # ---------------------------------------------------------------------------
 # Pages.
 
