@@ -67,6 +67,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kAttnBlock = 256, kAttnWaves = 4;
 constexpr uint32_t kTableKeys = 256;   // positions whose cache offsets a wave holds at a time
@@ -95,11 +97,26 @@ __device__ inline f32x4 mma16(u32x4 a, u32x4 b, f32x4 c)
 
 __device__ inline float as_f(uint32_t x) { return __builtin_bit_cast(float, x); }
 
+// x if it is finite, else some finite number.
+__device__ inline float finite(float x)
+{
+    float most = 3.40282346638528859812e38f;
+    asm("" : "+s"(most));   // one register and its negative, not two
+    return __builtin_amdgcn_fmed3f(x, -most, most);
+}
+
 // x, computed here: what depends on it is not moved out of a loop into registers
 // that the loop needs.
 __device__ inline uint32_t fresh(uint32_t x)
 {
     asm volatile("" : "+v"(x));
+    return x;
+}
+
+// The same of a number that is one for the wave.
+__device__ inline uint32_t fresh_uniform(uint32_t x)
+{
+    asm volatile("" : "+s"(x));
     return x;
 }
 
@@ -355,14 +372,14 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
     // Piece c of a row of d elements at p.  One that would reach past the end is
     // moved back to end with the row; masked() clears what earlier ones have, all
     // of it where the piece lies past the end altogether.
-    auto load_row_piece = [&](const char *p, int c, auto stream) {
-        const int at = (c * 4 + (int)j) * E;
+    auto load_row_piece = [&](const char *p, int c, uint32_t quarter, auto stream) {   // quarter: j
+        const int at = (c * 4 + (int)quarter) * E;
         if constexpr (EDGE == kTiny) return load_some<T, E>(p + at * sizeof(T), (int)A.d - at);
         return load16<stream>(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
     };
     auto masked = [&](u32x4 x, int c) {
         if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {   // the same for the whole launch
-            const int at = (c * 4 + (int)j) * E, twice = at - min(at, (int)A.d - E);
+            const int at = (c * 4 + (int)fresh(j)) * E, twice = at - min(at, (int)A.d - E);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 if constexpr (E == 8)
@@ -394,17 +411,18 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             end = min(begin + steps * kAttnStep, hi);
         }
         uint32_t wb = begin, we = end;
-        if (parts > 1) {
+        if (fresh_uniform(parts) > 1) {
             const uint32_t each = (end - begin + parts * kTile - 1) / kTile >> (2 - head_shift) << (KB == 2 ? 5 : 4);
             wb = min(begin + part * each, end);
             we = min(wb + each, end);
         }
 
         u32x4 q[NK];
+        const uint32_t qh = q0 + min(fresh(hh), q_n - 1), qj = EDGE == kTail ? j : fresh(j);
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
-            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)(q0 + (hh < q_n ? hh : 0)) * A.qs[1]) * sizeof(T);
-            q[c] = masked(load_row_piece(p, c, std::false_type()), c);
+            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)qh * A.qs[1]) * sizeof(T);
+            q[c] = masked(load_row_piece(p, c, qj, std::false_type()), c);
             if (hh >= q_n) q[c] = u32x4{0, 0, 0, 0};
         }
 
@@ -446,7 +464,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             for (int kb = 0; kb < KB; ++kb) {
                 const char *p = kbase + sh.table.k[wave][t + kb * 16 + hh];
 #pragma unroll
-                for (int c = 0; c < NK; ++c) kr[kb][c] = load_row_piece(p, c, std::bool_constant<STREAM>());
+                for (int c = 0; c < NK; ++c) kr[kb][c] = load_row_piece(p, c, j, std::bool_constant<STREAM>());
             }
             bits = (uint32_t)(sh.table.valid[wave][t / 64] >> (t % 64));
             if constexpr (KB == 1) bits &= 0xFFFFu;
@@ -548,18 +566,26 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             } else {
                 // A weight goes in as the sum of two 16-bit numbers, its leading bits
                 // and the rest: weights rounded to one would double the error of the
-                // output's own rounding, and the matrix units are idle enough.
+                // output's own rounding, and the matrix units are idle enough.  The
+                // leading part is 0 only if the weight is: an infinite value gives an
+                // infinity there, and what the rest (0, or of the other sign) makes of
+                // it is no number or the wrong one, so the rests' sums are kept apart and
+                // bounded before they are added.
                 u32x4 hi, lo;
 #pragma unroll
                 for (int x = 0; x < VK; x += 2) {
+                    const uint32_t a = __builtin_bit_cast(uint32_t, p[x]), b = __builtin_bit_cast(uint32_t, p[x + 1]);
                     if constexpr (TY == S_BF16) {
-                        const uint32_t a = __builtin_bit_cast(uint32_t, p[x]), b = __builtin_bit_cast(uint32_t, p[x + 1]);
                         hi[x / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);
                         const f32x2 rest = {p[x] - as_f(a & 0xFFFF0000u), p[x + 1] - as_f(b & 0xFFFF0000u)};
                         lo[x / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
                     } else {
-                        const auto h = __builtin_amdgcn_cvt_pkrtz(p[x], p[x + 1]);
-                        hi[x / 2] = __builtin_bit_cast(uint32_t, h);
+                        // positive numbers order as their bits do; the smallest stands for less
+                        const u16x2 least = __builtin_bit_cast(u16x2, min(a, 1u) | min(b, 1u) << 16);
+                        const u16x2 bits = __builtin_elementwise_max(
+                            __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(p[x], p[x + 1])), least);
+                        const f16x2 h = __builtin_bit_cast(f16x2, bits);
+                        hi[x / 2] = __builtin_bit_cast(uint32_t, bits);
                         lo[x / 2] = __builtin_bit_cast(
                             uint32_t, __builtin_amdgcn_cvt_pkrtz(p[x] - (float)h[0], p[x + 1] - (float)h[1]));
                     }
@@ -571,8 +597,11 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                     for (int w = 0; w < 4; ++w)
                         a[w] = __builtin_amdgcn_perm(vr[2 * w + 1][c / 8][c % 8 / 2], vr[2 * w][c / 8][c % 8 / 2],
                                                      c & 1 ? 0x07060302 : 0x05040100);
+                    const f32x4 rest = mma16<TY>(a, lo, f32x4{0, 0, 0, 0});
                     acc[c] = mma16<TY>(a, hi, acc[c]);
-                    acc[c] = mma16<TY>(a, lo, acc[c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[c][i] += finite(rest[i]);
+                    asm volatile("" : "+v"(acc[c]));   // added here: all rests at once would not fit the registers
                 }
             }
             if (tile < we) load_v(in_table);
@@ -580,7 +609,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
 
         // The segment's sums: final, or for the second launch at a place of its
         // own (work-groups and rows only go forward).
-        const uint32_t tid = fresh(threadIdx.x), eh = tid & 15, ej = tid >> 4 & 3;
+        const uint32_t tid = fresh(wave * 64 + __lane_id()), eh = tid & 15, ej = tid >> 4 & 3;
         const uint64_t place = (uint64_t)(group + r) * A.hq + q0;
         auto put = [&](uint32_t hx, uint32_t c, float sum, float total) {
             if (whole_row) store_out<TY>(A, r, q0 + hx, c, total == 0.0f ? 0.0f : sum / total);

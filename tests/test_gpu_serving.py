@@ -302,6 +302,53 @@ def test_attention_special_values():
     assert bool((out[2, :, 6] == math.inf).all() and torch.isfinite(out[2][:, torch.arange(64) != 6]).all())
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_attention_infinite_values(dtype):
+    """An infinity in a value that is attended to gives an infinity in its column, a NaN or two
+    infinities of both signs a NaN, whatever the weight; the other columns are as without them."""
+    d, dv = 64, 72
+    for seed, lens in enumerate(([1, 2, 40, 300], [900, 64, 31, 33])):
+        q, k, v, pages, lens = attention_case(70 + seed, DT[dtype], 4, 4, 2, d, dv, 16, lens, sharp=2.0)
+        at = lambda r, x: (int(pages[r, x // 16]), x % 16)
+        last = [int(x) - 1 for x in lens]
+        clean = v.clone()
+        for r in range(4):
+            for c in (1, 7, 8, 70):
+                v[at(r, last[r] // 2)][0, c] = math.inf
+            v[at(r, last[r])][1, 3] = -math.inf
+            v[at(r, 0)][0, 5] = math.nan
+            v[at(r, 0)][1, 6], v[at(r, last[r])][1, 6] = math.inf, -math.inf     # of a row of one position: -inf
+        out = torch.empty(4, 4, dv, dtype=DT[dtype], device="cuda")
+        E.paged_attention(q.cuda(), k.cuda(), v.cuda(), pages.cuda(), lens.cuda(), out)
+        out = out.cpu()
+        want, _, eo, _ = O.attention(q, k, clean, pages, lens, d ** -0.5)
+        for r in range(4):
+            for h in range(4):
+                special = {1: math.inf, 7: math.inf, 8: math.inf, 70: math.inf, 5: math.nan} if h < 2 else {
+                    3: -math.inf, 6: math.nan if last[r] else -math.inf}
+                for c, x in special.items():
+                    got = float(out[r, h, c])
+                    assert got == x or (math.isnan(x) and math.isnan(got)), (seed, r, h, c, got)
+                keep = torch.tensor([c not in special for c in range(dv)])
+                within(out[r, h][keep], want[r, h][keep], eo[r, h][keep], (seed, r, h))
+
+
+def test_attention_infinite_value_of_small_weight():
+    """The same far below the largest weight, down to 2^-100 of it."""
+    for dtype in DT.values():
+        for bits in (20, 37, 45, 100):
+            k = torch.zeros(2, 16, 1, 64, dtype=dtype)
+            v = torch.zeros(2, 16, 1, 64, dtype=dtype)
+            k[..., 0] = -bits * math.log(2.0)
+            k[0, 5, 0, 0] = 0.0
+            v[0, 9, 0, 3], v[1, 9, 0, 4] = math.inf, -math.inf
+            q = torch.zeros(1, 1, 64, dtype=dtype)
+            q[..., 0] = 1.0
+            out = torch.empty(1, 1, 64, dtype=dtype, device="cuda")
+            E.paged_attention(q.cuda(), k.cuda(), v.cuda(), ints([[0, 1]]).cuda(), ints([30]).cuda(), out, scale=1.0)
+            assert out[0, 0].tolist() == [0.0] * 3 + [math.inf, -math.inf] + [0.0] * 59, (dtype, bits)
+
+
 def test_attention_nothing_to_read():
     for n, cols in ((0, 3), (4, 0), (0, 0)):
         out = torch.full((2, 4, 8), 5.0, device="cuda")
