@@ -105,18 +105,17 @@ __device__ inline float finite(float x)
     return __builtin_amdgcn_fmed3f(x, -most, most);
 }
 
-// x, computed here: what depends on it is not moved out of a loop into registers
-// that the loop needs.
-__device__ inline uint32_t fresh(uint32_t x)
+// x, as far as the compiler knows another one for every `now`: what depends on it is
+// computed where `now` is known, not moved out of a loop into registers that the
+// loop needs.
+__device__ inline uint32_t fresh(uint32_t x, uint32_t now)
 {
-    asm volatile("" : "+v"(x));
+    asm("" : "+v"(x) : "s"(now));
     return x;
 }
-
-// The same of a number that is one for the wave.
-__device__ inline uint32_t fresh_uniform(uint32_t x)
+__device__ inline uint32_t fresh_uniform(uint32_t x, uint32_t now)
 {
-    asm volatile("" : "+s"(x));
+    asm("" : "+s"(x) : "s"(now));
     return x;
 }
 
@@ -261,12 +260,17 @@ __device__ inline void store_out(const AttnArgs &A, uint32_t r, uint32_t h, uint
 
 // Weights are held as 2^kBias exp2(score - m).  m is raised only where a score
 // passes it by more than kSlack (log2), which spares most tiles the exchange
-// between lanes and the rescale; a weight stays below 2^(kBias + kSlack).  The
-// bias keeps small binary16 weights out of its subnormals (their sum, the score and
-// every statistic are binary32).
-constexpr float kSlack = 8.0f;
+// between lanes and the rescale; a weight stays below 2^(kBias + kSlack).  With
+// binary16, whose numbers end at 2^16 and 2^-24, both leave most of the range to
+// the weights below m, and the second part of a weight is held kRests times as
+// large: with leading bits of 2^-24 or more and 11 bits below them a weight is off
+// by at most 2^-22 of itself or 2^-47 of the one at m, whichever is more.
 template <int TY>
-constexpr float kBias = TY == S_F16 ? 6.0f : 0.0f;
+constexpr float kSlack = TY == S_F16 ? 4.0f : 8.0f;
+template <int TY>
+constexpr float kBias = TY == S_F16 ? 11.0f : 0.0f;
+template <int TY>
+constexpr float kRests = TY == S_F16 ? 2048.0f : 1.0f;
 
 // The natural logarithm of the softmax's sum from a maximum (log2) and the sum
 // of the weights against it.
@@ -377,9 +381,9 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         if constexpr (EDGE == kTiny) return load_some<T, E>(p + at * sizeof(T), (int)A.d - at);
         return load16<stream>(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
     };
-    auto masked = [&](u32x4 x, int c) {
+    auto masked = [&](u32x4 x, int c, uint32_t now) {
         if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {   // the same for the whole launch
-            const int at = (c * 4 + (int)fresh(j)) * E, twice = at - min(at, (int)A.d - E);
+            const int at = (c * 4 + (int)fresh(j, now)) * E, twice = at - min(at, (int)A.d - E);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 if constexpr (E == 8)
@@ -411,18 +415,21 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             end = min(begin + steps * kAttnStep, hi);
         }
         uint32_t wb = begin, we = end;
-        if (fresh_uniform(parts) > 1) {
+        if (fresh_uniform(parts, r) > 1) {
             const uint32_t each = (end - begin + parts * kTile - 1) / kTile >> (2 - head_shift) << (KB == 2 ? 5 : 4);
             wb = min(begin + part * each, end);
             we = min(wb + each, end);
         }
 
         u32x4 q[NK];
-        const uint32_t qh = q0 + min(fresh(hh), q_n - 1), qj = EDGE == kTail ? j : fresh(j);
+        // The query's addresses need not wait for the run's, except where they would
+        // take registers of the loop (one row of 777: 11.1 us, or 11.2).
+        constexpr bool kLate = TY != S_F32 && VW == 16;
+        const uint32_t qh = q0 + min(kLate ? fresh(hh, r) : hh, q_n - 1), qj = kLate ? fresh(j, r) : j;
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
             const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)qh * A.qs[1]) * sizeof(T);
-            q[c] = masked(load_row_piece(p, c, qj, std::false_type()), c);
+            q[c] = masked(load_row_piece(p, c, qj, std::false_type()), c, r);
             if (hh >= q_n) q[c] = u32x4{0, 0, 0, 0};
         }
 
@@ -501,7 +508,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                 s[kb] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < NK; ++c) {
-                    const u32x4 k = masked(kr[kb][c], c);
+                    const u32x4 k = masked(kr[kb][c], c, tile);
                     if constexpr (TY == S_F32) {
 #pragma unroll
                         for (int f = 0; f < 4; ++f)
@@ -540,7 +547,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             }
 #pragma unroll
             for (int x = 0; x < VK; ++x) top = fmaxf(top, p[x]);
-            if (__any(top > m + kSlack)) {
+            if (__any(top > m + kSlack<TY>)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
                 const float mn = fmaxf(m, top);
@@ -586,8 +593,8 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                             __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(p[x], p[x + 1])), least);
                         const f16x2 h = __builtin_bit_cast(f16x2, bits);
                         hi[x / 2] = __builtin_bit_cast(uint32_t, bits);
-                        lo[x / 2] = __builtin_bit_cast(
-                            uint32_t, __builtin_amdgcn_cvt_pkrtz(p[x] - (float)h[0], p[x + 1] - (float)h[1]));
+                        const f32x2 rest = {(p[x] - (float)h[0]) * kRests<TY>, (p[x + 1] - (float)h[1]) * kRests<TY>};
+                        lo[x / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, f16x2));
                     }
                 }
 #pragma unroll
@@ -600,7 +607,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                     const f32x4 rest = mma16<TY>(a, lo, f32x4{0, 0, 0, 0});
                     acc[c] = mma16<TY>(a, hi, acc[c]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[c][i] += finite(rest[i]);
+                    for (int i = 0; i < 4; ++i) acc[c][i] = __builtin_fmaf(finite(rest[i]), 1.0f / kRests<TY>, acc[c][i]);
                     asm volatile("" : "+v"(acc[c]));   // added here: all rests at once would not fit the registers
                 }
             }
@@ -609,7 +616,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
 
         // The segment's sums: final, or for the second launch at a place of its
         // own (work-groups and rows only go forward).
-        const uint32_t tid = fresh(wave * 64 + __lane_id()), eh = tid & 15, ej = tid >> 4 & 3;
+        const uint32_t tid = fresh(wave * 64 + __lane_id(), r), eh = tid & 15, ej = tid >> 4 & 3;
         const uint64_t place = (uint64_t)(group + r) * A.hq + q0;
         auto put = [&](uint32_t hx, uint32_t c, float sum, float total) {
             if (whole_row) store_out<TY>(A, r, q0 + hx, c, total == 0.0f ? 0.0f : sum / total);

@@ -349,6 +349,36 @@ def test_attention_infinite_value_of_small_weight():
             assert out[0, 0].tolist() == [0.0] * 3 + [math.inf, -math.inf] + [0.0] * 59, (dtype, bits)
 
 
+def fine_bounds(q, k, v, pages, lens, scale):
+    """want, and the bound on the error of a kernel that holds weights in 22 bits or more, of the
+    row's largest weight not below 2^-47, whatever the type: the oracle's bound for binary32 inputs of
+    these values, the weights' share of the values' size, and the output's rounding."""
+    dt = q.dtype
+    want, _, eo, _ = O.attention(q.float(), k.float(), v.float(), pages, lens, scale)
+    size, _, _, _ = O.attention(q.float(), k.float(), v.float().abs(), pages, lens, scale)
+    floor = 2.0 ** -47 * float(v.float().abs().max()) * int(max(lens))
+    return want, eo + size * 2.0 ** -22 + floor + want.abs() * O.half_step(dt) + O.tiny(dt)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_attention_many_small_weights(dtype):
+    """One key in 32 with nearly all of the weight and value 0; the others, far below, make the output."""
+    dt, n, d = DT[dtype], 2048, 64
+    pages = torch.arange(n // 16, dtype=I32).view(1, -1)
+    for bits, size in ((18, 1.0), (22, 500.0), (26, 6000.0), (30, 60000.0), (34, 60000.0)):
+        g = gen(bits)
+        k, v = torch.zeros(n // 16, 16, 1, d), torch.rand(n // 16, 16, 1, d, generator=g) * 0.5 + 0.5
+        k[..., 0] = -bits * math.log(2.0) + torch.rand(n // 16, 16, 1, generator=g) * 0.4
+        k[::2, 7, 0, 0], v[::2, 7] = 0.0, 0.0
+        q = torch.zeros(1, 2, d)
+        q[:, 0, 0], q[:, 1, 0] = 1.0, 0.75
+        q, k, v = q.to(dt), k.to(dt), (v * size).to(dt)
+        want, bound = fine_bounds(q, k, v, pages, [n], 1.0)
+        out = torch.empty(1, 2, d, dtype=dt, device="cuda")
+        E.paged_attention(q.cuda(), k.cuda(), v.cuda(), pages.cuda(), ints([n]).cuda(), out, scale=1.0)
+        within(out, want, bound, (bits, size))
+
+
 def test_attention_nothing_to_read():
     for n, cols in ((0, 3), (4, 0), (0, 0)):
         out = torch.full((2, 4, 8), 5.0, device="cuda")
