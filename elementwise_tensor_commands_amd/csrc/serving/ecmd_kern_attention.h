@@ -65,7 +65,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -571,22 +570,29 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                     for (int c = 0; c < VW; ++c)
                         acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(vr[x][c / 4][c % 4]), p[x], acc[c], 0, 0, 0);
             } else {
-                // A weight goes in as the sum of two 16-bit numbers, its leading bits
-                // and the rest: weights rounded to one would double the error of the
-                // output's own rounding, and the matrix units are idle enough.  The
-                // leading part is 0 only if the weight is: an infinite value gives an
-                // infinity there, and what the rest (0, or of the other sign) makes of
-                // it is no number or the wrong one, so the rests' sums are kept apart and
-                // bounded before they are added.
-                u32x4 hi, lo;
+                // A weight goes in as the sum of 16-bit numbers, its leading bits and
+                // the rest: bfloat16 in three parts, which are all of its 24 bits, binary16
+                // in two (see kBias).  Fewer would show where values cancel, and the
+                // matrix units are idle enough.  The leading part is 0 only if the weight
+                // is: an infinite value gives an infinity there, and what the rest (0, or
+                // of the other sign) makes of it is no number or the wrong one, so the
+                // rests' sums are kept apart and bounded before they are added.
+                u32x4 hi, lo, last;
 #pragma unroll
                 for (int x = 0; x < VK; x += 2) {
-                    const uint32_t a = __builtin_bit_cast(uint32_t, p[x]), b = __builtin_bit_cast(uint32_t, p[x + 1]);
                     if constexpr (TY == S_BF16) {
-                        hi[x / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);
-                        const f32x2 rest = {p[x] - as_f(a & 0xFFFF0000u), p[x + 1] - as_f(b & 0xFFFF0000u)};
-                        lo[x / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
+                        // the leading halves of both numbers, which keep the rest
+                        auto split = [](float &f, float &g) {
+                            const uint32_t a = __builtin_bit_cast(uint32_t, f), b = __builtin_bit_cast(uint32_t, g);
+                            f -= as_f(a & 0xFFFF0000u);
+                            g -= as_f(b & 0xFFFF0000u);
+                            return __builtin_amdgcn_perm(b, a, 0x07060302);
+                        };
+                        hi[x / 2] = split(p[x], p[x + 1]);
+                        lo[x / 2] = split(p[x], p[x + 1]);
+                        last[x / 2] = split(p[x], p[x + 1]);
                     } else {
+                        const uint32_t a = __builtin_bit_cast(uint32_t, p[x]), b = __builtin_bit_cast(uint32_t, p[x + 1]);
                         // positive numbers order as their bits do; the smallest stands for less
                         const u16x2 least = __builtin_bit_cast(u16x2, min(a, 1u) | min(b, 1u) << 16);
                         const u16x2 bits = __builtin_elementwise_max(
@@ -604,7 +610,9 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                     for (int w = 0; w < 4; ++w)
                         a[w] = __builtin_amdgcn_perm(vr[2 * w + 1][c / 8][c % 8 / 2], vr[2 * w][c / 8][c % 8 / 2],
                                                      c & 1 ? 0x07060302 : 0x05040100);
-                    const f32x4 rest = mma16<TY>(a, lo, f32x4{0, 0, 0, 0});
+                    f32x4 rest = {0, 0, 0, 0};
+                    if constexpr (TY == S_BF16) rest = mma16<TY>(a, last, rest);
+                    rest = mma16<TY>(a, lo, rest);
                     acc[c] = mma16<TY>(a, hi, acc[c]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[c][i] = __builtin_fmaf(finite(rest[i]), 1.0f / kRests<TY>, acc[c][i]);

@@ -85,9 +85,11 @@ int cmd_rope_append(const cmd_arg args[10], int32_t layout, double mscale, int32
  * the positions x with  x < min(lens[r], P * page),  x >= lens[r] - window if
  * window > 0, and no hole under them:
  *      out = sum_x softmax_x(scale q . k_x) v_x,   lse = log sum_x exp(scale q . k_x)
- * Sums and softmax statistics are binary32.  A row that attends to nothing gets
- * out 0 and lse -inf.  What slots hold that no row attends to is of no account
- * (NaN included). */
+ * Scores, weights, sums and softmax statistics are binary32, but for f16 a weight
+ * meets the values held to within 2^-22 of itself or 2^-47 of its row's largest.
+ * A row that attends to nothing gets out 0 and lse -inf.  What slots hold that no
+ * row attends to is of no account (NaN included); an infinite value that is
+ * attended to with a weight that is not 0 in binary32 makes its column infinite. */
 int cmd_paged_attention(const cmd_arg args[7], float scale, int32_t window, void *workspace,
                         int64_t workspace_bytes, int32_t flags, void *hip_stream);
 /* Bytes of workspace that call needs (0: none), or a negative status. */

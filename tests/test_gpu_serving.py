@@ -379,6 +379,25 @@ def test_attention_many_small_weights(dtype):
         within(out, want, bound, (bits, size))
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_attention_values_that_cancel(dtype):
+    """Two keys of nearly one weight, values 1 and -1: what is left, tanh(s / 2), shows the weights' error."""
+    dt, b = DT[dtype], 16
+    s = (torch.arange(1, b + 1) * 1.1e-4 * torch.tensor([1.0, -1.0]).repeat(b // 2)).to(dt)
+    k, v = torch.zeros(b, 16, 1, 64, dtype=dt), torch.zeros(b, 16, 1, 64, dtype=dt)
+    k[:, 0, 0, 5], v[:, 0], v[:, 1] = s, 1.0, -1.0
+    q = torch.zeros(b, 1, 64, dtype=dt)
+    q[..., 5] = 1.0
+    out = torch.empty(b, 1, 64, dtype=dt, device="cuda")
+    E.paged_attention(q.cuda(), k.cuda(), v.cuda(), torch.arange(b, dtype=I32).view(b, 1).cuda(), ints([2] * b).cuda(), out, scale=1.0)
+    want = torch.tanh(s.double() / 2).view(b, 1, 1).expand(b, 1, 64)
+    # each weight: a score of three roundings and a difference, exp2 within 2^-22, held to 2^-22; the
+    # difference of two weights over their sum, three roundings; the output's
+    u = 2.0 ** -24
+    bound = s.double().abs().view(b, 1, 1) * 4 * u + 2.0 ** -21 + want.abs() * (4 * u + O.half_step(dt)) + O.tiny(dt)
+    within(out, want, bound)
+
+
 def test_attention_nothing_to_read():
     for n, cols in ((0, 3), (4, 0), (0, 0)):
         out = torch.full((2, 4, 8), 5.0, device="cuda")
