@@ -146,6 +146,20 @@ class Decoder:
         return self.forward(tokens, c.lens - 1, torch.where(alive > 0, rows, -1))
 
 
+def next_beams(logits, alive, beams):
+    """A beam search's choice in every group of ``beams`` rows: all of them go on from
+    the group's row that scored highest of those alive, the i-th with its i-th best
+    token.  Returns the parents [rows] (int32) and tokens [rows] (int64)."""
+    import torch
+    score = logits.amax(-1).masked_fill(alive == 0, -math.inf).view(-1, beams)
+    best = torch.arange(0, len(logits), beams, device=logits.device) + score.argmax(-1)
+    left, tokens = logits[best], []
+    for _ in range(beams):
+        tokens.append(left.argmax(-1))
+        left = left.scatter(-1, tokens[-1][:, None], -math.inf)
+    return best.repeat_interleave(beams).to(torch.int32), torch.stack(tokens, 1).flatten()
+
+
 def main(argv):
     import torch
     steps = int(argv[argv.index("--steps") + 1]) if "--steps" in argv else 64
@@ -157,16 +171,13 @@ def main(argv):
     # a prompt fills the first beam of its group; the others fork from it at the first step
     m.prefill([prompts[r // beams] if r % beams == 0 else [] for r in range(rows)])
     alive = torch.ones(rows, dtype=torch.int32, device="cuda")
-    group = torch.arange(rows, device="cuda") // beams * beams     # each row's group's first
-    parent = group.to(torch.int32)
+    parent = torch.arange(rows, dtype=torch.int32, device="cuda") // beams * beams     # each row's group's first
     tokens = torch.randint(0, m.vocab, (rows,), generator=g).cuda()
 
     def step():
-        out = m.decode(tokens, parent, alive)
-        # each beam goes on with its best token from the beam that scored highest in its group
-        top = out.view(rows // beams, beams, m.vocab).amax(-1).argmax(-1)
-        parent.copy_((group + top.repeat_interleave(beams)).to(torch.int32))
-        tokens.copy_(out.argmax(-1))
+        p, t = next_beams(m.decode(tokens, parent, alive), alive, beams)
+        parent.copy_(p)
+        tokens.copy_(t)
 
     def timed(name, f, n):
         torch.cuda.synchronize()

@@ -82,3 +82,45 @@ def test_the_command_runs_and_finds_the_gpu():
     r = subprocess.run([sys.executable, "-m", "elementwise_tensor_commands_amd.decode", "--steps", "4", "--beams", "2"],
                        cwd=root, capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and "replayed" in r.stdout, r.stdout + r.stderr
+
+
+def test_captured_beam_search_step():
+    """Steps replayed from a graph, a beam ended between them, against the same steps run eagerly."""
+    from elementwise_tensor_commands_amd.decode import next_beams
+    beams, rows = 3, 6
+    models, states = [], []
+    for _ in range(2):
+        m = Decoder(layers=2, vocab=211, hq=4, hk=2, d=32, rows=rows, n=90, page=4, cols=12, dtype=torch.float32)
+        m.prefill([[5, 9, 3, 7, 1], [], [], [2, 4], [], []])
+        models.append(m)
+        states.append(dict(tokens=torch.arange(rows).cuda(), parent=torch.tensor([0, 0, 0, 3, 3, 3], dtype=torch.int32).cuda(),
+                           alive=torch.ones(rows, dtype=torch.int32).cuda()))
+
+    def step(m, s):
+        p, t = next_beams(m.decode(s["tokens"], s["parent"], s["alive"]), s["alive"], beams)
+        s["parent"].copy_(p)
+        s["tokens"].copy_(t)
+
+    for m, s in zip(models, states):
+        step(m, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(models[1], states[1])
+    length = [6, 6, 6, 3, 3, 3]
+    for i in range(12):
+        if i in (4, 7):
+            for s in states:
+                s["alive"][{4: 5, 7: 0}[i]] = 0
+        step(models[0], states[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        for key in states[0]:
+            assert torch.equal(states[0][key], states[1][key]), (i, key)
+        a, b = (m.cache for m in models)
+        for x, y in ((a.pages, b.pages), (a.lens, b.lens), (a.refs, b.refs), (a.k[1], b.k[1]), (a.v[0], b.v[0])):
+            assert torch.equal(x, y), i
+        # those that go on never lose what their group has seen
+        alive = states[0]["alive"].tolist()
+        length = [(n + 1) if z else 0 for n, z in zip([max(length[r - r % beams:r - r % beams + beams]) for r in range(rows)], alive)]
+        assert a.lens.tolist() == length, i

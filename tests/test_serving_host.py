@@ -355,6 +355,24 @@ def test_frequencies():
 
 
 # ---------------------------------------------------------------------------
+# The small decoder's host part.
+
+def test_beams_go_on_from_a_living_row_with_its_tokens():
+    from elementwise_tensor_commands_amd.decode import next_beams
+    logits = torch.full((6, 9), -20.0)
+    logits[0, 4], logits[0, 2], logits[0, 8] = 5.0, 4.0, 3.0
+    logits[1, 1] = 9.0                                             # the highest, of a row that has ended
+    logits[2, 3] = 4.5
+    logits[3, 0], logits[3, 5], logits[3, 7] = -9.0, -8.0, -10.0   # the only one alive of its group
+    logits[4, 1], logits[5, 1] = 7.0, 8.0
+    parent, tokens = next_beams(logits, torch.tensor([1, 0, 1, 1, 0, 0], dtype=I32), 3)
+    assert parent.dtype == I32 and parent.tolist() == [0, 0, 0, 3, 3, 3]
+    assert tokens.dtype == torch.int64 and tokens.tolist() == [4, 2, 8, 5, 0, 7]
+    parent, tokens = next_beams(logits.half(), torch.ones(6, dtype=I32), 1)
+    assert parent.tolist() == list(range(6)) and tokens.tolist() == logits.argmax(-1).tolist()
+
+
+# ---------------------------------------------------------------------------
 # The kernels' own assembly.
 
 @pytest.mark.parametrize("name", ["kernels_rope", "kernels_pages", "kernels_attention_f16", "kernels_attention_bf16",
