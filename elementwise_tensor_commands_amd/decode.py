@@ -10,6 +10,7 @@ HIP graph.  Weights are random: it shows the calls, not a language.
 """
 from __future__ import annotations
 
+import argparse
 import math
 import sys
 
@@ -160,14 +161,31 @@ def next_beams(logits, alive, beams):
     return best.repeat_interleave(beams).to(torch.int32), torch.stack(tokens, 1).flatten()
 
 
+PROMPTS = (37, 120, 5, 64)      # tokens
+
+
+def arguments(argv):
+    """(steps of each half, eager and replayed; beams; table columns, of 16 positions,
+    that hold the longest sequence)."""
+    def positive(text):
+        if int(text) < 1:
+            raise ValueError
+        return int(text)
+
+    ap = argparse.ArgumentParser(prog="decode", description="A small decoder on the serving operators: times of a step.")
+    ap.add_argument("--steps", type=positive, default=64, help="decode steps, half of them replayed from a graph")
+    ap.add_argument("--beams", type=positive, default=4, help="beams of each of %d prompts" % len(PROMPTS))
+    a = ap.parse_args(argv)
+    return (a.steps + 1) // 2, a.beams, max(32, -(-(max(PROMPTS) + 1 + 2 * ((a.steps + 1) // 2)) // 16))
+
+
 def main(argv):
     import torch
-    steps = int(argv[argv.index("--steps") + 1]) if "--steps" in argv else 64
-    beams = int(argv[argv.index("--beams") + 1]) if "--beams" in argv else 4
-    rows = 4 * beams
-    m = Decoder(rows=rows, n=rows * 32, cols=32)
+    half, beams, cols = arguments(argv)
+    rows = len(PROMPTS) * beams
+    m = Decoder(rows=rows, n=rows * (cols + 1), cols=cols)
     g = torch.Generator().manual_seed(1)
-    prompts = [torch.randint(0, m.vocab, (n,), generator=g).tolist() for n in (37, 120, 5, 64)]
+    prompts = [torch.randint(0, m.vocab, (n,), generator=g).tolist() for n in PROMPTS]
     # a prompt fills the first beam of its group; the others fork from it at the first step
     m.prefill([prompts[r // beams] if r % beams == 0 else [] for r in range(rows)])
     alive = torch.ones(rows, dtype=torch.int32, device="cuda")
@@ -190,7 +208,7 @@ def main(argv):
         print("%s: %.1f us a step" % (name, a.elapsed_time(b) / n * 1e3), flush=True)
 
     step()
-    timed("eager", step, steps // 2)
+    timed("eager", step, half)
     alive[rows - 1] = 0                            # one sequence ends
     m.cache.compact()
     print("live pages %d, moved %d" % tuple(m.cache.stats.tolist()), flush=True)
@@ -198,7 +216,7 @@ def main(argv):
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
         step()
-    timed("replayed", graph.replay, steps // 2)
+    timed("replayed", graph.replay, half)
     print("lengths", m.cache.lens.tolist())
     return 0
 

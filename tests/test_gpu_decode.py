@@ -124,3 +124,12 @@ def test_captured_beam_search_step():
         alive = states[0]["alive"].tolist()
         length = [(n + 1) if z else 0 for n, z in zip([max(length[r - r % beams:r - r % beams + beams]) for r in range(rows)], alive)]
         assert a.lens.tolist() == length, i
+
+
+def test_the_command_of_one_step_and_of_many(capsys):
+    """One step is timed; the longest sequence of many grows to its last token."""
+    from elementwise_tensor_commands_amd.decode import PROMPTS, main
+    for steps, half in ((1, 1), (500, 250)):
+        assert main(["--steps", str(steps), "--beams", "2"]) == 0
+        lengths = eval(capsys.readouterr().out.split("lengths", 1)[1])
+        assert lengths == [n + 1 + 2 * half for n in PROMPTS for _ in range(2)][:-1] + [0]

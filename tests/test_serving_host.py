@@ -372,6 +372,20 @@ def test_beams_go_on_from_a_living_row_with_its_tokens():
     assert parent.tolist() == list(range(6)) and tokens.tolist() == logits.argmax(-1).tolist()
 
 
+def test_arguments_of_the_decoder(capsys):
+    from elementwise_tensor_commands_amd.decode import PROMPTS, arguments
+    assert arguments([]) == (32, 4, 32)
+    assert arguments(["--steps", "4", "--beams", "2"]) == (2, 2, 32)
+    for steps in (1, 2, 391, 392, 1000, 4097):
+        half, _, cols = arguments(["--steps", str(steps)])
+        assert half >= 1 and 2 * half >= steps
+        assert max(PROMPTS) + 1 + 2 * half <= 16 * cols              # no sequence outgrows its table
+    for bad in (["--steps"], ["--steps", "0"], ["--beams", "0"], ["--steps", "x"], ["--beams", "-3"], ["5"]):
+        with pytest.raises(SystemExit) as e:
+            arguments(bad)
+        assert e.value.code == 2 and "usage" in capsys.readouterr().err
+
+
 # ---------------------------------------------------------------------------
 # The kernels' own assembly.
 
