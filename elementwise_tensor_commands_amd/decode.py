@@ -119,6 +119,10 @@ class Decoder:
         import torch
         c, device = self.cache, self.embedding.device
         count = [len(p) for p in prompts]
+        room = c.pages.shape[1] * c.page
+        if len(count) > c.rows or max(count, default=0) > room:
+            raise ValueError("%d prompts of up to %d tokens: there is room for %d of %d" % (
+                len(count), max(count, default=0), c.rows, room))
         whole = count + [0] * (c.rows - len(count))
 
         def ints(a):
@@ -127,7 +131,7 @@ class Decoder:
         c.step(ints([-1] * c.rows), ints(whole))
         row = ints([r for r, p in enumerate(prompts) for _ in p])
         pos = ints([i for p in prompts for i in range(len(p))])
-        tokens = torch.tensor([t for p in prompts for t in p], device=device)
+        tokens = torch.tensor([t for p in prompts for t in p], dtype=torch.int64, device=device)
         # a token attends to its own row's pages up to itself
         logits = self.forward(tokens, pos, row, c.pages[row.long()], pos + 1)
         ends, at = [], 0
@@ -135,16 +139,19 @@ class Decoder:
             at += n
             if n:
                 ends.append(at - 1)
-        return logits[torch.tensor(ends, device=device)]
+        return logits[torch.tensor(ends, dtype=torch.int64, device=device)]
 
     def decode(self, tokens, parent, alive):
         """One step of every row: row r goes on from row parent[r] with tokens[r]
-        (int64); rows where alive [rows] (int32) is 0 end.  Returns the logits."""
+        (int64); rows where alive [rows] (int32) is 0 end.  A row whose table is full
+        keeps what it has: its token sees that, and is not written.  Returns the logits."""
         import torch
         c = self.cache
-        c.step(torch.where(alive > 0, parent, -1), alive)
+        parent = torch.where((alive > 0) & (parent < c.rows), parent, -1)
+        pos = torch.where(parent >= 0, c.lens[parent.clamp(min=0).long()], 0)
+        c.step(parent, alive)
         rows = torch.arange(c.rows, dtype=torch.int32, device=tokens.device)
-        return self.forward(tokens, c.lens - 1, torch.where(alive > 0, rows, -1))
+        return self.forward(tokens, pos, torch.where(c.lens > pos, rows, -1))
 
 
 def next_beams(logits, alive, beams):

@@ -133,3 +133,32 @@ def test_the_command_of_one_step_and_of_many(capsys):
         assert main(["--steps", str(steps), "--beams", "2"]) == 0
         lengths = eval(capsys.readouterr().out.split("lengths", 1)[1])
         assert lengths == [n + 1 + 2 * half for n in PROMPTS for _ in range(2)][:-1] + [0]
+
+
+def test_rows_at_the_end_of_their_table():
+    """A full row's next token is not written: not over its newest one, and not over that of a row
+    that shares the page.  Prompts that do not fit are refused."""
+    m = Decoder(layers=2, vocab=101, hq=4, hk=2, d=32, rows=3, n=20, page=4, cols=2, dtype=torch.float32)
+    c = m.cache
+    ones = torch.ones(3, dtype=torch.int32).cuda()
+    step = lambda tokens, parent: m.decode(torch.tensor(tokens).cuda(), torch.tensor(parent, dtype=torch.int32).cuda(), ones)
+    m.prefill([[1, 2, 3, 4, 5, 6], [7, 8], []])
+    step([9, 10, 11], [0, 1, 2])
+    step([12, 13, 14], [0, 1, 2])
+    assert c.lens.tolist() == [8, 4, 2]
+    full = int(c.pages[0, 1])
+    before = [x.clone() for x in c.k + c.v]
+    one = step([15, 16, 17], [0, 0, 1])                            # rows 0 and 1 are full and share both pages
+    assert c.lens.tolist() == [8, 8, 5] and c.pages[1].tolist() == c.pages[0].tolist()
+    for x, y in zip(c.k + c.v, before):
+        assert torch.equal(x[c.pages[0].long()], y[c.pages[0].long()])
+    assert int(c.pages[0, 1]) == full
+    # the token that found no room sees what the row holds, and no further step changes that
+    two = step([15, 16, 18], [0, 0, 2])
+    assert torch.equal(one[:2], two[:2])
+    with pytest.raises(ValueError):
+        m.prefill([[1] * 9])
+    with pytest.raises(ValueError):
+        m.prefill([[1]] * 4)
+    assert m.prefill([[1] * 8, [], [2]]).shape == (2, 101)
+    assert m.prefill([[], []]).shape == (0, 101) and c.lens.tolist() == [0, 0, 0]
