@@ -59,6 +59,11 @@ PyObject *pack_tensors(PyObject *const *args, Py_ssize_t n)
             PyErr_SetString(PyExc_TypeError, "a strided tensor expected");
             return nullptr;
         }
+        if (t.is_neg()) {   // its memory holds the opposite numbers
+            Py_DECREF(out);
+            PyErr_SetString(PyExc_TypeError, "a tensor with the negative bit set (resolve_neg() makes one without)");
+            return nullptr;
+        }
         const int64_t on = t.is_cuda() ? t.get_device() : -1;
         device = device == -2 || device == on ? on : -1;
         a->kind = CMD_ARG_TENSOR;

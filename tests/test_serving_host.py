@@ -75,6 +75,15 @@ def test_rope_refusals_of_options_and_aliases():
         assert "GPU" in _refused("CMD_E_ARG", E.rope, *args)
 
 
+def test_views_with_the_negative_bit_are_refused():
+    """Such a view's memory holds the opposite of its numbers."""
+    freq = torch.complex(torch.ones(4, dtype=torch.float64), torch.ones(4, dtype=torch.float64)).conj().imag
+    assert freq.is_neg()
+    with pytest.raises(TypeError, match="negative bit"):
+        E.rope(*rope_args(freq=freq))
+    assert "GPU" in _refused("CMD_E_ARG", E.rope, *rope_args(freq=freq.resolve_neg()))
+
+
 # ---------------------------------------------------------------------------
 # The append.
 
