@@ -3,6 +3,7 @@
 //
 //   pack(ranks, *tensors) -> (cmd_args, device, stream)
 //   scratch(bytes, device) -> (pointer, owner)
+//   wrote(*tensors)
 //
 // cmd_args holds one structure for each tensor, in order: the tensor of the
 // rank that its byte of `ranks` says; another rank is packed with sizes that the
@@ -11,6 +12,8 @@
 // without one).  Reading four attributes of each tensor from Python takes
 // about 1 us a tensor, as long as the kernels of a small call; this takes 0.1.
 // scratch is an uninitialised tensor of that many bytes on that GPU and its address.
+// wrote advances the tensors' version counters (None: nothing), as torch's own
+// in-place operations do, so that a backward pass that saved one of them notices.
 #include <Python.h>
 
 #include <c10/hip/HIPFunctions.h>
@@ -117,8 +120,28 @@ PyObject *scratch(PyObject *, PyObject *const *args, Py_ssize_t n)
     }
 }
 
+PyObject *wrote(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    try {
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            if (args[i] == Py_None) continue;
+            if (!THPVariable_Check(args[i])) {
+                PyErr_Format(PyExc_TypeError, "a torch.Tensor expected, got %s", Py_TYPE(args[i])->tp_name);
+                return nullptr;
+            }
+            const at::Tensor &t = THPVariable_Unpack(args[i]);
+            if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();   // inference tensors have none
+        }
+        Py_RETURN_NONE;
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 PyMethodDef methods[] = {
     {"scratch", (PyCFunction)(void (*)(void))scratch, METH_FASTCALL, "scratch(bytes, device) -> (pointer, owner)"},
+    {"wrote", (PyCFunction)(void (*)(void))wrote, METH_FASTCALL, "wrote(*tensors): advances their version counters"},
     {"pack", (PyCFunction)(void (*)(void))pack, METH_FASTCALL, "pack(ranks, *tensors) -> (cmd_args, device, stream)"},
     {nullptr, nullptr, 0, nullptr},
 };

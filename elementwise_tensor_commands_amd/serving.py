@@ -7,7 +7,10 @@ or ``stream``, errors are ``Error`` with the library's status and message, and
 nothing is launched after a failed check.  Scratch memory is the caller's
 ``workspace`` (a contiguous GPU tensor of at least the matching
 ``*_workspace`` bytes) or, without one, taken from torch's allocator on the
-launch's stream.
+launch's stream.  The version counters of what was written advance, as after
+torch's in-place operations, so a backward pass does not take a tensor that was
+saved before for what it was; no call records a gradient (``rope`` says how to
+take its own).
 
 A decode step of a model's attention:
 
@@ -122,6 +125,7 @@ def rope(x, pos, freq, out, *, layout="half", mscale=1.0, inverse=False, stream=
         _refuse(lib.cmd_rope(args, _layout(layout), mscale, bool(inverse), CHECK_ONLY, None))
     _check(lib.cmd_rope(args, _layout(layout), mscale, bool(inverse), 0,
                         current if stream is None else _handle(stream, dev)))
+    _binding.wrote(out)
 
 
 def rope_append(q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache, *, layout="half", mscale=1.0, stream=None):
@@ -134,6 +138,7 @@ def rope_append(q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache, *, layo
     if dev < 0:
         _refuse(lib.cmd_rope_append(args, _layout(layout), mscale, CHECK_ONLY, None))
     _check(lib.cmd_rope_append(args, _layout(layout), mscale, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(q_out, k_cache, v_cache)
 
 
 _ATTENTION = b"\3\4\4\2\1\3\2"
@@ -155,6 +160,7 @@ def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=No
     ptr, size, _owner = _scratch(workspace, lib.cmd_paged_attention_workspace(args, window), stream, dev)
     _check(lib.cmd_paged_attention(args, scale, window, ptr, size, 0,
                                    current if stream is None else _handle(stream, dev)))
+    _binding.wrote(out, lse)
 
 
 def paged_attention_workspace(q, k_cache, v_cache, pages, lens, out, *, window=0) -> int:
@@ -181,6 +187,7 @@ def page_assign(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_
         _refuse(lib.cmd_page_assign(args, page, None, 0, CHECK_ONLY, None))
     ptr, size, _owner = _scratch(workspace, lib.cmd_page_assign_workspace(args, page), stream, dev)
     _check(lib.cmd_page_assign(args, page, ptr, size, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(pages_out, lens_out, refs_out, src, dst, stats)
 
 
 def page_assign_workspace(pages, lens, refs, parent, add, page, pages_out, lens_out, refs_out, src, dst, stats) -> int:
@@ -204,6 +211,7 @@ def page_compact(pages, refs, pages_out, refs_out, src, dst, stats, *, workspace
         _refuse(lib.cmd_page_compact(args, None, 0, CHECK_ONLY, None))
     ptr, size, _owner = _scratch(workspace, lib.cmd_page_compact_workspace(args), stream, dev)
     _check(lib.cmd_page_compact(args, ptr, size, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(pages_out, refs_out, src, dst, stats)
 
 
 def page_compact_workspace(pages, refs, pages_out, refs_out, src, dst, stats) -> int:
@@ -223,6 +231,7 @@ def page_copy(pools, src, dst, *, stream=None):
     if dev < 0:
         _refuse(lib.cmd_page_copy(*pairs, CHECK_ONLY, None))
     _check(lib.cmd_page_copy(*pairs, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(*pools)
 
 
 def rope_frequencies(width, *, base=10000.0, factor=1.0, scaling="linear", trained=0, slow=1.0, fast=32.0):

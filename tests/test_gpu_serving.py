@@ -104,6 +104,36 @@ def test_rope_inverse_undoes():
     assert float((z - x).abs().max()) <= 4 * 1.5 * length * 3.01 * 2.0 ** -24
 
 
+def test_a_backward_pass_notices_what_was_written():
+    """A tensor that torch saved for a gradient and that a call wrote afterwards."""
+    pos, freq = torch.arange(3, dtype=I32, device="cuda").view(1, 3), E.rope_frequencies(8).cuda()
+    x = torch.ones(1, 3, 2, 8, device="cuda")
+    w = torch.ones_like(x, requires_grad=True)
+    y = (x * w).sum()
+    E.rope(x, pos, freq, torch.empty_like(x))                       # only read: as before
+    y.backward()
+    y = (x * w).sum()
+    E.rope(x, pos, freq, x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    # every output of every operator
+    args, out = step_state()
+    lse = torch.empty(out.shape[:2], device="cuda")
+    qkv, kc, vc = torch.ones(2, 6, 8, device="cuda"), torch.zeros(4, 2, 2, 8, device="cuda"), torch.zeros(4, 2, 2, 8, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=I32, device="cuda")
+    tables = [i(2, 2), i(2), i(4), i(2), i(2)], [i(2, 2), i(2), i(4), i(2), i(2), i(2)]
+    compact = [i(2, 2), i(4)], [i(2, 2), i(4), i(2), i(2), i(2)]
+    q_out = torch.empty(2, 2, 8, device="cuda")
+    for call, ins, outs in (
+            (lambda: E.paged_attention(*args, out, lse=lse), args, [out, lse]),
+            (lambda: E.rope_append(qkv[:, :2], qkv[:, 2:4], qkv[:, 4:], i(2), i(2), i(1, 2), freq, q_out, kc, vc), [qkv], [q_out, kc, vc]),
+            (lambda: E.page_assign(*tables[0], 2, *tables[1]), *tables), (lambda: E.page_compact(*compact[0], *compact[1]), *compact),
+            (lambda: E.page_copy([kc, vc], i(1), i(1) + 1), [], [kc, vc])):
+        versions = [t._version for t in [*ins, *outs]]
+        call()
+        assert [t._version for t in [*ins, *outs]] == versions[:len(ins)] + [n + 1 for n in versions[len(ins):]]
+
+
 # ---------------------------------------------------------------------------
 # The append.
 
@@ -586,7 +616,7 @@ def test_default_stream_by_its_handle(monkeypatch):
         return binding.scratch(size, device)
 
     binding = S._binding
-    monkeypatch.setattr(S, "_binding", types.SimpleNamespace(pack=binding.pack, scratch=scratch))
+    monkeypatch.setattr(S, "_binding", types.SimpleNamespace(**{**vars(binding), "scratch": scratch}))
     rng, pages, lens, refs = tables(3, 300, 7, 8, 5000, 1000)
     new = lambda *s: torch.full(s, 77, dtype=I32, device="cuda")
     ins = [pages.cuda(), ints(lens).cuda(), ints(refs).cuda(), torch.arange(300, dtype=I32).cuda(), torch.ones(300, dtype=I32).cuda()]

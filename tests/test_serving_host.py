@@ -84,6 +84,23 @@ def test_views_with_the_negative_bit_are_refused():
     assert "GPU" in _refused("CMD_E_ARG", E.rope, *rope_args(freq=freq.resolve_neg()))
 
 
+def test_version_counters():
+    """Advanced for what a call wrote, shared with views; not by a refused call, not of inference tensors."""
+    from elementwise_tensor_commands_amd import serving as S
+    args = rope_args()
+    before = [t._version for t in args]
+    _refused("CMD_E_ARG", E.rope, *args)
+    assert [t._version for t in args] == before
+    with torch.inference_mode():
+        none = torch.zeros(3)
+    x = torch.zeros(4, 4)
+    view = x[1:]
+    S._binding.wrote(view, None, none, args[0])
+    assert x._version == view._version == 1 and args[0]._version == before[0] + 1
+    with pytest.raises(TypeError):
+        S._binding.wrote(3)
+
+
 # ---------------------------------------------------------------------------
 # The append.
 
