@@ -1,5 +1,5 @@
-"""Build libecmd.so (the C ABI and its gfx950 kernels) and _binding.so (the
-compiled part of the Python binding) in-tree.
+"""Build libecmd.so (the C ABI and its gfx950 kernels) and, where torch is
+installed, _binding.so (the compiled part of the Python binding) in-tree.
 
     python elementwise_tensor_commands_amd/build.py [-v]
 
@@ -114,10 +114,14 @@ def _run_all(cmds):
 
 def binding_command(out: str):
     """The command that builds the Python extension module _binding: host code
-    against torch's and Python's headers, with the host compiler."""
+    against torch's and Python's headers, with the host compiler.  None where there
+    is no torch: the C library does without."""
     import importlib.util
     import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
     inc = [sysconfig.get_paths()["include"], os.path.join(torch, "include"),
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(rocm, "include")]
@@ -145,7 +149,11 @@ def build(asm: bool = True, verbose: bool = False) -> str:
             cmds.append([HIPCC, *FLAGS, *extra, "-x", "hip", "--offload-device-only", "-S",
                          os.path.join(CSRC, src), "-o", os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".s")])
     tmp_binding = BINDING + ".tmp%d" % os.getpid()
-    cmds.append(binding_command(tmp_binding))
+    binding = binding_command(tmp_binding)
+    if binding:
+        cmds.append(binding)
+    else:
+        sys.stderr.write("no torch: the library is built without the Python binding of the serving operators\n")
     if verbose:
         for c in cmds:
             print(" ".join(c))
@@ -155,7 +163,8 @@ def build(asm: bool = True, verbose: bool = False) -> str:
     _run_all([[HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs,
                "-L" + rocm_lib, "-lhiprtc", "-Wl,-rpath," + rocm_lib]])
     os.replace(tmp, LIB)
-    os.replace(tmp_binding, BINDING)
+    if binding:
+        os.replace(tmp_binding, BINDING)
     return LIB
 
 

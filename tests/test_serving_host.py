@@ -413,6 +413,36 @@ def test_arguments_of_the_decoder(capsys):
 
 
 # ---------------------------------------------------------------------------
+# The build.
+
+def build_module():
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("ecmd_build", os.path.join(ROOT, "elementwise_tensor_commands_amd", "build.py"))
+    B = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(B)
+    return B
+
+
+@pytest.mark.parametrize("with_torch", [True, False])
+def test_the_library_is_built_without_torch_too(monkeypatch, tmp_path, with_torch):
+    """Only the Python binding needs torch's headers; the C library does not."""
+    import importlib.util
+    B = build_module()
+    ran, moved = [], []
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" and not with_torch else find(name, *a))
+    monkeypatch.setattr(B, "BUILD", str(tmp_path))
+    monkeypatch.setattr(B, "PKG", str(tmp_path))
+    monkeypatch.setattr(B, "_run_all", ran.extend)
+    monkeypatch.setattr(B.os, "replace", lambda a, b: moved.append(b))
+    assert B.build(asm=False) == B.LIB
+    sources = [os.path.basename(x) for c in ran for x in c if x.endswith((".cpp", ".hip"))]
+    assert all(os.path.basename(s) in sources for s in B.SOURCES)
+    assert ("ecmd_binding.cpp" in sources) == with_torch
+    assert moved == [B.LIB] + [B.BINDING] * with_torch
+
+
+# ---------------------------------------------------------------------------
 # The kernels' own assembly.
 
 @pytest.mark.parametrize("name", ["kernels_rope", "kernels_pages", "kernels_attention_f16", "kernels_attention_bf16",
