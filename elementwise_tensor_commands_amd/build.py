@@ -1,5 +1,6 @@
 """Build libecmd.so (the C ABI and its gfx950 kernels) and, where torch is
-installed, _binding.so (the compiled part of the Python binding) in-tree.
+installed, _binding.*.so (the compiled part of the Python binding, for the
+interpreter that runs this) in-tree.
 
     python elementwise_tensor_commands_amd/build.py [-v]
 
@@ -25,13 +26,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libecmd.so")
-BINDING = os.path.join(PKG, "_binding.so")
+# with the interpreter's tag: another one, whose objects may differ, does not load it
+BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["ecmd_host.cpp", "ecmd_serial.cpp", "ecmd_jit.cpp", "kernels_linear.hip", "kernels_interp.hip",
            "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip", "serving/ecmd_serving.cpp",
@@ -117,7 +120,6 @@ def binding_command(out: str):
     against torch's and Python's headers, with the host compiler.  None where there
     is no torch: the C library does without."""
     import importlib.util
-    import sysconfig
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
@@ -165,6 +167,9 @@ def build(asm: bool = True, verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     if binding:
         os.replace(tmp_binding, BINDING)
+        untagged = os.path.join(PKG, "_binding.so")   # of earlier builds: any interpreter would load it
+        if untagged != BINDING and os.path.exists(untagged):
+            os.remove(untagged)
     return LIB
 
 

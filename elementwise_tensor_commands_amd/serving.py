@@ -56,8 +56,11 @@ def _pack(ranks: bytes, *tensors):
     global _binding
     if _binding is None:
         import torch  # noqa: F401  (first: the module links against its libraries)
-
-        from . import _binding as module
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError("the binding of the serving operators is not built for this interpreter and torch (%s); "
+                              "build it with `python elementwise_tensor_commands_amd/build.py`" % e) from e
         _binding = module
     return _binding.pack(ranks, *tensors)
 

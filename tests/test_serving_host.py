@@ -442,6 +442,22 @@ def test_the_library_is_built_without_torch_too(monkeypatch, tmp_path, with_torc
     assert moved == [B.LIB] + [B.BINDING] * with_torch
 
 
+def test_the_binding_is_this_interpreter_s():
+    """Its name has the interpreter's tag, so no other one loads it; without it the error says what to do."""
+    import subprocess
+    import sys
+    import sysconfig
+    B = build_module()
+    assert os.path.basename(B.BINDING) == "_binding" + sysconfig.get_config_var("EXT_SUFFIX")
+    assert os.path.exists(B.BINDING) and not os.path.exists(os.path.join(B.PKG, "_binding.so"))
+    code = ("import sys; sys.modules['elementwise_tensor_commands_amd._binding'] = None\n"
+            "import torch, elementwise_tensor_commands_amd as E\n"
+            "try:\n    E.page_copy([], torch.zeros(1), torch.zeros(1))\n"
+            "except ImportError as e:\n    print('said:', e)")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=200)
+    assert "said:" in r.stdout and "build.py" in r.stdout and "torch" in r.stdout, r.stdout + r.stderr
+
+
 # ---------------------------------------------------------------------------
 # The kernels' own assembly.
 
