@@ -572,12 +572,13 @@ int cmd_paged_attention(const cmd_arg args[7], float scale, int32_t window, void
     TRY(check_flags(flags));
     AttnPlan P;
     TRY(plan_attention(args, window, P));
-    if (!std::isfinite(scale)) return refuse(CMD_E_ARG, "scale is not finite");
+    const float scale_log2 = (float)((double)scale * 1.44269504088896340736);
+    if (!std::isfinite(scale_log2)) return refuse(CMD_E_ARG, "scale is not finite, or too large for binary32 in base 2");
     if (flags & CMD_CHECK_ONLY) return CMD_OK;
     if (P.nothing) return CMD_OK;
     TRY(check_workspace(workspace, workspace_bytes, P.workspace));
     AttnArgs &A = P.A;
-    A.scale_log2 = (float)((double)scale * 1.44269504088896340736);
+    A.scale_log2 = scale_log2;
     if (!A.direct) {
         A.ml = (float *)workspace;
         A.acc = A.ml + ((((uint64_t)A.runs_most + A.b) * A.hq * 2 + 3) & ~uint64_t(3));

@@ -199,6 +199,14 @@ def test_attention_refusals_of_options():
     assert "GPU" in _refused("CMD_E_ARG", E.paged_attention, *attention_args(), lse=torch.zeros(3, 4))
 
 
+def test_attention_scale_in_base_2():
+    """Scores are taken to base 2 in binary32: a scale that has no number there would make 0 * inf of a score of 0."""
+    for scale in (3.0e38, -2.4e38, math.inf, 1e300):
+        assert "scale" in _refused("CMD_E_ARG", E.paged_attention, *attention_args(), scale=scale)
+    for scale in (2.3e38, -1e30, 0.0, 1e-45):
+        assert "GPU" in _refused("CMD_E_ARG", E.paged_attention, *attention_args(), scale=scale)
+
+
 def test_attention_workspace():
     assert E.paged_attention_workspace(*attention_args(pages=i32(3, 1))) == 0           # too few keys to cut
     a = attention_args(pages=i32(3, 4096))
