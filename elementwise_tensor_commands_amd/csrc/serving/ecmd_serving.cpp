@@ -316,7 +316,6 @@ int cmd_rope(const cmd_arg args[4], int32_t layout, double mscale, int32_t inver
     for (int i = 0; i < 2; ++i) A.ps[i] = t[1].stride(i);
     A.fs = t[2].stride(0);
     A.tokens = (uint32_t)(b * n);
-    A.heads = (uint32_t)h;
     A.items = (uint32_t)items;
     A.tb = tokens_per_group(A.tokens, items, m);
     A.mscale = mscale;

@@ -41,7 +41,7 @@ struct RopeArgs {
     int64_t xs[3], os[3];            // element strides of batch, token, head
     int64_t ps[2], fs;               // of pos (batch, token) and freq
     uint32_t tokens, pairs, width;   // b * t, m, d
-    uint32_t heads, tb;              // heads; tokens per work-group
+    uint32_t tb;                     // tokens per work-group
     double mscale;
     int32_t inverse;
     Div31 by_t;                    // token index -> batch
@@ -132,7 +132,7 @@ struct PageBits {
 };
 
 // What one work-group does alone, in one launch and without a workspace.
-constexpr uint32_t kSmallPages = 4096, kSmallRows = 1024, kSmallEntries = 2048;
+constexpr uint32_t kSmallPages = 4096, kSmallRows = 1024, kSmallEntries = 3200;
 
 struct AssignArgs {
     const int32_t *pages, *lens, *refs, *parent, *add;

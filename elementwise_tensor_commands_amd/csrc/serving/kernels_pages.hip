@@ -8,7 +8,7 @@
 // population count, a selection two binary searches and one within a word.
 // What is left is integer reads and writes of the tables, a few microseconds of
 // dependent accesses and launches at any size met in practice, so the number of
-// launches is kept small: two to assign, three to compact.
+// launches is kept small: two to assign and two to compact, one where little is to do.
 //
 // Only integer atomics (reference counts) are used: results do not depend on
 // their order.
@@ -352,13 +352,13 @@ __global__ __launch_bounds__(kBlock) void k_compact(const CompactArgs A, uint32_
 }
 
 // ---------------------------------------------------------------------------
-// Small problems in one launch: one work-group, bits and counts in LDS.  On the
-// stream that is no faster (2000 pages, 32 rows of 64 entries: assigning 9.4 us
-// against 7.4 in two launches, compacting 7.4 against 6.3), but a caller's time is
-// mostly launches, 2.5 us each, and the workspace, 1.5 us: page_assign and
-// page_copy together 11.9 us a step against 15.7.  With four times the entries one
-// compute unit takes twice the two launches' time (16.7 us against 7.7), so the
-// limit is two entries to a work-item.
+// Small problems in one launch: one work-group, bits and counts in LDS.  Its time
+// grows with the entries and, less, the pages; two launches and their workspace are
+// the caller's 9.8 us to assign and 9.2 to compact at every such size.  Measured, a
+// call among others, 1000 pages and 4096: 2560 entries 8.0 and 8.3 us to assign, 6.4
+// and 8.1 to compact; 3200 entries 8.0 and 8.7, 7.9 and 9.2; 4096 entries 9.1 and
+// 10.4, 8.7 and 10.5; 12800 entries 18.5 and 20.4, 22.3 and 23.5.  So the limit is
+// 3200 entries, where neither is slower.
 
 constexpr uint32_t kSmallBlock = kSmallRows, kSmallWords = kSmallPages / 64;
 

@@ -692,3 +692,27 @@ def test_attention_more_rows_than_prefixes():
     b = 2100
     lens = [(i * 37) % 90 for i in range(b)]
     check_attention(*attention_case(1, torch.bfloat16, b, 2, 1, 32, 32, 16, lens), what=b)
+
+
+@pytest.mark.parametrize("entries", [3200, 3201])
+def test_pages_at_the_limit_of_one_launch(entries):
+    """The largest tables of one launch and the smallest of two, with the most pages of one."""
+    for rows, cols, n in ((64, 50, 4096), (1, 3200, 4095), (800, 4, 4096)) if entries == 3200 else (
+            (33, 97, 4096), (1, 3201, 4095), (1067, 3, 4096)):
+        rng, pages, lens, refs = tables(entries + rows, rows, cols, 4, n, n // 3)
+        parent = [rng.choice([r, rng.randrange(rows), -1]) for r in range(rows)]
+        add = [rng.choice([0, 1, 5, cols * 4]) for _ in range(rows)]
+        want = O.assign(pages.tolist(), lens, refs, parent, add, 4)
+        new = lambda *s: torch.full(s, 77, dtype=I32, device="cuda")
+        outs = [new(rows, cols), new(rows), new(n), new(rows), new(rows), new(2)]
+        ins = [pages.cuda(), ints(lens).cuda(), ints(refs).cuda(), ints(parent).cuda(), ints(add).cuda()]
+        assert (E.page_assign_workspace(*ins, 4, *outs) == 0) == (rows * cols <= 3200)
+        E.page_assign(*ins, 4, *outs)
+        for got, w in zip(outs, want):
+            assert got.cpu().tolist() == w
+        want = O.compact(pages.tolist(), refs, n // 2)
+        outs = [new(rows, cols), new(n), new(n // 2), new(n // 2), new(2)]
+        assert (E.page_compact_workspace(ins[0], ins[2], *outs) == 0) == (rows * cols <= 3200)
+        E.page_compact(ins[0], ins[2], *outs)
+        for got, w in zip(outs, want):
+            assert got.cpu().tolist() == w
