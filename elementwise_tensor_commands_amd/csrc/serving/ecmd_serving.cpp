@@ -228,6 +228,9 @@ int check_workspace(void *ws, int64_t given, int64_t need)
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
 
+// Work-groups of 256 in one launch: a grid's work-items are a 32-bit count.
+constexpr uint64_t kMaxGroups = (uint64_t(1) << 24) - 1;
+
 int check_layout(int32_t layout, double mscale)
 {
     if (layout != CMD_ROPE_HALF && layout != CMD_ROPE_INTERLEAVED)
@@ -262,13 +265,14 @@ int head_edge(int type, int layout, uint32_t pairs, uint32_t width)
 
 // Tokens of a work-group: about 1024 items (the four that each work-item loads at
 // once), while there remain enough groups for 256 compute units four times over
-// and the cosines stay within 16 KiB of LDS.
+// and the cosines stay within 16 KiB of LDS.  More where a launch cannot have so many
+// groups: the 288 GB of tokens that fill the memory then still take less than 64 KiB.
 uint32_t tokens_per_group(uint64_t tokens, uint64_t items, uint64_t pairs)
 {
     uint64_t tb = std::max<uint64_t>(1, 1024 / std::max<uint64_t>(1, items));
     tb = std::min(tb, std::max<uint64_t>(1, tokens / 1024));
     tb = std::min(tb, std::max<uint64_t>(1, 16384 / (8 * ((pairs + 7) / 8 * 8) + 16)));
-    return (uint32_t)tb;
+    return (uint32_t)std::max<uint64_t>(tb, ceil_div(tokens, kMaxGroups));
 }
 
 uint32_t turn_lds(uint32_t tb, uint32_t pairs) { return tb * ((pairs + 7) / 8 * 8) * 8; }
@@ -506,8 +510,8 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     A.window = (uint32_t)window;
     A.by_page = Div31(A.page);
     const uint64_t heads = (uint64_t)A.hk * A.head_tiles;
-    if ((uint64_t)(b + 8) * heads > (uint64_t)kMaxCount / 8 || (uint64_t)b * hq > (uint64_t)kMaxCount)
-        return refuse(CMD_E_LIMIT, "too many sequences times heads");
+    if ((uint64_t)(b + 8) * heads > kMaxGroups || (uint64_t)b * hq > (uint64_t)kMaxCount)
+        return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
     uint64_t keys = (uint64_t)A.cols * A.page;
     if (window) keys = std::min<uint64_t>(keys, (uint64_t)window);
     const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep, most = std::max<uint64_t>(1, steps * (uint64_t)b);
@@ -550,6 +554,8 @@ int plan_attention(const cmd_arg *args, int32_t window, AttnPlan &P)
     // to 32 columns.
     const uint64_t segments = std::min<uint64_t>(A.runs_most, steps);   // of a row, at most
     A.join = segments <= 16 ? 0 : (uint64_t)b * hq * ((dv + 31) / 32) <= 512 ? 2 : A.runs_most > 12 * (uint64_t)b ? 1 : 0;
+    // (work-groups of 1024 join only what is little)
+    if (!A.direct && (uint64_t)b * hq > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
     if (!A.direct) P.workspace = (int64_t)(((uint64_t)A.runs_most + b) * hq * (dv + 2) * 4 + 16);
     return CMD_OK;
 }
@@ -644,6 +650,7 @@ int plan_assign(const cmd_arg *args, int32_t page, AssignPlan &P)
     if (page < 1) return refuse(CMD_E_ARG, "pages of %d slots", page);
     if ((cols + 1) * (int64_t)page > kMaxCount) return refuse(CMD_E_LIMIT, "the table holds more than 2^31 positions");
     if (rows * cols > kMaxCount) return refuse(CMD_E_LIMIT, "the table has more than 2^31 - 1 entries");
+    if (rows > (int64_t)kMaxGroups) return refuse(CMD_E_LIMIT, "the table has too many rows for one launch");
     static const int share[11] = {-1, -1, -1, -1, -1, -1, -1, 2, -1, -1, -1};
     TRY(check_outputs(t, 11, 5, share));
     AssignArgs &A = P.A;
@@ -701,6 +708,8 @@ int plan_compact(const cmd_arg *args, CompactPlan &P)
     TRY(check_size(t[5], 0, t[4].size(0), "src"));
     TRY(check_size(t[6], 0, 2, "the two counts"));
     if (rows * cols > kMaxCount) return refuse(CMD_E_LIMIT, "the table has more than 2^31 - 1 entries");
+    if ((uint64_t)ceil_div(rows * cols, 256) + ceil_div(std::max(n, t[4].size(0)), 256) > kMaxGroups)
+        return refuse(CMD_E_LIMIT, "too many pages and entries for one launch");
     static const int share[7] = {-1, -1, 0, -1, -1, -1, -1};
     TRY(check_outputs(t, 7, 2, share));
     CompactArgs &A = P.A;
@@ -828,7 +837,7 @@ int cmd_page_copy(const cmd_arg *pools, int32_t npools, const cmd_arg *src, cons
             A.by_pieces = Div31(A.pieces);
             A.by_vecs = Div31(vecs);
             const uint64_t grid = A.per_group > 1 ? ceil_div(A.count, A.per_group) : (uint64_t)A.count * A.pieces;
-            if (grid > (uint64_t)kMaxCount) return refuse(CMD_E_LIMIT, "too many pairs for pages of this size");
+            if (grid > kMaxGroups) return refuse(CMD_E_LIMIT, "too many pairs for pages of this size");
             const int n = held;
             held = 0;
             const bool past = (uint64_t)count * n * 2 * vecs * width > kPastCaches;

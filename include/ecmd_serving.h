@@ -10,8 +10,9 @@
  *   - every status except CMD_E_LAUNCH is returned before any HIP call, and no
  *     GPU work is submitted after a failed check; calls are asynchronous;
  *   - strides are >= 0; an input may have stride 0 (broadcast); an output must
- *     be one-to-one; an output overlaps no other argument unless the call says
- *     so (then: the identical view);
+ *     be one-to-one, each of its dimensions, by ascending stride, stepping past
+ *     the smaller ones; an output overlaps no other argument unless the call
+ *     says so (then: the identical view);
  *   - the elements of a head (the last dimension of x, q, k, v, the caches and
  *     their outputs, where it has more than one) are neighbours: stride 1, else
  *     CMD_E_STRIDE.  Every other dimension, and all of the tables, lse and the
@@ -20,6 +21,9 @@
  *     take a workspace (16-byte aligned, apart from every argument; its contents
  *     need no preparation and mean nothing afterwards), sized by the matching
  *     *_workspace call;
+ *   - what one launch cannot hold is refused with CMD_E_LIMIT: 2^24 work-groups, of
+ *     a row and 16 query heads in attention, of a row in cmd_page_assign, of 256
+ *     entries and ids in cmd_page_compact, of 16 KiB of a page in cmd_page_copy;
  *   - cmd_last_error(NULL) describes the last failure on this thread.
  *
  * What the data say -- positions, row numbers, page ids, lengths, reference
@@ -129,7 +133,9 @@ int64_t cmd_page_compact_workspace(const cmd_arg args[7]);
 /* Copy page src[i] to page dst[i] in each of npools pools [N_k, page, heads, d] (rank 4,
  * any dtype of 2 or 4 bytes; each pool its own sizes), i = 0 .. C - 1.  Pairs with
  * either id outside a pool are skipped there.  No dst may appear twice or as
- * a src.  A page's elements lie one-to-one, in any order of strides. */
+ * a src.  A page's elements lie one-to-one, in any order of strides, as rows of
+ * neighbours at one distance, as a slice of one of a dense page's dimensions
+ * has them; else CMD_E_STRIDE. */
 int cmd_page_copy(const cmd_arg *pools, int32_t npools, const cmd_arg *src, const cmd_arg *dst, int32_t flags,
                   void *hip_stream);
 

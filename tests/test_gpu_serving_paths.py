@@ -258,6 +258,24 @@ def test_rope_past_the_caches(dtype, layout):
         assert same, (b, t, h, d, m)
 
 
+def test_rope_of_more_tokens_than_a_launch_has_groups():
+    """138 GB turned in place, where a token alone would fill a work-group: two to a group then."""
+    tokens, d, m = (1 << 24) + 5, 4104, 2048
+    x = torch.empty(1, tokens, 1, d, dtype=torch.float16, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    at = torch.cat([torch.randint(0, tokens, (200,), generator=g), torch.tensor([0, 1, tokens // 2, tokens - 2, tokens - 1])]).unique().cuda()
+    here = torch.randn(1, len(at), 1, d, generator=g).half().cuda()
+    x[:, at] = here
+    pos = torch.arange(tokens, dtype=I32, device="cuda").view(1, tokens)
+    freq = E.rope_frequencies(2 * m).cuda()
+    E.rope(x, pos, freq, x)
+    want, bound = O.rope(here, pos[:, at], freq, "half")
+    got = x[:, at].clone()
+    del x, pos
+    torch.cuda.empty_cache()
+    within(got, want, bound)
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_append_past_the_caches(dtype, layout):

@@ -318,6 +318,69 @@ def test_copy_refusals():
 
 
 # ---------------------------------------------------------------------------
+# What one launch holds: 2^24 - 1 work-groups.
+
+def made_up(dtype, shape, at, strides=None):
+    """A cmd_arg of a tensor that nothing reads: dense unless strides are given, `at` TB in."""
+    a = E.cmd_arg()
+    a.kind, a.dtype, a.ptr = 1, {"f16": 1, "f32": 2, "i32": 3, "bf16": 4, "f64": 5}[dtype], at << 40
+    step = 1
+    for i in reversed(range(len(shape))):
+        a.size[i], a.stride[i] = shape[i], step if strides is None else strides[i]
+        step *= max(1, shape[i])
+    return a
+
+
+def check_only(fn, args, *rest):
+    return getattr(E.lib, fn)(b"".join(bytes(a) for a in args), *rest, 1, None)
+
+
+def test_calls_larger_than_a_launch():
+    """Refused before any HIP call, as the header says, where no launch could hold them."""
+    from elementwise_tensor_commands_amd import serving as S  # noqa: F401  (argument types)
+    limit = -next(k for k in range(1, 40) if E.Error(-k, "").name == "CMD_E_LIMIT")
+
+    def attend(b, hk, group, cols):
+        q = made_up("f16", (b, hk * group, 8), 1)
+        cache = [made_up("f16", (4, 16, hk, 8), 2 + i) for i in range(2)]
+        none = E.cmd_arg()
+        return check_only("cmd_paged_attention", [q, *cache, made_up("i32", (b, cols), 4, (0, 0)), made_up("i32", (b,), 5),
+                                                  made_up("f16", (b, hk * group, 8), 6), none], 1.0, 0, None, 0)
+
+    assert attend(131000, 128, 1, 8) == 0
+    assert attend(131072, 128, 1, 8) == limit
+    assert attend(2048, 16, 500, 4096) == 0
+    assert attend(2048, 16, 520, 4096) == limit                    # the second launch
+
+    def assign(rows):
+        i = lambda at, *shape: made_up("i32", shape, at)
+        return check_only("cmd_page_assign", [i(1, rows, 2), i(2, rows), i(3, 9), i(4, rows), i(5, rows), i(6, rows, 2), i(7, rows),
+                                              i(8, 9), i(9, rows), i(10, rows), i(11, 2)], 4, None, 0)
+
+    assert assign((1 << 24) - 1) == 0
+    assert assign(1 << 24) == limit
+
+    def compact(rows, n):
+        i = lambda at, *shape: made_up("i32", shape, at)
+        return check_only("cmd_page_compact", [i(1, rows, 1), i(2, n), i(3, rows, 1), i(4, n), i(5, n // 2), i(6, n // 2), i(7, 2)], None, 0)
+
+    assert compact((1 << 31) - 1024, (1 << 31) - 1024) == 0
+    assert compact((1 << 31) - 1, (1 << 31) - 1) == limit
+
+    def copy(pairs):
+        src, dst, pool = made_up("i32", (pairs,), 1), made_up("i32", (pairs,), 2), made_up("f16", (9, 16, 8, 128), 3)
+        return E.lib.cmd_page_copy(bytes(pool), 1, bytes(src), bytes(dst), 1, None)
+
+    assert copy((1 << 23) - 1) == 0
+    assert copy(1 << 23) == limit
+
+    # rope and the append give their groups more tokens instead
+    for tokens in ((1 << 24) - 1, 1 << 24, (1 << 31) - 1):
+        x = made_up("f16", (1, tokens, 1, 4104), 3)
+        assert check_only("cmd_rope", [x, made_up("i32", (1, tokens), 1, (0, 0)), made_up("f64", (2048,), 2), x], 0, 1.0, 0) == 0
+
+
+# ---------------------------------------------------------------------------
 # The oracle and the tables of frequencies.
 
 def test_oracle_by_hand():
@@ -492,3 +555,13 @@ def test_own_assembly(name):
     if "attention" in name:
         kind = {"f16": "16x16x32_f16", "bf16": "16x16x32_bf16", "f32": "16x16x4_f32"}[name.rsplit("_", 1)[1]]
         assert text.count("v_mfma_f32_" + kind) > 100
+
+
+def test_copy_of_sliced_pages():
+    """Slices of one dimension of a dense page, keys beside values among them, are taken; of two, refused."""
+    s, d = i32(3), i32(3)
+    dense = torch.zeros(5, 16, 4, 64)
+    for pool in (dense[:, 2:9], dense[:, :, 1:3], dense[..., :40], dense[..., 5:6], dense.transpose(1, 2)[:, 1:3], dense[::2],
+                 torch.zeros(5, 16, 2, 4, 64)[:, :, 1], torch.zeros(5, 16, 4, 2, 64)[:, :, :, 0], torch.zeros(5, 2, 16, 4, 64)[:, 1]):
+        assert "GPU" in _refused("CMD_E_ARG", E.page_copy, [pool], s, d)
+    _refused("CMD_E_STRIDE", E.page_copy, [dense[:, :, 1:3, :40]], s, d)
