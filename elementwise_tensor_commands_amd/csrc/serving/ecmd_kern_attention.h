@@ -41,9 +41,10 @@
 //
 // Measured on one MI355X (a stream of independent reads reaches 6.2 TB/s there, a
 // copy 4.9): 64 rows of up to 8192 positions, 8 kv heads of 128, bfloat16, 987 MB:
-// 166 us, 5.9 TB/s, the join 6.5 us; two rows of up to 262143, 289 MB: 50 and 5.7
-// us.  One row of 777: 7.2 and 4.6 us, all of it the chain of dependent loads
-// (length, page, key) and of barriers.  Tried and dropped: as many splits for every
+// 168 us, 5.9 TB/s, the join 6.5 us; two rows of up to 262143, binary16, 289 MB: 52
+// and 5.7 us.  One row of 777: 7.4 and 4.7 us, nearly all of it the chain of dependent
+// loads (length, page, key) and of barriers; 0.3 us are the weights' further parts
+// and the bounding of their sums, which larger calls do not show.  Tried and dropped: as many splits for every
 // row (205 us on the first; equal runs 199), half of the registers as accumulation
 // registers, which the compiler prefers (32 moves there and back in every tile),
 // eight waves to a work-group (a compute unit alone reads no more than 55 to 70

@@ -9,11 +9,16 @@
 // streams the heads past them in 16-byte vectors, four to a work-item at once.
 //
 // Measured on one MI355X: 4 x 4096 tokens of 40 heads of 128, bfloat16, 336 MB: 60
-// us, 5.6 TB/s (one vector at a time 71, four 66, past the caches 60).  The append
-// of 16 ragged prompts, 36 + 4 heads, binary16, 212 MB: 45 us, 4.7 TB/s, its writes
-// scattered over pages (65 with one vector at a time; 52 with four).  One token of
-// each of 64 sequences: 4.3 us, of which the angles' chain of binary64 operations
-// overlaps the loads.
+// us, 5.6 TB/s (one vector at a time 71, four 66, past the caches 60); twice that, in
+// pairs of neighbours, 107 us, 6.3 TB/s.  The append of 16 ragged prompts, 36 + 4
+// heads, binary16, half of each head turned in pairs of neighbours, 212 MB: 45 us, 4.7
+// TB/s (65 with one vector at a time; 52 with four), no faster with the pages in
+// order: a token's 624 vectors leave a work-group of one token 384 of its 1024 loads
+// unused.  Whole heads turned by halves, two vectors an item, take 46 us for 235 MB, 5.2
+// TB/s.  One token of each of 64 sequences: 4.3 us, of which the angles' chain of
+// binary64 operations overlaps the loads.  Heads of odd width, whose vectors are off
+// 16 bytes and overlap at the ends: 10000 tokens of 20 heads of 101, 100 turned,
+// bfloat16, 81 MB: by halves 24 us, in neighbours 20; heads of 104 20 and 17.
 #include <hip/hip_runtime.h>
 
 #include "../ecmd_launch.h"
