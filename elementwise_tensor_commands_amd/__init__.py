@@ -467,5 +467,7 @@ def empty_staggered(specs, device="cuda", step=4096):
 
 
 # The serving operators (include/ecmd_serving.h) under this package's name.
-from .serving import (page_assign, page_assign_workspace, page_compact, page_compact_workspace,  # noqa: E402
-                      page_copy, paged_attention, paged_attention_workspace, rope, rope_append, rope_frequencies)
+from .serving import (page_assign, page_assign_workspace, page_bounds, page_compact, page_compact_workspace,  # noqa: E402
+                      page_copy, page_evict, page_mass, page_select, page_select_workspace, paged_attention,
+                      paged_attention_workspace, rope, rope_append, rope_frequencies, slot_move, tree_accept,
+                      tree_attention, tree_attention_workspace)

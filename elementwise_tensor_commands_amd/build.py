@@ -39,7 +39,10 @@ BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX")
 SOURCES = ["ecmd_host.cpp", "ecmd_serial.cpp", "ecmd_jit.cpp", "kernels_linear.hip", "kernels_interp.hip",
            "kernels_tiled.hip", "kernels_rows.hip", "kernels_gather.hip", "serving/ecmd_serving.cpp",
            "serving/kernels_rope.hip", "serving/kernels_attention_f16.hip", "serving/kernels_attention_bf16.hip",
-           "serving/kernels_attention_f32.hip", "serving/kernels_pages.hip"]
+           "serving/kernels_attention_f32.hip", "serving/kernels_pages.hip", "serving/ecmd_serving_cache.cpp",
+           "serving/kernels_tree_f16.hip", "serving/kernels_tree_bf16.hip", "serving/kernels_tree_f32.hip",
+           "serving/kernels_tree_join.hip", "serving/kernels_accept.hip", "serving/kernels_select.hip",
+           "serving/kernels_mass_f16.hip", "serving/kernels_mass_bf16.hip", "serving/kernels_mass_f32.hip"]
 # Device headers the run-time compiler needs: embedded into the library as text.
 JIT_HEADERS = ["ecmd_tape.h", "ecmd_eval.h", "ecmd_kern_linear.h", "ecmd_kern_rows.h", "ecmd_kern_tiled.h",
                "ecmd_kern_gather.h"]
@@ -55,7 +58,8 @@ FLAGS = [
 # Further flags of single sources.  Attention: matrix results in the general
 # registers; with the accumulation registers, which the compiler otherwise gives
 # half of the file, the loop moved 32 values there and back in every turn.
-FILE_FLAGS = {"serving/kernels_attention_%s.hip" % t: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for t in ("f16", "bf16", "f32")}
+FILE_FLAGS = {"serving/kernels_%s_%s.hip" % (k, t): ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+              for k in ("attention", "tree", "mass") for t in ("f16", "bf16", "f32")}
 
 # Options for run-time compilation: the device side of FLAGS.
 JIT_OPTIONS = ["--offload-arch=" + ARCH, "-O3", "-std=c++20", "-ffp-contract=off", "-fno-fast-math",

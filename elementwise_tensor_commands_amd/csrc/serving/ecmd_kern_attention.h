@@ -52,174 +52,12 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
 #include "../ecmd_launch.h"
-#include "ecmd_serving.h"
-#include "ecmd_wave.h"
+#include "ecmd_attn_tile.h"
 
 namespace ecmd {
 
 namespace {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-
-constexpr uint32_t kAttnBlock = 256, kAttnWaves = 4;
-constexpr uint32_t kTableKeys = 256;   // positions whose cache offsets a wave holds at a time
-
-template <int TY>
-struct AttnType {
-    typedef uint16_t T;
-    static constexpr int E = 8, KB = 2;   // elements of a 16-byte piece; key blocks of a tile
-};
-template <>
-struct AttnType<S_F32> {
-    typedef float T;
-    static constexpr int E = 4, KB = 1;
-};
-
-template <int TY>
-__device__ inline f32x4 mma16(u32x4 a, u32x4 b, f32x4 c)
-{
-    if constexpr (TY == S_BF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
-                                                       0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
-                                                      0, 0);
-}
-
-__device__ inline float as_f(uint32_t x) { return __builtin_bit_cast(float, x); }
-
-// x if it is finite, else some finite number.
-__device__ inline float finite(float x)
-{
-    float most = 3.40282346638528859812e38f;
-    asm("" : "+s"(most));   // one register and its negative, not two
-    return __builtin_amdgcn_fmed3f(x, -most, most);
-}
-
-// x, as far as the compiler knows another one for every `now`: what depends on it is
-// computed where `now` is known, not moved out of a loop into registers that the
-// loop needs.
-__device__ inline uint32_t fresh(uint32_t x, uint32_t now)
-{
-    asm("" : "+v"(x) : "s"(now));
-    return x;
-}
-__device__ inline uint32_t fresh_uniform(uint32_t x, uint32_t now)
-{
-    asm("" : "+s"(x) : "s"(now));
-    return x;
-}
-
-// 16 bytes at p, wherever that is.  STREAM: not to be kept in the caches.
-template <bool STREAM = false>
-__device__ inline u32x4 load16(const char *p)
-{
-    typedef u32x4 U __attribute__((aligned(2)));
-    if constexpr (STREAM) return __builtin_nontemporal_load((const U *)p);
-    else return *(const U *)p;
-}
-
-// The first n of N elements at p, the rest 0; nothing past them is read.
-template <class T, int N>
-__device__ inline u32x4 load_some(const char *p, int n)
-{
-    u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        if (e < n) {
-            T x;
-            __builtin_memcpy(&x, p + e * sizeof(T), sizeof x);
-            if constexpr (sizeof(T) == 2)
-                v[e / 2] |= (uint32_t)x << (16 * (e & 1));
-            else
-                v[e] = __builtin_bit_cast(uint32_t, x);
-        }
-    }
-    return v;
-}
-
-// Positions of row r that a launch looks at: [lo, hi).
-struct Span {
-    uint32_t lo, hi;
-};
-__device__ inline Span row_span(const AttnArgs &A, uint32_t r)
-{
-    const int32_t len = A.lens[(int64_t)r * A.lens_s];
-    const uint32_t held = A.cols * A.page;
-    Span s{0, 0};
-    if (len <= 0) return s;
-    s.hi = min((uint32_t)len, held);
-    if (A.window && (uint32_t)len > A.window) s.lo = min((uint32_t)len - A.window, s.hi);
-    return s;
-}
-
-// The rows' spans and the steps before each row, in LDS.
-struct Rows {
-    uint32_t *prefix;    // [b + 1]
-    uint32_t *lo, *hi;   // [b]
-    uint32_t all, longest;
-};
-__host__ __device__ inline uint32_t rows_lds(uint32_t b) { return (3 * b + 1) * 4; }
-
-// Up to 64 rows every wave makes the whole of it, the same values in the same
-// places, and waits for nobody; more rows are the first kAttnBlock work-items'
-// and end with a barrier.
-__device__ inline Rows make_rows(const AttnArgs &A, uint32_t *lds, uint32_t *scratch)
-{
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    Rows R{lds, lds + A.b + 1, lds + 2 * A.b + 1, 0, 0};
-    const bool alone = A.b <= 64;
-    uint32_t run = 0, most = 0;
-    for (uint32_t r0 = 0; r0 < A.b; r0 += kAttnBlock) {
-        const uint32_t r = alone ? lane : threadIdx.x < kAttnBlock ? r0 + threadIdx.x : A.b;
-        uint32_t x = 0;
-        if (r < A.b) {
-            const Span s = row_span(A, r);
-            R.lo[r] = s.lo;
-            R.hi[r] = s.hi;
-            x = (s.hi - s.lo + kAttnStep - 1) / kAttnStep;
-            most = max(most, x);
-        }
-        const uint32_t inc = wave_prefix(x);
-        uint32_t before = run;
-        if (alone) {
-            run = last_lane(inc);
-        } else {
-            if (lane == 63 && wave < kAttnWaves) scratch[wave] = inc;
-            __syncthreads();
-#pragma unroll
-            for (uint32_t w = 0; w < kAttnWaves; ++w) {
-                if (w < wave) before += scratch[w];
-                run += scratch[w];
-            }
-            __syncthreads();
-        }
-        if (r < A.b) R.prefix[r] = before + inc - x;
-    }
-    if (alone ? lane == 0 : threadIdx.x == 0) R.prefix[A.b] = run;
-    most = wave_max(most);
-    if (alone) {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    } else {
-        if (lane == 0 && wave < kAttnWaves) scratch[wave] = most;
-        __syncthreads();
-#pragma unroll
-        for (uint32_t w = 0; w < kAttnWaves; ++w) most = max(most, scratch[w]);
-    }
-    R.all = __builtin_amdgcn_readfirstlane(run);
-    R.longest = __builtin_amdgcn_readfirstlane(most);
-    return R;
-}
 
 // How the steps are dealt out, the same in every work-group and in the join.
 // Waves by heads or by positions: 1138 MB in 64 ragged rows take 209 us by heads
@@ -246,16 +84,24 @@ __device__ inline Deal deal_steps(const AttnArgs &A, const Rows &R)
     return D;
 }
 
-template <int TY>
+template <int TY, bool APART = true>
 __device__ inline void store_out(const AttnArgs &A, uint32_t r, uint32_t h, uint32_t c, float x)
 {
-    const int64_t at = (int64_t)r * A.os[0] + (int64_t)h * A.os[1] + c;
+    const Whose w = row_whose<APART>(A, r);
+    const int64_t at = (int64_t)w.b * A.os[0] + (int64_t)(w.h * A.hq + h) * A.os[1] + c;
     if constexpr (TY == S_F32)
         ((float *)A.out)[at] = x;
     else if constexpr (TY == S_BF16)
         ((__bf16 *)A.out)[at] = (__bf16)x;
     else
         ((_Float16 *)A.out)[at] = (_Float16)x;
+}
+
+template <bool APART = true>
+__device__ inline void store_lse(const AttnArgs &A, uint32_t r, uint32_t h, float x)
+{
+    const Whose w = row_whose<APART>(A, r);
+    A.lse[(int64_t)w.b * A.ls[0] + (int64_t)(w.h * A.hq + h) * A.ls[1]] = x;
 }
 
 // Weights are held as 2^kBias exp2(score - m).  m is raised only where a score
@@ -281,27 +127,21 @@ __device__ inline float log_sum(float top, float total)
     return ((top == -INFINITY ? 0.0f : top) - kBias<TY> + log2f(total)) * 0.69314718055994530942f;
 }
 
-// How pieces that reach past the end of a row of d or dv elements are read.
-enum AttnEdge {
-    kExact,   // there are none: d = 4 E NK
-    kTail,    // moved back to end with the row; keys' elements read twice are masked off
-    kTiny,    // element by element: rows shorter than a piece
-};
-
 // Waves of a SIMD that an instance asks for: what its registers (keys, values,
 // query, sums and the rest, about) leave room for without spills in the loop.
-template <int TY, int NK, int VW, AttnEdge EDGE>
+template <int TY, int NK, int VW, AttnEdge EDGE, bool APART>
 constexpr int attn_waves()
 {
     constexpr int KB = AttnType<TY>::KB, size = TY == S_F32 ? 4 : 2;
-    constexpr int regs = KB * NK * 4 + KB * VW * size + NK * 4 + VW * 4 + (TY == S_F32 ? 52 : 60) + (EDGE == kTail ? 10 : 0);
+    constexpr int regs = KB * NK * 4 + KB * VW * size + NK * 4 + VW * 4 + (TY == S_F32 ? 52 : 60) + (EDGE == kTail ? 10 : 0) + (APART ? 10 : 0);
     return regs > 268 ? 1 : regs > 172 ? 2 : regs > (TY == S_F32 ? 128 : 112) ? 3 : 4;
 }
 
 // VW: value columns of a lane (16 VW >= dv).  NK: 16-byte key pieces of a lane
 // (4 E NK >= d).  STREAM: the cache is larger than the last-level cache.
-template <int TY, int NK, int VW, AttnEdge EDGE, bool STREAM>
-__global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void k_attention(const AttnArgs A)
+// APART: the tables are the kv heads' own.
+template <int TY, int NK, int VW, AttnEdge EDGE, bool STREAM, bool APART>
+__global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE, APART>())) void k_attention(const AttnArgs A)
 {
     typedef typename AttnType<TY>::T T;
     constexpr int E = AttnType<TY>::E, KB = AttnType<TY>::KB;
@@ -338,7 +178,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         if (group >= A.b) return;
         r = group;
     } else {
-        R = make_rows(A, s_rows, s_scratch);
+        R = make_rows(A, s_rows, s_scratch, row_span<APART>);
         const Deal D = deal_steps(A, R);
         head_shift = D.head_shift;
         place(head_shift ? A.by_heads_much : A.by_heads);
@@ -395,14 +235,14 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         return x;
     };
 
-    const char *kbase = (const char *)A.k + (int64_t)kvh * A.kcs[2];
-    const char *vbase = (const char *)A.v + (int64_t)kvh * A.vcs[2];
-
     for (;;) {   // one row of the run
+        const Whose whose = row_whose<APART>(A, r);
+        const char *kbase = (const char *)A.k + (int64_t)(kvh + whose.h) * A.kcs[2];
+        const char *vbase = (const char *)A.v + (int64_t)(kvh + whose.h) * A.vcs[2];
         uint32_t begin, end, steps = 0;
         bool whole_row = true;
         if (A.direct) {
-            const Span span = row_span(A, r);
+            const Span span = row_span<APART>(A, r);
             begin = span.lo;
             end = span.hi;
         } else {
@@ -428,7 +268,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         const uint32_t qh = q0 + min(kLate ? fresh(hh, r) : hh, q_n - 1), qj = kLate ? fresh(j, r) : j;
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
-            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)qh * A.qs[1]) * sizeof(T);
+            const char *p = (const char *)A.q + ((int64_t)whose.b * A.qs[0] + (int64_t)(whose.h * A.hq + qh) * A.qs[1]) * sizeof(T);
             q[c] = masked(load_row_piece(p, c, qj, std::false_type()), c, r);
             if (hh >= q_n) q[c] = u32x4{0, 0, 0, 0};
         }
@@ -448,7 +288,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
             for (int g = 0; g < G; ++g) {
                 const uint32_t pos = min(at + g * 64 + lane, we - 1), col = A.by_page.div(pos);
                 in[g] = pos - col * A.page;
-                id[g] = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
+                id[g] = A.pages[(int64_t)whose.b * A.pages_s[0] + (int64_t)whose.h * A.pages_s[2] + (int64_t)col * A.pages_s[1]];
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -628,7 +468,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
         const uint32_t tid = fresh(wave * 64 + __lane_id(), r), eh = tid & 15, ej = tid >> 4 & 3;
         const uint64_t place = (uint64_t)(group + r) * A.hq + q0;
         auto put = [&](uint32_t hx, uint32_t c, float sum, float total) {
-            if (whole_row) store_out<TY>(A, r, q0 + hx, c, total == 0.0f ? 0.0f : sum / total);
+            if (whole_row) store_out<TY, APART>(A, r, q0 + hx, c, total == 0.0f ? 0.0f : sum / total);
             else A.acc[(place + hx) * A.dv + c] = sum;
         };
         auto put_statistics = [&](uint32_t hx, float top, float total) {
@@ -636,7 +476,7 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE>())) void 
                 A.ml[2 * (place + hx)] = top;
                 A.ml[2 * (place + hx) + 1] = total;
             } else if (A.lse) {
-                A.lse[(int64_t)r * A.ls[0] + (int64_t)(q0 + hx) * A.ls[1]] = log_sum<TY>(top, total);
+                store_lse<APART>(A, r, q0 + hx, log_sum<TY>(top, total));
             }
         };
         // Of `PARTS` waves with the same heads: common maximum, then sums through
@@ -735,14 +575,14 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArg
     extern __shared__ uint32_t s_rows[];
     __shared__ uint32_t s_scratch[kAttnWaves];
     const uint32_t lane = threadIdx.x & 63;
-    const Rows R = make_rows(A, s_rows, s_scratch);
+    const Rows R = make_rows(A, s_rows, s_scratch, row_span<true>);
     const uint32_t x = __builtin_amdgcn_readfirstlane(blockIdx.x * kAttnWaves + threadIdx.x / 64);
     if (x >= A.b * A.hq) return;
     const uint32_t r = A.by_heads.div(x), h = x - r * A.hq;   // by_heads: hq here
     const Segments S = row_segments(A, R, r);
     if (S.count == 0) {
         for (uint32_t c = lane; c < A.dv; c += 64) store_out<TY>(A, r, h, c, 0.0f);
-        if (lane == 0 && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = -INFINITY;
+        if (lane == 0 && A.lse) store_lse(A, r, h, -INFINITY);
         return;
     }
     if (S.count == 1) return;   // written by its work-group
@@ -788,7 +628,7 @@ __global__ __launch_bounds__(kAttnBlock) void k_attention_join_few(const AttnArg
 #pragma unroll
     for (uint32_t c = 0; c < 4; ++c)
         if (c * 64 + lane < A.dv) store_out<TY>(A, r, h, c * 64 + lane, total == 0.0f ? 0.0f : sum[c] / total);
-    if (lane == 0 && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = log_sum<TY>(m, total);
+    if (lane == 0 && A.lse) store_lse(A, r, h, log_sum<TY>(m, total));
 }
 
 // The same for rows cut into many.
@@ -806,12 +646,12 @@ __global__ __launch_bounds__(THREADS) void k_attention_join(const AttnArgs A)
     const uint32_t r = A.by_heads.div(blockIdx.x), h = blockIdx.x - r * A.hq;   // by_heads: hq here
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t c0 = blockIdx.y * COLS, c = c0 + threadIdx.x % COLS, g = threadIdx.x / COLS;
-    const Rows R = make_rows(A, s_rows, s_scratch);
+    const Rows R = make_rows(A, s_rows, s_scratch, row_span<true>);
     const Segments S = row_segments(A, R, r);
     const bool first_cols = blockIdx.y == 0 && threadIdx.x == 0;
     if (S.count == 0) {
         if (g == 0 && c < A.dv) store_out<TY>(A, r, h, c, 0.0f);
-        if (first_cols && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = -INFINITY;
+        if (first_cols && A.lse) store_lse(A, r, h, -INFINITY);
         return;
     }
     const uint32_t first = S.first, parts = S.count;
@@ -859,15 +699,17 @@ __global__ __launch_bounds__(THREADS) void k_attention_join(const AttnArgs A)
         for (uint32_t x = 1; x < kGroups; ++x) sum += s_sum[x * COLS + c - c0];
         store_out<TY>(A, r, h, c, total == 0.0f ? 0.0f : sum / total);
     }
-    if (first_cols && A.lse) A.lse[(int64_t)r * A.ls[0] + (int64_t)h * A.ls[1]] = log_sum<TY>(m, total);
+    if (first_cols && A.lse) store_lse(A, r, h, log_sum<TY>(m, total));
 }
 
 template <int TY, int NK, int VW, AttnEdge EDGE>
 int launch_attn_one(const AttnArgs &A, void *stream)
 {
-    const void *fn = EDGE != kTiny && A.stream
-                         ? reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, EDGE != kTiny>)
-                         : reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, false>);
+    // (what a table of a head's own names is little of a large cache, and kept)
+    const void *fn = A.apart_tables ? reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, false, true>)
+                     : EDGE != kTiny && A.stream
+                         ? reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, EDGE != kTiny, false>)
+                         : reinterpret_cast<const void *>(&k_attention<TY, NK, VW, EDGE, false, false>);
     return launch_kernel(fn, dim3(A.grid), dim3(kAttnBlock), A.direct ? 0 : rows_lds(A.b), stream, A);
 }
 

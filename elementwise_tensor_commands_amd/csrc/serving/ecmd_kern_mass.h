@@ -1,0 +1,192 @@
+// ecmd_kern_mass.h -- the weight that attention gave to every page of a row (device
+// code; one translation unit per element type instantiates it).
+//
+//   mass[j] = decay mass[j] + sum_h sum_{x in column j} exp(scale q_h . k_x - lse_h)
+//
+// The keys are read once and nothing else is large, so HBM bounds it.  A work-group
+// takes whole columns of a row, as many as make up 256 positions, and all heads of
+// them: a column's sum is then its own business, with no atomics and in one order.
+// Its waves take kv heads, or parts of the positions where there are fewer; scores come
+// from the matrix units, D[key][head], keys straight from memory to registers.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "../ecmd_launch.h"
+#include "ecmd_attn_tile.h"
+
+namespace ecmd {
+
+namespace {
+
+// Sum over the 16 lanes of a row of lanes, in every one of them.
+__device__ inline float row_sum(float x)
+{
+#define ECMD_ROTATE(CTRL) x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false))
+    ECMD_ROTATE(0x128);   // row_ror:8
+    ECMD_ROTATE(0x124);
+    ECMD_ROTATE(0x122);
+    ECMD_ROTATE(0x121);
+#undef ECMD_ROTATE
+    return x;
+}
+
+template <int TY, int NK, AttnEdge EDGE>
+__global__ __launch_bounds__(256) void k_mass(const MassArgs A)
+{
+    typedef typename AttnType<TY>::T T;
+    constexpr int E = AttnType<TY>::E, KB = 2;
+    constexpr uint32_t kTile = 16 * KB, kTiles = kMassKeys / kTile;
+    __shared__ uint64_t s_at[kMassKeys];
+    __shared__ uint32_t s_valid[kTiles];
+    __shared__ float s_part[kAttnWaves][kMassKeys], s_sum[kMassKeys];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, j = lane >> 4, hh = lane & 15;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t r = A.by_groups.div(blockIdx.x), c0 = (blockIdx.x - r * A.groups) * A.cols_group;
+    const uint32_t c1 = min(c0 + A.cols_group, A.cols);
+    const int32_t len = A.lens[(int64_t)r * A.lens_s];
+    const uint32_t hi = min((uint32_t)max(len, 0), A.cols * A.page);
+    const uint32_t lo = A.window && len > 0 && (uint32_t)len > A.window ? (uint32_t)len - A.window : 0;
+
+    // waves to a kv head (of the positions), kv heads at a time
+    const uint32_t hw = A.hk == 1 ? 4 : A.hk == 2 ? 2 : 1, head0 = wave / hw, tile0 = wave % hw;
+    float mine = 0.0f;   // column c0 + tid's sum
+    const uint32_t begin = c0 * A.page, end = min(c1 * A.page, hi);
+    // (pages of more than 256 slots are alone in their work-group and take turns)
+    for (uint32_t base = begin; base < end; base += kMassKeys) {
+        if (base + kMassKeys <= lo) continue;
+        const uint32_t n = min(kMassKeys, end - base);
+        {
+            const uint32_t pos = min(base + tid, end - 1), col = A.by_page.div(pos);
+            const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
+            const bool ok = tid < n && base + tid >= lo && id >= 0 && (uint32_t)id < A.n;
+            s_at[tid] = ok ? (uint64_t)((int64_t)id * A.kcs[0] + (int64_t)(pos - col * A.page) * A.kcs[1]) : 0;
+            const uint64_t bits = __ballot(ok);
+            if (lane == 0) {
+                s_valid[wave * 2] = (uint32_t)bits;
+                s_valid[wave * 2 + 1] = (uint32_t)(bits >> 32);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < kMassKeys / 64; ++k) s_part[wave][k * 64 + lane] = 0.0f;
+        }
+        __syncthreads();
+        const uint32_t tiles = (n + kTile - 1) / kTile;
+        for (uint32_t kvh = head0; kvh < A.hk; kvh += kAttnWaves / hw) {
+            const char *kbase = (const char *)A.k + (int64_t)kvh * A.kcs[2];
+            for (uint32_t g0 = 0; g0 < A.group; g0 += 16) {
+                const uint32_t q_n = min(16u, A.group - g0), head = kvh * A.group + g0 + min(hh, q_n - 1);
+                auto piece = [&](const char *p, int c) {
+                    const int at = (c * 4 + (int)j) * E;
+                    if constexpr (EDGE == kTiny) return load_some<T, E>(p + at * sizeof(T), (int)A.d - at);
+                    return load16(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
+                };
+                auto masked = [&](u32x4 x, int c) {
+                    if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {
+                        const int at = (c * 4 + (int)j) * E, twice = at - min(at, (int)A.d - E);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            if constexpr (E == 8)
+                                x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
+                            else
+                                x[w] &= w >= twice ? ~0u : 0u;
+                        }
+                    }
+                    return x;
+                };
+                u32x4 q[NK];
+                const char *qp = (const char *)A.q + (int64_t)r * A.qs[0] + (int64_t)head * A.qs[1];
+#pragma unroll
+                for (int c = 0; c < NK; ++c) q[c] = masked(piece(qp, c), c);
+                const float lse = A.lse[(int64_t)r * A.lse_s[0] + (int64_t)head * A.lse_s[1]];
+                const bool on = hh < q_n && lse != -INFINITY;
+                const float less = lse * 1.44269504088896340736f;
+                u32x4 kr[KB][NK];
+                auto load = [&](uint32_t t) {
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const char *p = kbase + s_at[t * kTile + kb * 16 + hh];
+#pragma unroll
+                        for (int c = 0; c < NK; ++c) kr[kb][c] = piece(p, c);
+                    }
+                };
+                if (tile0 < tiles) load(tile0);
+                for (uint32_t t = tile0; t < tiles; t += hw) {
+                    f32x4 s[KB];
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        s[kb] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                        for (int c = 0; c < NK; ++c) {
+                            const u32x4 k = masked(kr[kb][c], c);
+                            if constexpr (TY == S_F32) {
+#pragma unroll
+                                for (int f = 0; f < 4; ++f)
+                                    s[kb] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(k[f]), as_f(q[c][f]), s[kb], 0, 0, 0);
+                            } else {
+                                s[kb] = mma16<TY>(k, q[c], s[kb]);
+                            }
+                        }
+                    }
+                    if (t + hw < tiles) load(t + hw);
+                    const uint32_t valid = s_valid[t];
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        f32x4 w;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool ok = on && valid >> (kb * 16 + j * 4 + i) & 1;
+                            w[i] = row_sum(ok ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], A.scale_log2, -less)) : 0.0f);
+                        }
+                        if (hh < 4) {
+                            const float v = hh == 0 ? w[0] : hh == 1 ? w[1] : hh == 2 ? w[2] : w[3];
+                            s_part[wave][t * kTile + kb * 16 + j * 4 + hh] += v;
+                        }
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        float sum = 0.0f;
+#pragma unroll
+        for (uint32_t w = 0; w < kAttnWaves; ++w) sum += s_part[w][tid];
+        s_sum[tid] = sum;
+        __syncthreads();
+        if (A.page > kMassKeys) {   // one column: all of them are its
+            if (wave == 0) {
+                float all = s_sum[lane];
+#pragma unroll
+                for (uint32_t k = 1; k < kMassKeys / 64; ++k) all += s_sum[k * 64 + lane];
+                mine += wave_sum(all);
+            }
+        } else if (tid < c1 - c0) {
+            for (uint32_t k = 0; k < A.page; ++k) {
+                const uint32_t x = tid * A.page + k;
+                if (x < n) mine += s_sum[x];
+            }
+        }
+        __syncthreads();
+    }
+    if (tid < c1 - c0) {
+        const uint32_t c = c0 + tid;
+        const float was = A.mass[(int64_t)r * A.mass_s[0] + (int64_t)c * A.mass_s[1]];
+        A.out[(int64_t)r * A.out_s[0] + (int64_t)c * A.out_s[1]] = A.decay * was + mine;
+    }
+}
+
+template <int TY>
+int launch_mass_type(const MassArgs &A, void *stream)
+{
+    constexpr int E = AttnType<TY>::E, U = 8 / E;
+    const uint32_t d = A.d;
+    const void *fn = d < (uint32_t)E ? reinterpret_cast<const void *>(&k_mass<TY, U, kTiny>)
+                     : d == 64       ? reinterpret_cast<const void *>(&k_mass<TY, 2 * U, kExact>)
+                     : d < 64        ? reinterpret_cast<const void *>(&k_mass<TY, 2 * U, kTail>)
+                     : d == 128      ? reinterpret_cast<const void *>(&k_mass<TY, 4 * U, kExact>)
+                     : d < 128       ? reinterpret_cast<const void *>(&k_mass<TY, 4 * U, kTail>)
+                     : d == 256      ? reinterpret_cast<const void *>(&k_mass<TY, 8 * U, kExact>)
+                                     : reinterpret_cast<const void *>(&k_mass<TY, 8 * U, kTail>);
+    return launch_kernel(fn, dim3(A.b * A.groups), dim3(256), 0, stream, A);
+}
+
+}  // namespace
+
+}  // namespace ecmd

@@ -1,7 +1,7 @@
 // ecmd_serving.h -- kernel argument blocks of the serving operators and the
 // functions that launch them (internal to the library).
 //
-// The host (ecmd_serving.cpp) checks every argument and fills a block; a
+// The host (ecmd_serving.cpp, ecmd_serving_cache.cpp) checks every argument and fills a block; a
 // launcher picks the kernel instance and enqueues it.  Offsets within a tensor
 // are 64-bit throughout.
 #pragma once
@@ -82,7 +82,10 @@ struct AttnArgs {
     float *ml;                             // workspace: [runs + b, hq] (maximum, sum) pairs
     int64_t qs[2], os[2], ls[2];           // batch, head
     int64_t kcs[3], vcs[3];                // BYTE strides of page, slot, head
-    int64_t pages_s[2], lens_s;
+    int64_t pages_s[3], lens_s[2];         // batch, column, kv head; batch, kv head
+    // Tables of every kv head: each of a sequence's `apart` kv heads is a row of its
+    // own, with one kv head (b = sequences * apart, hq = group, hk = 1).  Otherwise 1.
+    uint32_t apart, apart_tables;
     uint32_t b, hq, hk, d, dv, group, head_tiles;
     uint32_t n, page, cols;
     uint32_t window;
@@ -98,6 +101,7 @@ struct AttnArgs {
     Div31 by_heads, by_heads_much;         // work-groups of eight runs: 8 heads; 8 heads >> head_shift
     Div31 by_tiles;                        // head_tiles
     Div31 by_runs, by_runs_much;
+    Div31 by_apart;
 };
 
 // Positions are dealt to work-groups in steps of this many: a tile for each of
@@ -183,5 +187,126 @@ int launch_assign(const AssignArgs &A, void *stream);
 int launch_compact(const CompactArgs &A, void *stream);
 // width: bytes of one vector (16, 8, 4 or 2); past: go past the caches
 int launch_copy(int width, bool past, const CopyArgs &A, uint32_t pools, uint32_t grid, void *stream);
+
+// --- trees of drafted tokens -------------------------------------------------
+
+constexpr uint32_t kMaxTree = 256;   // tokens of a tree
+constexpr uint32_t kTreeMaxRows = 1024;   // rows whose prefixes fit LDS beside the tree; more go direct
+
+struct TreeArgs {
+    const void *q, *k, *v;
+    const int32_t *pages, *lens, *parent;
+    void *out;
+    float *lse;                            // may be null
+    float *acc;                            // workspace: [runs + b, hk * m, dv] sums
+    float *ml;                             // workspace: [runs + b, hk * m] (maximum, sum) pairs; sum < 0: padding
+    int64_t qs[3], os[3], ls[3];           // batch, token, head
+    int64_t kcs[3], vcs[3];                // BYTE strides of page, slot, head
+    int64_t pages_s[2], lens_s, parent_s[2];
+    uint32_t b, t, hq, hk, d, dv, group;
+    uint32_t m;                            // query vectors of a kv head: t * group, token by token
+    uint32_t q_blocks, q_shift;            // work-groups that share them; 2^q_shift waves of one take apart
+    uint32_t n, page, cols, window;
+    uint32_t direct;                       // 1: a work-group to a row, kv head and block, no join
+    uint32_t runs, runs_whole, grid;       // as in AttnArgs
+    float scale_log2;                      // |scale| * log2(e)
+    uint32_t q_flip;                       // sign bits to flip in q: the scale is negative
+    Div31 by_page, by_units, by_blocks, by_group, by_runs, by_vectors;   // by_units: 8 * hk * q_blocks
+};
+
+int launch_tree_f16(const TreeArgs &A, void *stream);
+int launch_tree_bf16(const TreeArgs &A, void *stream);
+int launch_tree_f32(const TreeArgs &A, void *stream);
+int launch_tree_join(int type, const TreeArgs &A, void *stream);
+
+struct AcceptArgs {
+    const int32_t *tokens, *parent, *next, *lens;
+    int32_t *path, *lens_out, *last;
+    int64_t tokens_s[2], parent_s[2], next_s[2], path_s[2];
+    int64_t lens_s, lens_out_s, last_s;
+    uint32_t rows, t;
+};
+int launch_accept(const AcceptArgs &A, void *stream);
+
+constexpr int kMovePools = 24, kMoveFew = 4;   // of one launch
+struct MovePool {
+    char *base;
+    int64_t page_stride, slot_stride, head_stride;   // bytes
+    uint32_t n, head_vecs;
+    Div31 by_head;                                   // vectors of a head
+};
+template <int POOLS>
+struct MoveBlock {
+    const int32_t *pages, *lens, *path;
+    int64_t pages_s[2], lens_s, path_s[2];
+    uint32_t rows, cols, t, page;
+    uint32_t vecs, pieces;                           // vectors of a slot; work-groups that share them
+    Div31 by_page, by_pieces;
+    MovePool pool[POOLS];
+};
+typedef MoveBlock<kMovePools> MoveArgs;
+// width: bytes of one vector (16, 8, 4 or 2)
+int launch_move(int width, const MoveArgs &A, uint32_t pools, void *stream);
+
+// --- pages worth reading or keeping ----------------------------------------
+
+struct BoundsArgs {
+    const void *k;
+    void *bounds;
+    const int32_t *pages, *lens, *since;
+    int64_t kcs[3];                        // BYTE strides of page, slot, head
+    int64_t bs[3];                         // BYTE strides of page, head, least/largest
+    int64_t pages_s[2], lens_s, since_s;
+    uint32_t rows, cols, n, page, hk, d;
+    uint32_t head_items, items;            // 16-byte pieces of a head and of a slot
+    uint32_t many, parts;                  // columns of a work-group's turn; or its turns of a column (many = 1)
+    uint32_t groups;                       // work-groups of a row
+    Div31 by_page, by_items, by_head, by_many, by_parts, by_groups;
+};
+int launch_bounds(int type, const BoundsArgs &A, void *stream);
+
+struct SelectArgs {
+    const void *q, *bounds;
+    const int32_t *pages, *lens;
+    int32_t *pages_out, *lens_out;
+    uint64_t *keys;                        // workspace: [b, hk, cols] (null: a work-group scores and chooses alone)
+    int64_t qs[2];                         // BYTE strides of batch, head
+    int64_t bs[3];                         // BYTE strides of page, head, least/largest
+    int64_t pages_s[2], lens_s, pages_out_s[3], lens_out_s[2];
+    uint32_t b, hk, group, d, n, cols, page, take, first, last;
+    uint32_t groups;                       // work-groups that score a row and kv head
+    Div31 by_page, by_hk, by_groups;
+};
+int launch_select(int type, const SelectArgs &A, void *stream);
+constexpr uint32_t kSelectAlone = 4096;    // columns whose keys fit LDS beside another work-group's
+
+struct MassArgs {
+    const void *q, *k;
+    const int32_t *pages, *lens;
+    const float *lse, *mass;
+    float *out;
+    int64_t qs[2], kcs[3];                 // BYTE strides of batch, head; of page, slot, head
+    int64_t pages_s[2], lens_s, lse_s[2], mass_s[2], out_s[2];
+    uint32_t b, hk, group, d, n, cols, page, window;
+    uint32_t cols_group, groups;           // columns of a work-group; work-groups of a row
+    float scale_log2, decay;
+    Div31 by_page, by_groups;
+};
+int launch_mass_f16(const MassArgs &A, void *stream);
+int launch_mass_bf16(const MassArgs &A, void *stream);
+int launch_mass_f32(const MassArgs &A, void *stream);
+constexpr uint32_t kMassKeys = 256;        // positions of a work-group at a time
+
+struct EvictArgs {
+    const int32_t *pages, *lens, *refs, *budget;
+    const float *mass;
+    int32_t *pages_out, *refs_out, *count;
+    int64_t pages_s[2], mass_s[2], pages_out_s[2];
+    int64_t lens_s, refs_s, budget_s, refs_out_s, count_s;
+    uint32_t rows, cols, n, page, first, last;
+    uint32_t copy;                         // 1: refs_out is not refs
+    Div31 by_page;
+};
+int launch_evict(const EvictArgs &A, void *stream);
 
 }  // namespace ecmd

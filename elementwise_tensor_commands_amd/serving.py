@@ -1,5 +1,6 @@
 """Serving operators beside Commands: rotary positions, a paged key-value
-cache, attention of one new token over it, and the bookkeeping of its pages.
+cache, attention of one new token or of a tree of drafted tokens over it, the
+pages worth reading or keeping, and the bookkeeping of its pages.
 
 A thin layer over ``include/ecmd_serving.h``, which defines every
 operator; outputs are the caller's tensors, work goes to torch's current stream
@@ -19,7 +20,25 @@ A decode step of a model's attention:
     ecmd.rope_append(q, k, v, pos, row, pages2, freq, q, k_cache, v_cache)
     ecmd.paged_attention(q, k_cache, v_cache, pages2, lens2, out)
 
-``decode.py`` in this package runs it end to end.
+The same that reads only the pages a cheap score selects for each kv head:
+
+    ecmd.page_bounds(k_cache, pages2, lens2, lens, bounds)        # after the append: the new positions' keys
+    ecmd.page_select(q, bounds, pages2, lens2, page, picked, picked_lens)
+    ecmd.paged_attention(q, k_cache, v_cache, picked, picked_lens, out)
+
+that keeps rows within a budget of pages, by the weight attention gave them:
+
+    ecmd.page_mass(q, k_cache, pages2, lens2, lse, mass, mass, decay=0.95)
+    ecmd.page_evict(pages2, lens2, refs2, mass, budget, page, pages2, refs2, count)
+
+and that checks a tree of drafted tokens in one step (their keys and values appended
+at positions lens + i):
+
+    ecmd.tree_attention(q, k_cache, v_cache, pages, lens, parent, out)
+    ecmd.tree_accept(tokens, parent, next, lens, path, lens2, last)
+    ecmd.slot_move([k_cache, v_cache], pages, lens, path)         # the accepted ones to lens, lens + 1, ...
+
+``decode.py`` in this package runs them end to end.
 """
 from __future__ import annotations
 
@@ -42,7 +61,18 @@ for _name, _res, _sig in [
         ("cmd_page_assign_workspace", _i64, [_args, _i32]),
         ("cmd_page_compact", ctypes.c_int, [_args, _vp, _i64, _i32, _vp]),
         ("cmd_page_compact_workspace", _i64, [_args]),
-        ("cmd_page_copy", ctypes.c_int, [_args, _i32, _args, _args, _i32, _vp])]:
+        ("cmd_page_copy", ctypes.c_int, [_args, _i32, _args, _args, _i32, _vp]),
+        ("cmd_paged_attention_heads", ctypes.c_int, [_args, ctypes.c_float, _i32, _vp, _i64, _i32, _vp]),
+        ("cmd_paged_attention_heads_workspace", _i64, [_args, _i32]),
+        ("cmd_tree_attention", ctypes.c_int, [_args, ctypes.c_float, _i32, _vp, _i64, _i32, _vp]),
+        ("cmd_tree_attention_workspace", _i64, [_args, _i32]),
+        ("cmd_tree_accept", ctypes.c_int, [_args, _i32, _vp]),
+        ("cmd_slot_move", ctypes.c_int, [_args, _i32, _args, _i32, _vp]),
+        ("cmd_page_bounds", ctypes.c_int, [_args, _i32, _vp]),
+        ("cmd_page_select", ctypes.c_int, [_args, _i32, _i32, _i32, _vp, _i64, _i32, _vp]),
+        ("cmd_page_select_workspace", _i64, [_args, _i32, _i32, _i32]),
+        ("cmd_page_mass", ctypes.c_int, [_args, ctypes.c_float, ctypes.c_float, _i32, _i32, _vp]),
+        ("cmd_page_evict", ctypes.c_int, [_args, _i32, _i32, _i32, _i32, _vp])]:
     getattr(lib, _name).restype = _res
     getattr(lib, _name).argtypes = _sig
 
@@ -145,6 +175,20 @@ def rope_append(q, k, v, pos, row, pages, freq, q_out, k_cache, v_cache, *, layo
 
 
 _ATTENTION = b"\3\4\4\2\1\3\2"
+_ATTENTION_HEADS = b"\3\4\4\3\2\3\2"
+
+
+def _attention(pages):
+    """(ranks, the call and its workspace's) for tables of rows, or of rows and kv heads."""
+    if getattr(pages, "ndim", 2) == 3:
+        return _ATTENTION_HEADS, lib.cmd_paged_attention_heads, lib.cmd_paged_attention_heads_workspace
+    return _ATTENTION, lib.cmd_paged_attention, lib.cmd_paged_attention_workspace
+
+
+def _scale(scale, q) -> float:
+    if scale is None:
+        return 1.0 / math.sqrt(max(1, q.shape[-1])) if q.dim() else 1.0
+    return scale
 
 
 def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=None, window=0, workspace=None,
@@ -153,25 +197,144 @@ def paged_attention(q, k_cache, v_cache, pages, lens, out, *, lse=None, scale=No
     (cmd_paged_attention): q [B, hq, d] over the first lens[r] positions of row
     r -- the last ``window`` of them if that is not 0 -- into out [B, hq, dv],
     the log of the softmax's sum into lse [B, hq] (float32) if given.  scale:
-    1 / sqrt(d) by default."""
-    args, dev, current = _pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, lse)
-    if scale is None:
-        scale = 1.0 / math.sqrt(max(1, q.shape[-1])) if q.dim() else 1.0
+    1 / sqrt(d) by default.  pages [B, P] and lens [B] are the rows' tables, or pages
+    [B, hk, P] and lens [B, hk] one for every kv head, as ``page_select`` makes them
+    (cmd_paged_attention_heads)."""
+    ranks, call, size_of = _attention(pages)
+    args, dev, current = _pack(ranks, q, k_cache, v_cache, pages, lens, out, lse)
+    scale = _scale(scale, q)
     window = _int32(window)
     if dev < 0:
-        _refuse(lib.cmd_paged_attention(args, scale, window, None, 0, CHECK_ONLY, None))
-    ptr, size, _owner = _scratch(workspace, lib.cmd_paged_attention_workspace(args, window), stream, dev)
-    _check(lib.cmd_paged_attention(args, scale, window, ptr, size, 0,
-                                   current if stream is None else _handle(stream, dev)))
+        _refuse(call(args, scale, window, None, 0, CHECK_ONLY, None))
+    ptr, size, _owner = _scratch(workspace, size_of(args, window), stream, dev)
+    _check(call(args, scale, window, ptr, size, 0, current if stream is None else _handle(stream, dev)))
     _binding.wrote(out, lse)
 
 
 def paged_attention_workspace(q, k_cache, v_cache, pages, lens, out, *, window=0) -> int:
     """Bytes of workspace that paged_attention needs for these tensors."""
-    n = lib.cmd_paged_attention_workspace(_pack(_ATTENTION, q, k_cache, v_cache, pages, lens, out, None)[0],
-                                          _int32(window))
+    ranks, _, size_of = _attention(pages)
+    n = size_of(_pack(ranks, q, k_cache, v_cache, pages, lens, out, None)[0], _int32(window))
     _check(n)
     return n
+
+
+_TREE = b"\4\4\4\2\1\2\4\3"
+
+
+def tree_attention(q, k_cache, v_cache, pages, lens, parent, out, *, lse=None, scale=None, window=0, workspace=None,
+                   stream=None):
+    """Attention for a tree of drafted tokens over the paged cache
+    (cmd_tree_attention): token i of row r, q [B, T, hq, d], follows token parent[r,
+    i] < i (-1: the context; others: padding) and attends to the row's first lens[r]
+    positions, to the tokens above it and to itself, whose keys and values lie at
+    positions lens[r] + i.  out [B, T, hq, dv], lse [B, T, hq] (float32) if given."""
+    args, dev, current = _pack(_TREE, q, k_cache, v_cache, pages, lens, parent, out, lse)
+    scale = _scale(scale, q)
+    window = _int32(window)
+    if dev < 0:
+        _refuse(lib.cmd_tree_attention(args, scale, window, None, 0, CHECK_ONLY, None))
+    ptr, size, _owner = _scratch(workspace, lib.cmd_tree_attention_workspace(args, window), stream, dev)
+    _check(lib.cmd_tree_attention(args, scale, window, ptr, size, 0,
+                                  current if stream is None else _handle(stream, dev)))
+    _binding.wrote(out, lse)
+
+
+def tree_attention_workspace(q, k_cache, v_cache, pages, lens, parent, out, *, window=0) -> int:
+    """Bytes of workspace that tree_attention needs for these tensors."""
+    n = lib.cmd_tree_attention_workspace(_pack(_TREE, q, k_cache, v_cache, pages, lens, parent, out, None)[0],
+                                         _int32(window))
+    _check(n)
+    return n
+
+
+def tree_accept(tokens, parent, next, lens, path, lens_out, last, *, stream=None):
+    """The accepted path of a tree of drafted tokens (cmd_tree_accept): from token 0
+    on to the first child that is what the model went on with, next [B, T]; all
+    int32.  path [B, T]: its tokens, then -1; lens_out (which may be lens) = lens +
+    how many they are; last [B]: what follows the last of them."""
+    args, dev, current = _pack(b"\2\2\2\1\2\1\1", tokens, parent, next, lens, path, lens_out, last)
+    if dev < 0:
+        _refuse(lib.cmd_tree_accept(args, CHECK_ONLY, None))
+    _check(lib.cmd_tree_accept(args, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(path, lens_out, last)
+
+
+def slot_move(pools, pages, lens, path, *, stream=None):
+    """Move what position lens[r] + path[r, i] of row r holds to position lens[r] + i
+    in every pool [N, page, heads, d] (cmd_slot_move), in order, up to the first
+    negative entry.  lens: from before the path was accepted."""
+    pools = list(pools)
+    n = len(pools)
+    args, dev, current = _pack(b"\2\1\2" + b"\4" * n, pages, lens, path, *pools)
+    both = (args[3 * _SIZE:], n, args[:3 * _SIZE])
+    if dev < 0:
+        _refuse(lib.cmd_slot_move(*both, CHECK_ONLY, None))
+    _check(lib.cmd_slot_move(*both, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(*pools)
+
+
+def page_bounds(k_cache, pages, lens, since, bounds, *, stream=None):
+    """Keep up the least and largest key of every page (cmd_page_bounds) with
+    positions since[r] .. lens[r] - 1 of every row: bounds [N, hk, 2, d] of
+    k_cache's dtype.  Call it after the append of those positions."""
+    args, dev, current = _pack(b"\4\2\1\1\4", k_cache, pages, lens, since, bounds)
+    if dev < 0:
+        _refuse(lib.cmd_page_bounds(args, CHECK_ONLY, None))
+    _check(lib.cmd_page_bounds(args, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(bounds)
+
+
+_SELECT = b"\3\4\2\1\3\2"
+
+
+def page_select(q, bounds, pages, lens, page, pages_out, lens_out, *, first=1, last=2, workspace=None, stream=None):
+    """Choose the pages that q [B, hq, d] may care for most, for every sequence and kv
+    head (cmd_page_select): pages_out [B, hk, C] and lens_out [B, hk], tables for
+    ``paged_attention``.  The row's ``first`` first and ``last`` last pages are
+    always among them."""
+    page, first, last = _int32(page), _int32(first), _int32(last)
+    args, dev, current = _pack(_SELECT, q, bounds, pages, lens, pages_out, lens_out)
+    if dev < 0:
+        _refuse(lib.cmd_page_select(args, page, first, last, None, 0, CHECK_ONLY, None))
+    ptr, size, _owner = _scratch(workspace, lib.cmd_page_select_workspace(args, page, first, last), stream, dev)
+    _check(lib.cmd_page_select(args, page, first, last, ptr, size, 0,
+                               current if stream is None else _handle(stream, dev)))
+    _binding.wrote(pages_out, lens_out)
+
+
+def page_select_workspace(q, bounds, pages, lens, page, pages_out, lens_out, *, first=1, last=2) -> int:
+    """Bytes of workspace that page_select needs for these tensors."""
+    n = lib.cmd_page_select_workspace(_pack(_SELECT, q, bounds, pages, lens, pages_out, lens_out)[0], _int32(page),
+                                      _int32(first), _int32(last))
+    _check(n)
+    return n
+
+
+def page_mass(q, k_cache, pages, lens, lse, mass, mass_out, *, scale=None, decay=1.0, window=0, stream=None):
+    """Add the weight that attention gave to every page (cmd_page_mass): mass_out [B,
+    P] (float32; it may be mass) = decay * mass + the softmax weights of
+    ``paged_attention``, with its lse, over column j's positions and all heads."""
+    args, dev, current = _pack(b"\3\4\2\1\2\2\2", q, k_cache, pages, lens, lse, mass, mass_out)
+    scale = _scale(scale, q)
+    window = _int32(window)
+    if dev < 0:
+        _refuse(lib.cmd_page_mass(args, scale, decay, window, CHECK_ONLY, None))
+    _check(lib.cmd_page_mass(args, scale, decay, window, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(mass_out)
+
+
+def page_evict(pages, lens, refs, mass, budget, page, pages_out, refs_out, count, *, first=0, last=1, stream=None):
+    """Take the pages of least mass out of rows that hold more than budget [R] of them
+    (cmd_page_evict), but for the ``first`` first and ``last`` last: pages_out with
+    holes there (it may be pages), refs_out without their entries (it may be refs),
+    count [R] how many each row lost."""
+    page, first, last = _int32(page), _int32(first), _int32(last)
+    args, dev, current = _pack(b"\2\1\1\2\1\2\1\1", pages, lens, refs, mass, budget, pages_out, refs_out, count)
+    if dev < 0:
+        _refuse(lib.cmd_page_evict(args, page, first, last, CHECK_ONLY, None))
+    _check(lib.cmd_page_evict(args, page, first, last, 0, current if stream is None else _handle(stream, dev)))
+    _binding.wrote(pages_out, refs_out, count)
 
 
 _ASSIGN = b"\2\1\1\1\1\2\1\1\1\1\1"

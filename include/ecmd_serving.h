@@ -1,7 +1,8 @@
 /*
  * ecmd_serving.h -- C ABI of the serving operators on AMD Instinct MI355X
  * (gfx950): rotary positions, rotary positions with the write into a paged
- * key-value cache, attention of one new token over that cache, and the
+ * key-value cache, attention of one new token or of a tree of drafted tokens over
+ * that cache, the choice of pages worth reading or worth keeping, and the
  * bookkeeping of the cache's pages.  They run beside Commands (ecmd.h) on the
  * caller's stream and share the library's conventions:
  *
@@ -22,8 +23,12 @@
  *     need no preparation and mean nothing afterwards), sized by the matching
  *     *_workspace call;
  *   - what one launch cannot hold is refused with CMD_E_LIMIT: 2^24 work-groups, of
- *     a row and 16 query heads in attention, of a row in cmd_page_assign, of 256
- *     entries and ids in cmd_page_compact, of 16 KiB of a page in cmd_page_copy;
+ *     a row and 16 query heads in attention, of four query vectors (a token's head)
+ *     in cmd_tree_attention, of a row in cmd_page_assign, cmd_tree_accept and
+ *     cmd_page_evict, of a row and kv head in cmd_page_select, of 256 entries and ids
+ *     in cmd_page_compact, of 16 KiB of a page in cmd_page_copy, of a row and 256
+ *     vectors of a slot in cmd_slot_move, of a row and up to 256 positions in
+ *     cmd_page_mass;
  *   - cmd_last_error(NULL) describes the last failure on this thread.
  *
  * What the data say -- positions, row numbers, page ids, lengths, reference
@@ -98,6 +103,108 @@ int cmd_paged_attention(const cmd_arg args[7], float scale, int32_t window, void
                         int64_t workspace_bytes, int32_t flags, void *hip_stream);
 /* Bytes of workspace that call needs (0: none), or a negative status. */
 int64_t cmd_paged_attention_workspace(const cmd_arg args[7], int32_t window);
+
+/* The same over a page table of its own for every kv head: pages [B, hk, P] and
+ * lens [B, hk] in place of args 3 and 4, as cmd_page_select makes them.  Position x
+ * of kv head h is slot x % page of page pages[r, h, x / page]. */
+int cmd_paged_attention_heads(const cmd_arg args[7], float scale, int32_t window, void *workspace,
+                              int64_t workspace_bytes, int32_t flags, void *hip_stream);
+int64_t cmd_paged_attention_heads_workspace(const cmd_arg args[7], int32_t window);
+
+/* Attention for a tree of drafted tokens over the paged cache.  args:
+ *   0 q [B, T, hq, d]   1 k_cache [N, page, hk, d]   2 v_cache [N, page, hk, dv]
+ *   3 pages [B, P] int32   4 lens [B] int32   5 parent [B, T] int32
+ *   6 out [B, T, hq, dv]   7 lse [B, T, hq] f32, or kind 0: not wanted
+ * T <= 256; dtypes, heads and widths as in cmd_paged_attention.  lens[r] positions
+ * of row r are its context; its token i's key and value lie at position lens[r] + i
+ * (see cmd_rope_append), and the token follows token parent[r, i] < i, or the
+ * context itself if that is -1.  A token with another parent, or below such a one,
+ * is padding, and so are all of a row with a negative length: out 0, lse -inf.  A
+ * token attends to the context, to the tokens above it and to itself, of these to
+ * the `window` nearest (by steps up the tree, then back in the context) if window >
+ * 0; never to holes or to positions past the table:
+ *      out = sum_x softmax_x(scale q . k_x) v_x,   lse = log sum_x exp(scale q . k_x)
+ * T = 1, or parent[r, i] = i - 1, is attention of the next tokens of a sequence.
+ * Scores, weights, sums and softmax statistics are binary32, but with 16-bit types a
+ * weight meets the values as the sum of two numbers of the type, which hold it to
+ * within 2^-14 (bf16) or 2^-20 (f16) of itself, f16 to no better than 2^-35 of its
+ * row's largest.  A token that attends to nothing gets out 0 and lse -inf.  What a
+ * token does not attend to is of no account to it (NaN included); an infinite value
+ * that it does attend to makes its column infinite, where the weight is at least
+ * 2^-30 of the row's largest. */
+int cmd_tree_attention(const cmd_arg args[8], float scale, int32_t window, void *workspace, int64_t workspace_bytes,
+                       int32_t flags, void *hip_stream);
+int64_t cmd_tree_attention_workspace(const cmd_arg args[8], int32_t window);
+
+/* The accepted path of a tree of drafted tokens.  args, all int32:
+ *   0 tokens [B, T]   1 parent [B, T]   2 next [B, T]   3 lens [B]
+ *   4 path [B, T]   5 lens_out [B]   6 last [B]
+ * T <= 256.  Token 0, whose parent is -1, is the sequence's newest and stands; after
+ * token i the model goes on with next[r, i].  From token 0 on the path goes to the
+ * first token c with parent[r, c] = i < c and tokens[r, c] = next[r, i], until there
+ * is none.  path[r] holds the tokens of the path, ascending, then -1; lens_out =
+ * lens + how many they are (at most 2^31 - 1); last = next of the path's last.  A row
+ * whose token 0 has another parent, or whose length is negative, has an empty path:
+ * lens_out = lens, last -1.  lens_out may be the identical view as lens. */
+int cmd_tree_accept(const cmd_arg args[7], int32_t flags, void *hip_stream);
+
+/* Move the slots of a path's tokens to the end of their rows: in each of npools pools
+ * [N_k, page, heads, d] (rank 4, any dtype of 2 or 4 bytes, page alike), for row r and
+ * i = 0, 1, ... until path[r, i] is negative, what position lens[r] + path[r, i] holds
+ * goes to position lens[r] + i, one i after the other.  args: 0 pages [R, P]   1 lens
+ * [R]   2 path [R, T], all int32.  Entries path[r, i] <= i, positions past the table
+ * and holes (ids outside a pool are its holes) move nothing, nor do rows with a
+ * negative length.  T <= 256.  No slot that is written may belong to another row too.
+ * The elements of a slot's head are neighbours. */
+int cmd_slot_move(const cmd_arg *pools, int32_t npools, const cmd_arg args[3], int32_t flags, void *hip_stream);
+
+/* Keep up the least and largest key of every page.  args:
+ *   0 k_cache [N, page, hk, d]   1 pages [R, P] int32   2 lens [R] int32   3 since [R] int32
+ *   4 bounds [N, hk, 2, d]       (of the cache's dtype f16, bf16 or f32; bounds[i, h, 0]
+ *     the least, bounds[i, h, 1] the largest of what page i's slots hold, by element)
+ * Positions max(since, 0) .. min(lens, P * page) - 1 of every row are new: the bounds
+ * of a page whose first position is one of them are made from them, those of a page
+ * that held earlier ones are widened by them.  Other pages' bounds stay.  NaN counts
+ * as nothing (of NaN alone: least +inf, largest -inf).  No page with new positions may
+ * belong to two rows.  Bounds are a pool to cmd_page_copy: copied pages take theirs along. */
+int cmd_page_bounds(const cmd_arg args[5], int32_t flags, void *hip_stream);
+
+/* Choose for every sequence and kv head the pages that its query tokens may care for
+ * most.  args:
+ *   0 q [B, hq, d]   1 bounds [N, hk, 2, d]   2 pages [B, P] int32   3 lens [B] int32
+ *   4 pages_out [B, hk, C] int32   5 lens_out [B, hk] int32
+ * Candidates are the columns j < U = ceil(min(lens[r], P * page) / page) that are no
+ * holes, in all if they are at most C.  Else those among the first `first` and the last
+ * `last` of the U columns (first + last <= C), then the others by descending
+ *      score[h, j] = max over kv head h's query heads of sum_e max(q_e least_e, q_e largest_e)
+ * (what no key of the page can pass; sums of binary64, NaN the least) until they
+ * are C; the lower column wins a tie.  pages_out[r, h] names them by ascending column, then
+ * -1; lens_out is how many positions they hold: a table for cmd_paged_attention_heads.
+ * P <= 2^20. */
+int cmd_page_select(const cmd_arg args[6], int32_t page, int32_t first, int32_t last, void *workspace,
+                    int64_t workspace_bytes, int32_t flags, void *hip_stream);
+int64_t cmd_page_select_workspace(const cmd_arg args[6], int32_t page, int32_t first, int32_t last);
+
+/* The weight that attention gave to every page, added up.  args:
+ *   0 q [B, hq, d]   1 k_cache [N, page, hk, d]   2 pages [B, P] int32   3 lens [B] int32
+ *   4 lse [B, hq] f32   5 mass [B, P] f32   6 mass_out [B, P] f32 (may be the identical view as mass)
+ * with cmd_paged_attention's dtypes, positions and lse:
+ *      mass_out[r, j] = decay mass[r, j] + sum_h sum_x exp(scale q_h . k_x - lse[r, h])
+ * over the positions x of column j that row r attends to; heads whose lse is -inf add
+ * nothing.  Products and sums are binary32. */
+int cmd_page_mass(const cmd_arg args[7], float scale, float decay, int32_t window, int32_t flags, void *hip_stream);
+
+/* Take the pages of least mass out of rows that hold more than their budgets.  args:
+ *   0 pages [R, P] int32   1 lens [R] int32   2 refs [N] int32   3 mass [R, P] f32   4 budget [R] int32
+ *   5 pages_out [R, P] int32   6 refs_out [N] int32   7 count [R] int32
+ * Row r holds the columns j < U = ceil(min(lens[r], P * page) / page) that are no holes.
+ * While they are more than max(budget[r], 0), the one of least mass is taken out (the
+ * lower column wins a tie, NaN counts as more than any number), but for the first
+ * `first` and the last `last` of the U columns.  pages_out is the table with holes (-1) in
+ * their places (and where entries name no page), refs_out the counts less the entries
+ * taken out, count how many each row lost.  pages_out may be the identical view as
+ * pages, refs_out as refs.  P <= 2^20. */
+int cmd_page_evict(const cmd_arg args[8], int32_t page, int32_t first, int32_t last, int32_t flags, void *hip_stream);
 
 /* One step of a decode loop in the page tables: every sequence takes over its
  * parent's state (itself, another sequence: a fork, or none: it starts empty)
