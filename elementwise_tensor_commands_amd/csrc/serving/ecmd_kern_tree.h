@@ -14,8 +14,15 @@
 //   weights  exp2 of those in place, which makes them the operand of
 //   out      D[dv][query] += V^T P^T, with lane j loading the values of its keys.
 //
-// The four waves of a work-group split the positions where there are few queries,
-// and the queries where there are many.  Which tokens a token attends to is one bit
+// Two kernels.  k_tree_few takes keys and values from memory straight to registers;
+// the four waves of a work-group part the positions, or the queries where there are more.  It serves few queries,
+// where the caches' bytes are what counts, binary32, whose products run at a sixteenth of
+// the 16-bit rate and hide everything else, and rows off 16 bytes.  k_tree_many stages tiles of
+// 32 positions in LDS, once for all queries of a work-group, by loads from memory straight to
+// LDS that are two tiles ahead: three buffers (two of wide
+// heads), one barrier a tile.
+//
+// Which tokens a token attends to is one bit
 // mask per token, made in LDS from the parents by pointer doubling; a tile of 32
 // keys takes the 32 bits of it that lie above its keys, so only the tiles at the end
 // of a row (or at the start of a window) look at single keys.
@@ -156,16 +163,382 @@ __device__ inline uint32_t tree_share(const TreeArgs &A, const Rows &R)
     return R.longest <= 2 * share && A.b <= max(A.runs, A.runs_whole) ? 0 : share;
 }
 
-template <int TY, int NK, int VW, int NT>
-constexpr int tree_waves()
+
+// What a work-group does: the run of steps, its kv head and its block of queries.
+struct TreeRun {
+    uint32_t group, kvh, block;
+    uint32_t r, step, stop;
+    Rows R;
+};
+__device__ inline bool tree_run(const TreeArgs &A, uint32_t *s_rows, uint32_t *s_scratch, TreeRun &X)
+{
+    // Work-groups go to the eight dies in turn: those of a run follow each other on one.
+    const uint32_t u8 = A.by_units.div(blockIdx.x), in8 = blockIdx.x - u8 * A.by_units.d, unit = in8 / 8;
+    X.group = u8 * 8 + in8 % 8;
+    X.kvh = A.by_blocks.div(unit);
+    X.block = unit - X.kvh * A.q_blocks;
+    X.r = X.group;
+    X.step = X.stop = 0;
+    if (A.direct) return X.group < A.b;
+    X.R = make_rows(A, s_rows, s_scratch, tree_span);
+    const uint32_t share = tree_share(A, X.R);
+    if (share == 0) {
+        if (X.group >= A.b) return false;
+        X.step = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r]);
+        X.stop = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]);
+        return X.step != X.stop;
+    }
+    if ((uint64_t)X.group * share >= X.R.all) return false;
+    X.step = X.group * share;
+    X.stop = min(X.step + share, X.R.all);
+    uint32_t lo = 0, hi = A.b;   // the row with prefix[r] <= step < prefix[r + 1]
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (__builtin_amdgcn_readfirstlane(X.R.prefix[mid]) <= X.step) lo = mid;
+        else hi = mid;
+    }
+    X.r = lo;
+    return true;
+}
+// On to the next row of the run.
+__device__ inline bool tree_next(const TreeArgs &A, TreeRun &X, uint32_t steps)
+{
+    if (A.direct) return false;
+    X.step += steps;
+    if (X.step >= X.stop) return false;
+    do ++X.r;
+    while (__builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]) <= X.step);   // past empty rows
+    return true;
+}
+
+// One row of the run.
+struct Segment {
+    uint32_t begin, end, steps;
+    uint32_t len;                 // of the context
+    bool whole_row, last_part;
+};
+__device__ inline Segment tree_segment(const TreeArgs &A, const TreeRun &X)
+{
+    Segment S;
+    S.len = (uint32_t)A.lens[(int64_t)X.r * A.lens_s];   // negative: A.direct only, a row of padding
+    S.steps = 0;
+    S.whole_row = S.last_part = true;
+    if (A.direct) {
+        const Span span = tree_span(A, X.r);
+        S.begin = span.lo;
+        S.end = span.hi;
+    } else {
+        const uint32_t first = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r]);
+        const uint32_t last = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]);
+        const uint32_t here = min(X.stop, last), hi = __builtin_amdgcn_readfirstlane(X.R.hi[X.r]);
+        S.last_part = here == last;
+        S.whole_row = X.step == first && S.last_part;
+        S.steps = here - X.step;
+        S.begin = __builtin_amdgcn_readfirstlane(X.R.lo[X.r]) + (X.step - first) * kAttnStep;
+        S.end = min(S.begin + S.steps * kAttnStep, hi);
+    }
+    return S;
+}
+
+// The tree matters to the tiles past the context, to a window's start and to who is padding.
+__device__ inline bool tree_looks(const TreeArgs &A, const Segment &S)
+{
+    return S.last_part || A.window != 0 || S.end > S.len;
+}
+
+// Whether every query sees all of the TILE positions from t0 on, if they hold something.
+template <uint32_t TILE>
+__device__ inline bool tree_whole(const TreeArgs &A, uint32_t t0, uint32_t len)
+{
+    return t0 + TILE <= len && (A.window == 0 || t0 + A.window >= len + A.t);
+}
+// Which of the TILE positions from t0 on a token sees; lo: the first that its window holds.
+template <uint32_t TILE>
+__device__ inline uint32_t tree_sees(const uint32_t *mask, uint32_t words, uint32_t t0, uint32_t len, uint32_t lo)
+{
+    uint32_t see = ~0u;
+    if (t0 + TILE > len) {
+        if (t0 < len) {
+            see = (1u << (len - t0)) - 1 | mask[0] << (len - t0);   // len - t0 < TILE <= 32
+        } else {
+            const uint32_t o = t0 - len, at = o / 32;
+            const uint64_t two = (at < words ? mask[at] : 0) | (uint64_t)(at + 1 < words ? mask[at + 1] : 0) << 32;
+            see = (uint32_t)(two >> (o % 32));
+        }
+    }
+    if (lo > t0) see &= lo - t0 < 32 ? ~0u << (lo - t0) : 0;
+    return see;
+}
+
+// A lane's tile of queries: the token of its query and the first position of its window.
+struct Query {
+    uint32_t token, lo;
+};
+__device__ inline Query tree_query(const TreeArgs &A, uint32_t m, uint32_t len, const int32_t *s_info)
+{
+    Query Q{A.by_group.div(min(m, A.m - 1)), 0};
+    if (A.window) {
+        const uint32_t past = len + (uint32_t)max(s_info[Q.token], 0) + 1;
+        Q.lo = past > A.window ? past - A.window : 0;
+    }
+    return Q;
+}
+
+// Scores s of a tile to weights p: the running maximum m, its use mref, the sum l and the
+// sums acc follow.  see: which of the lane's keys the query sees (unless whole).
+template <int TY, int VK, int VW, int KB>
+__device__ inline void tree_weights(const f32x4 (&s)[KB], float (&p)[VK], f32x4 (&acc)[VW], float &m, float &mref, float &l,
+                                    float scale, bool whole, uint32_t see, uint32_t j)
+{
+    float x[VK], top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < VK; ++k) {
+        x[k] = s[k / 4][k % 4];
+        if (!whole) x[k] = see >> ((k / 4) * 16 + j * 4 + k % 4) & 1 ? x[k] : -INFINITY;
+        top = fmaxf(top, x[k]);
+    }
+    if (top != -INFINITY) top *= scale;   // (a scale of 0 times infinity)
+    if (__any(top > m + kTreeSlack<TY>)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m, top);
+        mref = mn == -INFINITY ? 0.0f : mn;
+        const float a = __builtin_amdgcn_exp2f(m - mref);
+        m = mn;
+        l *= a;
+#pragma unroll
+        for (int c = 0; c < VW; ++c) acc[c] *= a;
+    }
+    const float less = kTreeBias<TY> - mref;
+#pragma unroll
+    for (int k = 0; k < VK; ++k) {
+        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k], scale, less));
+        if (!whole) p[k] = see >> ((k / 4) * 16 + j * 4 + k % 4) & 1 ? p[k] : 0.0f;
+        l += p[k];
+    }
+}
+
+// A weight goes into the second product as the sum of two 16-bit numbers, its leading bits
+// and the rest: one would add its own rounding of half a step of the type to the
+// result's.  Both are positive wherever the weight is, since an infinite value times 0 would
+// be NaN: the rest is made 2^-20 of the weight larger, and binary16 has the smallest number
+// in place of 0 (only in tiles where every weight counts).
+template <int TY, int VK>
+__device__ inline void split_weights(const float (&p)[VK], u32x4 &hi, u32x4 &rest, bool whole)
+{
+    constexpr float more = 1.0f + 0x1p-20f;
+    const u16x2 least = __builtin_bit_cast(u16x2, whole ? 0x00010001u : 0u);
+#pragma unroll
+    for (int x = 0; x < VK; x += 2) {
+        const float f = p[x], g = p[x + 1];
+        if constexpr (TY == S_BF16) {
+            const uint32_t a = __builtin_bit_cast(uint32_t, f), b = __builtin_bit_cast(uint32_t, g);
+            hi[x / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);
+            rest[x / 2] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, __builtin_fmaf(g, more, -as_f(b & 0xFFFF0000u))),
+                                                __builtin_bit_cast(uint32_t, __builtin_fmaf(f, more, -as_f(a & 0xFFFF0000u))), 0x07060302);
+        } else {
+            // positive numbers order as their bits do
+            const f16x2 h = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(f, g));
+            const u16x2 e = __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf(f, more, -(float)h[0]),
+                                                                               __builtin_fmaf(g, more, -(float)h[1])));
+            hi[x / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, h), least));
+            rest[x / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, least));
+        }
+    }
+}
+
+template <int TY>
+constexpr uint32_t kTopExponent = TY == S_F16 ? 0x7C00u : TY == S_BF16 ? 0x7F80u : 0x7F800000u;
+
+// In a tile where some query does not see some key: clears the values of slots that hold
+// nothing (they may hold NaN), and says whether any left is no finite number.
+template <int TY, int VK, int VP, int PW>
+__device__ inline bool clear_values(u32x4 (&vr)[VK][VP], uint32_t now, uint32_t j)
+{
+    bool odd = false;
+#pragma unroll
+    for (int x = 0; x < VK; ++x) {
+        const uint32_t keep = now >> ((x / 4) * 16 + j * 4 + x % 4) & 1 ? ~0u : 0u;
+#pragma unroll
+        for (int c = 0; c < VP; ++c) {
+            vr[x][c] = vr[x][c] & u32x4{keep, keep, keep, keep};
+#pragma unroll
+            for (int w = 0; w < PW; ++w) {
+                odd |= (vr[x][c][w] & kTopExponent<TY>) == kTopExponent<TY>;
+                if constexpr (TY != S_F32) odd |= (vr[x][c][w] >> 16 & kTopExponent<TY>) == kTopExponent<TY>;
+            }
+        }
+    }
+    return odd;
+}
+
+// A weight of 0 times an infinity is NaN: where such values meet queries that do not see
+// them, a tile's values are added one by one.  At a row's end only, and hardly ever.
+template <int TY, int VK, int VW, class Column>
+__device__ inline void add_odd(const TreeArgs &A, uint32_t r, const char *vbase, uint32_t t0, uint32_t now, uint32_t see,
+                               const float (&p)[VK], f32x4 (&acc)[VW], uint32_t j, uint32_t hh, Column column)
+{
+    for (uint32_t key = 0; key < 4 * VK; ++key) {
+        if (!(now >> key & 1)) continue;
+        const uint32_t pos = t0 + key, col = A.by_page.div(pos);
+        const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
+        const char *v = vbase + (int64_t)id * A.vcs[0] + (int64_t)(pos - col * A.page) * A.vcs[1];
+        const int from = (int)((key % 16) / 4 * 16 + hh);
+        float w = 0.0f;
+#pragma unroll
+        for (int x = 0; x < VK; ++x)
+            if (key / 16 * 4 + key % 4 == (uint32_t)x) w = __shfl(p[x], from);   // key is uniform
+        if (see >> key & 1) {
+#pragma unroll
+            for (int c = 0; c < VW; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t at = column(j * 4 + i, c);
+                    if (at >= A.dv) continue;
+                    float value;
+                    if constexpr (TY == S_F32) value = ((const float *)v)[at];
+                    else if constexpr (TY == S_BF16) value = (float)((const __bf16 *)v)[at];
+                    else value = (float)((const _Float16 *)v)[at];
+                    acc[c][i] += w * value;
+                }
+        }
+    }
+}
+
+// Where a segment's sums go: out and lse, or a place of their own for the second launch
+// (work-groups and rows only go forward, so group + r is no other segment's).
+struct TreeOut {
+    uint32_t r, kvh;
+    uint64_t place;
+    bool whole_row, last_part, nobody;
+    const int32_t *info;
+};
+__device__ inline TreeOut tree_out(const TreeArgs &A, const TreeRun &X, const Segment &S, const int32_t *info)
+{
+    return TreeOut{X.r, X.kvh, (uint64_t)(X.group + X.r) * A.by_vectors.d + (uint64_t)X.kvh * A.m, S.whole_row, S.last_part,
+                   (int32_t)S.len < 0, info};
+}
+// query vector x's sum of weights; -1 for padding
+__device__ inline float known(const TreeArgs &A, const TreeOut &O, uint32_t x, float total)
+{
+    return O.last_part && (O.nobody || O.info[A.by_group.div(x)] < 0) ? -1.0f : total;
+}
+template <int TY>
+__device__ inline void put(const TreeArgs &A, const TreeOut &O, uint32_t x, uint32_t c, float sum, float total)
+{
+    if (!O.whole_row) {
+        A.acc[(O.place + x) * A.dv + c] = sum;
+        return;
+    }
+    const uint32_t tok = A.by_group.div(x), head = O.kvh * A.group + x - tok * A.group;
+    store_typed(TY, A.out, (int64_t)O.r * A.os[0] + (int64_t)tok * A.os[1] + (int64_t)head * A.os[2] + c,
+                total > 0.0f ? sum / total : total == 0.0f || total < 0.0f ? 0.0f : total);
+}
+template <int TY>
+__device__ inline void put_statistics(const TreeArgs &A, const TreeOut &O, uint32_t x, float top, float total)
+{
+    if (!O.whole_row) {
+        A.ml[2 * (O.place + x)] = top;
+        A.ml[2 * (O.place + x) + 1] = total;
+    } else if (A.lse) {
+        const uint32_t tok = A.by_group.div(x), head = O.kvh * A.group + x - tok * A.group;
+        A.lse[(int64_t)O.r * A.ls[0] + (int64_t)tok * A.ls[1] + (int64_t)head * A.ls[2]] = tree_log_sum<TY>(top, total);
+    }
+}
+
+// The sums of one tile of queries, q0 .. q0 + 15, out.  Waves with the same queries (every
+// hw-th of the four) join them through LDS first: common maximum, then sums, eight queries
+// at a time and four columns to a work-item.  All waves call it alike.
+template <int TY, int VW, bool TINY, class Column>
+__device__ inline void put_tile(const TreeArgs &A, const TreeOut &O, uint32_t q0, uint32_t hw, const f32x4 (&acc)[VW], float m,
+                                float l, uint32_t wave, uint32_t lane, float *s_join, float (*s_m)[16], float (*s_l)[16],
+                                Column column)
+{
+    constexpr uint32_t kRow = 16 * VW + 4;   // a query's row in the joining buffer (floats)
+    const uint32_t j = lane >> 4, hh = lane & 15, qw = wave & (hw - 1), part = wave / hw, parts = kAttnWaves / hw;
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (parts == 1) {
+        const uint32_t x = q0 + hh;
+        if (x < A.m) {
+            const float total = known(A, O, x, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < VW; ++c) {
+                    const uint32_t at = column(j * 4 + i, c);
+                    if (!TINY || at < A.dv) put<TY>(A, O, x, at, acc[c][i], total);
+                }
+            if (j == 0) put_statistics<TY>(A, O, x, m, total);
+        }
+        return;
+    }
+    __syncthreads();   // what lay in the buffer is done with
+    if (j == 0) {
+        s_m[wave][hh] = m;
+        s_l[wave][hh] = l;
+    }
+    __syncthreads();
+    float top = -INFINITY, total = 0.0f;
+    for (uint32_t w = qw; w < kAttnWaves; w += hw) top = fmaxf(top, s_m[w][hh]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    for (uint32_t w = qw; w < kAttnWaves; w += hw) total += s_l[w][hh] * __builtin_amdgcn_exp2f(s_m[w][hh] - ref);
+    const float factor = __builtin_amdgcn_exp2f(m - ref);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if (half) __syncthreads();
+        if ((hh >> 3) == (uint32_t)half) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < VW; ++c) s_join[(wave * 8 + (hh & 7)) * kRow + column(j * 4 + i, c)] = acc[c][i] * factor;
+        }
+        __syncthreads();
+        for (uint32_t y = part * 64 + lane; y < 8 * 4 * VW; y += parts * 64) {
+            const uint32_t g = y / (4 * VW), c = y % (4 * VW) * 4, x = q0 + half * 8 + g;
+            // lane g + 8 half of every wave of these has the statistics
+            const float all = __shfl(total, (int)(half * 8 + g)), best = __shfl(top, (int)(half * 8 + g));
+            if (x >= A.m) continue;
+            f32x4 sum = *(const f32x4 *)&s_join[(qw * 8 + g) * kRow + c];
+            for (uint32_t w = qw + hw; w < kAttnWaves; w += hw) sum += *(const f32x4 *)&s_join[(w * 8 + g) * kRow + c];
+            const float t = known(A, O, x, all);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+                if (c + k < A.dv) put<TY>(A, O, x, c + k, sum[k], t);
+            if (c == 0) put_statistics<TY>(A, O, x, best, t);
+        }
+    }
+}
+
+// Clears what an earlier piece has of piece c of a row of d elements, which was moved back
+// to end with the row.
+template <int E>
+__device__ inline u32x4 only_own(u32x4 x, int at, int d)
+{
+    const int twice = at - min(at, d - E);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if constexpr (E == 8)
+            x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
+        else
+            x[w] &= w >= twice ? ~0u : 0u;
+    }
+    return x;
+}
+
+// ---------------------------------------------------------------------------
+// Few queries, or binary32.
+
+template <int TY, int NK, int VW>
+constexpr int few_waves()
 {
     constexpr int KB = AttnType<TY>::KB, size = TY == S_F32 ? 4 : 2;
-    constexpr int regs = KB * NK * 4 + KB * VW * size + NT * (NK * 4 + VW * 4 + KB * 8) + 60;
+    constexpr int regs = KB * NK * 4 + KB * VW * size + NK * 4 + VW * 4 + KB * 8 + 60;
     return regs > 236 ? 1 : 2;
 }
 
-template <int TY, int NK, int VW, AttnEdge EDGE, int NT>
-__global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_tree(const TreeArgs A)
+template <int TY, int NK, int VW, AttnEdge EDGE>
+__global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_few(const TreeArgs A)
 {
     typedef typename AttnType<TY>::T T;
     constexpr int E = AttnType<TY>::E, KB = AttnType<TY>::KB;
@@ -173,14 +546,13 @@ __global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_
     constexpr int PE = VW < E ? VW : E, VP = VW / PE;   // elements of a value piece; pieces
     constexpr int PW = PE * (int)sizeof(T) / 4;         // words of a value piece
     constexpr uint32_t kTile = 16 * KB;
-    constexpr int kRow = 16 * VW + 4;                   // a query's row in the joining buffer (floats)
 
     __shared__ union {
         struct {
             uint64_t k[kAttnWaves][kTableKeys], v[kAttnWaves][kTableKeys];
             uint64_t valid[kAttnWaves][kTableKeys / 64];
         } table;
-        __attribute__((aligned(16))) float join[kAttnWaves][8][kRow];
+        __attribute__((aligned(16))) float join[kAttnWaves * 8 * (16 * VW + 4)];
     } sh;
     __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
     __shared__ uint32_t s_mask[kMaxTree * kTreeWords], s_real[kTreeWords];
@@ -192,126 +564,54 @@ __global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Tree tree{s_mask, s_info, s_real};
     const uint32_t words = (A.t + 31) / 32;
-
-    // Work-groups go to the eight dies in turn: those of a run follow each other on one.
-    const uint32_t u8 = A.by_units.div(blockIdx.x), in8 = blockIdx.x - u8 * A.by_units.d;
-    const uint32_t group = u8 * 8 + in8 % 8, unit = in8 / 8;
-    const uint32_t kvh = A.by_blocks.div(unit), block = unit - kvh * A.q_blocks;
-    uint32_t r, step = 0, stop = 0;
-    Rows R{};
-    if (A.direct) {
-        if (group >= A.b) return;
-        r = group;
-    } else {
-        R = make_rows(A, s_rows, s_scratch, tree_span);
-        const uint32_t share = tree_share(A, R);
-        if (share == 0) {
-            if (group >= A.b) return;
-            r = group;
-            step = __builtin_amdgcn_readfirstlane(R.prefix[r]);
-            stop = __builtin_amdgcn_readfirstlane(R.prefix[r + 1]);
-            if (step == stop) return;
-        } else {
-            if ((uint64_t)group * share >= R.all) return;
-            step = group * share;
-            stop = min(step + share, R.all);
-            uint32_t lo = 0, hi = A.b;   // the row with prefix[r] <= step < prefix[r + 1]
-            while (hi - lo > 1) {
-                const uint32_t mid = (lo + hi) / 2;
-                if (__builtin_amdgcn_readfirstlane(R.prefix[mid]) <= step) lo = mid;
-                else hi = mid;
-            }
-            r = lo;
-        }
-    }
+    TreeRun X;
+    if (!tree_run(A, s_rows, s_scratch, X)) return;
     const uint32_t qw = wave & ((1u << A.q_shift) - 1), part = wave >> A.q_shift, parts = kAttnWaves >> A.q_shift;
-    const uint32_t q0 = ((block << A.q_shift) + qw) * (16 * NT);   // the wave's first query vector
+    const uint32_t q0 = ((X.block << A.q_shift) + qw) * 16;   // the wave's first query vector
 
-    auto column = [&](uint32_t m, int piece) {
-        const uint32_t at = (piece * 16 + m) * PE;
-        return EDGE == kTiny ? at : min(at, A.dv - PE);
+    // Element c of the value piece of product c at row m of the result.
+    auto column = [&](uint32_t m, int c) {
+        const uint32_t at = (c / PE * 16 + m) * PE;
+        return (EDGE == kTiny ? at : min(at, A.dv - PE)) + c % PE;
     };
     auto load_row_piece = [&](const char *p, int c) {
         const int at = (c * 4 + (int)j) * E;
         if constexpr (EDGE == kTiny) return load_some<T, E>(p + at * sizeof(T), (int)A.d - at);
         return load16(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
     };
-    // clears what an earlier piece has of one that was moved back to end with the row
     auto masked = [&](u32x4 x, int c) {
-        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {
-            const int at = (c * 4 + (int)j) * E, twice = at - min(at, (int)A.d - E);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if constexpr (E == 8)
-                    x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
-                else
-                    x[w] &= w >= twice ? ~0u : 0u;
-            }
-        }
+        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) x = only_own<E>(x, (c * 4 + (int)j) * E, (int)A.d);
         return x;
     };
 
-    const char *kbase = (const char *)A.k + (int64_t)kvh * A.kcs[2];
-    const char *vbase = (const char *)A.v + (int64_t)kvh * A.vcs[2];
+    const char *kbase = (const char *)A.k + (int64_t)X.kvh * A.kcs[2];
+    const char *vbase = (const char *)A.v + (int64_t)X.kvh * A.vcs[2];
 
     for (;;) {   // one row of the run
-        const uint32_t len = (uint32_t)A.lens[(int64_t)r * A.lens_s];   // negative rows have no steps
-        uint32_t begin, end, steps = 0;
-        bool whole_row = true, last_part = true;
-        if (A.direct) {
-            const Span span = tree_span(A, r);
-            begin = span.lo;
-            end = span.hi;
-        } else {
-            const uint32_t first = __builtin_amdgcn_readfirstlane(R.prefix[r]);
-            const uint32_t last = __builtin_amdgcn_readfirstlane(R.prefix[r + 1]);
-            const uint32_t here = min(stop, last), hi = __builtin_amdgcn_readfirstlane(R.hi[r]);
-            last_part = here == last;
-            whole_row = step == first && last_part;
-            steps = here - step;
-            begin = __builtin_amdgcn_readfirstlane(R.lo[r]) + (step - first) * kAttnStep;
-            end = min(begin + steps * kAttnStep, hi);
-        }
-        const bool nobody = (int32_t)len < 0;   // A.direct only: a row of padding
-        // the tree matters to the tiles past the context, to a window's start and to who is padding
-        const bool looks = last_part || A.window != 0 || end > len;
-        if (looks) make_tree(A, r, tree);
-
-        uint32_t wb = begin, we = end;
+        const Segment S = tree_segment(A, X);
+        const uint32_t r = X.r, len = S.len;
+        if (tree_looks(A, S)) make_tree(A, r, tree);
+        uint32_t wb = S.begin, we = S.end;
         if (parts > 1) {
-            const uint32_t each = (end - begin + parts * kTile - 1) / (parts * kTile) * kTile;
-            wb = min(begin + part * each, end);
-            we = min(wb + each, end);
+            const uint32_t each = (we - wb + parts * kTile - 1) / (parts * kTile) * kTile;
+            wb = min(S.begin + part * each, S.end);
+            we = min(wb + each, S.end);
         }
         if (q0 >= A.m) we = wb;   // no queries of this wave's
 
-        u32x4 q[NT][NK];
-        uint32_t token[NT], lo[NT];   // of the lane's queries: the token, the first position that counts
+        u32x4 q[NK];
+        const Query Q = tree_query(A, q0 + hh, len, s_info);
+        {
+            const uint32_t head = X.kvh * A.group + min(q0 + hh, A.m - 1) - Q.token * A.group;
+            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)Q.token * A.qs[1] + (int64_t)head * A.qs[2]) * sizeof(T);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t m = min(q0 + n * 16 + hh, A.m - 1);
-            token[n] = A.by_group.div(m);
-            const uint32_t head = kvh * A.group + m - token[n] * A.group;
-            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)token[n] * A.qs[1] + (int64_t)head * A.qs[2]) * sizeof(T);
-#pragma unroll
-            for (int c = 0; c < NK; ++c) q[n][c] = masked(load_row_piece(p, c), c) ^ u32x4{A.q_flip, A.q_flip, A.q_flip, A.q_flip};
-            lo[n] = 0;
-            if (A.window) {
-                const uint32_t past = len + (uint32_t)max(s_info[token[n]], 0) + 1;
-                lo[n] = past > A.window ? past - A.window : 0;
-            }
+            for (int c = 0; c < NK; ++c) q[c] = masked(load_row_piece(p, c), c) ^ u32x4{A.q_flip, A.q_flip, A.q_flip, A.q_flip};
         }
 
-        f32x4 acc[NT][VW];
-        float m[NT], mref[NT], l[NT];
+        f32x4 acc[VW];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n] = -INFINITY;
-            mref[n] = 0.0f;
-            l[n] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < VW; ++c) acc[n][c] = f32x4{0, 0, 0, 0};
-        }
+        for (int c = 0; c < VW; ++c) acc[c] = f32x4{0, 0, 0, 0};
+        float m = -INFINITY, mref = 0.0f, l = 0.0f;
 
         // Offsets of the wave's next kTableKeys positions; what is no position of
         // this row's gets slot 0 of page 0, which exists, and a clear bit.
@@ -360,7 +660,7 @@ __global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_
                 const char *p = vbase + sh.table.v[wave][t + (x / 4) * 16 + j * 4 + x % 4];
 #pragma unroll
                 for (int c = 0; c < VP; ++c) {
-                    const uint32_t at = column(hh, c);
+                    const uint32_t at = column(hh, c * PE);
                     if constexpr (EDGE == kTiny)
                         vr[x][c] = load_some<T, PE>(p + at * sizeof(T), (int)A.dv - (int)at);
                     else if constexpr (PE * sizeof(T) == 16)
@@ -378,27 +678,22 @@ __global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_
             load_v(0);
         }
         while (tile < we) {
-            f32x4 s[NT][KB];
+            f32x4 s[KB];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) s[n][kb] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < KB; ++kb) {
+                s[kb] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < NK; ++c) {
                     const u32x4 k = masked(kr[kb][c], c);
+                    if constexpr (TY == S_F32) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if constexpr (TY == S_F32) {
-#pragma unroll
-                            for (int f = 0; f < 4; ++f)
-                                s[n][kb] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(k[f]), as_f(q[n][c][f]), s[n][kb], 0, 0, 0);
-                        } else {
-                            s[n][kb] = mma16<TY>(k, q[n][c], s[n][kb]);
-                        }
+                        for (int f = 0; f < 4; ++f)
+                            s[kb] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(k[f]), as_f(q[c][f]), s[kb], 0, 0, 0);
+                    } else {
+                        s[kb] = mma16<TY>(k, q[c], s[kb]);
                     }
                 }
+            }
             const uint32_t now = bits, t0 = tile;
             tile += kTile;
             in_table += kTile;
@@ -409,162 +704,27 @@ __global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_
                 }
                 load_k(in_table);
             }
-
             // Single keys matter past the context, at a window's start and at holes.
-            const bool whole = now == (KB == 2 ? 0xFFFFFFFFu : 0xFFFFu) && t0 + kTile <= len &&
-                               (A.window == 0 || t0 + A.window >= len + A.t);
-            uint32_t allow[NT];
-            bool odd = false;   // some query leaves out a value that is no finite number
+            const bool whole = now == (KB == 2 ? 0xFFFFFFFFu : 0xFFFFu) && tree_whole<kTile>(A, t0, len);
+            uint32_t see = 0;
+            bool odd = false;
             if (!whole) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    uint32_t see = ~0u;
-                    if (t0 + kTile > len) {
-                        const uint32_t *w = s_mask + token[n] * words;
-                        if (t0 < len) {
-                            see = (1u << (len - t0)) - 1 | w[0] << (len - t0);   // len - t0 < kTile <= 32
-                        } else {
-                            const uint32_t o = t0 - len, at = o / 32;
-                            const uint64_t two = (at < words ? w[at] : 0) | (uint64_t)(at + 1 < words ? w[at + 1] : 0) << 32;
-                            see = (uint32_t)(two >> (o % 32));
-                        }
-                    }
-                    if (lo[n] > t0) see &= lo[n] - t0 < 32 ? ~0u << (lo[n] - t0) : 0;
-                    allow[n] = see & now;
-                }
-#pragma unroll
-                for (int x = 0; x < VK; ++x) {
-                    // a slot that holds nothing may hold NaN: its value is cleared
-                    const bool ok = now >> ((x / 4) * 16 + j * 4 + x % 4) & 1;
-                    const uint32_t keep = ok ? ~0u : 0u;
-#pragma unroll
-                    for (int c = 0; c < VP; ++c) {
-                        vr[x][c] = vr[x][c] & u32x4{keep, keep, keep, keep};
-                        constexpr uint32_t top = TY == S_F16 ? 0x7C00u : TY == S_BF16 ? 0x7F80u : 0x7F800000u;
-#pragma unroll
-                        for (int w = 0; w < PW; ++w) {
-                            odd |= (vr[x][c][w] & top) == top;
-                            if constexpr (TY != S_F32) odd |= (vr[x][c][w] >> 16 & top) == top;
-                        }
-                    }
-                }
+                see = now & tree_sees<kTile>(s_mask + Q.token * words, words, t0, len, Q.lo);
+                odd = __any(clear_values<TY, VK, VP, PW>(vr, now, j));
             }
-
-            float p[NT][VK];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < VK; ++x) {
-                    p[n][x] = s[n][x / 4][x % 4] * A.scale_log2;
-                    if (!whole) p[n][x] = allow[n] >> ((x / 4) * 16 + j * 4 + x % 4) & 1 ? p[n][x] : -INFINITY;
-                    top = fmaxf(top, p[n][x]);
-                }
-                if (__any(top > m[n] + kTreeSlack<TY>)) {
-                    top = fmaxf(top, __shfl_xor(top, 16));
-                    top = fmaxf(top, __shfl_xor(top, 32));
-                    const float mn = fmaxf(m[n], top);
-                    mref[n] = mn == -INFINITY ? 0.0f : mn;
-                    const float a = __builtin_amdgcn_exp2f(m[n] - mref[n]);
-                    m[n] = mn;
-                    l[n] *= a;
-#pragma unroll
-                    for (int c = 0; c < VW; ++c) acc[n][c] *= a;
-                }
-#pragma unroll
-                for (int x = 0; x < VK; ++x) {
-                    p[n][x] = __builtin_amdgcn_exp2f(p[n][x] - (mref[n] - kTreeBias<TY>));
-                    l[n] += p[n][x];
-                }
-            }
-
-            // A weight of 0 times an infinity is NaN: where a query leaves such a value
-            // out, all values of that kind are taken out of the products and added one
-            // by one.  Tiles at a row's end only, and hardly ever.
-            if (!whole && __any(odd)) {
-                for (uint32_t key = 0; key < kTile; ++key) {
-                    if (!(now >> key & 1)) continue;
-                    const uint32_t pos = t0 + key, col = A.by_page.div(pos);
-                    const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
-                    const char *v = vbase + (int64_t)id * A.vcs[0] + (int64_t)(pos - col * A.page) * A.vcs[1];
-                    const uint32_t from = (key % 16) / 4 * 16 + hh;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float w = 0.0f;
-#pragma unroll
-                        for (int x = 0; x < VK; ++x) {
-                            const float got = __shfl(p[n][x], (int)from);
-                            if (key / 16 * 4 + key % 4 == (uint32_t)x) w = got;
-                        }
-                        if (!(allow[n] >> key & 1)) continue;
-#pragma unroll
-                        for (int c = 0; c < VW; ++c)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t at = column(j * 4 + i, c / PE) + c % PE;
-                                if (at >= A.dv) continue;
-                                float value;
-                                if constexpr (TY == S_F32) value = ((const float *)v)[at];
-                                else if constexpr (TY == S_BF16) value = (float)((const __bf16 *)v)[at];
-                                else value = (float)((const _Float16 *)v)[at];
-                                if (!(fabsf(value) < INFINITY)) acc[n][c][i] += w * value;
-                            }
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < VK; ++x)
-#pragma unroll
-                    for (int c = 0; c < VP; ++c)
-#pragma unroll
-                        for (int w = 0; w < PW; ++w) {
-                            constexpr uint32_t top = TY == S_F16 ? 0x7C00u : TY == S_BF16 ? 0x7F80u : 0x7F800000u;
-                            uint32_t y = vr[x][c][w];
-                            if ((y & top) == top) y &= TY == S_F32 ? 0u : 0xFFFF0000u;
-                            if constexpr (TY != S_F32)
-                                if ((y >> 16 & top) == top) y &= 0xFFFFu;
-                            vr[x][c][w] = y;
-                        }
-            }
-
-            if constexpr (TY == S_F32) {
+            float p[VK];
+            tree_weights<TY, VK, VW, KB>(s, p, acc, m, mref, l, A.scale_log2, whole, see, j);
+            if (odd) {
+                add_odd<TY, VK, VW>(A, r, vbase, t0, now, see, p, acc, j, hh, column);
+            } else if constexpr (TY == S_F32) {
 #pragma unroll
                 for (int x = 0; x < VK; ++x)
 #pragma unroll
                     for (int c = 0; c < VW; ++c)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            acc[n][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(vr[x][c / 4][c % 4]), p[n][x], acc[n][c], 0, 0, 0);
+                        acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(vr[x][c / 4][c % 4]), p[x], acc[c], 0, 0, 0);
             } else {
-                // A weight goes in as the sum of two 16-bit numbers, its leading bits and the
-                // rest: one would add its own rounding of half a step of the type to the result's.
-                // Both are positive wherever the weight is (bfloat16: the rest at least 2^-20 of the
-                // leading part; binary16: the smallest number), since an infinite value times 0
-                // would be NaN.
-                u32x4 hi[NT], rest[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int x = 0; x < VK; x += 2) {
-                        const float f = p[n][x], g = p[n][x + 1];
-                        const uint32_t a = __builtin_bit_cast(uint32_t, f), b = __builtin_bit_cast(uint32_t, g);
-                        if constexpr (TY == S_BF16) {
-                            const uint32_t h = __builtin_amdgcn_perm(b, a, 0x07060302);
-                            const uint32_t e = __builtin_amdgcn_perm(
-                                __builtin_bit_cast(uint32_t, g - as_f(b & 0xFFFF0000u)),
-                                __builtin_bit_cast(uint32_t, f - as_f(a & 0xFFFF0000u)), 0x07060302);
-                            const u16x2 least = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, h), u16x2{20 << 7, 20 << 7});
-                            hi[n][x / 2] = h;
-                            rest[n][x / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, e), least));
-                        } else {
-                            // positive numbers order as their bits do
-                            const u16x2 least = __builtin_bit_cast(u16x2, min(a, 1u) | min(b, 1u) << 16);
-                            const u16x2 h = __builtin_elementwise_max(__builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(f, g)), least);
-                            const f16x2 hf = __builtin_bit_cast(f16x2, h);
-                            const u16x2 e = __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(fmaxf(f - (float)hf[0], 0.0f), fmaxf(g - (float)hf[1], 0.0f)));
-                            hi[n][x / 2] = __builtin_bit_cast(uint32_t, h);
-                            rest[n][x / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, least));
-                        }
-                    }
+                u32x4 hi, rest;
+                split_weights<TY, VK>(p, hi, rest, whole);
 #pragma unroll
                 for (int c = 0; c < VW; ++c) {
                     u32x4 a;
@@ -572,135 +732,360 @@ __global__ __launch_bounds__(kAttnBlock, (tree_waves<TY, NK, VW, NT>())) void k_
                     for (int w = 0; w < 4; ++w)
                         a[w] = __builtin_amdgcn_perm(vr[2 * w + 1][c / 8][c % 8 / 2], vr[2 * w][c / 8][c % 8 / 2],
                                                      c & 1 ? 0x07060302 : 0x05040100);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, rest[n], acc[n][c]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, hi[n], acc[n][c]);
+                    acc[c] = mma16<TY>(a, rest, acc[c]);
+                    acc[c] = mma16<TY>(a, hi, acc[c]);
                 }
             }
             if (tile < we) load_v(in_table);
         }
-
-        // The segment's sums: final, or for the second launch at a place of its own
-        // (work-groups and rows only go forward).
-        const uint64_t place = (uint64_t)(group + r) * A.by_vectors.d + (uint64_t)kvh * A.m;
-        auto put = [&](uint32_t x, uint32_t c, float sum, float total) {   // query vector x
-            if (!whole_row) {
-                A.acc[(place + x) * A.dv + c] = sum;
-                return;
-            }
-            const uint32_t tok = A.by_group.div(x), head = kvh * A.group + x - tok * A.group;
-            store_typed(TY, A.out, (int64_t)r * A.os[0] + (int64_t)tok * A.os[1] + (int64_t)head * A.os[2] + c,
-                        total > 0.0f ? sum / total : total == 0.0f || total < 0.0f ? 0.0f : total);
-        };
-        auto put_statistics = [&](uint32_t x, float top, float total) {
-            if (!whole_row) {
-                A.ml[2 * (place + x)] = top;
-                A.ml[2 * (place + x) + 1] = total;
-            } else if (A.lse) {
-                const uint32_t tok = A.by_group.div(x), head = kvh * A.group + x - tok * A.group;
-                A.lse[(int64_t)r * A.ls[0] + (int64_t)tok * A.ls[1] + (int64_t)head * A.ls[2]] = tree_log_sum<TY>(top, total);
-            }
-        };
-        // the sum of weights, -1 for padding
-        auto known = [&](uint32_t x, float total) {
-            return last_part && (nobody || s_info[A.by_group.div(x)] < 0) ? -1.0f : total;
-        };
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            l[n] += __shfl_xor(l[n], 16);
-            l[n] += __shfl_xor(l[n], 32);
-        }
-        if (parts == 1) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint32_t x = q0 + n * 16 + hh;
-                if (x < A.m) {
-                    const float total = known(x, l[n]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int c = 0; c < VW; ++c) {
-                            const uint32_t at = column(j * 4 + i, c / PE) + c % PE;
-                            if (EDGE != kTiny || at < A.dv) put(x, at, acc[n][c][i], total);
-                        }
-                    if (j == 0) put_statistics(x, m[n], total);
-                }
-            }
-        } else {
-            // Waves with the same queries: common maximum, then sums through LDS, eight
-            // queries at a time and four columns to a work-item.
-            const uint32_t hw = 1u << A.q_shift;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if ((uint32_t)n * 16 >= A.m) break;   // the same for all waves: barriers follow
-                __syncthreads();   // the tables, or the buffers, are done with
-                if (j == 0) {
-                    s_m[wave][hh] = m[n];
-                    s_l[wave][hh] = l[n];
-                }
-                __syncthreads();
-                float top = -INFINITY, total = 0.0f;
-                for (uint32_t w = qw; w < kAttnWaves; w += hw) top = fmaxf(top, s_m[w][hh]);
-                const float ref = top == -INFINITY ? 0.0f : top;
-                for (uint32_t w = qw; w < kAttnWaves; w += hw) total += s_l[w][hh] * __builtin_amdgcn_exp2f(s_m[w][hh] - ref);
-                const float factor = __builtin_amdgcn_exp2f(m[n] - ref);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half) __syncthreads();
-                    if ((hh >> 3) == (uint32_t)half) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int c = 0; c < VW; ++c)
-                                sh.join[wave][hh & 7][column(j * 4 + i, c / PE) + c % PE] = acc[n][c][i] * factor;
-                    }
-                    __syncthreads();
-                    for (uint32_t y = part * 64 + lane; y < 8 * 4 * VW; y += parts * 64) {
-                        const uint32_t g = y / (4 * VW), c = y % (4 * VW) * 4, x = q0 + n * 16 + half * 8 + g;
-                        // lane g + 8 half of every wave of these has the statistics
-                        const float all = __shfl(total, (int)(half * 8 + g)), best = __shfl(top, (int)(half * 8 + g));
-                        if (x >= A.m) continue;
-                        f32x4 sum = *(const f32x4 *)&sh.join[qw][g][c];
-                        for (uint32_t w = qw + hw; w < kAttnWaves; w += hw) sum += *(const f32x4 *)&sh.join[w][g][c];
-                        const float t = known(x, all);
-#pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k)
-                            if (c + k < A.dv) put(x, c + k, sum[k], t);
-                        if (c == 0) put_statistics(x, best, t);
-                    }
-                }
-            }
-        }
-        if (A.direct) return;
-        step += steps;
-        if (step >= stop) return;
-        do ++r;
-        while (__builtin_amdgcn_readfirstlane(R.prefix[r + 1]) <= step);   // past empty rows
+        put_tile<TY, VW, EDGE == kTiny>(A, tree_out(A, X, S, s_info), q0, 1u << A.q_shift, acc, m, l, wave, lane, sh.join, s_m, s_l, column);
+        if (!tree_next(A, X, S.steps)) return;
         __syncthreads();
     }
 }
 
-template <int TY, int NK, int VW, AttnEdge EDGE>
-int launch_tree_one(const TreeArgs &A, void *stream)
+// ---------------------------------------------------------------------------
+// Many queries of 16 bits.
+
+constexpr uint32_t kStageKeys = 32, kStageTable = 256;   // positions of a tile; whose places are known ahead
+
+// 16 bytes from each lane's p to LDS, from address lds on, in the order of the lanes.  Written
+// out, for the compiler would let every later read of LDS wait for it: it does not
+// know that the buffers are read in turn.  wait_loads waits.  (No register is written but m0,
+// which holds the address, 16 bits of it, and which nothing else here uses.)
+__device__ inline void load_to_lds(const char *p, uint32_t lds)
 {
-    const void *fn = reinterpret_cast<const void *>(&k_tree<TY, NK, VW, EDGE, 1>);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
+}
+
+__device__ __attribute__((aligned(256))) const uint32_t g_zeros[128] = {};   // a row of a slot that holds nothing
+
+// The 16-byte pieces of a key of PIECES are rotated by a number that the key gives, so that
+// sixteen keys' pieces at one index lie in different banks (but for a few where PIECES is no
+// power of two).  Those of a value of PIECES are exchanged, two by two, so that what a
+// transposing read takes of four keys does.
+template <uint32_t PIECES>
+__device__ inline uint32_t key_turn(uint32_t key)
+{
+    return PIECES % 16 == 0 ? key & 15 : PIECES % 8 == 0 ? key >> 1 & 7 : key >> 2 & 3;
+}
+template <uint32_t PIECES>
+__device__ inline uint32_t value_turn(uint32_t key)
+{
+    return 2 * key & (PIECES - 1);
+}
+
+// Lane h of 16 gets element h of four rows, of which lane s reads four elements: number
+// 4 (s % 4) on, of row s / 4.  Two of them are the first operand of a product over 32 keys.
+__device__ inline u32x4 read_transposed(const char *low, const char *high)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 *Ptr;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)low));
+    const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)high));
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// A lane's number that the compiler is to keep, not to make anew.
+__device__ inline uint32_t kept(uint32_t x)
+{
+    asm("" : "+v"(x));
+    return x;
+}
+
+// All of the LDS traffic so far is done, and all but N of the loads (to LDS too).  (The
+// instruction's fields: bits 3:0 and 15:14 loads, 6:4 exports, 11:8 LDS.)
+template <int N>
+__device__ inline void wait_loads()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);
+    asm volatile("" ::: "memory");
+}
+__device__ inline void group_barrier()
+{
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Rows' starts are multiples of 16 bytes and so are d and dv (of 2-byte elements): see
+// plan_tree.  NK: 32 elements of a key; VW: 16 of a value; NT: tiles of 16 queries of a wave.
+template <int TY, int NK, int VW, int NT>
+__global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void k_tree_many(const TreeArgs A)
+{
+    typedef uint16_t T;
+    constexpr int KB = 2, VK = 8;
+    constexpr uint32_t KP = 4 * NK, VPieces = 2 * VW;                // 16-byte pieces of a key and of a value
+    constexpr uint32_t kLoads = 2 * NK + VW;                         // of 1024 bytes: a tile's keys, then its values
+    constexpr int KU = (2 * NK + 3) / 4, VU = (VW + 3) / 4, PER = KU + VU;   // of a wave
+    static_assert(kAttnWaves == 4);
+
+    // Tiles' buffers: their places count 16 bits in a load to LDS, so they come first (by
+    // their alignment) and end within 64 KiB.
+    constexpr uint32_t kRing = kLoads * 3 <= 64 ? 3 : 2, kAhead = kRing - 1;
+    static_assert(kLoads * kRing <= 64);
+    __shared__ __attribute__((aligned(1024))) char s_ring[kRing][kLoads * 1024];
+    __shared__ uint64_t s_k[2][kStageTable], s_v[2][kStageTable];    // where a position's key and value lie
+    __shared__ uint32_t s_valid[2][kStageTable / kStageKeys];
+    __shared__ uint32_t s_mask[kMaxTree * kTreeWords], s_real[kTreeWords];
+    __shared__ int32_t s_info[kMaxTree];
+    extern __shared__ uint32_t s_rows[];   // unless A.direct
+    __shared__ uint32_t s_scratch[kAttnWaves];
+
+    const uint32_t tid = threadIdx.x, lane = tid & 63, j = lane >> 4, hh = lane & 15;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Tree tree{s_mask, s_info, s_real};
+    const uint32_t words = (A.t + 31) / 32;
+    TreeRun X;
+    if (!tree_run(A, s_rows, s_scratch, X)) return;
+    const uint32_t q0 = (X.block * kAttnWaves + wave) * (16 * NT);   // the wave's first query vector
+
+    auto column = [&](uint32_t m, int c) { return (uint32_t)c * 16 + m; };
+    const char *kbase = (const char *)A.k + (int64_t)X.kvh * A.kcs[2];
+    const char *vbase = (const char *)A.v + (int64_t)X.kvh * A.vcs[2];
+
+    // What the lane reads of a tile: pieces c * 4 + j of key hh (and 16 + hh); of the values of
+    // keys 4 j + hh / 4 (and + 16) four elements for each product.
+    uint32_t k_at[NK], v_at[VW];
+#pragma unroll
+    for (int c = 0; c < NK; ++c) k_at[c] = (hh * KP + (c * 4 + j + key_turn<KP>(hh)) % KP) * 16;
+#pragma unroll
+    for (int c = 0; c < VW; ++c) {
+        const uint32_t key = j * 4 + hh / 4;
+        v_at[c] = 2 * NK * 1024 + (key * VPieces + ((2 * c + (hh & 3) / 2) ^ value_turn<VPieces>(key))) * 16 + (hh & 1) * 8;
+    }
+    // What it loads: places in LDS go up with the lanes; of which key, and which of its bytes
+    // (kNone: past a key's end, zeros).
+    constexpr uint32_t kNone = ~0u;
+    uint32_t k_key[KU], k_of[KU], v_key[VU], v_of[VU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+        const uint32_t x = min(u * kAttnWaves + wave, 2u * NK - 1) * 64 + lane, key = x / KP;
+        const uint32_t piece = (x - key * KP + KP - key_turn<KP>(key)) % KP;
+        k_key[u] = kept(key);
+        k_of[u] = kept(piece * 8 < A.d ? piece * 16 : kNone);
+    }
+#pragma unroll
+    for (int u = 0; u < VU; ++u) {
+        const uint32_t x = (u * kAttnWaves + wave) * 64 + lane, key = x / VPieces, piece = (x - key * VPieces) ^ value_turn<VPieces>(key);
+        v_key[u] = kept(key);
+        v_of[u] = kept(piece * 8 < A.dv ? piece * 16 : 0);   // (of columns past the end nothing is kept)
+    }
+    const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)&s_ring[0][0];
+
+    for (;;) {   // one row of the run
+        const Segment S = tree_segment(A, X);
+        const uint32_t r = X.r, len = S.len;
+        if (tree_looks(A, S)) make_tree(A, r, tree);
+
+        u32x4 q[NT][NK];
+        Query Q[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t m = min(q0 + n * 16 + hh, A.m - 1);
+            Q[n] = tree_query(A, m, len, s_info);
+            const uint32_t head = X.kvh * A.group + m - Q[n].token * A.group;
+            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)Q[n].token * A.qs[1] + (int64_t)head * A.qs[2]) * sizeof(T);
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+                const uint32_t at = (c * 4 + j) * 8;
+                q[n][c] = u32x4{0, 0, 0, 0};
+                if (at < A.d) q[n][c] = load16(p + at * sizeof(T)) ^ u32x4{A.q_flip, A.q_flip, A.q_flip, A.q_flip};
+            }
+        }
+        f32x4 acc[NT][VW];
+        float m[NT], mref[NT], l[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n] = -INFINITY;
+            mref[n] = 0.0f;
+            l[n] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < VW; ++c) acc[n][c] = f32x4{0, 0, 0, 0};
+        }
+
+        const uint32_t tiles = (S.end - S.begin + kStageKeys - 1) / kStageKeys;
+        constexpr uint32_t kChunk = kStageTable / kStageKeys;   // tiles whose places a table holds
+        // Pages of positions 256 chunk + tid of the segment: looked up a chunk ahead.
+        auto look = [&](uint32_t chunk) {
+            const uint32_t pos = min(S.begin + chunk * kStageTable + tid, S.end - 1);
+            return A.pages[(int64_t)r * A.pages_s[0] + (int64_t)A.by_page.div(pos) * A.pages_s[1]];
+        };
+        auto note = [&](uint32_t chunk, int32_t id) {
+            const uint32_t pos = S.begin + chunk * kStageTable + tid;
+            bool ok = pos < S.end && id >= 0 && (uint32_t)id < A.n;
+            if (pos >= len && ok) ok = s_real[(pos - len) / 32] >> ((pos - len) % 32) & 1;   // pos < len + t
+            const int64_t page = id, slot = pos - A.by_page.div(pos) * A.page;
+            s_k[chunk & 1][tid] = (uint64_t)(ok ? kbase + page * A.kcs[0] + slot * A.kcs[1] : (const char *)g_zeros);
+            s_v[chunk & 1][tid] = (uint64_t)(ok ? vbase + page * A.vcs[0] + slot * A.vcs[1] : (const char *)g_zeros);
+            const uint64_t bits = __ballot(ok);
+            if (lane == 0) {
+                s_valid[chunk & 1][wave * 2] = (uint32_t)bits;
+                s_valid[chunk & 1][wave * 2 + 1] = (uint32_t)(bits >> 32);
+            }
+        };
+        // Tile t's pieces from memory into a buffer.
+        auto load = [&](uint32_t t, uint32_t ring) {   // ring: the buffer
+            const uint64_t *ks = s_k[t / kChunk & 1] + t % kChunk * kStageKeys, *vs = s_v[t / kChunk & 1] + t % kChunk * kStageKeys;
+            const char *p[PER];
+#pragma unroll
+            for (int u = 0; u < KU; ++u) p[u] = (const char *)(ks[k_key[u]] + k_of[u]);
+#pragma unroll
+            for (int u = 0; u < VU; ++u) p[KU + u] = (const char *)(vs[v_key[u]] + v_of[u]);
+            if (A.d != 32 * NK) {
+#pragma unroll
+                for (int u = 0; u < KU; ++u)
+                    if (k_of[u] == kNone) p[u] = (const char *)g_zeros;
+            }
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                load_to_lds(p[u], ring0 + (ring * kLoads + (u < KU ? min(u * kAttnWaves + wave, 2u * NK - 1)
+                                                                   : 2 * NK + (u - KU) * kAttnWaves + wave)) * 1024);
+        };
+        // WHOLE: every query sees every key.  Otherwise (at a row's end, at holes, where a window
+        // starts) slots that hold nothing have given zeros, and single keys are left out.
+        auto compute = [&](auto WHOLE, uint32_t t, const char *ring, uint32_t now) {
+            constexpr bool whole = decltype(WHOLE)::value;
+            const uint32_t t0 = S.begin + t * kStageKeys;
+            f32x4 s[NT][KB];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n][kb] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < NK; ++c) {
+                    const u32x4 k = *(const u32x4 *)(ring + k_at[c] + kb * 16 * KP * 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[n][kb] = mma16<TY>(k, q[n][c], s[n][kb]);
+                }
+            }
+            auto value = [&](int c) { return read_transposed(ring + v_at[c], ring + v_at[c] + 16 * VPieces * 16); };
+            uint32_t see[NT] = {};
+            bool odd = false;
+            if constexpr (!whole) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) see[n] = now & tree_sees<kStageKeys>(s_mask + Q[n].token * words, words, t0, len, Q[n].lo);
+#pragma unroll
+                for (int c = 0; c < VW; ++c) {
+                    const u32x4 a = value(c);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        odd |= (a[w] & kTopExponent<TY>) == kTopExponent<TY> || (a[w] >> 16 & kTopExponent<TY>) == kTopExponent<TY>;
+                }
+                odd = __any(odd);
+            }
+            u32x4 hi[NT], rest[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float p[VK];
+                tree_weights<TY, VK, VW, KB>(s[n], p, acc[n], m[n], mref[n], l[n], A.scale_log2, whole, see[n], j);
+                if (odd) add_odd<TY, VK, VW>(A, r, vbase, t0, now, see[n], p, acc[n], j, hh, column);
+                split_weights<TY, VK>(p, hi[n], rest[n], whole);
+            }
+            if (odd) return;
+#pragma unroll
+            for (int c = 0; c < VW; ++c) {
+                const u32x4 a = value(c);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, rest[n], acc[n][c]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, hi[n], acc[n][c]);
+            }
+        };
+
+        int32_t id = 0;
+        if (tiles) {
+            note(0, look(0));
+            id = look(1);
+            __syncthreads();
+            load(0, 0);
+            if (kAhead == 2 && tiles > 1) load(1, 1);
+            // what else is on its way (the query, the next table's pages) is waited for here: a
+            // wait in the loop would be for the loads to LDS too
+            wait_loads<0>();
+        }
+        auto look_ahead = [&](uint32_t t) {
+            if (t % kChunk == kChunk - 1 - kAhead) {   // the next load is of the next table
+                note(t / kChunk + 1, id);
+                id = look(t / kChunk + 2);
+            }
+        };
+        uint32_t t = 0, turn = 0;   // turn: t % kRing
+        while (t < tiles) {
+            uint32_t now = 0;
+            const char *here = nullptr;
+            bool whole;
+            for (;;) {   // whole tiles, in a loop of their own
+                // Tile t is in its buffer, and the one after it may be on its way; what was in the
+                // buffer that is loaded next is done with by all, and so is the table that is written next.
+                if (kAhead == 2 && t + 1 < tiles) wait_loads<PER>();
+                else wait_loads<0>();
+                group_barrier();
+                if (t + kAhead < tiles) load(t + kAhead, turn == 0 ? kRing - 1 : turn - 1);
+                here = s_ring[turn];
+                turn = turn + 1 == kRing ? 0 : turn + 1;
+                now = __builtin_amdgcn_readfirstlane(s_valid[t / kChunk & 1][t % kChunk]);
+                whole = now == 0xFFFFFFFFu && tree_whole<kStageKeys>(A, S.begin + t * kStageKeys, len);
+                if (!whole) break;
+                if (q0 < A.m) compute(std::true_type(), t, here, now);
+                look_ahead(t);
+                if (++t == tiles) break;
+            }
+            if (whole) break;
+            if (q0 < A.m) compute(std::false_type(), t, here, now);
+            wait_loads<0>();   // its own: see above
+            look_ahead(t);
+            ++t;
+        }
+        const TreeOut O = tree_out(A, X, S, s_info);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            put_tile<TY, VW, true>(A, O, q0 + n * 16, kAttnWaves, acc[n], m[n], l[n], wave, lane, nullptr, nullptr, nullptr, column);
+        if (!tree_next(A, X, S.steps)) return;
+        __syncthreads();
+    }
+}
+
+template <int TY, int NK, int VW>
+int launch_tree_many(const TreeArgs &A, void *stream)
+{
+    const void *fn = reinterpret_cast<const void *>(&k_tree_many<TY, NK, VW, 1>);
+    if constexpr (NK <= 4)
+        if (A.tiles == 2) fn = reinterpret_cast<const void *>(&k_tree_many<TY, NK, VW, 2>);
     return launch_kernel(fn, dim3(A.grid), dim3(kAttnBlock), A.direct ? 0 : rows_lds(A.b), stream, A);
 }
 
-// The instance: the smallest that holds d and dv (see tree_tiles on the host for the
-// number of tiles).
+template <int TY, int NK, int VW, AttnEdge EDGE>
+int launch_tree_few(const TreeArgs &A, void *stream)
+{
+    return launch_kernel(reinterpret_cast<const void *>(&k_tree_few<TY, NK, VW, EDGE>), dim3(A.grid), dim3(kAttnBlock),
+                         A.direct ? 0 : rows_lds(A.b), stream, A);
+}
+
+// The instance: the smallest that holds d and dv.
 template <int TY>
 int launch_tree_type(const TreeArgs &A, void *stream)
 {
     constexpr int E = AttnType<TY>::E, U = 8 / E;   // 4 U pieces of 16 bytes: 32 elements
     const uint32_t d = A.d, dv = A.dv;
-    if (d < (uint32_t)E || dv < (uint32_t)E) return launch_tree_one<TY, 8 * U, 16, kTiny>(A, stream);
+    if constexpr (TY != S_F32) {
+        if (A.tiles) {
+            if (d <= 64 && dv <= 64) return launch_tree_many<TY, 2, 4>(A, stream);
+            if (dv <= 128)
+                return d <= 96    ? launch_tree_many<TY, 3, 8>(A, stream)
+                       : d <= 128 ? launch_tree_many<TY, 4, 8>(A, stream)
+                       : d <= 192 ? launch_tree_many<TY, 6, 8>(A, stream)
+                                  : launch_tree_many<TY, 8, 16>(A, stream);
+            return d <= 192 ? launch_tree_many<TY, 6, 16>(A, stream) : launch_tree_many<TY, 8, 16>(A, stream);
+        }
+    }
+    if (d < (uint32_t)E || dv < (uint32_t)E) return launch_tree_few<TY, 8 * U, 16, kTiny>(A, stream);
     if (d <= 64 && dv <= 64)
-        return d == 64 ? launch_tree_one<TY, 2 * U, 4, kExact>(A, stream) : launch_tree_one<TY, 2 * U, 4, kTail>(A, stream);
+        return d == 64 ? launch_tree_few<TY, 2 * U, 4, kExact>(A, stream) : launch_tree_few<TY, 2 * U, 4, kTail>(A, stream);
     if (d <= 128 && dv <= 128)
-        return d == 128 ? launch_tree_one<TY, 4 * U, 8, kExact>(A, stream) : launch_tree_one<TY, 4 * U, 8, kTail>(A, stream);
-    return d == 256 ? launch_tree_one<TY, 8 * U, 16, kExact>(A, stream) : launch_tree_one<TY, 8 * U, 16, kTail>(A, stream);
+        return d == 128 ? launch_tree_few<TY, 4 * U, 8, kExact>(A, stream) : launch_tree_few<TY, 4 * U, 8, kTail>(A, stream);
+    return d == 256 ? launch_tree_few<TY, 8 * U, 16, kExact>(A, stream) : launch_tree_few<TY, 8 * U, 16, kTail>(A, stream);
 }
 
 }  // namespace

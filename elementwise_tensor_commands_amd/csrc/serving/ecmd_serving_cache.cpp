@@ -96,8 +96,14 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     A.page = (uint32_t)std::max<int64_t>(1, page);
     A.cols = n > 0 && page > 0 ? (uint32_t)cols : 0;   // a cache without slots: every row is empty
     A.window = (uint32_t)window;
-    // Few query vectors: the waves of a work-group part the positions; many: them.
-    const uint32_t need = ceil_div(A.m, 16);
+    // From 33 query vectors of 16 bits on, tiles are staged for all of a work-group's, if
+    // every row of the caches starts at a multiple of 16 bytes and is one; a wave takes two
+    // tiles of 16 from 65 on, as far as the registers go.  Otherwise the waves part the
+    // positions of up to 16 (32) vectors, the vectors of more.
+    bool even = P.type != S_F32 && (d * esize) % 16 == 0 && (dv * esize) % 16 == 0 && (uintptr_t)A.k % 16 == 0 && (uintptr_t)A.v % 16 == 0;
+    for (int i = 0; i < 3; ++i) even = even && A.kcs[i] % 16 == 0 && A.vcs[i] % 16 == 0;
+    A.tiles = !even || A.m <= 32 ? 0 : A.m > 64 && d <= 128 && dv <= 128 ? 2 : 1;
+    const uint32_t need = ceil_div(A.m, 16 * std::max(1u, A.tiles));
     A.q_shift = need >= 3 ? 2 : need - 1;
     A.q_blocks = ceil_div(need, 1u << A.q_shift);
     const uint64_t units = (uint64_t)A.hk * A.q_blocks;

@@ -127,7 +127,7 @@ int64_t cmd_paged_attention_heads_workspace(const cmd_arg args[7], int32_t windo
  * T = 1, or parent[r, i] = i - 1, is attention of the next tokens of a sequence.
  * Scores, weights, sums and softmax statistics are binary32, but with 16-bit types a
  * weight meets the values as the sum of two numbers of the type, which hold it to
- * within 2^-14 (bf16) or 2^-20 (f16) of itself, f16 to no better than 2^-35 of its
+ * within 2^-14 (bf16) or 2^-20 (f16) of itself, f16 to no better than 2^-34 of its
  * row's largest.  A token that attends to nothing gets out 0 and lse -inf.  What a
  * token does not attend to is of no account to it (NaN included); an infinite value
  * that it does attend to makes its column infinite, where the weight is at least

@@ -30,7 +30,7 @@ def attend(q, k, v, scale, split, least):
 
 
 SPLIT = {torch.bfloat16: 2.0 ** -14, torch.float16: 2.0 ** -20, torch.float32: 0.0}
-LEAST = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -35, torch.float32: 0.0}
+LEAST = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -34, torch.float32: 0.0}
 
 
 def above(parents):

@@ -57,8 +57,8 @@ def tree_state(case, dtype, seed, reach=1.0):
     b, t, hq, hk, d, dv, page, cols, window = case
     g, rng = gen(seed), random.Random(seed)
     n = b * cols + 1
-    kg, kc = cache(g, n, page, hk, d, DT[dtype], extra=seed % 3)
-    vg, vc = cache(g, n, page, hk, dv, DT[dtype], extra=seed % 2)
+    kg, kc = cache(g, n, page, hk, d, DT[dtype], extra=(0, 8, 5)[seed % 3])
+    vg, vc = cache(g, n, page, hk, dv, DT[dtype], extra=(0, 16)[seed % 2])
     q = randn(g, b, t, hq, d, dtype=DT[dtype])
     pages = table(rng, n, b, cols)
     lens = [rng.choice([int(cols * page * reach) - t, rng.randint(0, cols * page)]) for _ in range(b)]
@@ -92,6 +92,25 @@ def test_tree_attention(case, dtype):
     assert torch.equal(again, out)
 
 
+MANY = [  # of many query vectors, rows of the caches at multiples of 16 bytes
+    (2, 12, 8, 2, 64, 64, 16, 20, 0), (1, 40, 8, 2, 56, 48, 16, 30, 70), (2, 20, 2, 1, 96, 128, 16, 30, 0), (1, 100, 2, 1, 72, 104, 8, 60, 0),
+    (2, 11, 4, 1, 128, 128, 16, 40, 0), (3, 33, 8, 2, 128, 64, 16, 25, 100), (1, 256, 4, 2, 120, 128, 64, 16, 0), (2, 50, 1, 1, 192, 128, 16, 20, 0),
+    (1, 20, 6, 2, 160, 96, 32, 12, 0), (2, 18, 2, 1, 192, 192, 16, 18, 40), (1, 34, 4, 4, 256, 256, 16, 18, 0), (1, 40, 1, 1, 8, 8, 16, 30, 0),
+    (1, 70, 2, 2, 200, 136, 5, 60, 0), (9, 10, 16, 4, 128, 128, 16, 8, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_tree_attention_of_many_query_vectors(case, dtype):
+    q, (kg, vg), (kc, vc), pages, lens, parent, window = tree_state(MANY[case], dtype, 6 * case + 100)
+    want, want_lse, eo, el = C.tree(q, kc, vc, pages, lens, parent, 1.0 / math.sqrt(q.shape[3]), window)
+    out, lse = torch.full(want.shape, 7.0, dtype=DT[dtype], device="cuda"), torch.full(want_lse.shape, 7.0, device="cuda")
+    E.tree_attention(q.cuda(), kg, vg, pages.cuda(), lens.cuda(), parent.cuda(), out, lse=lse, window=window)
+    within(out, want, eo, MANY[case])
+    within(lse, want_lse, el, MANY[case])
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_tree_attention_of_a_long_context(dtype):
     """Rows cut into segments, whole rows, many query vectors: the second launch."""
@@ -109,12 +128,13 @@ def test_tree_attention_of_a_long_context(dtype):
         within(lse, want_lse, el, case)
 
 
+@pytest.mark.parametrize("hq", [4, 16])
 @pytest.mark.parametrize("dtype", list(DT))
-def test_tree_attention_leaves_out_what_it_does_not_attend_to(dtype):
+def test_tree_attention_leaves_out_what_it_does_not_attend_to(dtype, hq):
     """Infinities and NaN in slots that some tokens see and others do not."""
     dt = DT[dtype]
     g = gen(5)
-    b, t, hq, hk, d, page, cols = 1, 6, 4, 2, 64, 8, 6
+    b, t, hk, d, page, cols = 1, 6, 2, 64, 8, 6
     q, k, v = randn(g, b, t, hq, d, dtype=dt), randn(g, cols, page, hk, d, dtype=dt), randn(g, cols, page, hk, d, dtype=dt)
     parent, length = [[-1, 0, 0, 1, -2, 2]], 21          # token 4 is padding
     slot = lambda i: divmod(length + i, page)
