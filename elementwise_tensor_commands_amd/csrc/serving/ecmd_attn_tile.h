@@ -141,11 +141,12 @@ struct Rows {
 };
 __host__ __device__ inline uint32_t rows_lds(uint32_t b) { return (3 * b + 1) * 4; }
 
+// A row that holds something counts for `extra` steps more.
 // Up to 64 rows every wave makes the whole of it, the same values in the same
 // places, and waits for nobody; more rows are the first kAttnBlock work-items'
 // and end with a barrier.
 template <class Args, class SpanOf>
-__device__ inline Rows make_rows(const Args &A, uint32_t *lds, uint32_t *scratch, SpanOf span_of)
+__device__ inline Rows make_rows(const Args &A, uint32_t *lds, uint32_t *scratch, SpanOf span_of, uint32_t extra = 0)
 {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Rows R{lds, lds + A.b + 1, lds + 2 * A.b + 1, 0, 0};
@@ -159,6 +160,7 @@ __device__ inline Rows make_rows(const Args &A, uint32_t *lds, uint32_t *scratch
             R.lo[r] = s.lo;
             R.hi[r] = s.hi;
             x = (s.hi - s.lo + kAttnStep - 1) / kAttnStep;
+            if (x) x += extra;
             most = max(most, x);
         }
         const uint32_t inc = wave_prefix(x);

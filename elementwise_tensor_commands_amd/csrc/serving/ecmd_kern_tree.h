@@ -19,8 +19,7 @@
 // where the caches' bytes are what counts, binary32, whose products run at a sixteenth of
 // the 16-bit rate and hide everything else, and rows off 16 bytes.  k_tree_many stages tiles of
 // 32 positions in LDS, once for all queries of a work-group, by loads from memory straight to
-// LDS that are two tiles ahead: three buffers (two of wide
-// heads), one barrier a tile.
+// LDS that are up to three tiles ahead, one barrier a tile.
 //
 // Which tokens a token attends to is one bit
 // mask per token, made in LDS from the parents by pointer doubling; a tile of 32
@@ -89,52 +88,85 @@ struct Tree {
 };
 constexpr uint32_t kTreeWords = kMaxTree / 32;
 
-__device__ inline void make_tree(const TreeArgs &A, uint32_t r, const Tree &T)
+// A lane's token's parent, to be loaded ahead of make_tree.
+__device__ inline int32_t tree_parent(const TreeArgs &A, uint32_t r)
+{
+    const uint32_t i = min(threadIdx.x, A.t - 1);
+    return A.parent[(int64_t)r * A.parent_s[0] + (int64_t)i * A.parent_s[1]];
+}
+
+// By pointer doubling: in every turn a token takes over what the token that it points to has,
+// and points where that one does.  Up to 64 tokens one wave does it, by exchanges between
+// its lanes (64 tokens, 32 of them in a row: 2 us instead of 7 with barriers).
+__device__ inline void make_tree(const TreeArgs &A, int32_t p, const Tree &T)
 {
     const uint32_t i = threadIdx.x, words = (A.t + 31) / 32;
-    uint32_t mask[kTreeWords];
-    int32_t jump = -1;
-    uint32_t bad = 0;
-    if (i < kTreeWords) T.real[i] = 0;
-    if (i < A.t) {
-        const int32_t p = A.parent[(int64_t)r * A.parent_s[0] + (int64_t)i * A.parent_s[1]];
-        const bool fine = p >= 0 && (uint32_t)p < i;
-        bad = !fine && p != -1;
-        jump = fine ? p : -1;
-#pragma unroll
-        for (uint32_t w = 0; w < kTreeWords; ++w) mask[w] = w == i / 32 ? 1u << (i % 32) : 0;
+    const bool fine = i < A.t && p >= 0 && (uint32_t)p < i;
+    int32_t jump = i >= A.t ? -1 : fine ? p : p == -1 ? -1 : -2;   // the next token up; -1: none, -2: padding
+    if (A.t <= 64) {
+        if (i < 64) {
+            uint64_t mask = i < A.t ? uint64_t(1) << i : 0;
+            while (__any(jump >= 0)) {
+                const int32_t from = jump >= 0 ? jump : (int32_t)i;
+                const uint64_t more = __shfl(mask, from);
+                const int32_t next = __shfl(jump, from);
+                if (jump >= 0) {
+                    mask |= more;
+                    jump = next;
+                }
+            }
+            const bool real = i < A.t && jump == -1;
+            const int32_t above = real ? (int32_t)__popcll(mask) - 1 : -1;
+            const uint64_t all = __ballot(real);
+            if (A.window && __any(above >= 0 && (uint32_t)above >= A.window))
+                for (uint32_t x = 0; x < A.t; ++x) {
+                    const int32_t at = __shfl(above, (int)x);
+                    if ((uint32_t)(above - at) >= A.window) mask &= ~(uint64_t(1) << x);   // (of tokens above i)
+                }
+            if (i < A.t) {
+                T.mask[i * words] = (uint32_t)mask;
+                if (words > 1) T.mask[i * words + 1] = (uint32_t)(mask >> 32);
+                T.info[i] = above;
+            }
+            if (i < 2) T.real[i] = (uint32_t)(all >> 32 * i);
+        }
+        __syncthreads();
+        return;
     }
-    // info: the next token up that the mask does not have yet, or -1, with bit 30 for padding
+    uint32_t mask[kTreeWords];
+    if (i < kTreeWords) T.real[i] = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kTreeWords; ++w) mask[w] = i < A.t && w == i / 32 ? 1u << (i % 32) : 0;
     for (;;) {
         if (i < A.t) {
 #pragma unroll
             for (uint32_t w = 0; w < kTreeWords; ++w)
                 if (w < words) T.mask[i * words + w] = mask[w];
-            T.info[i] = jump < 0 ? (bad ? -2 : -1) : jump;
+            T.info[i] = jump;
         }
         if (!__syncthreads_or(jump >= 0)) break;
-        if (i < A.t && jump >= 0) {
+        if (jump >= 0) {
             const uint32_t up = (uint32_t)jump;
 #pragma unroll
             for (uint32_t w = 0; w < kTreeWords; ++w)
                 if (w < words) mask[w] |= T.mask[up * words + w];
             jump = T.info[up];
-            bad = jump == -2;
         }
         __syncthreads();
     }
+    const bool real = i < A.t && jump == -1;
     int32_t above = -1;
-    if (i < A.t && !bad) {
+    if (real) {
 #pragma unroll
         for (uint32_t w = 0; w < kTreeWords; ++w) above += __popc(mask[w]);
     }
     __syncthreads();
     if (i < A.t) {
-        T.info[i] = bad ? -1 : above;
-        if (!bad) atomicOr(&T.real[i / 32], 1u << (i % 32));
+        T.info[i] = above;
+        if (real) atomicOr(&T.real[i / 32], 1u << (i % 32));
     }
     __syncthreads();
-    if (A.window && i < A.t && !bad && (uint32_t)above >= A.window) {
+    if (A.window && real && (uint32_t)above >= A.window) {
         for (uint32_t x = 0; x < i; ++x)
             if (T.mask[i * words + x / 32] >> (x % 32) & 1)
                 if ((uint32_t)(above - T.info[x]) >= A.window) T.mask[i * words + x / 32] &= ~(1u << (x % 32));
@@ -154,6 +186,11 @@ __device__ inline Span tree_span(const TreeArgs &A, uint32_t r)
     return s;
 }
 
+// Steps that a row's end counts for beside its positions: its tree, its tiles of single keys
+// and its sums take about as long as two steps (16 rows of up to 8192, 64 tokens: the
+// work-groups' ends 123 to 169 us without).
+constexpr uint32_t kTreeExtra = 2;
+
 // Steps of a run, the same in every work-group and in the join; 0: runs are rows.
 __device__ inline uint32_t tree_share(const TreeArgs &A, const Rows &R)
 {
@@ -170,6 +207,14 @@ struct TreeRun {
     uint32_t r, step, stop;
     Rows R;
 };
+__device__ inline bool tree_next_row(const TreeArgs &A, TreeRun &X)
+{
+    X.step = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]);
+    if (X.step >= X.stop) return false;
+    do ++X.r;
+    while (__builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]) <= X.step);   // past empty rows
+    return true;
+}
 __device__ inline bool tree_run(const TreeArgs &A, uint32_t *s_rows, uint32_t *s_scratch, TreeRun &X)
 {
     // Work-groups go to the eight dies in turn: those of a run follow each other on one.
@@ -180,7 +225,7 @@ __device__ inline bool tree_run(const TreeArgs &A, uint32_t *s_rows, uint32_t *s
     X.r = X.group;
     X.step = X.stop = 0;
     if (A.direct) return X.group < A.b;
-    X.R = make_rows(A, s_rows, s_scratch, tree_span);
+    X.R = make_rows(A, s_rows, s_scratch, tree_span, kTreeExtra);
     const uint32_t share = tree_share(A, X.R);
     if (share == 0) {
         if (X.group >= A.b) return false;
@@ -198,17 +243,15 @@ __device__ inline bool tree_run(const TreeArgs &A, uint32_t *s_rows, uint32_t *s
         else hi = mid;
     }
     X.r = lo;
-    return true;
+    // a run that starts with what a row's end counts for starts with the next row
+    return X.step + kTreeExtra < __builtin_amdgcn_readfirstlane(X.R.prefix[lo + 1]) || tree_next_row(A, X);
 }
 // On to the next row of the run.
 __device__ inline bool tree_next(const TreeArgs &A, TreeRun &X, uint32_t steps)
 {
     if (A.direct) return false;
     X.step += steps;
-    if (X.step >= X.stop) return false;
-    do ++X.r;
-    while (__builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]) <= X.step);   // past empty rows
-    return true;
+    return X.step < X.stop && tree_next_row(A, X);
 }
 
 // One row of the run.
@@ -229,7 +272,7 @@ __device__ inline Segment tree_segment(const TreeArgs &A, const TreeRun &X)
         S.end = span.hi;
     } else {
         const uint32_t first = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r]);
-        const uint32_t last = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]);
+        const uint32_t last = __builtin_amdgcn_readfirstlane(X.R.prefix[X.r + 1]) - kTreeExtra;
         const uint32_t here = min(X.stop, last), hi = __builtin_amdgcn_readfirstlane(X.R.hi[X.r]);
         S.last_part = here == last;
         S.whole_row = X.step == first && S.last_part;
@@ -274,29 +317,24 @@ __device__ inline uint32_t tree_sees(const uint32_t *mask, uint32_t words, uint3
 struct Query {
     uint32_t token, lo;
 };
-__device__ inline Query tree_query(const TreeArgs &A, uint32_t m, uint32_t len, const int32_t *s_info)
+__device__ inline uint32_t tree_lo(const TreeArgs &A, uint32_t token, uint32_t len, const int32_t *s_info)
 {
-    Query Q{A.by_group.div(min(m, A.m - 1)), 0};
-    if (A.window) {
-        const uint32_t past = len + (uint32_t)max(s_info[Q.token], 0) + 1;
-        Q.lo = past > A.window ? past - A.window : 0;
-    }
-    return Q;
+    if (!A.window) return 0;
+    const uint32_t past = len + (uint32_t)max(s_info[token], 0) + 1;
+    return past > A.window ? past - A.window : 0;
 }
 
-// Scores s of a tile to weights p: the running maximum m, its use mref, the sum l and the
-// sums acc follow.  see: which of the lane's keys the query sees (unless whole).
-template <int TY, int VK, int VW, int KB>
-__device__ inline void tree_weights(const f32x4 (&s)[KB], float (&p)[VK], f32x4 (&acc)[VW], float &m, float &mref, float &l,
+// Scores x of a tile to weights p: the running maximum m, its use mref, the sum l and the
+// sums acc follow.  A lane has one query and keys 4 j + k % 4 of every 16; see: which of the
+// tile's the query sees (unless whole).
+template <int TY, int VK, int N>
+__device__ inline void tree_weights(const float (&x)[VK], float (&p)[VK], f32x4 (&acc)[N], float &m, float &mref, float &l,
                                     float scale, bool whole, uint32_t see, uint32_t j)
 {
-    float x[VK], top = -INFINITY;
+    auto sees = [&](int k) { return see >> ((k / 4) * 16 + j * 4 + k % 4) & 1; };
+    float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < VK; ++k) {
-        x[k] = s[k / 4][k % 4];
-        if (!whole) x[k] = see >> ((k / 4) * 16 + j * 4 + k % 4) & 1 ? x[k] : -INFINITY;
-        top = fmaxf(top, x[k]);
-    }
+    for (int k = 0; k < VK; ++k) top = fmaxf(top, whole || sees(k) ? x[k] : -INFINITY);
     if (top != -INFINITY) top *= scale;   // (a scale of 0 times infinity)
     if (__any(top > m + kTreeSlack<TY>)) {
         top = fmaxf(top, __shfl_xor(top, 16));
@@ -307,13 +345,13 @@ __device__ inline void tree_weights(const f32x4 (&s)[KB], float (&p)[VK], f32x4 
         m = mn;
         l *= a;
 #pragma unroll
-        for (int c = 0; c < VW; ++c) acc[c] *= a;
+        for (int c = 0; c < N; ++c) acc[c] *= a;
     }
     const float less = kTreeBias<TY> - mref;
 #pragma unroll
     for (int k = 0; k < VK; ++k) {
         p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[k], scale, less));
-        if (!whole) p[k] = see >> ((k / 4) * 16 + j * 4 + k % 4) & 1 ? p[k] : 0.0f;
+        if (!whole) p[k] = sees(k) ? p[k] : 0.0f;
         l += p[k];
     }
 }
@@ -323,27 +361,34 @@ __device__ inline void tree_weights(const f32x4 (&s)[KB], float (&p)[VK], f32x4 
 // result's.  Both are positive wherever the weight is, since an infinite value times 0 would
 // be NaN: the rest is made 2^-20 of the weight larger, and binary16 has the smallest number
 // in place of 0 (only in tiles where every weight counts).
-template <int TY, int VK>
-__device__ inline void split_weights(const float (&p)[VK], u32x4 &hi, u32x4 &rest, bool whole)
+template <int TY>
+__device__ inline void split_pair(float f, float g, uint32_t &hi, uint32_t &rest, bool whole)
 {
     constexpr float more = 1.0f + 0x1p-20f;
-    const u16x2 least = __builtin_bit_cast(u16x2, whole ? 0x00010001u : 0u);
+    if constexpr (TY == S_BF16) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, f), b = __builtin_bit_cast(uint32_t, g);
+        hi = __builtin_amdgcn_perm(b, a, 0x07060302);
+        rest = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, __builtin_fmaf(g, more, -as_f(b & 0xFFFF0000u))),
+                                     __builtin_bit_cast(uint32_t, __builtin_fmaf(f, more, -as_f(a & 0xFFFF0000u))), 0x07060302);
+    } else {
+        // positive numbers order as their bits do
+        const u16x2 least = __builtin_bit_cast(u16x2, whole ? 0x00010001u : 0u);
+        const f16x2 h = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(f, g));
+        const u16x2 e = __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf(f, more, -(float)h[0]),
+                                                                           __builtin_fmaf(g, more, -(float)h[1])));
+        hi = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, h), least));
+        rest = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, least));
+    }
+}
+template <int TY, int VK>
+__device__ inline void split_weights(const float (&p)[VK], u32x4 (&hi)[VK / 8], u32x4 (&rest)[VK / 8], bool whole)
+{
 #pragma unroll
     for (int x = 0; x < VK; x += 2) {
-        const float f = p[x], g = p[x + 1];
-        if constexpr (TY == S_BF16) {
-            const uint32_t a = __builtin_bit_cast(uint32_t, f), b = __builtin_bit_cast(uint32_t, g);
-            hi[x / 2] = __builtin_amdgcn_perm(b, a, 0x07060302);
-            rest[x / 2] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, __builtin_fmaf(g, more, -as_f(b & 0xFFFF0000u))),
-                                                __builtin_bit_cast(uint32_t, __builtin_fmaf(f, more, -as_f(a & 0xFFFF0000u))), 0x07060302);
-        } else {
-            // positive numbers order as their bits do
-            const f16x2 h = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(f, g));
-            const u16x2 e = __builtin_bit_cast(u16x2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf(f, more, -(float)h[0]),
-                                                                               __builtin_fmaf(g, more, -(float)h[1])));
-            hi[x / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, h), least));
-            rest[x / 2] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(e, least));
-        }
+        uint32_t a, b;
+        split_pair<TY>(p[x], p[x + 1], a, b, whole);
+        hi[x / 8][x % 8 / 2] = a;
+        rest[x / 8][x % 8 / 2] = b;
     }
 }
 
@@ -374,33 +419,33 @@ __device__ inline bool clear_values(u32x4 (&vr)[VK][VP], uint32_t now, uint32_t 
 
 // A weight of 0 times an infinity is NaN: where such values meet queries that do not see
 // them, a tile's values are added one by one.  At a row's end only, and hardly ever.
-template <int TY, int VK, int VW, class Column>
+template <int TY, int VK, int N, class Column>
 __device__ inline void add_odd(const TreeArgs &A, uint32_t r, const char *vbase, uint32_t t0, uint32_t now, uint32_t see,
-                               const float (&p)[VK], f32x4 (&acc)[VW], uint32_t j, uint32_t hh, Column column)
+                               const float (&p)[VK], f32x4 (&acc)[N], uint32_t j, uint32_t hh, Column column)
 {
     for (uint32_t key = 0; key < 4 * VK; ++key) {
         if (!(now >> key & 1)) continue;
         const uint32_t pos = t0 + key, col = A.by_page.div(pos);
         const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)col * A.pages_s[1]];
         const char *v = vbase + (int64_t)id * A.vcs[0] + (int64_t)(pos - col * A.page) * A.vcs[1];
-        const int from = (int)((key % 16) / 4 * 16 + hh);
         float w = 0.0f;
 #pragma unroll
         for (int x = 0; x < VK; ++x)
-            if (key / 16 * 4 + key % 4 == (uint32_t)x) w = __shfl(p[x], from);   // key is uniform
-        if (see >> key & 1) {
+            if (key / 16 * 4 + key % 4 == (uint32_t)x) w = __shfl(p[x], (int)(key % 16 / 4 * 16 + hh));   // key is uniform
+        if (!(see >> key & 1)) continue;
 #pragma unroll
-            for (int c = 0; c < VW; ++c)
+        for (int c = 0; c < N; ++c) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t at = column(j * 4 + i, c);
-                    if (at >= A.dv) continue;
-                    float value;
-                    if constexpr (TY == S_F32) value = ((const float *)v)[at];
-                    else if constexpr (TY == S_BF16) value = (float)((const __bf16 *)v)[at];
-                    else value = (float)((const _Float16 *)v)[at];
-                    acc[c][i] += w * value;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = column(j * 4 + i, c);
+                if (at >= A.dv) continue;
+                float value;
+                if constexpr (TY == S_F32) value = ((const float *)v)[at];
+                else if constexpr (TY == S_BF16) value = (float)((const __bf16 *)v)[at];
+                else value = (float)((const _Float16 *)v)[at];
+                acc[c][i] += w * value;
+            }
+            asm volatile("" ::: "memory");   // not all values at once: registers
         }
     }
 }
@@ -444,6 +489,29 @@ __device__ inline void put_statistics(const TreeArgs &A, const TreeOut &O, uint3
         const uint32_t tok = A.by_group.div(x), head = O.kvh * A.group + x - tok * A.group;
         A.lse[(int64_t)O.r * A.ls[0] + (int64_t)tok * A.ls[1] + (int64_t)head * A.ls[2]] = tree_log_sum<TY>(top, total);
     }
+}
+
+// The same of four neighbouring columns from c on, in one store.
+template <int TY>
+__device__ inline void put4(const TreeArgs &A, const TreeOut &O, uint32_t x, uint32_t c, f32x4 sum, float total)
+{
+    if (!O.whole_row) {
+        *(f32x4 *)&A.acc[(O.place + x) * A.dv + c] = sum;   // dv is a multiple of 4 here
+        return;
+    }
+    const uint32_t tok = A.by_group.div(x), head = O.kvh * A.group + x - tok * A.group;
+    const float to = total > 0.0f ? 1.0f : total == 0.0f || total < 0.0f ? 0.0f : total, by = total > 0.0f ? total : 1.0f;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 Out __attribute__((aligned(2)));
+    uint16_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v = to == 0.0f ? 0.0f : sum[i] / by * to;
+        if constexpr (TY == S_BF16) y[i] = __builtin_bit_cast(uint16_t, round_to<__bf16>(v));
+        else y[i] = __builtin_bit_cast(uint16_t, round_to<_Float16>(v));
+    }
+    *(Out *)((uint16_t *)A.out + (int64_t)O.r * A.os[0] + (int64_t)tok * A.os[1] + (int64_t)head * A.os[2] + c) =
+        u32x2{y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16};
 }
 
 // The sums of one tile of queries, q0 .. q0 + 15, out.  Waves with the same queries (every
@@ -590,7 +658,7 @@ __global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_
     for (;;) {   // one row of the run
         const Segment S = tree_segment(A, X);
         const uint32_t r = X.r, len = S.len;
-        if (tree_looks(A, S)) make_tree(A, r, tree);
+        if (tree_looks(A, S)) make_tree(A, tree_parent(A, r), tree);
         uint32_t wb = S.begin, we = S.end;
         if (parts > 1) {
             const uint32_t each = (we - wb + parts * kTile - 1) / (parts * kTile) * kTile;
@@ -600,7 +668,8 @@ __global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_
         if (q0 >= A.m) we = wb;   // no queries of this wave's
 
         u32x4 q[NK];
-        const Query Q = tree_query(A, q0 + hh, len, s_info);
+        const uint32_t token = A.by_group.div(min(q0 + hh, A.m - 1));
+        const Query Q{token, tree_lo(A, token, len, s_info)};
         {
             const uint32_t head = X.kvh * A.group + min(q0 + hh, A.m - 1) - Q.token * A.group;
             const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)Q.token * A.qs[1] + (int64_t)head * A.qs[2]) * sizeof(T);
@@ -712,8 +781,10 @@ __global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_
                 see = now & tree_sees<kTile>(s_mask + Q.token * words, words, t0, len, Q.lo);
                 odd = __any(clear_values<TY, VK, VP, PW>(vr, now, j));
             }
-            float p[VK];
-            tree_weights<TY, VK, VW, KB>(s, p, acc, m, mref, l, A.scale_log2, whole, see, j);
+            float x[VK], p[VK];
+#pragma unroll
+            for (int k = 0; k < VK; ++k) x[k] = s[k / 4][k % 4];
+            tree_weights<TY, VK>(x, p, acc, m, mref, l, A.scale_log2, whole, see, j);
             if (odd) {
                 add_odd<TY, VK, VW>(A, r, vbase, t0, now, see, p, acc, j, hh, column);
             } else if constexpr (TY == S_F32) {
@@ -723,7 +794,7 @@ __global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_
                     for (int c = 0; c < VW; ++c)
                         acc[c] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_f(vr[x][c / 4][c % 4]), p[x], acc[c], 0, 0, 0);
             } else {
-                u32x4 hi, rest;
+                u32x4 hi[1], rest[1];
                 split_weights<TY, VK>(p, hi, rest, whole);
 #pragma unroll
                 for (int c = 0; c < VW; ++c) {
@@ -732,8 +803,8 @@ __global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_
                     for (int w = 0; w < 4; ++w)
                         a[w] = __builtin_amdgcn_perm(vr[2 * w + 1][c / 8][c % 8 / 2], vr[2 * w][c / 8][c % 8 / 2],
                                                      c & 1 ? 0x07060302 : 0x05040100);
-                    acc[c] = mma16<TY>(a, rest, acc[c]);
-                    acc[c] = mma16<TY>(a, hi, acc[c]);
+                    acc[c] = mma16<TY>(a, rest[0], acc[c]);
+                    acc[c] = mma16<TY>(a, hi[0], acc[c]);
                 }
             }
             if (tile < we) load_v(in_table);
@@ -747,7 +818,7 @@ __global__ __launch_bounds__(kAttnBlock, (few_waves<TY, NK, VW>())) void k_tree_
 // ---------------------------------------------------------------------------
 // Many queries of 16 bits.
 
-constexpr uint32_t kStageKeys = 32, kStageTable = 256;   // positions of a tile; whose places are known ahead
+constexpr uint32_t kStageKeys = 32, kStageTable = kAttnBlock;   // positions of a tile; whose places are known ahead
 
 // 16 bytes from each lane's p to LDS, from address lds on, in the order of the lanes.  Written
 // out, for the compiler would let every later read of LDS wait for it: it does not
@@ -760,23 +831,32 @@ __device__ inline void load_to_lds(const char *p, uint32_t lds)
 
 __device__ __attribute__((aligned(256))) const uint32_t g_zeros[128] = {};   // a row of a slot that holds nothing
 
-// The 16-byte pieces of a key of PIECES are rotated by a number that the key gives, so that
-// sixteen keys' pieces at one index lie in different banks (but for a few where PIECES is no
-// power of two).  Those of a value of PIECES are exchanged, two by two, so that what a
-// transposing read takes of four keys does.
+// Where a row of PIECES 16-byte pieces has piece x, for a number that the key gives: another
+// place for each of neighbouring keys, so that what is read at once lies in different banks
+// (but for a little where PIECES is no power of two).
+template <uint32_t PIECES>
+__device__ inline uint32_t turned(uint32_t x, uint32_t turn)
+{
+    if constexpr ((PIECES & (PIECES - 1)) == 0) return x ^ (turn & (PIECES - 1));
+    else return (x + (turn >> 2 & 3)) % PIECES;
+}
+template <uint32_t PIECES>
+__device__ inline uint32_t turned_back(uint32_t x, uint32_t turn)
+{
+    if constexpr ((PIECES & (PIECES - 1)) == 0) return x ^ (turn & (PIECES - 1));
+    else return (x + PIECES - (turn >> 2 & 3)) % PIECES;
+}
+// Keys: sixteen keys' pieces at one index.  (Rows of 128 bytes: two lie side by side.)
 template <uint32_t PIECES>
 __device__ inline uint32_t key_turn(uint32_t key)
 {
-    return PIECES % 16 == 0 ? key & 15 : PIECES % 8 == 0 ? key >> 1 & 7 : key >> 2 & 3;
+    return PIECES == 8 ? key >> 1 : key & 15;
 }
-template <uint32_t PIECES>
-__device__ inline uint32_t value_turn(uint32_t key)
-{
-    return 2 * key & (PIECES - 1);
-}
+// Values: two neighbouring pieces of four keys.
+__device__ inline uint32_t value_turn(uint32_t key) { return 2 * key; }
 
 // Lane h of 16 gets element h of four rows, of which lane s reads four elements: number
-// 4 (s % 4) on, of row s / 4.  Two of them are the first operand of a product over 32 keys.
+// 4 (s % 4) on, of row s / 4.  Two of them are a product's first operand over its lane's keys.
 __device__ inline u32x4 read_transposed(const char *low, const char *high)
 {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -811,22 +891,23 @@ __device__ inline void group_barrier()
 
 // Rows' starts are multiples of 16 bytes and so are d and dv (of 2-byte elements): see
 // plan_tree.  NK: 32 elements of a key; VW: 16 of a value; NT: tiles of 16 queries of a wave.
+// A lane has query lane % 16 of each and keys 4 j + i of every 16, j = lane / 16.
 template <int TY, int NK, int VW, int NT>
-__global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void k_tree_many(const TreeArgs A)
+__global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 >= 640 ? 1 : 2)) void k_tree_many(const TreeArgs A)
 {
     typedef uint16_t T;
     constexpr int KB = 2, VK = 8;
-    constexpr uint32_t KP = 4 * NK, VPieces = 2 * VW;                // 16-byte pieces of a key and of a value
-    constexpr uint32_t kLoads = 2 * NK + VW;                         // of 1024 bytes: a tile's keys, then its values
-    constexpr int KU = (2 * NK + 3) / 4, VU = (VW + 3) / 4, PER = KU + VU;   // of a wave
-    static_assert(kAttnWaves == 4);
+    constexpr uint32_t KP = 4 * NK, VPieces = 2 * VW;                 // 16-byte pieces of a key and of a value
+    constexpr uint32_t kLoads = 2 * NK + VW;                          // of 1024 bytes: a tile's keys, then its values
+    // A wave's; where they do not come out even, the last one more than once.
+    constexpr int KU = (2 * NK + kAttnWaves - 1) / kAttnWaves, VU = (VW + kAttnWaves - 1) / kAttnWaves, PER = KU + VU;
 
     // Tiles' buffers: their places count 16 bits in a load to LDS, so they come first (by
     // their alignment) and end within 64 KiB.
     constexpr uint32_t kRing = kLoads * 3 <= 64 ? 3 : 2, kAhead = kRing - 1;
     static_assert(kLoads * kRing <= 64);
     __shared__ __attribute__((aligned(1024))) char s_ring[kRing][kLoads * 1024];
-    __shared__ uint64_t s_k[2][kStageTable], s_v[2][kStageTable];    // where a position's key and value lie
+    __shared__ uint64_t s_k[2][kStageTable], s_v[2][kStageTable];     // where a position's key and value lie
     __shared__ uint32_t s_valid[2][kStageTable / kStageKeys];
     __shared__ uint32_t s_mask[kMaxTree * kTreeWords], s_real[kTreeWords];
     __shared__ int32_t s_info[kMaxTree];
@@ -841,19 +922,18 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
     if (!tree_run(A, s_rows, s_scratch, X)) return;
     const uint32_t q0 = (X.block * kAttnWaves + wave) * (16 * NT);   // the wave's first query vector
 
-    auto column = [&](uint32_t m, int c) { return (uint32_t)c * 16 + m; };
     const char *kbase = (const char *)A.k + (int64_t)X.kvh * A.kcs[2];
     const char *vbase = (const char *)A.v + (int64_t)X.kvh * A.vcs[2];
 
-    // What the lane reads of a tile: pieces c * 4 + j of key hh (and 16 + hh); of the values of
-    // keys 4 j + hh / 4 (and + 16) four elements for each product.
+    // What the lane reads of a tile: pieces c * 4 + j of key hh (and 16 + hh); of the values four
+    // elements of key 4 j + hh / 4 (and 16 on) for each product.
     uint32_t k_at[NK], v_at[VW];
 #pragma unroll
-    for (int c = 0; c < NK; ++c) k_at[c] = (hh * KP + (c * 4 + j + key_turn<KP>(hh)) % KP) * 16;
+    for (int c = 0; c < NK; ++c) k_at[c] = (hh * KP + turned<KP>(c * 4 + j, key_turn<KP>(hh))) * 16;
 #pragma unroll
     for (int c = 0; c < VW; ++c) {
         const uint32_t key = j * 4 + hh / 4;
-        v_at[c] = 2 * NK * 1024 + (key * VPieces + ((2 * c + (hh & 3) / 2) ^ value_turn<VPieces>(key))) * 16 + (hh & 1) * 8;
+        v_at[c] = 2 * NK * 1024 + (key * VPieces + turned<VPieces>(2 * c + (hh & 3) / 2, value_turn(key))) * 16 + (hh & 1) * 8;
     }
     // What it loads: places in LDS go up with the lanes; of which key, and which of its bytes
     // (kNone: past a key's end, zeros).
@@ -862,13 +942,14 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
         const uint32_t x = min(u * kAttnWaves + wave, 2u * NK - 1) * 64 + lane, key = x / KP;
-        const uint32_t piece = (x - key * KP + KP - key_turn<KP>(key)) % KP;
+        const uint32_t piece = turned_back<KP>(x - key * KP, key_turn<KP>(key));
         k_key[u] = kept(key);
         k_of[u] = kept(piece * 8 < A.d ? piece * 16 : kNone);
     }
 #pragma unroll
     for (int u = 0; u < VU; ++u) {
-        const uint32_t x = (u * kAttnWaves + wave) * 64 + lane, key = x / VPieces, piece = (x - key * VPieces) ^ value_turn<VPieces>(key);
+        const uint32_t x = min(u * kAttnWaves + wave, VW - 1u) * 64 + lane, key = x / VPieces;
+        const uint32_t piece = turned_back<VPieces>(x - key * VPieces, value_turn(key));
         v_key[u] = kept(key);
         v_of[u] = kept(piece * 8 < A.dv ? piece * 16 : 0);   // (of columns past the end nothing is kept)
     }
@@ -877,39 +958,11 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
     for (;;) {   // one row of the run
         const Segment S = tree_segment(A, X);
         const uint32_t r = X.r, len = S.len;
-        if (tree_looks(A, S)) make_tree(A, r, tree);
-
-        u32x4 q[NT][NK];
-        Query Q[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t m = min(q0 + n * 16 + hh, A.m - 1);
-            Q[n] = tree_query(A, m, len, s_info);
-            const uint32_t head = X.kvh * A.group + m - Q[n].token * A.group;
-            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)Q[n].token * A.qs[1] + (int64_t)head * A.qs[2]) * sizeof(T);
-#pragma unroll
-            for (int c = 0; c < NK; ++c) {
-                const uint32_t at = (c * 4 + j) * 8;
-                q[n][c] = u32x4{0, 0, 0, 0};
-                if (at < A.d) q[n][c] = load16(p + at * sizeof(T)) ^ u32x4{A.q_flip, A.q_flip, A.q_flip, A.q_flip};
-            }
-        }
-        f32x4 acc[NT][VW];
-        float m[NT], mref[NT], l[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n] = -INFINITY;
-            mref[n] = 0.0f;
-            l[n] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < VW; ++c) acc[n][c] = f32x4{0, 0, 0, 0};
-        }
-
         const uint32_t tiles = (S.end - S.begin + kStageKeys - 1) / kStageKeys;
         constexpr uint32_t kChunk = kStageTable / kStageKeys;   // tiles whose places a table holds
         // Pages of positions 256 chunk + tid of the segment: looked up a chunk ahead.
         auto look = [&](uint32_t chunk) {
-            const uint32_t pos = min(S.begin + chunk * kStageTable + tid, S.end - 1);
+            const uint32_t pos = min(S.begin + chunk * kStageTable + tid, max(S.end, 1u) - 1);
             return A.pages[(int64_t)r * A.pages_s[0] + (int64_t)A.by_page.div(pos) * A.pages_s[1]];
         };
         auto note = [&](uint32_t chunk, int32_t id) {
@@ -925,8 +978,44 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
                 s_valid[chunk & 1][wave * 2 + 1] = (uint32_t)(bits >> 32);
             }
         };
+        // everything that the row's start waits for, asked for at once
+        const bool looks = tree_looks(A, S);
+        const int32_t parent = looks ? tree_parent(A, r) : -1;
+        int32_t id0 = 0, id = 0;
+        if (tiles) {
+            id0 = look(0);
+            id = look(1);
+        }
+        u32x4 q[NT][NK];
+        Query Q[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t m = min(q0 + n * 16 + hh, A.m - 1);
+            Q[n].token = A.by_group.div(m);
+            const uint32_t head = X.kvh * A.group + m - Q[n].token * A.group;
+            const char *p = (const char *)A.q + ((int64_t)r * A.qs[0] + (int64_t)Q[n].token * A.qs[1] + (int64_t)head * A.qs[2]) * sizeof(T);
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+                const uint32_t at = (c * 4 + j) * 8;
+                q[n][c] = u32x4{0, 0, 0, 0};
+                if (at < A.d) q[n][c] = load16(p + at * sizeof(T)) ^ u32x4{A.q_flip, A.q_flip, A.q_flip, A.q_flip};
+            }
+        }
+        if (looks) make_tree(A, parent, tree);
+        f32x4 acc[NT][VW];
+        float m[NT], mref[NT], l[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            Q[n].lo = tree_lo(A, Q[n].token, len, s_info);
+            m[n] = -INFINITY;
+            mref[n] = 0.0f;
+            l[n] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < VW; ++c) acc[n][c] = f32x4{0, 0, 0, 0};
+        }
+
         // Tile t's pieces from memory into a buffer.
-        auto load = [&](uint32_t t, uint32_t ring) {   // ring: the buffer
+        auto load = [&](uint32_t t, uint32_t buffer) {
             const uint64_t *ks = s_k[t / kChunk & 1] + t % kChunk * kStageKeys, *vs = s_v[t / kChunk & 1] + t % kChunk * kStageKeys;
             const char *p[PER];
 #pragma unroll
@@ -940,8 +1029,8 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
             }
 #pragma unroll
             for (int u = 0; u < PER; ++u)
-                load_to_lds(p[u], ring0 + (ring * kLoads + (u < KU ? min(u * kAttnWaves + wave, 2u * NK - 1)
-                                                                   : 2 * NK + (u - KU) * kAttnWaves + wave)) * 1024);
+                load_to_lds(p[u], ring0 + (buffer * kLoads + (u < KU ? min(u * kAttnWaves + wave, 2u * NK - 1)
+                                                                     : 2 * NK + min((u - KU) * kAttnWaves + wave, VW - 1u))) * 1024);
         };
         // WHOLE: every query sees every key.  Otherwise (at a row's end, at holes, where a window
         // starts) slots that hold nothing have given zeros, and single keys are left out.
@@ -975,12 +1064,14 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
                 }
                 odd = __any(odd);
             }
-            u32x4 hi[NT], rest[NT];
+            u32x4 hi[NT][1], rest[NT][1];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float p[VK];
-                tree_weights<TY, VK, VW, KB>(s[n], p, acc[n], m[n], mref[n], l[n], A.scale_log2, whole, see[n], j);
-                if (odd) add_odd<TY, VK, VW>(A, r, vbase, t0, now, see[n], p, acc[n], j, hh, column);
+                float x[VK], p[VK];
+#pragma unroll
+                for (int k = 0; k < VK; ++k) x[k] = s[n][k / 4][k % 4];
+                tree_weights<TY, VK>(x, p, acc[n], m[n], mref[n], l[n], A.scale_log2, whole, see[n], j);
+                if (odd) add_odd<TY, VK, VW>(A, r, vbase, t0, now, see[n], p, acc[n], j, hh, [&](uint32_t m, int c) { return c * 16 + m; });
                 split_weights<TY, VK>(p, hi[n], rest[n], whole);
             }
             if (odd) return;
@@ -988,19 +1079,18 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
             for (int c = 0; c < VW; ++c) {
                 const u32x4 a = value(c);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, rest[n], acc[n][c]);
+                for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, rest[n][0], acc[n][c]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, hi[n], acc[n][c]);
+                for (int n = 0; n < NT; ++n) acc[n][c] = mma16<TY>(a, hi[n][0], acc[n][c]);
             }
         };
 
-        int32_t id = 0;
         if (tiles) {
-            note(0, look(0));
-            id = look(1);
+            note(0, id0);
             __syncthreads();
-            load(0, 0);
-            if (kAhead == 2 && tiles > 1) load(1, 1);
+#pragma unroll
+            for (uint32_t t = 0; t < kAhead; ++t)
+                if (t < tiles) load(t, t);
             // what else is on its way (the query, the next table's pages) is waited for here: a
             // wait in the loop would be for the loads to LDS too
             wait_loads<0>();
@@ -1040,8 +1130,17 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 > 640 ? 1 : 2)) void
         }
         const TreeOut O = tree_out(A, X, S, s_info);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            put_tile<TY, VW, true>(A, O, q0 + n * 16, kAttnWaves, acc[n], m[n], l[n], wave, lane, nullptr, nullptr, nullptr, column);
+        for (int n = 0; n < NT; ++n) {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+            const uint32_t x = q0 + n * 16 + hh;
+            if (x >= A.m) continue;
+            const float total = known(A, O, x, l[n]);
+#pragma unroll
+            for (int c = 0; c < VW; ++c)
+                if (c * 16 + j * 4 < A.dv) put4<TY>(A, O, x, c * 16 + j * 4, acc[n][c], total);
+            if (j == 0) put_statistics<TY>(A, O, x, m[n], total);
+        }
         if (!tree_next(A, X, S.steps)) return;
         __syncthreads();
     }
@@ -1051,8 +1150,9 @@ template <int TY, int NK, int VW>
 int launch_tree_many(const TreeArgs &A, void *stream)
 {
     const void *fn = reinterpret_cast<const void *>(&k_tree_many<TY, NK, VW, 1>);
-    if constexpr (NK <= 4)
+    if constexpr (NK <= 4) {
         if (A.tiles == 2) fn = reinterpret_cast<const void *>(&k_tree_many<TY, NK, VW, 2>);
+    }
     return launch_kernel(fn, dim3(A.grid), dim3(kAttnBlock), A.direct ? 0 : rows_lds(A.b), stream, A);
 }
 

@@ -206,7 +206,8 @@ struct TreeArgs {
     uint32_t b, t, hq, hk, d, dv, group;
     uint32_t m;                            // query vectors of a kv head: t * group, token by token
     uint32_t tiles;                        // 16 query vectors of a wave where tiles are staged (1 or 2); 0: they are not
-    uint32_t q_blocks, q_shift;            // work-groups that share them; 2^q_shift waves of one take apart
+    uint32_t join_shift, join_turn;        // the join: 2^shift work-items to a query vector; vectors of a work-group
+    uint32_t q_blocks, q_shift;            // work-groups that share them; 2^q_shift waves of one take apart (not staged)
     uint32_t n, page, cols, window;
     uint32_t direct;                       // 1: a work-group to a row, kv head and block, no join
     uint32_t runs, runs_whole, grid;       // as in AttnArgs

@@ -97,15 +97,15 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     A.cols = n > 0 && page > 0 ? (uint32_t)cols : 0;   // a cache without slots: every row is empty
     A.window = (uint32_t)window;
     // From 33 query vectors of 16 bits on, tiles are staged for all of a work-group's, if
-    // every row of the caches starts at a multiple of 16 bytes and is one; a wave takes two
-    // tiles of 16 from 65 on, as far as the registers go.  Otherwise the waves part the
-    // positions of up to 16 (32) vectors, the vectors of more.
+    // every row of the caches starts at a multiple of 16 bytes and is one; a wave takes 32
+    // vectors from 65 on, as far as the registers go.  Otherwise the waves part the positions
+    // of up to 16 (32) vectors, the vectors of more.
     bool even = P.type != S_F32 && (d * esize) % 16 == 0 && (dv * esize) % 16 == 0 && (uintptr_t)A.k % 16 == 0 && (uintptr_t)A.v % 16 == 0;
     for (int i = 0; i < 3; ++i) even = even && A.kcs[i] % 16 == 0 && A.vcs[i] % 16 == 0;
     A.tiles = !even || A.m <= 32 ? 0 : A.m > 64 && d <= 128 && dv <= 128 ? 2 : 1;
-    const uint32_t need = ceil_div(A.m, 16 * std::max(1u, A.tiles));
+    const uint32_t need = ceil_div(A.m, 16);
     A.q_shift = need >= 3 ? 2 : need - 1;
-    A.q_blocks = ceil_div(need, 1u << A.q_shift);
+    A.q_blocks = A.tiles ? ceil_div(A.m, 64 * A.tiles) : ceil_div(need, 1u << A.q_shift);
     const uint64_t units = (uint64_t)A.hk * A.q_blocks;
     if ((uint64_t)(b + 8) * units > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
     uint64_t keys = (uint64_t)A.cols * A.page;
@@ -113,8 +113,7 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep, most = std::max<uint64_t>(1, steps * (uint64_t)b);
     const uint64_t row_bytes = keys * (uint64_t)((d + dv) * esize);
     A.direct = (steps <= 6 && row_bytes <= (256 << 10)) || b > kTreeMaxRows || most > (uint64_t(1) << 30);
-    const uint64_t want = 512;
-    A.runs = (uint32_t)std::min(std::max<uint64_t>(1, want / units), std::min<uint64_t>(most, kAttnMaxRuns));
+    A.runs = (uint32_t)std::min(std::max<uint64_t>(1, 512 / units), std::min<uint64_t>(most, kAttnMaxRuns));
     A.runs_whole = (uint64_t)b * units >= 128 && (uint64_t)b * units <= 2048 ? A.b : 0;
     auto eight = [](uint64_t x) { return (x + 7) / 8 * 8; };
     A.grid = (uint32_t)((A.direct ? eight(b) : eight(std::max(A.runs, std::max(A.runs_whole, A.b <= A.runs ? A.b : 0)))) * units);
@@ -124,6 +123,10 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     A.by_group = Div31(A.group);
     A.by_runs = Div31(A.runs);
     A.by_vectors = Div31(A.hk * A.m);
+    // The join: a vector to a work-group while there are at most 2048, else as many as make 1024 work-groups.
+    while (4u << A.join_shift < A.dv) ++A.join_shift;
+    const uint32_t vectors = A.b * A.hk * A.m, places = 256 >> A.join_shift;
+    A.join_turn = vectors <= 2048 ? 1 : ceil_div(ceil_div(vectors, 1024), places) * places;
     if (!A.direct) P.workspace = (int64_t)((((uint64_t)A.runs + b) * A.hk * A.m * (dv + 2)) * 4 + 16);
     return CMD_OK;
 }
