@@ -507,7 +507,11 @@ int cmd_page_mass(const cmd_arg args[7], float scale, float decay, int32_t windo
         return refuse(CMD_E_LIMIT, "the table holds more than 2^30 positions");
     MassArgs A{};
     A.page = (uint32_t)std::max<int64_t>(1, page);
-    A.cols_group = std::max(1u, kMassKeys / A.page);
+    // Columns of a work-group: of about 64 positions (64 rows of up to 8192, bf16: 256 take 102
+    // us, 128 96, 64 93 and 32 104), and of 32 where that leaves less than two work-groups for
+    // each compute unit (3 rows of up to 1500, f32: 58 us at 256, 14.6 at 32).
+    A.cols_group = std::max(1u, 64 / A.page);
+    if ((uint64_t)b * ceil_div(cols, A.cols_group) < 512) A.cols_group = std::max(1u, 32 / A.page);
     A.groups = ceil_div(cols, A.cols_group);
     if ((uint64_t)b * A.groups > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times pages for one launch");
     if ((flags & CMD_CHECK_ONLY) || b == 0 || cols == 0) return CMD_OK;
