@@ -271,7 +271,7 @@ struct SelectArgs {
     const void *q, *bounds;
     const int32_t *pages, *lens;
     int32_t *pages_out, *lens_out;
-    uint64_t *keys;                        // workspace: [b, hk, cols] (null: a work-group scores and chooses alone)
+    uint64_t *keys;                        // workspace: [b, hk, cols]
     int64_t qs[2];                         // BYTE strides of batch, head
     int64_t bs[3];                         // BYTE strides of page, head, least/largest
     int64_t pages_s[2], lens_s, pages_out_s[3], lens_out_s[2];
@@ -280,7 +280,6 @@ struct SelectArgs {
     Div31 by_page, by_hk, by_groups;
 };
 int launch_select(int type, const SelectArgs &A, void *stream);
-constexpr uint32_t kSelectAlone = 4096;    // columns whose keys fit LDS beside another work-group's
 
 struct MassArgs {
     const void *q, *k;

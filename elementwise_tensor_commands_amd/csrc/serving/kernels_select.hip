@@ -137,86 +137,173 @@ __global__ __launch_bounds__(256) void k_bounds(const BoundsArgs A)
 // ---------------------------------------------------------------------------
 // The `want` largest of n keys (0: no candidate), of which there are more than that:
 // the keys above `key`, and of those at it the first `ties` (all of them: kAll), by radix,
-// eight bits at a time from bit `top` down.  It ends as soon as a digit's keys are
-// wanted altogether: two or three turns where keys differ as measured data do.
+// eight bits at a time from the highest in which two of them differ (those of kForced are
+// taken out first: they would differ from all).  It ends as soon as a digit's keys are
+// wanted altogether: two turns where keys differ as measured data do.
 struct Cut {
     uint64_t key;
     uint32_t ties;
 };
 constexpr uint32_t kAll = ~0u;
+constexpr uint64_t kForced = ~uint64_t(0);
 
-template <uint32_t THREADS>
-struct CutScratch {
-    uint32_t bins[256];
-    uint32_t digit, above, inside;
-    uint32_t wave[2][THREADS / 64];
+struct Keys {
+    uint32_t held, forced;   // candidates, and those of kForced
+    uint64_t ones, zeros;    // bits that are 1 (0) in one of the others
 };
 
-template <uint32_t THREADS, class Get>
-__device__ inline Cut cut_largest(uint32_t n, uint32_t want, int top, Get get, CutScratch<THREADS> &S)
-{
-    const uint32_t tid = threadIdx.x, lane = tid & 63;
-    uint64_t prefix = 0, mask = 0;
-    for (int shift = top; shift >= 0; shift -= 8) {
-        for (uint32_t b = tid; b < 256; b += THREADS) S.bins[b] = 0;
-        __syncthreads();
-        for (uint32_t i = tid; i < n; i += THREADS) {
-            const uint64_t k = get(i);
-            if (k && (k & mask) == prefix) atomicAdd(&S.bins[(uint32_t)(k >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (tid < 64) {   // lane 0 has the four largest digits
-            uint32_t c[4], sum = 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                c[x] = S.bins[255 - 4 * lane - x];
-                sum += c[x];
-            }
-            const uint32_t upto = wave_prefix(sum);
-            uint32_t before = upto - sum;
-            if (before < want && want <= upto) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (before < want && want <= before + c[x]) {
-                        S.digit = 255 - 4 * lane - x;
-                        S.above = before;
-                        S.inside = c[x];
-                    }
-                    before += c[x];
-                }
-            }
-        }
-        __syncthreads();
-        prefix |= (uint64_t)S.digit << shift;
-        mask |= uint64_t(255) << shift;
-        want -= S.above;
-        if (S.inside == want) return Cut{prefix, kAll};   // whatever the lower bits are
-        // (the barriers at the start of the next turn keep S until all have read it)
-    }
-    return Cut{prefix, want};
-}
+// Keys' columns in work-items: column (base + k) THREADS + tid for k < PER, and all of a row's where PER
+// times THREADS reaches them (in registers then); each(f): f(key) of all of the work-item's.
+template <uint32_t THREADS, int PER>
+struct CutScratch {
+    static constexpr uint32_t N = PER * THREADS / 64;
+    uint32_t bins[3][256];   // one in use, one read by those who are late, one made zero
+    uint32_t wave[2][THREADS / 64];
+    uint64_t bits[2][THREADS / 64];
+    uint32_t ties[N], in[N];
+};
 
-// Whether key k of column i is on the upper side, for columns in ascending order of
-// THREADS at a time (all work-items call it alike): `seen` counts the ties so far.
-template <uint32_t THREADS>
-__device__ inline bool chosen(uint64_t k, const Cut &C, int top, uint32_t &seen, CutScratch<THREADS> &S)
+template <uint32_t THREADS, int PER, class Each>
+__device__ inline Keys look_over(Each each, CutScratch<THREADS, PER> &S)
 {
-    const uint64_t whole = top >= 56 ? ~uint64_t(0) : (uint64_t(1) << (top + 8)) - 1;
-    const uint64_t x = k & whole;
-    if (C.ties == kAll) return k && x >= C.key;
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const bool tie = k && x == C.key;
-    const uint64_t ties = __ballot(tie);
-    if (lane == 0) S.wave[0][wave] = (uint32_t)__popcll(ties);
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    Keys K{};
+    each([&](uint64_t k) {
+        K.held += k != 0;
+        K.forced += k == kForced;
+        K.ones |= k == kForced ? 0 : k;
+        K.zeros |= k == 0 ? 0 : ~k;
+    });
+    auto any = [](uint64_t x) {
+        auto both = [](uint32_t a, uint32_t b) { return a | b; };
+        return (uint64_t)last_lane(wave_scan((uint32_t)(x >> 32), 0u, both)) << 32 | last_lane(wave_scan((uint32_t)x, 0u, both));
+    };
+    K.held = wave_sum(K.held);
+    K.forced = wave_sum(K.forced);
+    K.ones = any(K.ones);
+    K.zeros = any(K.zeros);
+    if (lane == 0) {
+        S.wave[0][wave] = K.held;
+        S.wave[1][wave] = K.forced;
+        S.bits[0][wave] = K.ones;
+        S.bits[1][wave] = K.zeros;
+    }
+    for (uint32_t b = tid; b < 512; b += THREADS) S.bins[b / 256][b % 256] = 0;
     __syncthreads();
-    uint32_t rank = seen + (uint32_t)__popcll(ties & ((uint64_t(1) << lane) - 1));
+    K = Keys{};
 #pragma unroll
     for (uint32_t w = 0; w < THREADS / 64; ++w) {
-        if (w < wave) rank += S.wave[0][w];
-        seen += S.wave[0][w];
+        K.held += S.wave[0][w];
+        K.forced += S.wave[1][w];
+        K.ones |= S.bits[0][w];
+        K.zeros |= S.bits[1][w];
+    }
+    return K;
+}
+
+// After look_over.  One barrier a turn: every wave adds up the digits itself.
+template <uint32_t THREADS, int PER, class Each>
+__device__ inline Cut cut_largest(uint32_t want, const Keys &K, Each each, CutScratch<THREADS, PER> &S)
+{
+    const uint32_t tid = threadIdx.x, lane = tid & 63;
+    if (want <= K.forced) return Cut{kForced, want};
+    want -= K.forced;
+    const uint64_t differ = K.ones & K.zeros;
+    if (differ == 0) return Cut{K.ones, want};
+    const int top = 63 - __clzll((long long)differ);
+    uint64_t mask = ~((uint64_t(2) << top) - 1), prefix = K.ones & mask;
+    uint32_t turn = 0;
+    for (int shift = max(top - 7, 0);; shift = max(shift - 8, 0)) {
+        uint32_t *bins = S.bins[turn];
+        each([&](uint64_t k) {
+            if (k && k != kForced && (k & mask) == prefix) atomicAdd(&bins[(uint32_t)(k >> shift) & 255], 1);
+        });
+        turn = turn == 2 ? 0 : turn + 1;
+        if (shift < top - 7)   // (the second is zero from the start)
+            for (uint32_t b = tid; b < 256; b += THREADS) S.bins[turn][b] = 0;
+        __syncthreads();
+        uint32_t c[4], sum = 0;   // lane 0 has the four largest digits
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            c[x] = bins[255 - 4 * lane - x];
+            sum += c[x];
+        }
+        const uint32_t upto = wave_prefix(sum);
+        uint32_t before = upto - sum;
+        const uint64_t here = __ballot(before < want && want <= upto);   // one lane
+        uint32_t digit = 0, above = 0, inside = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (before < want && want <= before + c[x]) {
+                digit = 255 - 4 * lane - x;
+                above = before;
+                inside = c[x];
+            }
+            before += c[x];
+        }
+        const int who = __ffsll((unsigned long long)here) - 1;
+        digit = (uint32_t)__builtin_amdgcn_readlane((int)digit, who);
+        above = (uint32_t)__builtin_amdgcn_readlane((int)above, who);
+        inside = (uint32_t)__builtin_amdgcn_readlane((int)inside, who);
+        prefix |= (uint64_t)digit << shift;
+        mask |= uint64_t(255) << shift;
+        want -= above;
+        if (inside == want) return Cut{prefix, kAll};   // whatever the lower bits are
+        if (shift == 0) return Cut{prefix, want};
+    }
+}
+
+// at[k]: how many of all before column (k, tid), in the columns' order, are in; returns how
+// many there are.  `part` is not written again before the caller's next barrier.
+template <uint32_t THREADS, int PER>
+__device__ inline uint32_t rank_columns(const bool (&in)[PER], uint32_t (&at)[PER], uint32_t *part)
+{
+    constexpr uint32_t W = THREADS / 64, N = PER * W, V = (N + 63) / 64;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const uint64_t these = __ballot(in[k]);
+        at[k] = (uint32_t)__popcll(these & ((uint64_t(1) << lane) - 1));
+        if (lane == 0) part[k * W + wave] = (uint32_t)__popcll(these);
     }
     __syncthreads();
-    return k && (x > C.key || (tie && rank < C.ties));
+    uint32_t before[V], sum = 0;
+#pragma unroll
+    for (uint32_t v = 0; v < V; ++v) {
+        before[v] = sum;
+        sum += lane * V + v < N ? part[lane * V + v] : 0;
+    }
+    const uint32_t upto = wave_prefix(sum);
+#pragma unroll
+    for (uint32_t v = 0; v < V; ++v) before[v] += upto - sum;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const uint32_t x = __builtin_amdgcn_readfirstlane(k * W + wave);
+#pragma unroll
+        for (uint32_t v = 0; v < V; ++v)
+            if (x % V == v) at[k] += (uint32_t)__builtin_amdgcn_readlane((int)before[v], x / V);
+    }
+    return last_lane(upto);
+}
+
+// Which keys are on the upper side, of PER THREADS columns in ascending order (all
+// work-items call it alike): `seen` counts the ties so far.
+template <uint32_t THREADS, int PER>
+__device__ inline void choose(const uint64_t (&key)[PER], const Cut &C, uint32_t &seen, bool (&in)[PER], CutScratch<THREADS, PER> &S)
+{
+    if (C.ties == kAll) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) in[k] = key[k] && key[k] >= C.key;
+        return;
+    }
+    bool tie[PER];
+    uint32_t at[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) tie[k] = key[k] && key[k] == C.key;
+    const uint32_t all = rank_columns<THREADS, PER>(tie, at, S.ties);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) in[k] = key[k] && (key[k] > C.key || (tie[k] && seen + at[k] < C.ties));
+    seen += all;
 }
 
 // Doubles as integers of the same order; NaN the least.
@@ -230,9 +317,6 @@ __device__ inline uint64_t sortable(double x)
 // ---------------------------------------------------------------------------
 // Selection.
 
-constexpr uint32_t kSelectHeads = 8;   // query heads in LDS at a time
-constexpr uint64_t kForced = ~uint64_t(0);
-
 struct RowPages {
     uint32_t used, hi;   // columns in use; positions
 };
@@ -242,208 +326,219 @@ __device__ inline RowPages row_pages(const int32_t *lens, int64_t at, uint32_t c
     return RowPages{hi ? by_page.div(hi - 1) + 1 : 0, hi};
 }
 
-// Scores of columns [c0, c1) of row r and kv head h into keys[c - c0] (LDS or memory).
-// Eight lanes share a page: each has NP pieces of its bounds, for up to four query
-// heads at a time.  Products and sums are binary64: whole numbers come of them, so
+template <int CTRL>
+__device__ inline double moved(double x)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Scores of a work-group's columns of a row and kv head into keys.  Eight lanes share a
+// page: each has NP pieces of its bounds and of HEADS query heads at a time (in registers:
+// from LDS their reading took longer than the sums).  A page's id is asked for two turns
+// ahead, its bounds one.  Products and sums are binary64: whole numbers come of them, so
 // what another order of summing would round otherwise must not show.
-template <int TY, int NP>
-__device__ inline void score_columns(const SelectArgs &A, uint32_t r, uint32_t h, uint32_t used, uint32_t c0, uint32_t c1,
-                                     uint64_t *keys, double *s_q)
+template <int TY, int NP, int HEADS, AttnEdge EDGE>
+__global__ __launch_bounds__(256) void k_select_score(const SelectArgs A)
 {
     typedef typename AttnType<TY>::T T;
-    constexpr int E = AttnType<TY>::E;
-    const uint32_t tid = threadIdx.x, width = 8 * E * NP;
-    const uint32_t sub = tid & 7;
-    for (uint32_t g0 = 0; g0 < A.group; g0 += kSelectHeads) {
-        const uint32_t heads = min(kSelectHeads, A.group - g0);
-        __syncthreads();   // the heads before are done with
-        for (uint32_t i = tid; i < heads * width; i += blockDim.x) {
-            const uint32_t g = i / width, e = i - g * width;
-            double x = 0.0;
-            if (e < A.d) {
-                const char *p = (const char *)A.q + (int64_t)r * A.qs[0] + (int64_t)(h * A.group + g0 + g) * A.qs[1] + e * sizeof(T);
-                if constexpr (TY == S_F32) x = *(const float *)p;
-                else if constexpr (TY == S_BF16) x = (double)(float)*(const __bf16 *)p;
-                else x = (double)(float)*(const _Float16 *)p;
-            }
-            s_q[i] = x;
-        }
-        __syncthreads();
-        for (uint32_t base = c0; base < c1; base += blockDim.x / 8) {
-            const uint32_t c = base + tid / 8;
-            int32_t id = -1;
-            if (c < c1) id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
-            const bool held = id >= 0 && (uint32_t)id < A.n;
-            const bool forced = c < A.first || c + A.last >= used;
-            float lo[NP][E], hi[NP][E];
-            const char *b = (const char *)A.bounds + (int64_t)(held ? id : 0) * A.bs[0] + (int64_t)h * A.bs[1];
-            if (held && !forced) {
+    constexpr int E = AttnType<TY>::E, W = E * NP;
+    constexpr uint32_t kTurn = 256 / 8;
+    const uint32_t x = A.by_groups.div(blockIdx.x), part = blockIdx.x - x * A.groups;
+    const uint32_t r = A.by_hk.div(x), h = x - r * A.hk, sub = threadIdx.x & 7;
+    const RowPages R = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
+    const uint32_t each = (R.used + A.groups - 1) / A.groups, c0 = min(part * each, R.used), c1 = min(c0 + each, R.used);
+    if (c0 >= c1) return;
+    uint64_t *keys = A.keys + (uint64_t)x * A.cols;
+    const int32_t *pages = A.pages + (int64_t)r * A.pages_s[0];
+    // Pieces that would reach past the end are moved back to end with it, and what two of them
+    // then hold is 0 in the second.
+    auto pieces = [&](const char *p, u32x4 (&x)[NP]) {
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    const uint32_t at = (p * 8 + sub) * E;
-                    u32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-                    if (at + E <= A.d) {
-                        x = load16(b + at * sizeof(T));
-                        y = load16(b + A.bs[2] + at * sizeof(T));
-                    } else if (at < A.d) {
-                        x = load_some<T, E>(b + at * sizeof(T), (int)(A.d - at));
-                        y = load_some<T, E>(b + A.bs[2] + at * sizeof(T), (int)(A.d - at));
+        for (int i = 0; i < NP; ++i) {
+            const uint32_t at = (i * 8 + sub) * E;
+            if constexpr (EDGE == kTiny) x[i] = load_some<T, E>(p + at * sizeof(T), (int)A.d - (int)at);
+            else x[i] = load16(p + (EDGE == kTail ? min(at, A.d - E) : at) * sizeof(T));
+        }
+    };
+    auto masked = [&](u32x4 x, int i) {
+        if (EDGE == kTail && (uint32_t)(i + 1) * 8 * E > A.d) {
+            const int at = (i * 8 + (int)sub) * E, twice = at - min(at, (int)A.d - E);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if constexpr (E == 8)
+                    x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
+                else
+                    x[w] &= w >= twice ? ~0u : 0u;
+            }
+        }
+        return x;
+    };
+    struct Page {
+        uint32_t c;
+        bool held, scored;
+        u32x4 lo[NP], hi[NP];
+    };
+    auto id_of = [&](uint32_t c) { return c < c1 ? pages[(int64_t)c * A.pages_s[1]] : -1; };
+    auto ask = [&](Page &P, uint32_t c, int32_t id) {
+        P.c = c;
+        P.held = id >= 0 && (uint32_t)id < A.n;
+        P.scored = P.held && c >= A.first && c + A.last < R.used && R.used > A.take;   // (few pages: all that are held)
+        if (!P.scored) return;
+        const char *b = (const char *)A.bounds + (int64_t)id * A.bs[0] + (int64_t)h * A.bs[1];
+        pieces(b, P.lo);
+        pieces(b + A.bs[2], P.hi);
+    };
+    for (uint32_t g0 = 0; g0 < A.group; g0 += HEADS) {
+        Page P{}, next{};
+        const uint32_t c = c0 + threadIdx.x / 8;
+        int32_t id0 = id_of(c), id = id_of(c + kTurn);
+        float q[HEADS][W];   // (past the last head, it once more: the largest score is the same)
+#pragma unroll
+        for (int u = 0; u < HEADS; ++u) {
+            u32x4 x[NP];
+            pieces((const char *)A.q + (int64_t)r * A.qs[0] + (int64_t)(h * A.group + min(g0 + u, A.group - 1)) * A.qs[1], x);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) to_floats<TY>(masked(x[i], i), &q[u][i * E]);
+        }
+        ask(P, c, id0);
+        // a key is written a turn later, before that turn's loads: the wait for them is for it too
+        uint64_t ready = 0;
+        auto write = [&](uint32_t c) {
+            if (sub == 0 && c < c1) keys[c] = ready;
+        };
+        for (uint32_t base = c0; base < c1; base += kTurn) {
+            if (base != c0) write(P.c - kTurn);
+            const uint64_t old = g0 && P.c < c1 ? keys[P.c] : 0;   // its own
+            ask(next, P.c + kTurn, id);
+            id = id_of(P.c + 2 * kTurn);
+            double sum[HEADS] = {};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float lo[E], hi[E];
+                to_floats<TY>(masked(P.lo[i], i), lo);
+                to_floats<TY>(masked(P.hi[i], i), hi);
+#pragma unroll
+                for (int u = 0; u < HEADS; ++u) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        asm volatile("" : "+v"(q[u][i * E + e]));   // not kept as binary64: twice the registers
+                        const float x = q[u][i * E + e];
+                        sum[u] = __builtin_fma((double)x, (double)(x < 0.0f ? lo[e] : hi[e]), sum[u]);
                     }
-                    to_floats<TY>(x, lo[p]);
-                    to_floats<TY>(y, hi[p]);
                 }
             }
             uint64_t best = 0;
-            for (uint32_t g = 0; g < heads; g += 4) {
-                double sum[4] = {0.0, 0.0, 0.0, 0.0};
-                if (held && !forced) {
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (g + u >= heads) break;
-                            const double *q = s_q + (g + u) * width + (p * 8 + sub) * E;
-#pragma unroll
-                            for (int e = 0; e < E; ++e) sum[u] = __builtin_fma(q[e], (double)(q[e] < 0.0 ? lo[p][e] : hi[p][e]), sum[u]);
-                        }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (g + u >= heads) break;
-                    sum[u] += __shfl_xor(sum[u], 1);
-                    sum[u] += __shfl_xor(sum[u], 2);
-                    sum[u] += __shfl_xor(sum[u], 4);
-                    const uint64_t k = sortable(sum[u]);
-                    best = k > best ? k : best;
-                }
+            for (int u = 0; u < HEADS; ++u) {
+                sum[u] += moved<0xB1>(sum[u]);    // lane ^ 1
+                sum[u] += moved<0x4E>(sum[u]);    // lane ^ 2
+                sum[u] += moved<0x141>(sum[u]);   // 7 - lane of eight: the other four's, all alike
+                const uint64_t k = sortable(sum[u]);
+                best = k > best ? k : best;
             }
-            if (sub == 0 && c < c1) {
-                uint64_t k = !held ? 0 : forced ? kForced : best;
-                if (g0) {
-                    const uint64_t old = keys[c - c0];
-                    k = old > k ? old : k;
-                }
-                keys[c - c0] = k;
-            }
+            ready = !P.held ? 0 : P.scored ? best : kForced;
+            ready = old > ready ? old : ready;
+            P = next;
         }
+        write(P.c - kTurn);
     }
 }
 
-// The table of row r and kv head h from the keys of its columns.
-template <uint32_t THREADS, class Get>
-__device__ inline void choose_columns(const SelectArgs &A, uint32_t r, uint32_t h, const RowPages &P, Get get,
-                                      CutScratch<THREADS> &S)
+// The table of a row and kv head from the keys of its columns.  IN: all of them are in
+// registers; otherwise they are read from memory in every turn.
+template <uint32_t THREADS, int PER, bool IN>
+__global__ __launch_bounds__(THREADS) void k_select_choose(const SelectArgs A)
 {
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
-    uint32_t held = 0;
-    for (uint32_t c = tid; c < P.used; c += THREADS) held += get(c) != 0;
-    held = wave_sum(held);
-    if (lane == 0) S.wave[0][wave] = held;
-    __syncthreads();
-    held = 0;
+    __shared__ CutScratch<THREADS, PER> S;
+    const uint32_t tid = threadIdx.x;
+    const uint32_t r = A.by_hk.div(blockIdx.x), h = blockIdx.x - r * A.hk;
+    const uint64_t *keys = A.keys + (uint64_t)blockIdx.x * A.cols;
+    const int32_t *pages = A.pages + (int64_t)r * A.pages_s[0];
+    uint64_t key[PER] = {};
+    int32_t id[PER] = {};
+    auto read = [&](uint32_t base) {   // (keys past a row's end are not written, and not used)
 #pragma unroll
-    for (uint32_t w = 0; w < THREADS / 64; ++w) held += S.wave[0][w];
-    __syncthreads();
+        for (int k = 0; k < PER; ++k) {
+            const uint32_t c = min(base + k * THREADS + tid, A.cols - 1);
+            key[k] = keys[c];
+            id[k] = pages[(int64_t)c * A.pages_s[1]];
+        }
+    };
+    if (IN && A.cols) read(0);
+    const RowPages P = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
+    auto end = [&](uint32_t base) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (base + k * THREADS + tid >= P.used) key[k] = 0;
+    };
+    if (IN) end(0);
+    auto each = [&](auto f) {
+        if constexpr (IN) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k) f(key[k]);
+        } else {
+            for (uint32_t c = tid; c < P.used; c += THREADS) f(keys[c]);
+        }
+    };
+    const Keys K = look_over<THREADS, PER>(each, S);
     Cut C{0, kAll};   // all of them
-    if (held > A.take) C = cut_largest<THREADS>(P.used, A.take, 56, get, S);
+    if (K.held > A.take) C = cut_largest<THREADS, PER>(A.take, K, each, S);
     int32_t *out = A.pages_out + (int64_t)r * A.pages_out_s[0] + (int64_t)h * A.pages_out_s[1];
-    uint32_t count = 0, seen = 0;
-    __syncthreads();
-    const uint32_t all = min(held, A.take);
+    const uint32_t all = min(K.held, A.take);
     if (all == 0 && tid == 0) A.lens_out[(int64_t)r * A.lens_out_s[0] + (int64_t)h * A.lens_out_s[1]] = 0;
-    for (uint32_t base = 0; base < P.used && count < all; base += THREADS) {
-        const uint32_t c = base + tid;
-        const uint64_t k = c < P.used ? get(c) : 0;
-        const bool in = chosen<THREADS>(k, C, 56, seen, S);
-        const uint64_t these = __ballot(in);
-        if (lane == 0) S.wave[1][wave] = (uint32_t)__popcll(these);
-        __syncthreads();
-        uint32_t at = count + (uint32_t)__popcll(these & ((uint64_t(1) << lane) - 1));
+    uint32_t count = 0, seen = 0;
+    for (uint32_t base = 0; base < P.used && count < all; base += PER * THREADS) {
+        if (!IN) {
+            __syncthreads();   // the ranks of the turn before are done with
+            read(base);
+            end(base);
+        }
+        bool in[PER];
+        uint32_t at[PER];
+        choose<THREADS, PER>(key, C, seen, in, S);
+        const uint32_t n = rank_columns<THREADS, PER>(in, at, S.in);
 #pragma unroll
-        for (uint32_t w = 0; w < THREADS / 64; ++w) {
-            if (w < wave) at += S.wave[1][w];
-            count += S.wave[1][w];
-        }
-        __syncthreads();
-        if (in) {
-            out[(int64_t)at * A.pages_out_s[2]] = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
-            if (at + 1 == all)
+        for (int k = 0; k < PER; ++k) {
+            if (!in[k]) continue;
+            const uint32_t c = base + k * THREADS + tid, to = count + at[k];
+            out[(int64_t)to * A.pages_out_s[2]] = id[k];
+            if (to + 1 == all)
                 A.lens_out[(int64_t)r * A.lens_out_s[0] + (int64_t)h * A.lens_out_s[1]] =
-                    (int32_t)(at * A.page + (c + 1 == P.used ? P.hi - c * A.page : A.page));
+                    (int32_t)(to * A.page + (c + 1 == P.used ? P.hi - c * A.page : A.page));
         }
+        count += n;
     }
     for (uint32_t i = all + tid; i < A.take; i += THREADS) out[(int64_t)i * A.pages_out_s[2]] = -1;
 }
 
-// One work-group to a row and kv head: scores, keys in LDS, choice.
-template <int TY, int NP>
-__global__ __launch_bounds__(256) void k_select_alone(const SelectArgs A)
+template <int TY, int NP, AttnEdge EDGE>
+int launch_score(const SelectArgs &A, void *stream)
 {
-    extern __shared__ __attribute__((aligned(16))) uint64_t s_dynamic[];
-    __shared__ CutScratch<256> S;
-    const uint32_t r = A.by_hk.div(blockIdx.x), h = blockIdx.x - r * A.hk;
-    const RowPages P = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
-    uint64_t *keys = s_dynamic;
-    double *s_q = (double *)(s_dynamic + (A.cols + 1) / 2 * 2);
-    if (P.used <= A.take) {   // all that are held: no scores
-        for (uint32_t c = threadIdx.x; c < P.used; c += 256) {
-            const int32_t id = A.pages[(int64_t)r * A.pages_s[0] + (int64_t)c * A.pages_s[1]];
-            keys[c] = id >= 0 && (uint32_t)id < A.n ? kForced : 0;
-        }
-    } else {
-        score_columns<TY, NP>(A, r, h, P.used, 0, P.used, keys, s_q);
-    }
-    __syncthreads();
-    choose_columns<256>(A, r, h, P, [&](uint32_t c) { return keys[c]; }, S);
-}
-
-// Many columns and few rows: A.groups work-groups score a row and kv head, one chooses.
-template <int TY, int NP>
-__global__ __launch_bounds__(256) void k_select_score(const SelectArgs A)
-{
-    extern __shared__ __attribute__((aligned(16))) uint64_t s_dynamic[];
-    const uint32_t x = A.by_groups.div(blockIdx.x), part = blockIdx.x - x * A.groups;
-    const uint32_t r = A.by_hk.div(x), h = x - r * A.hk;
-    const RowPages P = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
-    const uint32_t each = (P.used + A.groups - 1) / A.groups, c0 = min(part * each, P.used), c1 = min(c0 + each, P.used);
-    if (c0 < c1) score_columns<TY, NP>(A, r, h, P.used, c0, c1, A.keys + (uint64_t)x * A.cols + c0, (double *)s_dynamic);
-}
-
-__global__ __launch_bounds__(1024) void k_select_choose(const SelectArgs A)
-{
-    __shared__ CutScratch<1024> S;
-    const uint32_t r = A.by_hk.div(blockIdx.x), h = blockIdx.x - r * A.hk;
-    const RowPages P = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
-    const uint64_t *keys = A.keys + (uint64_t)blockIdx.x * A.cols;
-    choose_columns<1024>(A, r, h, P, [&](uint32_t c) { return keys[c]; }, S);
-}
-
-template <int TY, int NP>
-int launch_select_one(const SelectArgs &A, void *stream)
-{
-    constexpr int E = AttnType<TY>::E;
-    const uint32_t q_lds = std::min(A.group, kSelectHeads) * 8 * E * NP * 8;
-    if (!A.keys)
-        return launch_kernel(reinterpret_cast<const void *>(&k_select_alone<TY, NP>), dim3(A.b * A.hk), dim3(256),
-                             (A.cols + 1) / 2 * 16 + q_lds, stream, A);
-    const int rc = launch_kernel(reinterpret_cast<const void *>(&k_select_score<TY, NP>), dim3(A.b * A.hk * A.groups), dim3(256),
-                                 q_lds, stream, A);
-    if (rc) return rc;
-    return launch_kernel(reinterpret_cast<const void *>(&k_select_choose), dim3(A.b * A.hk), dim3(1024), 0, stream, A);
+    constexpr int HEADS = AttnType<TY>::E * NP <= 16 ? 4 : 2;
+    const void *fn = A.group == 1 ? reinterpret_cast<const void *>(&k_select_score<TY, NP, 1, EDGE>)
+                                  : reinterpret_cast<const void *>(&k_select_score<TY, NP, HEADS, EDGE>);
+    return launch_kernel(fn, dim3(A.b * A.hk * A.groups), dim3(256), 0, stream, A);
 }
 
 template <int TY>
 int launch_select_type(const SelectArgs &A, void *stream)
 {
-    constexpr int U = 8 / AttnType<TY>::E;
-    return A.d <= 64 ? launch_select_one<TY, U>(A, stream)
-           : A.d <= 128 ? launch_select_one<TY, 2 * U>(A, stream)
-                        : launch_select_one<TY, 4 * U>(A, stream);
+    constexpr int E = AttnType<TY>::E, U = 8 / E;
+    return A.d < (uint32_t)E ? launch_score<TY, U, kTiny>(A, stream)
+           : A.d == 64       ? launch_score<TY, U, kExact>(A, stream)
+           : A.d < 64        ? launch_score<TY, U, kTail>(A, stream)
+           : A.d == 128      ? launch_score<TY, 2 * U, kExact>(A, stream)
+           : A.d < 128       ? launch_score<TY, 2 * U, kTail>(A, stream)
+           : A.d == 256      ? launch_score<TY, 4 * U, kExact>(A, stream)
+                             : launch_score<TY, 4 * U, kTail>(A, stream);
 }
 
 // ---------------------------------------------------------------------------
-// Eviction.  A work-group to a row.  Keys of up to kSelectAlone columns stay in LDS, those
-// of longer rows are made anew from the masses in each turn.
+// Eviction.  A work-group to a row, whose keys are in registers (IN) or made anew from the
+// masses in each turn.
 
 __global__ __launch_bounds__(256) void k_evict_refs(const EvictArgs A)
 {
@@ -451,62 +546,94 @@ __global__ __launch_bounds__(256) void k_evict_refs(const EvictArgs A)
     if (i < A.n) A.refs_out[(int64_t)i * A.refs_out_s] = A.refs[(int64_t)i * A.refs_s];
 }
 
-template <bool KEPT>
-__global__ __launch_bounds__(256) void k_evict(const EvictArgs A)
+template <uint32_t THREADS, int PER, bool IN>
+__global__ __launch_bounds__(THREADS) void k_evict(const EvictArgs A)
 {
-    extern __shared__ uint64_t s_keys[];
-    __shared__ CutScratch<256> S;
-    const uint32_t r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
-    const RowPages P = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
+    __shared__ CutScratch<THREADS, PER> S;
+    __shared__ uint32_t s_held[THREADS / 64];
+    const uint32_t r = blockIdx.x, tid = threadIdx.x;
     const int32_t *pages = A.pages + (int64_t)r * A.pages_s[0];
     const float *mass = A.mass + (int64_t)r * A.mass_s[0];
     int32_t *out = A.pages_out + (int64_t)r * A.pages_out_s[0];
+    uint64_t key[PER];
+    int32_t id[PER] = {};
+    float x[PER] = {};
+    auto read = [&](uint32_t base) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const uint32_t c = min(base + k * THREADS + tid, A.cols - 1);
+            id[k] = pages[(int64_t)c * A.pages_s[1]];
+            x[k] = mass[(int64_t)c * A.mass_s[1]];
+        }
+    };
+    if (IN && A.cols) read(0);
+    const uint32_t budget = (uint32_t)max(A.budget[(int64_t)r * A.budget_s], 0);
+    const RowPages P = row_pages(A.lens, (int64_t)r * A.lens_s, A.cols, A.page, A.by_page);
     // the less mass, the larger; 0: not to be taken out
-    auto make = [&](uint32_t c, int32_t id) {
-        if (id < 0 || (uint32_t)id >= A.n || c < A.first || c + A.last >= P.used) return uint64_t(0);
-        const float x = mass[(int64_t)c * A.mass_s[1]];
+    auto make = [&](uint32_t c, int32_t id, float x) {
+        if (c >= P.used || id < 0 || (uint32_t)id >= A.n || c < A.first || c + A.last >= P.used) return uint64_t(0);
         uint32_t b = __builtin_bit_cast(uint32_t, x == 0.0f ? 0.0f : x);
         b = x != x ? ~0u : b >> 31 ? ~b : b | 1u << 31;
         return uint64_t(1) << 32 | (uint32_t)~b;
     };
-    uint32_t held = 0, loose = 0;
-    for (uint32_t c = tid; c < P.used; c += 256) {
-        const int32_t id = pages[(int64_t)c * A.pages_s[1]];
-        held += id >= 0 && (uint32_t)id < A.n;
-        const uint64_t k = make(c, id);
-        loose += k != 0;
-        if (KEPT) s_keys[c] = k;
+    auto end = [&](uint32_t base) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) key[k] = make(base + k * THREADS + tid, id[k], x[k]);
+    };
+    uint32_t held = 0;
+    if (IN) {
+        end(0);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) held += k * THREADS + tid < P.used && id[k] >= 0 && (uint32_t)id[k] < A.n;
+    } else {
+        for (uint32_t c = tid; c < P.used; c += THREADS) {
+            const int32_t id = pages[(int64_t)c * A.pages_s[1]];
+            held += id >= 0 && (uint32_t)id < A.n;
+        }
     }
     held = wave_sum(held);
-    loose = wave_sum(loose);
-    if (lane == 0) {
-        S.wave[0][wave] = held;
-        S.wave[1][wave] = loose;
-    }
-    __syncthreads();
-    held = loose = 0;
+    if ((tid & 63) == 0) s_held[tid / 64] = held;
+    auto each = [&](auto f) {
+        if constexpr (IN) {
 #pragma unroll
-    for (uint32_t w = 0; w < 4; ++w) {
-        held += S.wave[0][w];
-        loose += S.wave[1][w];
-    }
-    __syncthreads();
-    const uint32_t budget = (uint32_t)max(A.budget[(int64_t)r * A.budget_s], 0);
-    const uint32_t over = held > budget ? min(held - budget, loose) : 0;
-    auto get = [&](uint32_t c) { return KEPT ? s_keys[c] : make(c, pages[(int64_t)c * A.pages_s[1]]); };
+            for (int k = 0; k < PER; ++k) f(key[k]);
+        } else {
+            for (uint32_t c = tid; c < P.used; c += THREADS) f(make(c, pages[(int64_t)c * A.pages_s[1]], mass[(int64_t)c * A.mass_s[1]]));
+        }
+    };
+    const Keys K = look_over<THREADS, PER>(each, S);
+    held = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < THREADS / 64; ++w) held += s_held[w];
+    const uint32_t over = held > budget ? min(held - budget, K.held) : 0;
     Cut C{0, kAll};
-    if (over && over < loose) C = cut_largest<256>(P.used, over, 24, get, S);
-    __syncthreads();
+    if (over && over < K.held) C = cut_largest<THREADS, PER>(over, K, each, S);
     uint32_t seen = 0;
-    for (uint32_t base = 0; base < A.cols; base += 256) {
-        const uint32_t c = base + tid;
-        const int32_t id = c < A.cols ? pages[(int64_t)c * A.pages_s[1]] : -1;
-        bool gone = false;
-        if (over && base < P.used) gone = chosen<256>(c < P.used ? get(c) : 0, C, 24, seen, S);
-        if (gone) atomicSub(&A.refs_out[(int64_t)id * A.refs_out_s], 1);
-        if (c < A.cols) out[(int64_t)c * A.pages_out_s[1]] = gone || id < 0 || (uint32_t)id >= A.n ? -1 : id;
+    for (uint32_t base = 0; base < A.cols; base += PER * THREADS) {
+        if (!IN) {
+            __syncthreads();   // the ranks of the turn before are done with
+            read(base);
+            end(base);
+        }
+        bool gone[PER] = {};
+        if (over) choose<THREADS, PER>(key, C, seen, gone, S);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const uint32_t c = base + k * THREADS + tid;
+            if (c >= A.cols) continue;
+            if (gone[k]) atomicSub(&A.refs_out[(int64_t)id[k] * A.refs_out_s], 1);
+            out[(int64_t)c * A.pages_out_s[1]] = gone[k] || id[k] < 0 || (uint32_t)id[k] >= A.n ? -1 : id[k];
+        }
     }
     if (tid == 0) A.count[(int64_t)r * A.count_s] = (int32_t)over;
+}
+
+// A work-group to a row of so many columns, whose keys fit the registers of 256 or 1024 work-items or none's.
+template <class Args>
+int launch_by_columns(uint32_t cols, uint32_t rows, void (*few)(Args), void (*many)(Args), void (*any)(Args), void *stream, const Args &A)
+{
+    auto *fn = cols <= 1024 ? few : cols <= 8192 ? many : any;
+    return launch_kernel(reinterpret_cast<const void *>(fn), dim3(rows), dim3(cols <= 1024 ? 256 : 1024), 0, stream, A);
 }
 
 }  // namespace
@@ -521,9 +648,12 @@ int launch_bounds(int type, const BoundsArgs &A, void *stream)
 
 int launch_select(int type, const SelectArgs &A, void *stream)
 {
-    return type == S_F16    ? launch_select_type<S_F16>(A, stream)
-           : type == S_BF16 ? launch_select_type<S_BF16>(A, stream)
-                            : launch_select_type<S_F32>(A, stream);
+    const int rc = type == S_F16    ? launch_select_type<S_F16>(A, stream)
+                   : type == S_BF16 ? launch_select_type<S_BF16>(A, stream)
+                                    : launch_select_type<S_F32>(A, stream);
+    if (rc) return rc;
+    return launch_by_columns(A.cols, A.b * A.hk, &k_select_choose<256, 4, true>, &k_select_choose<1024, 8, true>,
+                             &k_select_choose<1024, 4, false>, stream, A);
 }
 
 int launch_evict(const EvictArgs &A, void *stream)
@@ -532,9 +662,7 @@ int launch_evict(const EvictArgs &A, void *stream)
         if (const int rc = launch_kernel(reinterpret_cast<const void *>(&k_evict_refs), dim3((A.n + 255) / 256), dim3(256), 0, stream, A))
             return rc;
     if (A.rows == 0) return 0;
-    if (A.cols <= kSelectAlone)
-        return launch_kernel(reinterpret_cast<const void *>(&k_evict<true>), dim3(A.rows), dim3(256), A.cols * 8, stream, A);
-    return launch_kernel(reinterpret_cast<const void *>(&k_evict<false>), dim3(A.rows), dim3(256), 0, stream, A);
+    return launch_by_columns(A.cols, A.rows, &k_evict<256, 4, true>, &k_evict<1024, 8, true>, &k_evict<1024, 4, false>, stream, A);
 }
 
 }  // namespace ecmd
