@@ -495,12 +495,20 @@ __device__ inline void put_statistics(const TreeArgs &A, const TreeOut &O, uint3
 template <int TY>
 __device__ inline void put4(const TreeArgs &A, const TreeOut &O, uint32_t x, uint32_t c, f32x4 sum, float total)
 {
+    typedef f32x4 F __attribute__((aligned(4)));
     if (!O.whole_row) {
-        *(f32x4 *)&A.acc[(O.place + x) * A.dv + c] = sum;   // dv is a multiple of 4 here
+        *(F *)&A.acc[(O.place + x) * A.dv + c] = sum;
         return;
     }
     const uint32_t tok = A.by_group.div(x), head = O.kvh * A.group + x - tok * A.group;
     const float to = total > 0.0f ? 1.0f : total == 0.0f || total < 0.0f ? 0.0f : total, by = total > 0.0f ? total : 1.0f;
+    if constexpr (TY == S_F32) {
+        f32x4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = to == 0.0f ? 0.0f : sum[i] / by * to;
+        *(F *)((float *)A.out + (int64_t)O.r * A.os[0] + (int64_t)tok * A.os[1] + (int64_t)head * A.os[2] + c) = y;
+        return;
+    }
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     typedef u32x2 Out __attribute__((aligned(2)));
     uint16_t y[4];
@@ -570,9 +578,12 @@ __device__ inline void put_tile(const TreeArgs &A, const TreeOut &O, uint32_t q0
             f32x4 sum = *(const f32x4 *)&s_join[(qw * 8 + g) * kRow + c];
             for (uint32_t w = qw + hw; w < kAttnWaves; w += hw) sum += *(const f32x4 *)&s_join[(w * 8 + g) * kRow + c];
             const float t = known(A, O, x, all);
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k)
-                if (c + k < A.dv) put<TY>(A, O, x, c + k, sum[k], t);
+            if (c + 4 <= A.dv) {
+                put4<TY>(A, O, x, c, sum, t);
+            } else {
+                for (uint32_t k = 0; k < 4; ++k)
+                    if (c + k < A.dv) put<TY>(A, O, x, c + k, sum[k], t);
+            }
             if (c == 0) put_statistics<TY>(A, O, x, best, t);
         }
     }

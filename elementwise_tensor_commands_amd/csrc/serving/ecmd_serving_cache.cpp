@@ -103,17 +103,26 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     bool even = P.type != S_F32 && (d * esize) % 16 == 0 && (dv * esize) % 16 == 0 && (uintptr_t)A.k % 16 == 0 && (uintptr_t)A.v % 16 == 0;
     for (int i = 0; i < 3; ++i) even = even && A.kcs[i] % 16 == 0 && A.vcs[i] % 16 == 0;
     A.tiles = !even || A.m <= 32 ? 0 : A.m > 64 && d <= 128 && dv <= 128 ? 2 : 1;
-    const uint32_t need = ceil_div(A.m, 16);
-    A.q_shift = need >= 3 ? 2 : need - 1;
-    A.q_blocks = A.tiles ? ceil_div(A.m, 64 * A.tiles) : ceil_div(need, 1u << A.q_shift);
-    const uint64_t units = (uint64_t)A.hk * A.q_blocks;
-    if ((uint64_t)(b + 8) * units > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
     uint64_t keys = (uint64_t)A.cols * A.page;
     if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + 2 * kMaxTree);
     const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep, most = std::max<uint64_t>(1, steps * (uint64_t)b);
     const uint64_t row_bytes = keys * (uint64_t)((d + dv) * esize);
     A.direct = (steps <= 6 && row_bytes <= (256 << 10)) || b > kTreeMaxRows || most > (uint64_t(1) << 30);
-    A.runs = (uint32_t)std::min(std::max<uint64_t>(1, 512 / units), std::min<uint64_t>(most, kAttnMaxRuns));
+    // While less than a work-group for each compute unit comes of it, waves part
+    // positions rather than vectors (12 rows of 4 tokens, 32 heads over 2, up to 164 positions, f32:
+    // 55 to 32 us; past that, a tile read for fewer vectors costs more: 16 rows of 28 tokens, 24
+    // heads over 8, 60 positions, f32: 25 to 32 us).
+    const uint32_t need = ceil_div(A.m, 16);
+    auto blocks = [&] { return A.tiles ? ceil_div(A.m, 64 * A.tiles) : ceil_div(need, 1u << A.q_shift); };
+    A.q_shift = need >= 3 ? 2 : need - 1;
+    while (!A.tiles && A.q_shift && (A.direct ? (uint64_t)b : most) * A.hk * blocks() < 256) --A.q_shift;
+    A.q_blocks = blocks();
+    const uint64_t units = (uint64_t)A.hk * A.q_blocks;
+    if ((uint64_t)(b + 8) * units > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
+    // Work-groups at once (2 rows of 27 tokens, 4 heads of 192 over 1, up to 56404 positions, bf16:
+    // 512 runs take 71 us, 256 54).
+    const uint64_t fit = A.tiles && (d > 128 || dv > 128) ? 256 : 512;
+    A.runs = (uint32_t)std::min(std::max<uint64_t>(1, fit / units), std::min<uint64_t>(most, kAttnMaxRuns));
     A.runs_whole = (uint64_t)b * units >= 128 && (uint64_t)b * units <= 2048 ? A.b : 0;
     auto eight = [](uint64_t x) { return (x + 7) / 8 * 8; };
     A.grid = (uint32_t)((A.direct ? eight(b) : eight(std::max(A.runs, std::max(A.runs_whole, A.b <= A.runs ? A.b : 0)))) * units);
