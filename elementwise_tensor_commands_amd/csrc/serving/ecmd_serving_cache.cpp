@@ -451,7 +451,7 @@ int plan_select(const cmd_arg *args, int32_t page, int32_t first, int32_t last, 
     // A turn of columns a work-group at least, and no more work-groups than fit at once and half
     // as many again (64 rows of 8 heads and up to 512 columns: 512 take 95 us with the attention after
     // it, 1024 92, 2048 89, 4096 93).
-    A.groups = (uint32_t)std::min<uint64_t>(ceil_div(cols, 32), std::max<uint64_t>(1, ceil_div(2048, rows)));
+    A.groups = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(ceil_div(cols, 32), ceil_div(2048, rows)));
     A.by_groups = Div31(A.groups);
     if (rows * A.groups > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
     P.workspace = (int64_t)(rows * cols * 8);

@@ -7,6 +7,10 @@ prefills a few prompts of different lengths in one packed batch, forks each into
 beams, decodes with a beam search's reordering, ends a sequence, packs the live
 pages together halfway, and prints the time of a step, eager and replayed from a
 HIP graph.  Weights are random: it shows the calls, not a language.
+
+A ``Decoder`` also checks trees of drafted tokens (``verify``), reads only the pages
+that a query may care for (``decode(take=...)``) and keeps rows within a budget of
+pages (``decode(budget=...)``).
 """
 from __future__ import annotations
 
@@ -14,7 +18,8 @@ import argparse
 import math
 import sys
 
-from . import (Command, page_assign, page_compact, page_copy, paged_attention, rope_append, rope_frequencies)
+from . import (Command, page_assign, page_bounds, page_compact, page_copy, page_evict, page_mass, page_select,
+               paged_attention, rope, rope_append, rope_frequencies, slot_move, tree_accept, tree_attention)
 
 
 class PagedCache:
@@ -24,9 +29,12 @@ class PagedCache:
     pages [rows, cols], lens [rows] and refs [n] are the current tables (int32, on
     the GPU).  Nothing here waits for the GPU or reads from it; ``stats`` holds
     what the last ``step`` (pages wanted, given) or ``compact`` (live, moved)
-    counted, for a server that looks at it now and then."""
+    counted, for a server that looks at it now and then.
 
-    def __init__(self, layers, n, page, heads, d, rows, cols, dv=None, dtype=None, device="cuda"):
+    select: the least and largest keys of every page are kept too, for ``attend_some``;
+    weigh: the weight that attention gave to every column of the tables, for ``evict``."""
+
+    def __init__(self, layers, n, page, heads, d, rows, cols, dv=None, dtype=None, device="cuda", select=False, weigh=False):
         import torch
         dtype = dtype or torch.bfloat16
 
@@ -41,6 +49,12 @@ class PagedCache:
         self.src, self.dst = table(max(rows, n // 2)), table(max(rows, n // 2))
         self.stats = table(2)
         self.rows = rows
+        # a page's bounds are copied with it
+        self.bounds = [torch.zeros(n, heads, 2, d, dtype=dtype, device=device) for _ in range(layers if select else 0)]
+        self.mass = torch.zeros(rows, cols, device=device) if weigh else None
+        self.count = table(rows)
+        # as masses: of a row's columns the last are the least
+        self.order = -torch.arange(cols, dtype=torch.float32, device=device).repeat(rows, 1)
 
     def step(self, parent, add):
         """Every row takes over row parent[r]'s sequence (-1: starts empty) and
@@ -48,7 +62,9 @@ class PagedCache:
         src, dst = self.src[:self.rows], self.dst[:self.rows]
         page_assign(self.pages, self.lens, self.refs, parent, add, self.page, self._pages, self._lens, self.refs, src,
                     dst, self.stats)
-        page_copy(self.k + self.v, src, dst)
+        page_copy(self.k + self.v + self.bounds, src, dst)
+        if self.mass is not None:
+            self.mass.copy_(self.mass[parent.clamp(min=0).long()] * ((parent >= 0) & (parent < self.rows))[:, None])
         # copied back rather than swapped: a captured step finds them in their places
         self.pages.copy_(self._pages)
         self.lens.copy_(self._lens)
@@ -63,10 +79,47 @@ class PagedCache:
         paged_attention(q, self.k[layer], self.v[layer], self.pages if pages is None else pages,
                         self.lens if lens is None else lens, out, window=window)
 
+    def attend_some(self, layer, q, out, since, take):
+        """``attend`` over the ``take`` pages of each row and kv head that q may care for
+        most; since [rows]: the positions from there on were appended after the last such call."""
+        import torch
+        heads = self.k[layer].shape[2]
+        page_bounds(self.k[layer], self.pages, self.lens, since, self.bounds[layer])
+        pages = torch.empty(self.rows, heads, take, dtype=torch.int32, device=q.device)
+        lens = torch.empty(self.rows, heads, dtype=torch.int32, device=q.device)
+        page_select(q, self.bounds[layer], self.pages, self.lens, self.page, pages, lens, first=min(1, take - 1), last=1)
+        paged_attention(q, self.k[layer], self.v[layer], pages, lens, out)
+
+    def attend_weighed(self, layer, q, out, decay=1.0):
+        """``attend`` that adds the weight every page got to ``decay`` times what it had."""
+        import torch
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        paged_attention(q, self.k[layer], self.v[layer], self.pages, self.lens, out, lse=lse)
+        page_mass(q, self.k[layer], self.pages, self.lens, lse, self.mass, self.mass, decay=decay)
+
+    def evict(self, budget):
+        """Take the pages of least weight out of rows that hold more than budget [rows],
+        but for the first and the last; ``count`` says how many."""
+        page_evict(self.pages, self.lens, self.refs, self.mass, budget, self.page, self.pages, self.refs, self.count,
+                   first=1, last=1)
+
+    def attend_tree(self, layer, q, parent, lens, out):
+        """Attention of trees of tokens, q [rows, T, hq, d], that lie at positions lens + i."""
+        tree_attention(q, self.k[layer], self.v[layer], self.pages, lens, parent, out)
+
+    def keep(self, path, old, lens):
+        """Of the tokens at positions old + i keep those of a path: they move to old, old +
+        1, ..., rows end at lens, and the pages past that are free again."""
+        slot_move(self.k + self.v, self.pages, old, path)
+        budget = (lens + (self.page - 1)) // self.page
+        page_evict(self.pages, self.lens, self.refs, self.order, budget, self.page, self.pages, self.refs, self.count,
+                   first=0, last=0)
+        self.lens.copy_(lens)
+
     def compact(self):
         """Move the live pages to the lowest ids (then the end of the pools is free)."""
         page_compact(self.pages, self.refs, self.pages, self._refs, self.src, self.dst, self.stats)
-        page_copy(self.k + self.v, self.src, self.dst)
+        page_copy(self.k + self.v + self.bounds, self.src, self.dst)
         self.refs.copy_(self._refs)
 
 
@@ -75,7 +128,7 @@ class Decoder:
     layer, the logits a product with the embedding."""
 
     def __init__(self, layers=2, vocab=1000, hq=8, hk=2, d=64, rows=12, n=256, page=16, cols=32, dtype=None, seed=0,
-                 device="cuda"):
+                 device="cuda", select=False, weigh=False):
         import torch
         dtype = dtype or torch.bfloat16
         g = torch.Generator().manual_seed(seed)
@@ -89,16 +142,16 @@ class Decoder:
         self.qkv = [weight(width, (hq + 2 * hk) * d) for _ in range(layers)]
         self.o = [weight(width, width) for _ in range(layers)]
         self.freq = rope_frequencies(d).to(device)
-        self.cache = PagedCache(layers, n, page, hk, d, rows, cols, dtype=dtype, device=device)
+        self.cache = PagedCache(layers, n, page, hk, d, rows, cols, dtype=dtype, device=device, select=select, weigh=weigh)
         names = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float32: "f32"}
         self.add = Command()                       # out = x + y, in place in x
         x, y = self.add.load(names[dtype]), self.add.load(names[dtype])
         self.add.store(self.add.add(x, y))
 
-    def forward(self, tokens, pos, row, pages=None, lens=None):
+    def forward(self, tokens, pos, row, pages=None, lens=None, attend=None):
         """Logits [T, vocab] of T tokens at positions pos of rows row, whose slots the
         cache has; pages and lens: what each token attends to (by default token t is
-        row t's newest)."""
+        row t's newest); attend(layer, q, out) in place of the cache's."""
         import torch
         hq, hk, d = self.hq, self.hk, self.d
         x = self.embedding[tokens]
@@ -107,7 +160,10 @@ class Decoder:
             q, k, v = h[:, :hq], h[:, hq:hq + hk], h[:, hq + hk:]
             self.cache.append(layer, q, k, v, pos, row, self.freq, q)          # q turned in place
             out = torch.empty(len(tokens), hq, d, dtype=x.dtype, device=x.device)
-            self.cache.attend(layer, q, out, pages, lens)
+            if attend is None:
+                self.cache.attend(layer, q, out, pages, lens)
+            else:
+                attend(layer, q, out)
             y = torch.matmul(out.view(len(tokens), hq * d), self.o[layer])
             self.add.launch(x.view(-1), y.view(-1), x.view(-1))
         return torch.matmul(x, self.embedding.t())
@@ -134,6 +190,8 @@ class Decoder:
         tokens = torch.tensor([t for p in prompts for t in p], dtype=torch.int64, device=device)
         # a token attends to its own row's pages up to itself
         logits = self.forward(tokens, pos, row, c.pages[row.long()], pos + 1)
+        for k, bounds in zip(c.k, c.bounds):
+            page_bounds(k, c.pages, c.lens, ints([0] * c.rows), bounds)
         ends, at = [], 0
         for n in count:
             at += n
@@ -141,17 +199,68 @@ class Decoder:
                 ends.append(at - 1)
         return logits[torch.tensor(ends, dtype=torch.int64, device=device)]
 
-    def decode(self, tokens, parent, alive):
+    def decode(self, tokens, parent, alive, take=0, budget=None):
         """One step of every row: row r goes on from row parent[r] with tokens[r]
         (int64); rows where alive [rows] (int32) is 0 end.  A row whose table is full
-        keeps what it has: its token sees that, and is not written.  Returns the logits."""
+        keeps what it has: its token sees that, and is not written.  take: how many pages of
+        each kv head are read (0: all; of a decoder with ``select``).  budget [rows]
+        (int32; of one with ``weigh``): how many pages a row keeps after it.  Returns the logits."""
         import torch
         c = self.cache
         parent = torch.where((alive > 0) & (parent < c.rows), parent, -1)
         pos = torch.where(parent >= 0, c.lens[parent.clamp(min=0).long()], 0)
         c.step(parent, alive)
         rows = torch.arange(c.rows, dtype=torch.int32, device=tokens.device)
-        return self.forward(tokens, pos, torch.where(c.lens > pos, rows, -1))
+        attend = None
+        if take:
+            attend = lambda layer, q, out: c.attend_some(layer, q, out, pos, take)
+        elif budget is not None:
+            attend = lambda layer, q, out: c.attend_weighed(layer, q, out, 0.9 if layer == 0 else 1.0)
+        logits = self.forward(tokens, pos, torch.where(c.lens > pos, rows, -1), attend=attend)
+        if budget is not None:
+            c.evict(budget)
+        return logits
+
+    def verify(self, tokens, parent, alive):
+        """One step that checks a tree of drafted tokens in every row: tokens [rows, T]
+        (int32), token 0 the row's newest, which ``decode`` would be given; token i > 0 a guess
+        of what follows token parent[r, i] < i (int32; -1 for token 0, others are padding).
+        Rows keep the longest path of guesses that are what the model goes on with
+        (greedily) and lose the others.  Rows where alive is 0 end.  Returns path [rows, T]
+        (the tokens kept, ascending, then -1) and last [rows], the next newest.  (A
+        decoder with ``select`` or ``weigh`` has bounds and weights of ``decode`` alone.)"""
+        import torch
+        c, device = self.cache, tokens.device
+        rows, t = tokens.shape
+        hq, hk, d = self.hq, self.hk, self.d
+        every = torch.arange(rows, dtype=torch.int32, device=device)
+        old = torch.where(alive > 0, c.lens, 0)
+        c.step(torch.where(alive > 0, every, -1), alive * t)
+        slot = old[:, None] + torch.arange(t, dtype=torch.int32, device=device)
+        # rows that have ended, and tokens without a slot, are padding
+        parent = torch.where((alive > 0)[:, None] & (slot < c.pages.shape[1] * c.page), parent, -2)
+        depth, up = (parent >= 0).to(torch.int32), parent.clamp(min=-1).long()
+        for _ in range(t.bit_length()):             # steps up the tree, doubling
+            depth = depth + torch.where(up >= 0, depth.gather(1, up.clamp(min=0)), 0)
+            up = torch.where(up >= 0, up.gather(1, up.clamp(min=0)), -1)
+        pos, slot = (old[:, None] + depth).view(1, -1), slot.reshape(-1)
+        row = torch.where(parent >= -1, every[:, None], -1).view(-1)
+        x = self.embedding[tokens.view(-1).long()]
+        for layer in range(len(self.o)):
+            h = torch.matmul(x, self.qkv[layer]).view(rows * t, hq + 2 * hk, d)
+            turned = h[None, :, :hq + hk]
+            rope(turned, pos, self.freq, turned)    # by its depth; its slot is another place
+            q, k, v = h[:, :hq], h[:, hq:hq + hk], h[:, hq + hk:]
+            c.append(layer, q, k, v, slot, row, self.freq[:0], q)
+            out = torch.empty(rows, t, hq, d, dtype=x.dtype, device=device)
+            c.attend_tree(layer, q.unflatten(0, (rows, t)), parent, old, out)
+            y = torch.matmul(out.view(rows * t, hq * d), self.o[layer])
+            self.add.launch(x.view(-1), y.view(-1), x.view(-1))
+        follow = torch.matmul(x, self.embedding.t()).argmax(-1).to(torch.int32).view(rows, t)
+        path, lens, last = torch.empty_like(parent), torch.empty_like(old), torch.empty_like(old)
+        tree_accept(tokens, parent, follow, old, path, lens, last)
+        c.keep(path, old, lens)
+        return path, last
 
 
 def next_beams(logits, alive, beams):

@@ -1,0 +1,203 @@
+"""The decoder of decode.py with trees of drafted tokens, selected pages and budgets of
+pages: the operators of each together, against decoding without them."""
+import random
+
+import pytest
+import torch
+
+from elementwise_tensor_commands_amd.decode import Decoder
+
+pytestmark = pytest.mark.gpu
+
+I32 = torch.int32
+KW = dict(layers=2, vocab=61, hq=4, hk=2, d=32, rows=5, page=4, cols=16, dtype=torch.float32)
+# Both sides' sums have at most 128 + 32 + 64 products of binary32 numbers, of sizes that the
+# layers at most square-root-of-terms-fold: half a step a term, through two layers' sums and the
+# last product, twice (each side is off by as much).
+CLOSE = 2 * 5 * (128 + 32 + 64) * 2.0 ** -24
+PROMPTS = [[5, 9, 3, 7, 1], [2] * 11, [4], [], [8, 8, 1]]
+
+
+def ints(a):
+    return torch.tensor(a, dtype=I32).cuda()
+
+
+def refs_are_the_table_s(c, n):
+    refs = [0] * n
+    for row, length in zip(c.pages.tolist(), c.lens.tolist()):
+        for j, p in enumerate(row):
+            assert p < 0 or j * c.page < length
+            if p >= 0:
+                refs[p] += 1
+    assert c.refs.tolist() == refs
+
+
+def greedy(steps):
+    """Every row's first `steps` tokens after its prompt, one at a time; row 3 starts empty."""
+    m = Decoder(n=90, **KW)
+    m.prefill(PROMPTS)
+    newest, out = torch.tensor([11, 12, 13, 14, 15]).cuda(), [[11], [12], [13], [14], [15]]
+    own = ints([0, 1, 2, 3, 4])
+    for _ in range(steps):
+        newest = m.decode(newest, own, torch.ones(5, dtype=I32).cuda()).argmax(-1)
+        for r, x in enumerate(newest.tolist()):
+            out[r].append(x)
+    return out, m
+
+
+def test_verified_guesses_are_what_decoding_gives():
+    """Trees with the right guesses, some right for a while, some wrong at once, in any order of
+    branches: the rows go on as without guesses, and no page is lost."""
+    want, plain = greedy(30)
+    m = Decoder(n=90, **KW)
+    m.prefill(PROMPTS)
+    rng = random.Random(5)
+    have = [1] * 5                                                  # tokens of want that are known: the newest is the last
+    newest = [x[0] for x in want]
+    while min(have) < 20:
+        t = rng.choice([1, 2, 7, 12])
+        tokens, parent = [[0] * t for _ in range(5)], [[-2] * t for _ in range(5)]
+        for r in range(5):
+            tokens[r][0], parent[r][0] = newest[r], -1
+            ends = [(0, 0)]                                         # tokens on a right path, and how far along
+            for i in range(1, t):
+                at, far = rng.choice(ends)
+                good = rng.random() < 0.7
+                # (what decoding gave next, or any other token: not both of one parent)
+                right = want[r][min(have[r] + far, len(want[r]) - 1)]
+                taken = [tokens[r][x] for x in range(1, i) if parent[r][x] == at]
+                tokens[r][i] = right if good and right not in taken else (right + 1 + rng.randrange(59)) % 61
+                parent[r][i] = at
+                if tokens[r][i] == right and right not in taken:
+                    ends.append((i, far + 1))
+            if r == 2 and t > 3:
+                parent[r][t - 1] = -7                               # padding
+        path, last = m.verify(ints(tokens), ints(parent), torch.ones(5, dtype=I32).cuda())
+        path, last = path.tolist(), last.tolist()
+        for r in range(5):
+            kept = [x for x in path[r] if x >= 0]
+            assert kept[0] == 0 and path[r] == kept + [-1] * (t - len(kept))
+            got = [tokens[r][x] for x in kept[1:]] + [last[r]]
+            assert got == want[r][have[r]:have[r] + len(got)], (r, got)
+            # no guess that went on was left out
+            assert not any(parent[r][x] == kept[-1] and tokens[r][x] == last[r] for x in range(kept[-1] + 1, t))
+            have[r] += len(got)
+            newest[r] = last[r]
+        assert m.cache.lens.tolist() == [len(p) + h - 1 for p, h in zip(PROMPTS, have)]
+        refs_are_the_table_s(m.cache, 90)
+        if max(have) > 26:
+            break
+    # what the caches hold is what decoding wrote, but for the order of its sums
+    a, b = m.cache, plain.cache
+    for r in range(5):
+        n = min(int(a.lens[r]), int(b.lens[r]))
+        for x, y in zip(a.k + a.v, b.k + b.v):
+            got, ref = (torch.stack([z[int(c.pages[r, i // 4]), i % 4] for i in range(n)]) for z, c in ((x, a), (y, b)))
+            assert float((got - ref).abs().max()) <= CLOSE * float(ref.abs().max())
+
+
+def test_verify_of_ended_and_full_rows():
+    m = Decoder(n=90, **dict(KW, cols=3))
+    m.prefill(PROMPTS)
+    alive = ints([1, 1, 0, 1, 0])
+    tokens = ints([[3, 1, 2]] * 5)
+    path, last = m.verify(tokens, ints([[-1, 0, 1]] * 5), alive)
+    kept = (path >= 0).sum(1).tolist()
+    assert kept[2] == kept[4] == 0 and last.tolist()[2] == -1
+    assert kept[1] == 1                                             # eleven tokens of twelve: one more has a slot
+    assert m.cache.lens.tolist() == [5 + kept[0], 12, 0, kept[3], 0]
+    refs_are_the_table_s(m.cache, 90)
+    path, last = m.verify(tokens, ints([[-1, 0, 1]] * 5), alive)    # a full row: no token of it has one
+    assert path[1].tolist() == [-1] * 3 and int(m.cache.lens[1]) == 12
+    refs_are_the_table_s(m.cache, 90)
+
+
+def test_decoding_of_selected_pages():
+    """With room for all pages the logits are decoding's; with less they are those of the pages chosen,
+    and the bounds follow forks and packed pages."""
+    plain, m, few = (Decoder(n=90, select=x, **KW) for x in (False, True, True))
+    for x in (plain, m, few):
+        x.prefill(PROMPTS)
+    g = torch.Generator().manual_seed(2)
+    for i, plan in enumerate([[0, 1, 2, 3, 4], [0, 0, 1, 3, 1], [1, 1, -1, 2, 4], [0, 1, 2, 3, 4]]):
+        tokens, parent = torch.randint(0, 61, (5,), generator=g).cuda(), ints(plan)
+        alive = (parent >= 0).to(I32)
+        a, b = plain.decode(tokens, parent, alive), m.decode(tokens, parent, alive, take=16)
+        on = (alive > 0).cpu()
+        assert float((a - b)[on].abs().max()) <= CLOSE * float(a.abs().max())
+        c = few.decode(tokens, parent, alive, take=2)
+        assert torch.isfinite(c).all() and c.shape == a.shape
+        if i == 1:
+            for x in (plain, m, few):
+                x.cache.compact()
+        # the bounds are those of the keys that the pages hold
+        for layer in range(2):
+            for r in range(5):
+                for j in range(-(-int(m.cache.lens[r]) // 4)):
+                    p, n = int(m.cache.pages[r, j]), min(4, int(m.cache.lens[r]) - 4 * j)
+                    keys = m.cache.k[layer][p, :n]
+                    assert torch.equal(m.cache.bounds[layer][p, :, 0], keys.amin(0))
+                    assert torch.equal(m.cache.bounds[layer][p, :, 1], keys.amax(0))
+
+
+def test_decoding_within_a_budget_of_pages():
+    plain, wide, m = (Decoder(n=90, weigh=x, **KW) for x in (False, True, True))
+    for x in (plain, wide, m):
+        x.prefill(PROMPTS)
+    g = torch.Generator().manual_seed(4)
+    own, ones = ints([0, 1, 2, 3, 4]), torch.ones(5, dtype=I32).cuda()
+    for i in range(14):
+        tokens = torch.randint(0, 61, (5,), generator=g).cuda()
+        parent = ints([0, 1, 1, 3, 4]) if i == 5 else own
+        a = plain.decode(tokens, parent, ones)
+        b = wide.decode(tokens, parent, ones, budget=ints([16] * 5))
+        assert float((a - b).abs().max()) <= CLOSE * float(a.abs().max())
+        assert wide.cache.count.tolist() == [0] * 5
+        # all weight of the rows that hold something: heads times layers, and what is left of earlier steps
+        total = wide.cache.mass.sum(1)
+        if i == 0:                                                  # scores below 100: each weight within 100 (d + 2) 2^-23
+            assert float((total - 8.0).abs().max()) <= 1e-3
+        c = m.decode(tokens, parent, ones, budget=ints([3, 3, 3, 2, 99]))
+        assert torch.isfinite(c).all()
+        held = (m.cache.pages >= 0).sum(1).tolist()
+        assert max(held[:3]) <= 3 and held[3] <= 2
+        refs_are_the_table_s(m.cache, 90)
+        for r in range(5):                                          # the first and the last stay
+            n = -(-int(m.cache.lens[r]) // 4)
+            assert int(m.cache.pages[r, 0]) >= 0 and int(m.cache.pages[r, n - 1]) >= 0
+
+
+def test_captured_verify():
+    """Checks replayed from a graph, with eager work between, against the same run eagerly."""
+    models, states = [], []
+    for _ in range(2):
+        m = Decoder(n=90, **KW)
+        m.prefill(PROMPTS)
+        models.append(m)
+        states.append(dict(tokens=ints([[11, 3, 5], [12, 1, 2], [13, 9, 9], [14, 0, 7], [15, 1, 1]]),
+                           parent=ints([[-1, 0, 0], [-1, 0, 1], [-1, 0, 1], [-1, 0, 0], [-1, 0, -2]]),
+                           alive=torch.ones(5, dtype=I32).cuda()))
+
+    def step(m, s):
+        path, last = m.verify(s["tokens"], s["parent"], s["alive"])
+        s["path"] = s.get("path", torch.empty_like(path)).copy_(path)
+        s["tokens"].copy_(torch.stack([last, (last * 7 + 1) % 61, (last * 3 + 2) % 61], 1))
+
+    for m, s in zip(models, states):
+        step(m, s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(models[1], states[1])
+    for i in range(8):
+        if i == 4:
+            for s in states:
+                s["alive"][1] = 0
+        step(models[0], states[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        for key in states[0]:
+            assert torch.equal(states[0][key], states[1][key]), (i, key)
+        a, b = (m.cache for m in models)
+        for x, y in ((a.pages, b.pages), (a.lens, b.lens), (a.refs, b.refs), (a.k[1], b.k[1]), (a.v[0], b.v[0])):
+            assert torch.equal(x, y), i
