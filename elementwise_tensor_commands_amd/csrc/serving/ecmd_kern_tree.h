@@ -15,11 +15,21 @@
 //   out      D[dv][query] += V^T P^T, with lane j loading the values of its keys.
 //
 // Two kernels.  k_tree_few takes keys and values from memory straight to registers;
-// the four waves of a work-group part the positions, or the queries where there are more.  It serves few queries,
-// where the caches' bytes are what counts, binary32, whose products run at a sixteenth of
-// the 16-bit rate and hide everything else, and rows off 16 bytes.  k_tree_many stages tiles of
+// the four waves of a work-group part the positions, or the queries where there are more.
+// It serves few queries or positions, where the chain from a row's length to its first key is
+// what counts (one row of 777, 8 tokens of 32 heads over 8, f16: 13 us and 5 for the join),
+// binary32, whose products run at a sixteenth of the 16-bit rate and hide everything else (5
+// rows, 23 tokens of 12 heads of 80 and 64, a window of 1000: 30 us and 7.5), and rows off
+// 16 bytes.  k_tree_many stages tiles of
 // 32 positions in LDS, once for all queries of a work-group, by loads from memory straight to
-// LDS that are up to three tiles ahead, one barrier a tile.
+// LDS that are up to two tiles ahead, one barrier a tile; values are read from there transposed.
+// One row of 131072, 64 tokens of 32 heads over 8 of 128, bf16: 249 us.  In copies that
+// leave a part out: without products 158, without reading LDS 196, without arithmetic on scores
+// 206, without loads 211; products alone 134, loads alone 150, arithmetic alone 81.  So nothing
+// bounds it alone: a SIMD holds two waves (256 registers: 32 queries, their sums and weights),
+// too few to hide each of the parts behind the others, and the products are half as many again
+// as the formula's (weights in two parts).  Four tiles in flight, tiles of 64, eight waves to a
+// work-group, products of 32 queries and priorities for waves in products all took as long.
 //
 // Which tokens a token attends to is one bit
 // mask per token, made in LDS from the parents by pointer doubling; a tile of 32

@@ -96,17 +96,22 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     A.page = (uint32_t)std::max<int64_t>(1, page);
     A.cols = n > 0 && page > 0 ? (uint32_t)cols : 0;   // a cache without slots: every row is empty
     A.window = (uint32_t)window;
-    // From 33 query vectors of 16 bits on, tiles are staged for all of a work-group's, if
-    // every row of the caches starts at a multiple of 16 bytes and is one; a wave takes 32
-    // vectors from 65 on, as far as the registers go.  Otherwise the waves part the positions
-    // of up to 16 (32) vectors, the vectors of more.
-    bool even = P.type != S_F32 && (d * esize) % 16 == 0 && (dv * esize) % 16 == 0 && (uintptr_t)A.k % 16 == 0 && (uintptr_t)A.v % 16 == 0;
-    for (int i = 0; i < 3; ++i) even = even && A.kcs[i] % 16 == 0 && A.vcs[i] % 16 == 0;
-    A.tiles = !even || A.m <= 32 ? 0 : A.m > 64 && d <= 128 && dv <= 128 ? 2 : 1;
     uint64_t keys = (uint64_t)A.cols * A.page;
     if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + 2 * kMaxTree);
     const uint64_t steps = (keys + kAttnStep - 1) / kAttnStep, most = std::max<uint64_t>(1, steps * (uint64_t)b);
     const uint64_t row_bytes = keys * (uint64_t)((d + dv) * esize);
+    // Tiles of 16-bit keys and values are staged for all query vectors of a work-group, if every
+    // row of the caches starts at a multiple of 16 bytes and is one: from 65 vectors on, and from
+    // 17 on where steps and heads are more than the compute units.  (8 tokens of 32 heads over 8, us
+    // not staged and staged: 16 rows of up to 8192 positions 76 and 62, one of 6000 23.0 and
+    // 22.6, one of 3000 19.7 and 21.1; 16 tokens: 123 and 74, one row of 777 18.3 and 21.0; 4
+    // tokens, 16 rows: 66 and 66; 64 tokens, two rows of 60: 27 and 20.)  A wave takes 32 vectors from
+    // 65 on, as far as the registers go (17 tokens: 83, with 16 97; 9 tokens: 73, with 16 68).
+    // Otherwise the waves part the positions of up to 16 (32) vectors, the vectors of more.
+    bool even = P.type != S_F32 && (d * esize) % 16 == 0 && (dv * esize) % 16 == 0 && (uintptr_t)A.k % 16 == 0 && (uintptr_t)A.v % 16 == 0;
+    for (int i = 0; i < 3; ++i) even = even && A.kcs[i] % 16 == 0 && A.vcs[i] % 16 == 0;
+    if (A.m <= 64) even = even && A.m > 16 && most * A.hk > 256;
+    A.tiles = !even ? 0 : A.m > 64 && d <= 128 && dv <= 128 ? 2 : 1;
     A.direct = (steps <= 6 && row_bytes <= (256 << 10)) || b > kTreeMaxRows || most > (uint64_t(1) << 30);
     // While less than a work-group for each compute unit comes of it, waves part
     // positions rather than vectors (12 rows of 4 tokens, 32 heads over 2, up to 164 positions, f32:

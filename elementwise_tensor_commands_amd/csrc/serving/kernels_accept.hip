@@ -14,7 +14,8 @@ constexpr uint32_t kPerLane = kMaxTree / 64;
 
 // One wave to a row, four tokens to a lane.  A step of the path is a comparison of all
 // tokens' parents and names at once and the first that fits, so it takes two exchanges
-// and no memory: the chain of steps is what the time goes to.
+// and no memory: the chain of steps is what the time goes to (128 rows of 56 tokens, paths of
+// seven: 4.8 us, one of 20 tokens: 2.2; the smallest kernel takes about 2).
 __global__ __launch_bounds__(64) void k_accept(const AcceptArgs A)
 {
     __shared__ int32_t s_next[kMaxTree], s_path[kMaxTree];
@@ -82,7 +83,9 @@ struct Vec<2> {
 // A work-group to a row, a pool and 256 vectors of a slot.  Every work-item moves its
 // own vector of one slot after the other; a path ascends with path[i] >= i, so no
 // write reaches a slot that is still to be read, and eight loads may go ahead of their
-// writes.  No two work-items share a byte: there is nothing to wait for.
+// writes.  No two work-items share a byte: there is nothing to wait for.  128 rows, up to seven
+// tokens each, 16 pools of 2 KB a slot: 7 us for 27 MB, two thirds of it from lengths over paths and
+// pages to the first slot.
 template <int W, int POOLS>
 __global__ __launch_bounds__(256) void k_move(const MoveBlock<POOLS> A)
 {

@@ -55,7 +55,9 @@ __device__ inline u32x4 from_floats(const float *f)
 // Bounds.  A work-item takes a 16-byte piece of a page's slots, one after the other,
 // eight loads ahead: neighbours read neighbours, so whole slots are read where heads
 // lie side by side, and nothing is exchanged.  A last piece that would reach past its
-// head is moved back to end with it; what two pieces then both write is the same.
+// head is moved back to end with it; what two pieces then both write is the same.  16 ragged
+// prompts of up to 4000 positions, 4 heads of 96, f16 (28 MB): 2.7 us here, 7.3 with the caller's
+// part; after a decode step of 64 rows 5.6: a chain from lengths over pages to slots.
 template <int TY>
 __global__ __launch_bounds__(256) void k_bounds(const BoundsArgs A)
 {
@@ -339,7 +341,10 @@ __device__ inline double moved(double x)
 // page: each has NP pieces of its bounds and of HEADS query heads at a time (in registers:
 // from LDS their reading took longer than the sums).  A page's id is asked for two turns
 // ahead, its bounds one.  Products and sums are binary64: whole numbers come of them, so
-// what another order of summing would round otherwise must not show.
+// what another order of summing would round otherwise must not show.  That is what bounds it:
+// an element of a head takes five instructions (compare, select, two conversions, the product) of
+// four cycles each, 64 rows of 8 kv heads by four query heads of 128 over up to 512 pages
+// 31 us, where the bounds' bytes would take 7.
 template <int TY, int NP, int HEADS, AttnEdge EDGE>
 __global__ __launch_bounds__(256) void k_select_score(const SelectArgs A)
 {
@@ -448,7 +453,9 @@ __global__ __launch_bounds__(256) void k_select_score(const SelectArgs A)
 }
 
 // The table of a row and kv head from the keys of its columns.  IN: all of them are in
-// registers; otherwise they are read from memory in every turn.
+// registers; otherwise they are read from memory in every turn.  512 tables of up to 512
+// columns 5.3 us, 4 of 4097 columns 8.3: lengths and keys from memory, then two or three
+// turns of a barrier each.
 template <uint32_t THREADS, int PER, bool IN>
 __global__ __launch_bounds__(THREADS) void k_select_choose(const SelectArgs A)
 {
@@ -538,7 +545,8 @@ int launch_select_type(const SelectArgs &A, void *stream)
 
 // ---------------------------------------------------------------------------
 // Eviction.  A work-group to a row, whose keys are in registers (IN) or made anew from the
-// masses in each turn.
+// masses in each turn.  256 rows of 640 columns: 5.2 us, and 1.2 for the copy of the counts
+// before it, which other rows' subtractions may not precede.
 
 __global__ __launch_bounds__(256) void k_evict_refs(const EvictArgs A)
 {

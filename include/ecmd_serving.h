@@ -154,7 +154,7 @@ int cmd_tree_accept(const cmd_arg args[7], int32_t flags, void *hip_stream);
  * goes to position lens[r] + i, one i after the other.  args: 0 pages [R, P]   1 lens
  * [R]   2 path [R, T], all int32.  Entries path[r, i] <= i, positions past the table
  * and holes (ids outside a pool are its holes) move nothing, nor do rows with a
- * negative length.  T <= 256.  No slot that is written may belong to another row too.
+ * negative length.  T <= 256.  No slot that is written may lie in another row or column too.
  * The elements of a slot's head are neighbours. */
 int cmd_slot_move(const cmd_arg *pools, int32_t npools, const cmd_arg args[3], int32_t flags, void *hip_stream);
 
@@ -166,7 +166,7 @@ int cmd_slot_move(const cmd_arg *pools, int32_t npools, const cmd_arg args[3], i
  * of a page whose first position is one of them are made from them, those of a page
  * that held earlier ones are widened by them.  Other pages' bounds stay.  NaN counts
  * as nothing (of NaN alone: least +inf, largest -inf).  No page with new positions may
- * belong to two rows.  Bounds are a pool to cmd_page_copy: copied pages take theirs along. */
+ * stand in two rows or columns.  Bounds are a pool to cmd_page_copy: copied pages take theirs along. */
 int cmd_page_bounds(const cmd_arg args[5], int32_t flags, void *hip_stream);
 
 /* Choose for every sequence and kv head the pages that its query tokens may care for

@@ -69,6 +69,30 @@ def test_page_evict_of_long_tables(cols):
 
 
 # ---------------------------------------------------------------------------
+# Up to 64 query vectors under wide tables: the library goes by the tables' size, so the same rows
+# with columns of holes behind them take the kernel that stages tiles.
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", [
+    (2, 20, 2, 1, 96, 128, 16, 30, 0), (2, 11, 4, 1, 128, 128, 16, 40, 0), (2, 50, 1, 1, 192, 128, 16, 20, 0), (1, 20, 6, 2, 160, 96, 32, 12, 0),
+    (2, 18, 2, 1, 192, 192, 16, 18, 40), (1, 34, 4, 4, 256, 256, 16, 18, 0), (1, 40, 1, 1, 8, 8, 16, 30, 0), (9, 10, 16, 4, 128, 128, 16, 8, 0),
+    (3, 17, 2, 2, 64, 64, 16, 30, 0), (2, 8, 8, 2, 128, 128, 16, 33, 50), (4, 32, 1, 1, 48, 64, 5, 70, 0), (2, 9, 7, 1, 72, 40, 17, 20, 9),
+])
+def test_tree_attention_under_wide_tables(case, dtype):
+    q, (kg, vg), (kc, vc), pages, lens, parent, window = tree_state(case, dtype, 6 * sum(case))     # slots at multiples of 16 bytes
+    b, t, hq, hk, d, dv, page, cols, _ = case
+    assert 16 < t * hq // hk <= 64
+    wide = torch.cat([pages, torch.full((b, 257 * 128 // page + 1), -1, dtype=I32)], 1)
+    want, want_lse, eo, el = C.tree(q, kc, vc, pages, lens, parent, 1.0 / math.sqrt(d), window)
+    out, lse = new(*want.shape, dtype=q.dtype), new(*want_lse.shape, dtype=torch.float32)
+    E.tree_attention(q.cuda(), kg, vg, wide.cuda(), lens.cuda(), parent.cuda(), out, lse=lse, window=window)
+    # a length past the shorter table: its window ends elsewhere
+    same = [r for r in range(b) if int(lens[r]) <= cols * page]
+    within(out[same], want[same], eo[same], case)
+    within(lse[same], want_lse[same], el[same], case)
+
+
+# ---------------------------------------------------------------------------
 # Caches past 32-bit offsets: pages 2^31 elements apart, and a bit.
 
 @pytest.mark.parametrize("dtype,t,hq", [("bf16", 7, 2), ("bf16", 40, 8), ("f32", 9, 2)])
