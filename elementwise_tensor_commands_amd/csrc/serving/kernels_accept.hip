@@ -14,8 +14,8 @@ constexpr uint32_t kPerLane = kMaxTree / 64;
 
 // One wave to a row, four tokens to a lane.  A step of the path is a comparison of all
 // tokens' parents and names at once and the first that fits, so it takes two exchanges
-// and no memory: the chain of steps is what the time goes to (128 rows of 56 tokens, paths of
-// seven: 4.8 us, one of 20 tokens: 2.2; the smallest kernel takes about 2).
+// and no memory: the chain of steps is what the time goes to (128 rows of eight guesses of seven
+// tokens: 3.3 us, one of four of five: 2.1; the smallest kernel takes about 2).
 __global__ __launch_bounds__(64) void k_accept(const AcceptArgs A)
 {
     __shared__ int32_t s_next[kMaxTree], s_path[kMaxTree];

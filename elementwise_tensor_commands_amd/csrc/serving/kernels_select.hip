@@ -56,8 +56,8 @@ __device__ inline u32x4 from_floats(const float *f)
 // eight loads ahead: neighbours read neighbours, so whole slots are read where heads
 // lie side by side, and nothing is exchanged.  A last piece that would reach past its
 // head is moved back to end with it; what two pieces then both write is the same.  16 ragged
-// prompts of up to 4000 positions, 4 heads of 96, f16 (28 MB): 2.7 us here, 7.3 with the caller's
-// part; after a decode step of 64 rows 5.6: a chain from lengths over pages to slots.
+// prompts of up to 4000 positions, 4 heads of 96, f16 (28 MB): 6.9 us, 4.0 TB/s; after a decode
+// step of 64 rows 5.3: a chain from lengths over pages to slots.
 template <int TY>
 __global__ __launch_bounds__(256) void k_bounds(const BoundsArgs A)
 {
@@ -344,7 +344,7 @@ __device__ inline double moved(double x)
 // what another order of summing would round otherwise must not show.  That is what bounds it:
 // an element of a head takes five instructions (compare, select, two conversions, the product) of
 // four cycles each, 64 rows of 8 kv heads by four query heads of 128 over up to 512 pages
-// 31 us, where the bounds' bytes would take 7.
+// 27 us, where the bounds' bytes would take 10.
 template <int TY, int NP, int HEADS, AttnEdge EDGE>
 __global__ __launch_bounds__(256) void k_select_score(const SelectArgs A)
 {
@@ -545,7 +545,7 @@ int launch_select_type(const SelectArgs &A, void *stream)
 
 // ---------------------------------------------------------------------------
 // Eviction.  A work-group to a row, whose keys are in registers (IN) or made anew from the
-// masses in each turn.  256 rows of 640 columns: 5.2 us, and 1.2 for the copy of the counts
+// masses in each turn.  256 rows of 1024 columns: 6.2 us, and 2.0 for the copy of the counts
 // before it, which other rows' subtractions may not precede.
 
 __global__ __launch_bounds__(256) void k_evict_refs(const EvictArgs A)
