@@ -190,19 +190,33 @@ __global__ __launch_bounds__(256) void k_mass(const MassArgs A)
     }
 }
 
+template <int TY, int NK, AttnEdge EDGE>
+int launch_mass_one(const MassArgs &A, void *stream)
+{
+    return launch_kernel(reinterpret_cast<const void *>(&k_mass<TY, NK, EDGE>), dim3(A.b * A.groups), dim3(256), 0, stream, A);
+}
+template <int TY, int NK>
+int launch_mass_edge(const MassArgs &A, void *stream)
+{
+    return A.d == (uint32_t)(NK * 4 * AttnType<TY>::E) ? launch_mass_one<TY, NK, kExact>(A, stream)
+                                                       : launch_mass_one<TY, NK, kTail>(A, stream);
+}
+
 template <int TY>
 int launch_mass_type(const MassArgs &A, void *stream)
 {
     constexpr int E = AttnType<TY>::E, U = 8 / E;
     const uint32_t d = A.d;
-    const void *fn = d < (uint32_t)E ? reinterpret_cast<const void *>(&k_mass<TY, U, kTiny>)
-                     : d == 64       ? reinterpret_cast<const void *>(&k_mass<TY, 2 * U, kExact>)
-                     : d < 64        ? reinterpret_cast<const void *>(&k_mass<TY, 2 * U, kTail>)
-                     : d == 128      ? reinterpret_cast<const void *>(&k_mass<TY, 4 * U, kExact>)
-                     : d < 128       ? reinterpret_cast<const void *>(&k_mass<TY, 4 * U, kTail>)
-                     : d == 256      ? reinterpret_cast<const void *>(&k_mass<TY, 8 * U, kExact>)
-                                     : reinterpret_cast<const void *>(&k_mass<TY, 8 * U, kTail>);
-    return launch_kernel(fn, dim3(A.b * A.groups), dim3(256), 0, stream, A);
+    // the smallest that holds d
+    if (d < (uint32_t)E) return launch_mass_one<TY, U, kTiny>(A, stream);
+    if (d <= 64) return launch_mass_edge<TY, 2 * U>(A, stream);
+    if constexpr (TY == S_F32) {
+        if (d <= 80) return launch_mass_edge<TY, 5>(A, stream);
+    }
+    return d <= 96    ? launch_mass_edge<TY, 3 * U>(A, stream)
+           : d <= 128 ? launch_mass_edge<TY, 4 * U>(A, stream)
+           : d <= 192 ? launch_mass_edge<TY, 6 * U>(A, stream)
+                      : launch_mass_edge<TY, 8 * U>(A, stream);
 }
 
 }  // namespace

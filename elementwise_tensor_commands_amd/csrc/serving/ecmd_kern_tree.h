@@ -17,9 +17,9 @@
 // Two kernels.  k_tree_few takes keys and values from memory straight to registers;
 // the four waves of a work-group part the positions, or the queries where there are more.
 // It serves few queries or positions, where the chain from a row's length to its first key is
-// what counts (one row of 777, 8 tokens of 32 heads over 8, f16: 13 us and 5 for the join),
+// what counts (one row of 777, 8 tokens of 32 heads over 8, f16: 13 us and 4 for the join),
 // binary32, whose products run at a sixteenth of the 16-bit rate and hide everything else (5
-// rows, 23 tokens of 12 heads of 80 and 64, a window of 1000: 30 us and 7.5), and rows off
+// rows, 23 tokens of 12 heads of 80 and 64, a window of 1000: 18 us and 6), and rows off
 // 16 bytes.  k_tree_many stages tiles of
 // 32 positions in LDS, once for all queries of a work-group, by loads from memory straight to
 // LDS that are up to two tiles ahead, one barrier a tile; values are read from there transposed.
@@ -623,7 +623,7 @@ constexpr int few_waves()
 {
     constexpr int KB = AttnType<TY>::KB, size = TY == S_F32 ? 4 : 2;
     constexpr int regs = KB * NK * 4 + KB * VW * size + NK * 4 + VW * 4 + KB * 8 + 60;
-    return regs > 236 ? 1 : 2;
+    return regs > 200 ? 1 : 2;   // (what the compiler takes is about 60 more)
 }
 
 template <int TY, int NK, int VW, AttnEdge EDGE>
@@ -1184,6 +1184,13 @@ int launch_tree_few(const TreeArgs &A, void *stream)
                          A.direct ? 0 : rows_lds(A.b), stream, A);
 }
 
+template <int TY, int NK, int VW>
+int launch_tree_edge(const TreeArgs &A, void *stream)
+{
+    return A.d == (uint32_t)(NK * 4 * AttnType<TY>::E) ? launch_tree_few<TY, NK, VW, kExact>(A, stream)
+                                                       : launch_tree_few<TY, NK, VW, kTail>(A, stream);
+}
+
 // The instance: the smallest that holds d and dv.
 template <int TY>
 int launch_tree_type(const TreeArgs &A, void *stream)
@@ -1202,11 +1209,20 @@ int launch_tree_type(const TreeArgs &A, void *stream)
         }
     }
     if (d < (uint32_t)E || dv < (uint32_t)E) return launch_tree_few<TY, 8 * U, 16, kTiny>(A, stream);
-    if (d <= 64 && dv <= 64)
-        return d == 64 ? launch_tree_few<TY, 2 * U, 4, kExact>(A, stream) : launch_tree_few<TY, 2 * U, 4, kTail>(A, stream);
-    if (d <= 128 && dv <= 128)
-        return d == 128 ? launch_tree_few<TY, 4 * U, 8, kExact>(A, stream) : launch_tree_few<TY, 4 * U, 8, kTail>(A, stream);
-    return d == 256 ? launch_tree_few<TY, 8 * U, 16, kExact>(A, stream) : launch_tree_few<TY, 8 * U, 16, kTail>(A, stream);
+    if (d <= 64 && dv <= 64) return launch_tree_edge<TY, 2 * U, 4>(A, stream);
+    // In binary32 products are what counts: no more of them than there are (heads of 80 and 64, 5 rows
+    // in a window of 1000, 23 tokens: 26 us, by the instance for 128 38).
+    if constexpr (TY == S_F32) {
+        if (d <= 80 && dv <= 64) return launch_tree_edge<TY, 5, 4>(A, stream);
+    }
+    if (dv <= 128) {
+        if (d <= 96) return launch_tree_edge<TY, 3 * U, 8>(A, stream);
+        if (d <= 128) return launch_tree_edge<TY, 4 * U, 8>(A, stream);
+        if (d <= 192) return launch_tree_edge<TY, 6 * U, 8>(A, stream);
+    } else if (d <= 192 && (TY != S_F32 || dv <= 192)) {
+        return launch_tree_edge<TY, 6 * U, TY == S_F32 ? 12 : 16>(A, stream);
+    }
+    return launch_tree_edge<TY, 8 * U, 16>(A, stream);
 }
 
 }  // namespace

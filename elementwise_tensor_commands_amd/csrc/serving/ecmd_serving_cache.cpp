@@ -137,10 +137,13 @@ int plan_tree(const cmd_arg *args, int32_t window, TreePlan &P)
     A.by_group = Div31(A.group);
     A.by_runs = Div31(A.runs);
     A.by_vectors = Div31(A.hk * A.m);
-    // The join: a vector to a work-group while there are at most 2048, else as many as make 1024 work-groups.
+    // The join: a vector to a work-group where there are at most 2048 and a row may be in more
+    // than a dozen segments (8 heads, one row of 60000 positions 33 us, several 91; 4 rows of
+    // 8192, 16 segments each, 29 and 33; 5 rows, 8 each, 27.3 and 25.5); else as many as make 2048
+    // work-groups (32768 vectors, with the attention before it: 512 178 us, 1024 177, 2048 174, 4096 177).
     while (4u << A.join_shift < A.dv) ++A.join_shift;
     const uint32_t vectors = A.b * A.hk * A.m, places = 256 >> A.join_shift;
-    A.join_turn = vectors <= 2048 ? 1 : ceil_div(ceil_div(vectors, 1024), places) * places;
+    A.join_turn = vectors <= 2048 && A.runs > 12 * A.b ? 1 : ceil_div(ceil_div(vectors, 2048), places) * places;
     if (!A.direct) P.workspace = (int64_t)((((uint64_t)A.runs + b) * A.hk * A.m * (dv + 2)) * 4 + 16);
     return CMD_OK;
 }
@@ -525,7 +528,7 @@ int cmd_page_mass(const cmd_arg args[7], float scale, float decay, int32_t windo
     A.page = (uint32_t)std::max<int64_t>(1, page);
     // Columns of a work-group: of about 64 positions (64 rows of up to 8192, bf16: 256 take 102
     // us, 128 96, 64 93 and 32 104), and of 32 where that leaves less than two work-groups for
-    // each compute unit (3 rows of up to 1500, f32: 58 us at 256, 14.6 at 32).
+    // each compute unit (3 rows of up to 1500, f32: 58 us at 256, 14.6 at 32, 8.7 with d's own products).
     A.cols_group = std::max(1u, 64 / A.page);
     if ((uint64_t)b * ceil_div(cols, A.cols_group) < 512) A.cols_group = std::max(1u, 32 / A.page);
     A.groups = ceil_div(cols, A.cols_group);

@@ -530,17 +530,25 @@ int launch_score(const SelectArgs &A, void *stream)
     return launch_kernel(fn, dim3(A.b * A.hk * A.groups), dim3(256), 0, stream, A);
 }
 
+template <int TY, int NP>
+int launch_score_edge(const SelectArgs &A, void *stream)
+{
+    return A.d == (uint32_t)(NP * 8 * AttnType<TY>::E) ? launch_score<TY, NP, kExact>(A, stream) : launch_score<TY, NP, kTail>(A, stream);
+}
+
+// The instance: the smallest that holds d.
 template <int TY>
 int launch_select_type(const SelectArgs &A, void *stream)
 {
     constexpr int E = AttnType<TY>::E, U = 8 / E;
-    return A.d < (uint32_t)E ? launch_score<TY, U, kTiny>(A, stream)
-           : A.d == 64       ? launch_score<TY, U, kExact>(A, stream)
-           : A.d < 64        ? launch_score<TY, U, kTail>(A, stream)
-           : A.d == 128      ? launch_score<TY, 2 * U, kExact>(A, stream)
-           : A.d < 128       ? launch_score<TY, 2 * U, kTail>(A, stream)
-           : A.d == 256      ? launch_score<TY, 4 * U, kExact>(A, stream)
-                             : launch_score<TY, 4 * U, kTail>(A, stream);
+    if (A.d < (uint32_t)E) return launch_score<TY, 1, kTiny>(A, stream);
+    if (A.d <= 64) return launch_score_edge<TY, U>(A, stream);
+    if constexpr (TY == S_F32) {
+        if (A.d <= 96) return launch_score_edge<TY, 3>(A, stream);
+    }
+    return A.d <= 128   ? launch_score_edge<TY, 2 * U>(A, stream)
+           : A.d <= 192 ? launch_score_edge<TY, 3 * U>(A, stream)
+                        : launch_score_edge<TY, 4 * U>(A, stream);
 }
 
 // ---------------------------------------------------------------------------

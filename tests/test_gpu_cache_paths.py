@@ -92,6 +92,38 @@ def test_tree_attention_under_wide_tables(case, dtype):
     within(lse[same], want_lse[same], el[same], case)
 
 
+# Widths between those of test_gpu_cache_ops.py: an instance to each range of them.
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", [
+    (2, 6, 2, 1, 192, 192, 16, 9, 0), (1, 9, 3, 3, 150, 160, 8, 12, 20), (2, 5, 2, 2, 80, 48, 16, 8, 0), (1, 7, 4, 4, 72, 60, 7, 20, 0),
+    (2, 4, 4, 1, 88, 100, 16, 9, 0), (1, 11, 2, 1, 192, 64, 16, 10, 0), (1, 3, 2, 2, 137, 128, 16, 10, 9), (1, 6, 2, 1, 130, 200, 16, 7, 0),
+    (1, 5, 2, 2, 100, 193, 16, 7, 0), (2, 3, 3, 1, 80, 80, 16, 9, 0),
+])
+def test_tree_attention_of_other_widths(case, dtype):
+    q, (kg, vg), (kc, vc), pages, lens, parent, window = tree_state(case, dtype, sum(case))
+    want, want_lse, eo, el = C.tree(q, kc, vc, pages, lens, parent, 1.0 / math.sqrt(q.shape[3]), window)
+    out, lse = new(*want.shape, dtype=q.dtype), new(*want_lse.shape, dtype=torch.float32)
+    E.tree_attention(q.cuda(), kg, vg, pages.cuda(), lens.cuda(), parent.cuda(), out, lse=lse, window=window)
+    within(out, want, eo, case)
+    within(lse, want_lse, el, case)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_page_select_of_other_widths(dtype):
+    for d, hq in ((3, 1), (4, 4), (7, 2), (48, 2), (64, 3), (80, 4), (96, 2), (97, 6), (128, 1), (150, 4), (192, 8), (200, 2), (256, 3)):
+        g, rng = gen(d), random.Random(d)
+        bounds = torch.sort(randn(g, 60, 1, 2, d, dtype=DT[dtype]), dim=2).values
+        bounds[5], bounds[6, :, 1] = math.nan, math.inf
+        q = randn(g, 2, hq, d, dtype=DT[dtype])
+        q[0, 0, 0] = 0.0                                               # 0 times infinity
+        pages, lens = table(rng, 60, 2, 50), ints([200, 151])
+        want, want_lens = C.select(q, bounds, pages, lens, 4, 9, 1, 2)
+        out, out_lens = new(2, 1, 9), new(2, 1)
+        E.page_select(q.cuda(), bounds.cuda(), pages.cuda(), lens.cuda(), 4, out, out_lens)
+        assert torch.equal(out.cpu(), want) and torch.equal(out_lens.cpu(), want_lens), d
+
+
 # ---------------------------------------------------------------------------
 # Caches past 32-bit offsets: pages 2^31 elements apart, and a bit.
 
