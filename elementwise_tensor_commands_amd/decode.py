@@ -111,7 +111,9 @@ class PagedCache:
         """Of the tokens at positions old + i keep those of a path: they move to old, old +
         1, ..., rows end at lens, and the pages past that are free again."""
         slot_move(self.k + self.v, self.pages, old, path)
-        budget = (lens + (self.page - 1)) // self.page
+        import torch
+        # as many pages as they hold up to there (holes hold none): the last ones go
+        budget = ((self.pages >= 0) & (-self.order < (lens + (self.page - 1))[:, None] // self.page)).sum(1, dtype=torch.int32)
         page_evict(self.pages, self.lens, self.refs, self.order, budget, self.page, self.pages, self.refs, self.count,
                    first=0, last=0)
         self.lens.copy_(lens)

@@ -167,6 +167,23 @@ def test_decoding_within_a_budget_of_pages():
             assert int(m.cache.pages[r, 0]) >= 0 and int(m.cache.pages[r, n - 1]) >= 0
 
 
+def test_verify_of_rows_with_holes():
+    """Rows that lost pages to a budget give the slots of rejected tokens back too."""
+    m = Decoder(n=90, weigh=True, **KW)
+    m.prefill(PROMPTS)
+    g = torch.Generator().manual_seed(6)
+    own, ones = ints([0, 1, 2, 3, 4]), torch.ones(5, dtype=I32).cuda()
+    for i in range(9):
+        if i % 3 < 2:
+            m.decode(torch.randint(0, 61, (5,), generator=g).cuda(), own, ones, budget=ints([2, 2, 2, 2, 99]))
+        else:
+            before = m.cache.lens.tolist()
+            path, _ = m.verify(torch.randint(0, 61, (5, 11), generator=g).to(I32).cuda(), ints([[-1] + list(range(10))] * 5), ones)
+            assert m.cache.lens.tolist() == [x + int((p >= 0).sum()) for x, p in zip(before, path)]
+        refs_are_the_table_s(m.cache, 90)
+    assert any(x < 0 for x in m.cache.pages[1, :2].tolist() + m.cache.pages[1, 2:4].tolist())
+
+
 def test_captured_verify():
     """Checks replayed from a graph, with eager work between, against the same run eagerly."""
     models, states = [], []
