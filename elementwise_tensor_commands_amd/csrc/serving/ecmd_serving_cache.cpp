@@ -456,9 +456,8 @@ int plan_select(const cmd_arg *args, int32_t page, int32_t first, int32_t last, 
     A.by_page = Div31(A.page);
     A.by_hk = Div31(A.hk);
     const uint64_t rows = (uint64_t)b * hk;
-    // A turn of columns a work-group at least, and no more work-groups than fit at once and half
-    // as many again (64 rows of 8 heads and up to 512 columns: 512 take 95 us with the attention after
-    // it, 1024 92, 2048 89, 4096 93).
+    // A turn of columns to a work-group at least, and about 2048 work-groups (64 rows of 8 heads and
+    // up to 512 columns: 512 take 95 us with the attention after it, 1024 92, 2048 89, 4096 93).
     A.groups = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(ceil_div(cols, 32), ceil_div(2048, rows)));
     A.by_groups = Div31(A.groups);
     if (rows * A.groups > kMaxGroups) return refuse(CMD_E_LIMIT, "too many sequences times heads for one launch");
