@@ -127,11 +127,11 @@ int64_t cmd_paged_attention_heads_workspace(const cmd_arg args[7], int32_t windo
  * T = 1, or parent[r, i] = i - 1, is attention of the next tokens of a sequence.
  * Scores, weights, sums and softmax statistics are binary32, but with 16-bit types a
  * weight meets the values as the sum of two numbers of the type, which hold it to
- * within 2^-14 (bf16) or 2^-20 (f16) of itself, f16 to no better than 2^-34 of its
- * row's largest.  A token that attends to nothing gets out 0 and lse -inf.  What a
+ * within 1.01 x 2^-16 (bf16) or 2^-21 (f16) of itself, f16 to no better than 2^-34 of
+ * its row's largest.  A token that attends to nothing gets out 0 and lse -inf.  What a
  * token does not attend to is of no account to it (NaN included); an infinite value
  * that it does attend to makes its column infinite, where the weight is at least
- * 2^-30 of the row's largest. */
+ * 2^-90 of the row's largest. */
 int cmd_tree_attention(const cmd_arg args[8], float scale, int32_t window, void *workspace, int64_t workspace_bytes,
                        int32_t flags, void *hip_stream);
 int64_t cmd_tree_attention_workspace(const cmd_arg args[8], int32_t window);
