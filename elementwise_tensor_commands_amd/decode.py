@@ -226,7 +226,7 @@ class Decoder:
     def verify(self, tokens, parent, alive):
         """One step that checks a tree of drafted tokens in every row: tokens [rows, T]
         (int32), token 0 the row's newest, which ``decode`` would be given; token i > 0 a guess
-        of what follows token parent[r, i] < i (int32; -1 for token 0, others are padding).
+        of what follows token parent[r, i] < i (int32; -1 for token 0, any other number: padding).
         Rows keep the longest path of guesses that are what the model goes on with
         (greedily) and lose the others.  Rows where alive is 0 end.  Returns path [rows, T]
         (the tokens kept, ascending, then -1) and last [rows], the next newest.  (A
@@ -241,10 +241,7 @@ class Decoder:
         slot = old[:, None] + torch.arange(t, dtype=torch.int32, device=device)
         # rows that have ended, and tokens without a slot, are padding
         parent = torch.where((alive > 0)[:, None] & (slot < c.pages.shape[1] * c.page), parent, -2)
-        depth, up = (parent >= 0).to(torch.int32), parent.clamp(min=-1).long()
-        for _ in range(t.bit_length()):             # steps up the tree, doubling
-            depth = depth + torch.where(up >= 0, depth.gather(1, up.clamp(min=0)), 0)
-            up = torch.where(up >= 0, up.gather(1, up.clamp(min=0)), -1)
+        parent, depth = tree_depths(parent)
         pos, slot = (old[:, None] + depth).view(1, -1), slot.reshape(-1)
         row = torch.where(parent >= -1, every[:, None], -1).view(-1)
         x = self.embedding[tokens.view(-1).long()]
@@ -263,6 +260,21 @@ class Decoder:
         tree_accept(tokens, parent, follow, old, path, lens, last)
         c.keep(path, old, lens)
         return path, last
+
+
+def tree_depths(parent):
+    """Of trees given by parents [rows, T] (int32): the same with -2 for every token that is
+    padding, as ``tree_attention`` takes it (its parent is neither -1 nor a token before it, or
+    it is below such a one), and how many tokens of its tree are above each."""
+    import torch
+    t = parent.shape[1]
+    parent = torch.where((parent >= -1) & (parent < torch.arange(t, device=parent.device)), parent, -2)
+    depth, up = (parent >= 0).to(torch.int32), parent.long()
+    for _ in range(t.bit_length()):                 # steps up the tree, doubling
+        at = up.clamp(min=0)
+        depth = depth + torch.where(up >= 0, depth.gather(1, at), 0)
+        up = torch.where(up >= 0, up.gather(1, at), up)
+    return torch.where(up == -2, -2, parent), depth
 
 
 def next_beams(logits, alive, beams):

@@ -1,0 +1,60 @@
+"""The parts of decode.py that need no GPU."""
+import random
+
+import pytest
+import torch
+
+from elementwise_tensor_commands_amd.decode import tree_depths
+
+I32 = torch.int32
+
+
+def plain(parents):
+    """(parents, depths) by walking up from every token; depths of padding: None."""
+    out, depths = [], []
+    for i, p in enumerate(parents):
+        if p == -1 or (0 <= p < i and depths[p] is not None):
+            out.append(p)
+            depths.append(0 if p == -1 else depths[p] + 1)
+        else:
+            out.append(-2)
+            depths.append(None)
+    return out, depths
+
+
+def test_depths_of_a_tree_by_hand():
+    parent, depth = tree_depths(torch.tensor([[-1, 0, 0, 1, 3, 4, -2, 6, 6]], dtype=I32))
+    assert parent.tolist() == [[-1, 0, 0, 1, 3, 4, -2, -2, -2]] and parent.dtype == I32
+    assert depth[0, :6].tolist() == [0, 1, 1, 2, 3, 4] and depth.dtype == I32
+
+
+@pytest.mark.parametrize("bad", [0, 1, 4, 2 ** 31 - 1, -2, -3, -2 ** 31])
+def test_a_parent_that_is_no_token_before_it_is_padding(bad):
+    """Of token i: i + 0, i + 1, ..., past the tree, or negative; and what is below it."""
+    for i in range(5):
+        row = [-1, 0, 1, 0, 3]
+        row[i] = min(i + bad, 2 ** 31 - 1) if bad >= 0 else bad
+        want, depths = plain(row)
+        parent, depth = tree_depths(torch.tensor([[-1, 0, 1, 0, 3], row], dtype=I32))
+        assert parent.tolist() == [[-1, 0, 1, 0, 3], want]
+        assert [d for d, x in zip(depth[1].tolist(), depths) if x is not None] == [x for x in depths if x is not None]
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 8, 65, 256])
+def test_depths_of_any_trees(t):
+    rng = random.Random(t)
+    rows = [[i - 1 for i in range(t)]]                              # a chain
+    for _ in range(40):
+        rows.append([rng.choice([-1, i - 1, i - 1, i - 1, rng.randrange(max(1, i)), rng.choice([i, i + 3, t, 2 ** 31 - 1, -2, -7])])
+                     if i else -1 for i in range(t)])
+    parent, depth = tree_depths(torch.tensor(rows, dtype=I32))
+    for r, row in enumerate(rows):
+        want, depths = plain(row)
+        assert parent[r].tolist() == want
+        assert all(x is None or int(depth[r, i]) == x for i, x in enumerate(depths))
+
+
+def test_no_trees():
+    for shape in ((0, 5), (3, 0)):
+        parent, depth = tree_depths(torch.zeros(shape, dtype=I32))
+        assert parent.shape == depth.shape == shape
