@@ -228,8 +228,10 @@ class Decoder:
         (int32), token 0 the row's newest, which ``decode`` would be given; token i > 0 a guess
         of what follows token parent[r, i] < i (int32; -1 for token 0, any other number: padding).
         Rows keep the longest path of guesses that are what the model goes on with
-        (greedily) and lose the others.  Rows where alive is 0 end.  Returns path [rows, T]
-        (the tokens kept, ascending, then -1) and last [rows], the next newest.  (A
+        (greedily) and lose the others.  Rows where alive is 0 end.  A token without a slot, since
+        the table is full or no page was free, is padding: a row that has none for token 0 stays as it
+        is.  Returns path [rows, T] (the tokens kept, ascending, then -1: none of a row that stays
+        or has ended) and last [rows], the next newest (-1 of those).  (A
         decoder with ``select`` or ``weigh`` has bounds and weights of ``decode`` alone.)"""
         import torch
         c, device = self.cache, tokens.device
@@ -239,8 +241,10 @@ class Decoder:
         old = torch.where(alive > 0, c.lens, 0)
         c.step(torch.where(alive > 0, every, -1), alive * t)
         slot = old[:, None] + torch.arange(t, dtype=torch.int32, device=device)
-        # rows that have ended, and tokens without a slot, are padding
-        parent = torch.where((alive > 0)[:, None] & (slot < c.pages.shape[1] * c.page), parent, -2)
+        # rows that have ended, and tokens without a slot (the table is full, or no page was free), are padding
+        there = (alive > 0)[:, None] & (slot < c.pages.shape[1] * c.page)
+        there &= c.pages.gather(1, torch.where(there, slot // c.page, 0).long()) >= 0
+        parent = torch.where(there, parent, -2)
         parent, depth = tree_depths(parent)
         pos, slot = (old[:, None] + depth).view(1, -1), slot.reshape(-1)
         row = torch.where(parent >= -1, every[:, None], -1).view(-1)

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from elementwise_tensor_commands_amd.decode import Decoder
-from test_gpu_decode_cache import KW, PROMPTS, ints, refs_are_the_table_s
+from test_gpu_decode_cache import CLOSE, KW, PROMPTS, greedy, ints, refs_are_the_table_s
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,38 @@ def test_any_parent_that_is_no_token_before_it_is_padding():
     for r in range(5):
         for a, b in zip(held(models[0].cache, r), held(models[1].cache, r)):
             assert torch.equal(a, b)
+
+
+def test_verify_without_enough_free_pages():
+    """Tokens that no page was left for are not kept, nor what follows them; what is kept is what
+    decoding gives, and the rows go on from there when there are pages again."""
+    want, plain = greedy(24)
+    m = Decoder(n=9, **KW)                                          # two pages are free: row 0 gets both
+    m.prefill(PROMPTS)
+    t = 12
+    # a wrong guess in the first slot after the newest token's, then right ones: what is kept moves down
+    tokens = [[w[0], (w[1] + 1) % 61] + w[1:t - 1] for w in want]
+    path, last = m.verify(ints(tokens), ints([[-1, 0, 0] + list(range(2, t - 1))] * 5), torch.ones(5, dtype=I32).cuda())
+    # of the prompts of 5, 11, 1, 0 and 3 tokens: slots up to 16, 12, 4, 0 and 4
+    room = [11, 1, 3, 0, 1]
+    for r, n in enumerate(room):
+        kept = [0] + list(range(2, n)) if n else []
+        assert path[r].tolist() == kept + [-1] * (t - len(kept)), r
+        assert int(last[r]) == (want[r][len(kept)] if n else -1)
+        assert int(m.cache.lens[r]) == len(PROMPTS[r]) + len(kept)
+        for a, b in zip(held(m.cache, r), held(plain.cache, r)):
+            assert float((a - b[:len(a)]).abs().max()) <= CLOSE * float(b[:len(a)].abs().max())
+    refs_are_the_table_s(m.cache, 9)
+    # row 0 ends: its pages are the others' from the next step on
+    m.cache.step(ints([-1, 1, 2, 3, 4]), ints([0] * 5))
+    have = [len([x for x in p if x >= 0]) for p in path.tolist()]
+    alive = ints([0, 1, 1, 1, 1])
+    newest = [want[r][have[r]] for r in range(5)]
+    tokens = [[newest[r]] + want[r][have[r] + 1:have[r] + 4] for r in range(5)]
+    path, last = m.verify(ints(tokens), ints([[-1, 0, 1, 2]] * 5), alive)
+    assert (path >= 0).sum(1).tolist() == [0, 4, 4, 4, 4]
+    for r in range(1, 5):
+        assert int(last[r]) == want[r][have[r] + 4]
+        for a, b in zip(held(m.cache, r), held(plain.cache, r)):
+            assert float((a - b[:len(a)]).abs().max()) <= CLOSE * float(b[:len(a)].abs().max())
+    refs_are_the_table_s(m.cache, 9)
