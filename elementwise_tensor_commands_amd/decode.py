@@ -248,7 +248,7 @@ class Decoder:
         parent, depth = tree_depths(parent)
         pos, slot = (old[:, None] + depth).view(1, -1), slot.reshape(-1)
         row = torch.where(parent >= -1, every[:, None], -1).view(-1)
-        x = self.embedding[tokens.view(-1).long()]
+        x = self.embedding[torch.where(parent >= -1, tokens, 0).view(-1).long()]    # (padding's may be anything)
         for layer in range(len(self.o)):
             h = torch.matmul(x, self.qkv[layer]).view(rows * t, hq + 2 * hk, d)
             turned = h[None, :, :hq + hk]

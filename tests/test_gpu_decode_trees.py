@@ -41,6 +41,24 @@ def test_any_parent_that_is_no_token_before_it_is_padding():
             assert torch.equal(a, b)
 
 
+def test_padding_s_tokens_may_be_anything():
+    """Of padding, of what is below it and of rows that have ended: no row of the embedding is read for them."""
+    models = [Decoder(n=90, **KW) for _ in range(2)]
+    alive = ints([1, 0, 1, 1, 1])
+    parent = ints([[-1, 0, 5, 2, 1, -2]] * 5)
+    got = []
+    for m, odd in zip(models, (2 ** 31 - 1, 0)):
+        m.prefill(PROMPTS)
+        tokens = [[11 + r, 3, odd, odd, 9, -odd] for r in range(5)]
+        tokens[1] = [odd, -odd, odd, odd, odd, 61 if odd else 0]
+        got.append(m.verify(ints(tokens), parent, alive))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    for r in range(5):
+        for a, b in zip(held(models[0].cache, r), held(models[1].cache, r)):
+            assert torch.equal(a, b)
+
+
 def test_verify_without_enough_free_pages():
     """Tokens that no page was left for are not kept, nor what follows them; what is kept is what
     decoding gives, and the rows go on from there when there are pages again."""
