@@ -31,8 +31,9 @@ class PagedCache:
     what the last ``step`` (pages wanted, given) or ``compact`` (live, moved)
     counted, for a server that looks at it now and then.
 
-    select: the least and largest keys of every page are kept too, for ``attend_some``;
-    weigh: the weight that attention gave to every column of the tables, for ``evict``."""
+    select: the least and largest keys of every page are kept too (by ``bound``, after every
+    append), for ``attend_some``; weigh: the weight that attention gave to every column of the
+    tables, for ``evict``."""
 
     def __init__(self, layers, n, page, heads, d, rows, cols, dv=None, dtype=None, device="cuda", select=False, weigh=False):
         import torch
@@ -73,6 +74,12 @@ class PagedCache:
         """Turn q into q_out, and k and v into the slots of positions pos of rows row."""
         rope_append(q, k, v, pos, row, self.pages, freq, q_out, self.k[layer], self.v[layer], layout=layout)
 
+    def bound(self, layer, since):
+        """Keep up the bounds of pages with positions since [rows] .. lens - 1, which were
+        appended after the last call; nothing without ``select``."""
+        if self.bounds:
+            page_bounds(self.k[layer], self.pages, self.lens, since, self.bounds[layer])
+
     def attend(self, layer, q, out, pages=None, lens=None, window=0):
         """Attention of one query token a row over what the rows hold, or over other
         tables and lengths: a prompt's token t of row r has r's pages and length t + 1."""
@@ -81,10 +88,10 @@ class PagedCache:
 
     def attend_some(self, layer, q, out, since, take):
         """``attend`` over the ``take`` pages of each row and kv head that q may care for
-        most; since [rows]: the positions from there on were appended after the last such call."""
+        most; since [rows]: the positions from there on were appended after the last ``bound``."""
         import torch
         heads = self.k[layer].shape[2]
-        page_bounds(self.k[layer], self.pages, self.lens, since, self.bounds[layer])
+        self.bound(layer, since)
         pages = torch.empty(self.rows, heads, take, dtype=torch.int32, device=q.device)
         lens = torch.empty(self.rows, heads, dtype=torch.int32, device=q.device)
         page_select(q, self.bounds[layer], self.pages, self.lens, self.page, pages, lens, first=min(1, take - 1), last=1)
@@ -109,7 +116,8 @@ class PagedCache:
 
     def keep(self, path, old, lens):
         """Of the tokens at positions old + i keep those of a path: they move to old, old +
-        1, ..., rows end at lens, and the pages past that are free again."""
+        1, ..., rows end at lens, and the pages past that are free again.  (Rejected keys
+        never enter the bounds: these are kept up from here.)"""
         slot_move(self.k + self.v, self.pages, old, path)
         import torch
         # as many pages as they hold up to there (holes hold none): the last ones go
@@ -117,6 +125,8 @@ class PagedCache:
         page_evict(self.pages, self.lens, self.refs, self.order, budget, self.page, self.pages, self.refs, self.count,
                    first=0, last=0)
         self.lens.copy_(lens)
+        for layer in range(len(self.bounds)):
+            self.bound(layer, old)
 
     def compact(self):
         """Move the live pages to the lowest ids (then the end of the pools is free)."""
@@ -192,8 +202,8 @@ class Decoder:
         tokens = torch.tensor([t for p in prompts for t in p], dtype=torch.int64, device=device)
         # a token attends to its own row's pages up to itself
         logits = self.forward(tokens, pos, row, c.pages[row.long()], pos + 1)
-        for k, bounds in zip(c.k, c.bounds):
-            page_bounds(k, c.pages, c.lens, ints([0] * c.rows), bounds)
+        for layer in range(len(c.bounds)):
+            c.bound(layer, ints([0] * c.rows))
         ends, at = [], 0
         for n in count:
             at += n
@@ -213,11 +223,17 @@ class Decoder:
         pos = torch.where(parent >= 0, c.lens[parent.clamp(min=0).long()], 0)
         c.step(parent, alive)
         rows = torch.arange(c.rows, dtype=torch.int32, device=tokens.device)
-        attend = None
-        if take:
-            attend = lambda layer, q, out: c.attend_some(layer, q, out, pos, take)
-        elif budget is not None:
-            attend = lambda layer, q, out: c.attend_weighed(layer, q, out, 0.9 if layer == 0 else 1.0)
+
+        def attend(layer, q, out):
+            if take:
+                c.attend_some(layer, q, out, pos, take)
+                return
+            c.bound(layer, pos)
+            if budget is None:
+                c.attend(layer, q, out)
+            else:
+                c.attend_weighed(layer, q, out, 0.9 if layer == 0 else 1.0)
+
         logits = self.forward(tokens, pos, torch.where(c.lens > pos, rows, -1), attend=attend)
         if budget is not None:
             c.evict(budget)
@@ -231,8 +247,8 @@ class Decoder:
         (greedily) and lose the others.  Rows where alive is 0 end.  A token without a slot, since
         the table is full or no page was free, is padding: a row that has none for token 0 stays as it
         is.  Returns path [rows, T] (the tokens kept, ascending, then -1: none of a row that stays
-        or has ended) and last [rows], the next newest (-1 of those).  (A
-        decoder with ``select`` or ``weigh`` has bounds and weights of ``decode`` alone.)"""
+        or has ended) and last [rows], the next newest (-1 of those).  (The
+        weights of a decoder with ``weigh`` are those of ``decode`` with a budget alone.)"""
         import torch
         c, device = self.cache, tokens.device
         rows, t = tokens.shape
