@@ -216,9 +216,16 @@ class Decoder:
         (int64); rows where alive [rows] (int32) is 0 end.  A row whose table is full
         keeps what it has: its token sees that, and is not written.  take: how many pages of
         each kv head are read (0: all; of a decoder with ``select``).  budget [rows]
-        (int32; of one with ``weigh``): how many pages a row keeps after it.  Returns the logits."""
+        (int32; of one with ``weigh``, and not with take): how many pages a row keeps after it.
+        Returns the logits."""
         import torch
         c = self.cache
+        if take and budget is not None:
+            raise ValueError("take and budget: pages that a step does not read get no weight to keep them by")
+        if take and not c.bounds:
+            raise ValueError("take is of a decoder with select")
+        if budget is not None and c.mass is None:
+            raise ValueError("budget is of a decoder with weigh")
         parent = torch.where((alive > 0) & (parent < c.rows), parent, -1)
         pos = torch.where(parent >= 0, c.lens[parent.clamp(min=0).long()], 0)
         c.step(parent, alive)
