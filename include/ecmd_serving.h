@@ -176,9 +176,10 @@ int cmd_page_bounds(const cmd_arg args[5], int32_t flags, void *hip_stream);
  * Candidates are the columns j < U = ceil(min(lens[r], P * page) / page) that are no
  * holes, in all if they are at most C.  Else those among the first `first` and the last
  * `last` of the U columns (first + last <= C), then the others by descending
- *      score[h, j] = max over kv head h's query heads of sum_e max(q_e least_e, q_e largest_e)
+ *      score[h, j] = max over kv head h's query heads of sum_e q_e (q_e < 0 ? least_e : largest_e)
  * (what no key of the page can pass; sums of binary64, NaN the least) until they
- * are C; the lower column wins a tie.  pages_out[r, h] names them by ascending column, then
+ * are C; the lower column wins a tie.  Bounds of NaN alone (least +inf, largest -inf)
+ * make a score -inf or NaN, and so does 0 times an infinity: such pages come last.  pages_out[r, h] names them by ascending column, then
  * -1; lens_out is how many positions they hold: a table for cmd_paged_attention_heads.
  * P <= 2^20. */
 int cmd_page_select(const cmd_arg args[6], int32_t page, int32_t first, int32_t last, void *workspace,
