@@ -251,7 +251,7 @@ class Decoder:
         (int32), token 0 the row's newest, which ``decode`` would be given; token i > 0 a guess
         of what follows token parent[r, i] < i (int32; -1 for token 0, any other number: padding).
         Rows keep the longest path of guesses that are what the model goes on with
-        (greedily) and lose the others.  Rows where alive is 0 end.  A token without a slot, since
+        (greedily) and lose the others; guesses may begin alike.  Rows where alive is 0 end.  A token without a slot, since
         the table is full or no page was free, is padding: a row that has none for token 0 stays as it
         is.  Returns path [rows, T] (the tokens kept, ascending, then -1: none of a row that stays
         or has ended) and last [rows], the next newest (-1 of those).  (The
@@ -269,6 +269,7 @@ class Decoder:
         there &= c.pages.gather(1, torch.where(there, slot // c.page, 0).long()) >= 0
         parent = torch.where(there, parent, -2)
         parent, depth = tree_depths(parent)
+        parent = merge_alike(tokens, parent)
         pos, slot = (old[:, None] + depth).view(1, -1), slot.reshape(-1)
         row = torch.where(parent >= -1, every[:, None], -1).view(-1)
         x = self.embedding[torch.where(parent >= -1, tokens, 0).view(-1).long()]    # (padding's may be anything)
@@ -302,6 +303,25 @@ def tree_depths(parent):
         depth = depth + torch.where(up >= 0, depth.gather(1, at), 0)
         up = torch.where(up >= 0, up.gather(1, at), up)
     return torch.where(up == -2, -2, parent), depth
+
+
+def merge_alike(tokens, parent):
+    """Parents [rows, T] (of ``tree_depths``) with tokens merged whose paths from the root on are
+    alike: what is below such a token follows the first of them, and the others are padding.
+    Then a token's followers differ, and only one of them can be right."""
+    import torch
+    t = parent.shape[1]
+    up, real = parent.long(), parent > -2
+    # alike[r, i, j]: the last 1, 2, 4, ... tokens of the paths to i and j are the same, or all of both
+    alike = (tokens[:, :, None] == tokens[:, None]) & real[:, :, None] & real[:, None]
+    for _ in range(t.bit_length()):
+        at, more = up.clamp(min=0), up >= 0
+        above = alike.gather(1, at[:, :, None].expand(-1, -1, t)).gather(2, at[:, None].expand(-1, t, -1))
+        alike = alike & torch.where(more[:, :, None] & more[:, None], above, more[:, :, None] == more[:, None])
+        up = torch.where(more, up.gather(1, at), up)
+    first = (torch.arange(t, 0, -1, dtype=torch.int32, device=parent.device) * alike).argmax(2) if t else parent.long()
+    merged = torch.where(parent >= 0, first.gather(1, parent.clamp(min=0).long()), parent).to(parent.dtype)
+    return torch.where(real & (first != torch.arange(t, device=parent.device)), -2, merged)
 
 
 def next_beams(logits, alive, beams):

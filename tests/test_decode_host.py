@@ -4,7 +4,7 @@ import random
 import pytest
 import torch
 
-from elementwise_tensor_commands_amd.decode import Decoder, tree_depths
+from elementwise_tensor_commands_amd.decode import Decoder, merge_alike, tree_depths
 
 I32 = torch.int32
 
@@ -54,10 +54,39 @@ def test_depths_of_any_trees(t):
         assert all(x is None or int(depth[r, i]) == x for i, x in enumerate(depths))
 
 
+def test_guesses_that_begin_alike_are_merged_by_hand():
+    # 0 -> 1 -> 2 and 0 -> 3 -> 4, tokens 1 and 3 the same: 4 follows 1
+    tokens = torch.tensor([[9, 5, 6, 5, 7], [9, 5, 6, 5, 6], [9, 5, 6, 4, 6]], dtype=I32)
+    parent = torch.tensor([[-1, 0, 1, 0, 3]] * 3, dtype=I32)
+    got = merge_alike(tokens, parent)
+    assert got.tolist() == [[-1, 0, 1, -2, 1], [-1, 0, 1, -2, -2], [-1, 0, 1, 0, 3]] and got.dtype == I32
+
+
+@pytest.mark.parametrize("t", [1, 2, 5, 17, 64, 200])
+def test_merged_guesses(t):
+    """Against the paths themselves: each once, by the first token that ends it, its parent the path one shorter."""
+    rng = random.Random(t)
+    for words in (1, 2, 5):
+        rows = [[i - 1 for i in range(t)]] + [[rng.choice([i - 1, rng.randrange(max(1, i)), rng.randrange(max(1, i)), -1, -2 if rng.random() < 0.3 else 0])
+                                               if i else -1 for i in range(t)] for _ in range(15)]
+        parent, _ = tree_depths(torch.tensor(rows, dtype=I32))
+        tokens = torch.tensor([[rng.randrange(words) for _ in range(t)] for _ in rows], dtype=I32)
+        got = merge_alike(tokens, parent)
+        for r in range(len(rows)):
+            paths, ends = [], {}
+            for i, p in enumerate(parent[r].tolist()):
+                path = None if p == -2 else ((paths[p] if p >= 0 else ()) + (int(tokens[r, i]),))
+                paths.append(path)
+                first = ends.setdefault(path, i)
+                want = -2 if path is None or first != i else ends[path[:-1]] if p >= 0 else -1
+                assert int(got[r, i]) == want, (r, i)
+
+
 def test_no_trees():
     for shape in ((0, 5), (3, 0)):
         parent, depth = tree_depths(torch.zeros(shape, dtype=I32))
         assert parent.shape == depth.shape == shape
+        assert merge_alike(torch.zeros(shape, dtype=I32), parent).shape == shape
 
 
 def test_refused_kinds_of_steps():

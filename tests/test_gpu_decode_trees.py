@@ -92,3 +92,32 @@ def test_verify_without_enough_free_pages():
         for a, b in zip(held(m.cache, r), held(plain.cache, r)):
             assert float((a - b[:len(a)]).abs().max()) <= CLOSE * float(b[:len(a)].abs().max())
     refs_are_the_table_s(m.cache, 9)
+
+
+def test_guesses_that_begin_alike():
+    """Chains drawn apart, the first tokens of which are the same: the longest right one is kept,
+    wherever it stands, and the rows go on as without guesses."""
+    want, plain = greedy(24)
+    m = Decoder(n=90, **KW)
+    m.prefill(PROMPTS)
+    have = [1] * 5
+    for turn, far in enumerate([(1, 3, 2), (4, 0, 4), (0, 1, 4), (2, 2, 2)]):        # how long each of three chains is right
+        tokens, parent = [], []
+        for r in range(5):
+            row, up = [want[r][have[r] - 1]], [-1]
+            for x in far:
+                for i in range(4):
+                    right = want[r][have[r] + i]
+                    row.append(right if i < x else (right + 1 + i) % 61)
+                    up.append(0 if i == 0 else len(row) - 2)
+            tokens.append(row)
+            parent.append(up)
+        path, last = m.verify(ints(tokens), ints(parent), torch.ones(5, dtype=I32).cuda())
+        for r in range(5):
+            kept = [x for x in path[r].tolist() if x >= 0]
+            assert len(kept) == 1 + max(far), (turn, r)
+            assert [tokens[r][x] for x in kept] + [int(last[r])] == want[r][have[r] - 1:have[r] + len(kept)]
+            have[r] += len(kept)
+            for a, b in zip(held(m.cache, r), held(plain.cache, r)):
+                assert float((a - b[:len(a)]).abs().max()) <= CLOSE * float(b[:len(a)].abs().max())
+        refs_are_the_table_s(m.cache, 90)
