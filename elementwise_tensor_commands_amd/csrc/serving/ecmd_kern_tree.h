@@ -1212,12 +1212,21 @@ int launch_tree_type(const TreeArgs &A, void *stream)
         }
     }
     if (d < (uint32_t)E || dv < (uint32_t)E) return launch_tree_few<TY, 8 * U, 16, kTiny>(A, stream);
-    if (d <= 64 && dv <= 64) return launch_tree_edge<TY, 2 * U, 4>(A, stream);
-    // In binary32 products are what counts: no more of them than there are (heads of 80 and 64, 5 rows
-    // in a window of 1000, 23 tokens: 26 us, by the instance for 128 38).
+    // In binary32 products are what counts, so no more of them than there are: of keys in steps of 16
+    // elements up to 96 (a piece of each of the four lanes), of values in steps of 64 (a piece of each
+    // of the sixteen).  12 heads, 23 tokens, 5 rows in a window of 1000, by these and by the next
+    // larger one that both types share: 80 and 64 25 and 38 us, 80 and 80 30 and 33, 96 and 64 25 and 31,
+    // 128 and 64 27 and 33, 64 and 128 29 and 33; 8 whole rows of up to 3000, 16 tokens of 16 heads over
+    // 4: 80 and 80 44 and 48, 96 and 64 40 and 47, 64 and 128 50 and 55.
     if constexpr (TY == S_F32) {
-        if (d <= 80 && dv <= 64) return launch_tree_edge<TY, 5, 4>(A, stream);
+        if (dv <= 64 && d <= 128)
+            return d <= 64   ? launch_tree_edge<TY, 4, 4>(A, stream)
+                   : d <= 80 ? launch_tree_edge<TY, 5, 4>(A, stream)
+                   : d <= 96 ? launch_tree_edge<TY, 6, 4>(A, stream)
+                             : launch_tree_edge<TY, 8, 4>(A, stream);
+        if (dv <= 128 && d <= 80) return d <= 64 ? launch_tree_edge<TY, 4, 8>(A, stream) : launch_tree_edge<TY, 5, 8>(A, stream);
     }
+    if (d <= 64 && dv <= 64) return launch_tree_edge<TY, 2 * U, 4>(A, stream);
     if (dv <= 128) {
         if (d <= 96) return launch_tree_edge<TY, 3 * U, 8>(A, stream);
         if (d <= 128) return launch_tree_edge<TY, 4 * U, 8>(A, stream);
