@@ -1,5 +1,7 @@
-"""Attention for trees of heads of every width's instance."""
+"""Attention for trees of more rows than one wave deals out, of more than the dealing holds, and of
+heads of every width's instance."""
 import math
+import random
 
 import pytest
 import torch
@@ -7,7 +9,7 @@ import torch
 import cache_oracle as C
 import elementwise_tensor_commands_amd as E
 from test_gpu_cache_ops import tree_state
-from test_gpu_serving import DT, within
+from test_gpu_serving import DT, ints, within
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,36 @@ def check(case, dtype, seed, lens=None):
 ])
 def test_heads_of_other_widths(case):
     check(case, "f32", sum(case))
+
+
+def spread(rng, b, cols, page, t):
+    """Mostly short rows, some empty, some of no length, a few long, a few past the table."""
+    held = cols * page
+    return ints([rng.choice([0, -1, rng.randint(0, 40), rng.randint(0, 40), rng.randint(0, held)] + [held - t, held, held + 3] * (r % 16 == 3))
+                 for r in range(b)])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", [
+    # past 64 rows the work-group deals them together; past 256 in several turns
+    (65, 3, 4, 2, 32, 32, 16, 60, 0), (100, 3, 2, 1, 64, 64, 16, 60, 50), (130, 5, 1, 1, 40, 24, 16, 60, 0), (300, 2, 2, 1, 16, 16, 16, 60, 0),
+    (100, 20, 1, 1, 64, 64, 16, 60, 0), (70, 18, 4, 2, 64, 32, 16, 60, 100), (257, 20, 1, 1, 16, 16, 8, 110, 0),
+    (90, 3, 2, 1, 64, 64, 16, 60, 300), (80, 18, 4, 2, 64, 32, 16, 60, 310),
+    # as many as are dealt, and more: each row a work-group's
+    (1024, 1, 2, 1, 16, 8, 16, 60, 0), (1025, 1, 2, 1, 16, 8, 16, 60, 0), (1030, 17, 1, 1, 8, 8, 16, 52, 20),
+])
+def test_many_rows(case, dtype):
+    b, t, hq, hk, d, dv, page, cols, window = case
+    size = check(case, dtype, 6 * sum(case), spread(random.Random(sum(case)), b, cols, page, t))
+    if window == 0:                                                 # (a short window goes without dealing)
+        assert (size > 0) == (b <= 1024)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("case", [(65, 2, 2, 1, 16, 16, 16, 60, 0), (140, 2, 1, 1, 16, 16, 16, 60, 0), (300, 1, 1, 1, 16, 16, 16, 60, 0),
+                                  (140, 20, 1, 1, 16, 16, 16, 60, 0)])
+def test_many_rows_of_nearly_one_length(case, dtype):
+    """Runs that are whole rows."""
+    b, t, page, cols = case[0], case[1], case[6], case[7]
+    rng = random.Random(b)
+    check(case, dtype, 6 * sum(case), ints([cols * page - t - rng.randint(0, 60) for _ in range(b)]))
