@@ -42,6 +42,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
+
 #include "../ecmd_launch.h"
 #include "ecmd_attn_tile.h"
 
@@ -847,7 +849,8 @@ constexpr uint32_t kStageKeys = 32, kStageTable = kAttnBlock;   // positions of 
 // 16 bytes from each lane's p to LDS, from address lds on, in the order of the lanes.  Written
 // out, for the compiler would let every later read of LDS wait for it: it does not
 // know that the buffers are read in turn.  wait_loads waits.  (No register is written but m0,
-// which holds the address, 16 bits of it, and which nothing else here uses.)
+// which holds the address, 16 bits of it.  The compiler keeps m0 for itself and cannot be told
+// so; it uses it for nothing in these kernels, which their assembly is tested for.)
 __device__ inline void load_to_lds(const char *p, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
@@ -926,17 +929,25 @@ __global__ __launch_bounds__(kAttnBlock, (NK * 64 + VW * 32 >= 640 ? 1 : 2)) voi
     // A wave's; where they do not come out even, the last one more than once.
     constexpr int KU = (2 * NK + kAttnWaves - 1) / kAttnWaves, VU = (VW + kAttnWaves - 1) / kAttnWaves, PER = KU + VU;
 
-    // Tiles' buffers: their places count 16 bits in a load to LDS, so they come first (by
-    // their alignment) and end within 64 KiB.
+    // Tiles' buffers: their places count 16 bits in a load to LDS, so they come first, in the one
+    // object that there is (what a launch adds lies behind it), and end within 64 KiB.
     constexpr uint32_t kRing = kLoads * 3 <= 64 ? 3 : 2, kAhead = kRing - 1;
-    static_assert(kLoads * kRing <= 64);
-    __shared__ __attribute__((aligned(1024))) char s_ring[kRing][kLoads * 1024];
-    __shared__ uint64_t s_k[2][kStageTable], s_v[2][kStageTable];     // where a position's key and value lie
-    __shared__ uint32_t s_valid[2][kStageTable / kStageKeys];
-    __shared__ uint32_t s_mask[kMaxTree * kTreeWords], s_real[kTreeWords];
-    __shared__ int32_t s_info[kMaxTree];
+    struct Stage {
+        char ring[kRing][kLoads * 1024];
+        uint64_t k[2][kStageTable], v[2][kStageTable];     // where a position's key and value lie
+        uint32_t valid[2][kStageTable / kStageKeys];
+        uint32_t mask[kMaxTree * kTreeWords], real[kTreeWords];
+        int32_t info[kMaxTree];
+        uint32_t scratch[kAttnWaves];
+    };
+    static_assert(offsetof(Stage, ring) == 0 && sizeof(Stage::ring) <= 64 << 10);
+    __shared__ __attribute__((aligned(1024))) Stage sh;
+    auto &s_ring = sh.ring;
+    auto &s_k = sh.k, &s_v = sh.v;
+    auto &s_valid = sh.valid;
+    uint32_t *const s_mask = sh.mask, *const s_real = sh.real, *const s_scratch = sh.scratch;
+    int32_t *const s_info = sh.info;
     extern __shared__ uint32_t s_rows[];   // unless A.direct
-    __shared__ uint32_t s_scratch[kAttnWaves];
 
     const uint32_t tid = threadIdx.x, lane = tid & 63, j = lane >> 4, hh = lane & 15;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
