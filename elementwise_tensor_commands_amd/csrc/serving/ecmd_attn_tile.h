@@ -106,6 +106,22 @@ enum AttnEdge {
     kTiny,    // element by element: rows shorter than a piece
 };
 
+// Clears what an earlier piece has of the piece from element `at` on of a row of d elements,
+// which was moved back to end with the row.
+template <int E>
+__device__ inline u32x4 only_own(u32x4 x, int at, int d)
+{
+    const int twice = at - min(at, d - E);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if constexpr (E == 8)
+            x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
+        else
+            x[w] &= w >= twice ? ~0u : 0u;
+    }
+    return x;
+}
+
 // Positions of row r that a launch looks at: [lo, hi).
 struct Span {
     uint32_t lo, hi;

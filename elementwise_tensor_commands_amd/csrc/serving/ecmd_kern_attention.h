@@ -222,16 +222,8 @@ __global__ __launch_bounds__(kAttnBlock, (attn_waves<TY, NK, VW, EDGE, APART>())
         return load16<stream>(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
     };
     auto masked = [&](u32x4 x, int c, uint32_t now) {
-        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {   // the same for the whole launch
-            const int at = (c * 4 + (int)fresh(j, now)) * E, twice = at - min(at, (int)A.d - E);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if constexpr (E == 8)
-                    x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
-                else
-                    x[w] &= w >= twice ? ~0u : 0u;
-            }
-        }
+        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d)   // the same for the whole launch
+            x = only_own<E>(x, (c * 4 + (int)fresh(j, now)) * E, (int)A.d);
         return x;
     };
 

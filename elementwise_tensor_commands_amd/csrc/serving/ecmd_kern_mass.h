@@ -58,16 +58,7 @@ __global__ __launch_bounds__(256) void k_mass(const MassArgs A)
         return load16(p + (EDGE == kTail ? min(at, (int)A.d - E) : at) * sizeof(T));
     };
     auto masked = [&](u32x4 x, int c) {
-        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) {
-            const int at = (c * 4 + (int)j) * E, twice = at - min(at, (int)A.d - E);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if constexpr (E == 8)
-                    x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
-                else
-                    x[w] &= w >= twice ? ~0u : 0u;
-            }
-        }
+        if (EDGE == kTail && (uint32_t)(c + 1) * 4 * E > A.d) x = only_own<E>(x, (c * 4 + (int)j) * E, (int)A.d);
         return x;
     };
     auto kv_head = [&](uint32_t item) { return parts == 1 ? item : item / parts; };

@@ -604,22 +604,6 @@ __device__ inline void put_tile(const TreeArgs &A, const TreeOut &O, uint32_t q0
     }
 }
 
-// Clears what an earlier piece has of piece c of a row of d elements, which was moved back
-// to end with the row.
-template <int E>
-__device__ inline u32x4 only_own(u32x4 x, int at, int d)
-{
-    const int twice = at - min(at, d - E);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if constexpr (E == 8)
-            x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
-        else
-            x[w] &= w >= twice ? ~0u : 0u;
-    }
-    return x;
-}
-
 // ---------------------------------------------------------------------------
 // Few queries, or binary32.
 

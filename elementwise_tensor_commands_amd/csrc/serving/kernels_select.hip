@@ -369,16 +369,7 @@ __global__ __launch_bounds__(256) void k_select_score(const SelectArgs A)
         }
     };
     auto masked = [&](u32x4 x, int i) {
-        if (EDGE == kTail && (uint32_t)(i + 1) * 8 * E > A.d) {
-            const int at = (i * 8 + (int)sub) * E, twice = at - min(at, (int)A.d - E);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if constexpr (E == 8)
-                    x[w] &= (2 * w >= twice ? 0xFFFFu : 0u) | (2 * w + 1 >= twice ? 0xFFFF0000u : 0u);
-                else
-                    x[w] &= w >= twice ? ~0u : 0u;
-            }
-        }
+        if (EDGE == kTail && (uint32_t)(i + 1) * 8 * E > A.d) x = only_own<E>(x, (i * 8 + (int)sub) * E, (int)A.d);
         return x;
     };
     struct Page {
