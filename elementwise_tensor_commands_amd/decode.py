@@ -58,14 +58,16 @@ class PagedCache:
         self.order = -torch.arange(cols, dtype=torch.float32, device=device).repeat(rows, 1)
 
     def step(self, parent, add):
-        """Every row takes over row parent[r]'s sequence (-1: starts empty) and
-        grows by add[r] positions, whose slots the coming ``append`` fills."""
+        """Every row takes over row parent[r]'s sequence (-1, or what is no row: starts empty)
+        and grows by add[r] positions, whose slots the coming ``append`` fills."""
+        import torch
         src, dst = self.src[:self.rows], self.dst[:self.rows]
         page_assign(self.pages, self.lens, self.refs, parent, add, self.page, self._pages, self._lens, self.refs, src,
                     dst, self.stats)
         page_copy(self.k + self.v + self.bounds, src, dst)
         if self.mass is not None:
-            self.mass.copy_(self.mass[parent.clamp(min=0).long()] * ((parent >= 0) & (parent < self.rows))[:, None])
+            from_row = (parent >= 0) & (parent < self.rows)
+            self.mass.copy_(torch.where(from_row[:, None], self.mass[torch.where(from_row, parent, 0).long()], 0.0))
         # copied back rather than swapped: a captured step finds them in their places
         self.pages.copy_(self._pages)
         self.lens.copy_(self._lens)

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import cache_oracle as C
-from elementwise_tensor_commands_amd.decode import Decoder
+from elementwise_tensor_commands_amd.decode import Decoder, PagedCache
 from test_gpu_decode_cache import CLOSE, KW, PROMPTS, ints, refs_are_the_table_s
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,18 @@ def test_pages_are_chosen_by_the_keys_they_hold():
                 kk, vv = (torch.stack([z[p, s, h] for p, s in at]).double() for z in (k, v))
                 want = torch.softmax(q[r, 2 * h:2 * h + 2].cpu().double() @ kk.t() / math.sqrt(32), -1) @ vv
                 assert float((out[r, 2 * h:2 * h + 2].cpu() - want).abs().max()) <= CLOSE * float(vv.abs().max()), (layer, r, h)
+
+
+def test_weights_follow_their_rows():
+    """A step's rows take their parents' weights; rows whose parent is none start with none, whatever was there."""
+    c = PagedCache(1, 20, 4, 2, 8, 5, 6, weigh=True)
+    c.step(ints([-1] * 5), ints([5, 1, 9, 0, 3]))
+    c.mass.copy_(torch.arange(30.0).view(5, 6))
+    c.mass[4, 2], c.mass[3, 0] = math.inf, math.nan
+    was = c.mass.clone()
+    c.step(ints([2, -1, 2 ** 31 - 1, 5, 1]), ints([1, 0, 2, 0, -1]))
+    assert torch.equal(c.mass, torch.stack([was[2], was[0] * 0, was[0] * 0, was[0] * 0, was[1]]))
+    assert c.lens.tolist() == [10, 0, 2, 0, 1]
+    refs_are_the_table_s(c, 20)
+    c.step(ints([0, 4, -2 ** 31, -7, 4]), ints([0] * 5))
+    assert torch.equal(c.mass, torch.stack([was[2], was[1], was[0] * 0, was[0] * 0, was[1]]))
