@@ -224,6 +224,8 @@ class Decoder:
         c = self.cache
         if take and budget is not None:
             raise ValueError("take and budget: pages that a step does not read get no weight to keep them by")
+        if take < 0:
+            raise ValueError("take is a number of pages, or 0")
         if take and not c.bounds:
             raise ValueError("take is of a decoder with select")
         if budget is not None and c.mass is None:
@@ -250,17 +252,21 @@ class Decoder:
 
     def verify(self, tokens, parent, alive):
         """One step that checks a tree of drafted tokens in every row: tokens [rows, T]
-        (int32), token 0 the row's newest, which ``decode`` would be given; token i > 0 a guess
-        of what follows token parent[r, i] < i (int32; -1 for token 0, any other number: padding).
-        Rows keep the longest path of guesses that are what the model goes on with
-        (greedily) and lose the others; guesses may begin alike.  Rows where alive is 0 end.  A token without a slot, since
-        the table is full or no page was free, is padding: a row that has none for token 0 stays as it
-        is.  Returns path [rows, T] (the tokens kept, ascending, then -1: none of a row that stays
-        or has ended) and last [rows], the next newest (-1 of those).  (The
-        weights of a decoder with ``weigh`` are those of ``decode`` with a budget alone.)"""
+        (int32, T <= 256), token 0 the row's newest, which ``decode`` would be given; token
+        i > 0 a guess of what follows token parent[r, i] < i (int32; -1 for token 0, any other
+        number: padding).  Rows keep the longest path of guesses that are what the model goes
+        on with (greedily) and lose the others; guesses may begin alike.  Rows where alive is 0
+        end.  A token without a slot, since the table is full or no page was free, is padding:
+        a row that has none for token 0 stays as it is.  Returns path [rows, T] (the tokens
+        kept, ascending, then -1: none of a row that stays or has ended) and last [rows], the
+        next newest (-1 of those).  (The weights of a decoder with ``weigh`` are those of
+        ``decode`` with a budget alone.)"""
         import torch
         c, device = self.cache, tokens.device
         rows, t = tokens.shape
+        if t > 256 or rows != c.rows:
+            raise ValueError("trees of up to 256 tokens in each of %d rows, got %s" % (c.rows, tuple(tokens.shape)))
+        parent = parent.expand(rows, t)
         hq, hk, d = self.hq, self.hk, self.d
         every = torch.arange(rows, dtype=torch.int32, device=device)
         old = torch.where(alive > 0, c.lens, 0)

@@ -101,3 +101,14 @@ def test_refused_kinds_of_steps():
                     with pytest.raises(ValueError):
                         m.decode(*args, **how)
             assert m.cache.lens.tolist() == [0, 0, 0]
+        with pytest.raises(ValueError):
+            m.decode(*args, take=-1)
+
+
+def test_refused_trees():
+    """Before the tables change: trees that the operators refuse."""
+    m = Decoder(rows=3, n=8, cols=4, device="cpu")
+    for shape, like in (((3, 257), None), ((2, 4), None), ((4, 4), None), ((3, 4), (3, 5)), ((3, 4), (2, 4))):
+        with pytest.raises((ValueError, RuntimeError)):
+            m.verify(torch.zeros(shape, dtype=I32), torch.zeros(like or shape, dtype=I32) - 1, torch.ones(3, dtype=I32))
+    assert m.cache.lens.tolist() == [0, 0, 0] and bool((m.cache.pages == -1).all())

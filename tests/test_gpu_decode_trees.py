@@ -121,3 +121,20 @@ def test_guesses_that_begin_alike():
             for a, b in zip(held(m.cache, r), held(plain.cache, r)):
                 assert float((a - b[:len(a)]).abs().max()) <= CLOSE * float(b[:len(a)].abs().max())
         refs_are_the_table_s(m.cache, 90)
+
+
+def test_one_tree_for_all_rows_and_none():
+    """A parent for every row or one for all; trees of no tokens change nothing but the rows that end."""
+    models = [Decoder(n=90, **KW) for _ in range(2)]
+    tokens, alive = ints([[11 + r, 3, 5, 7] for r in range(5)]), ints([1, 1, 1, 0, 1])
+    got = []
+    for m, parent in zip(models, ([[-1, 0, 0, 2]] * 5, [[-1, 0, 0, 2]])):
+        m.prefill(PROMPTS)
+        got.append(m.verify(tokens, ints(parent), alive))
+        refs_are_the_table_s(m.cache, 90)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    c, before = models[0].cache, models[0].cache.lens.clone()
+    path, last = models[0].verify(tokens[:, :0], ints([[]] * 5), ints([1, 1, 0, 1, 1]))
+    before[2] = 0
+    assert path.shape == (5, 0) and last.tolist() == [-1] * 5 and torch.equal(c.lens, before)
+    refs_are_the_table_s(c, 90)
