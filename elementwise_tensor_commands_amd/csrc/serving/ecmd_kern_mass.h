@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256) void k_mass(const MassArgs A)
 #pragma unroll
                 for (int c = 0; c < NK; ++c) q[c] = masked(qn[c], c);
                 const bool on = lse_n != -INFINITY;
-                const float less = lse_n * 1.44269504088896340736f;
+                const float lse = lse_n;
                 load_q(item + item_step < items ? item + item_step : item0);   // (or of the next turn)
                 for (uint32_t t = tile0; t < tiles; t += hw) {
                     f32x4 s[KB];
@@ -143,7 +143,10 @@ __global__ __launch_bounds__(256) void k_mass(const MassArgs A)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const bool ok = on && valid >> (kb * 16 + j * 4 + i) & 1;
-                            w[i] = row_sum(ok ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], A.scale_log2, -less)) : 0.0f);
+                            // the difference first, then base 2: it is small where a weight counts,
+                            // scores and log-sums need not be
+                            const float below = __builtin_fmaf(s[kb][i], A.scale, -lse);
+                            w[i] = row_sum(ok ? __builtin_amdgcn_exp2f(below * 1.44269504088896340736f) : 0.0f);
                         }
                         if (hh < 4) {
                             const float v = hh == 0 ? w[0] : hh == 1 ? w[1] : hh == 2 ? w[2] : w[3];

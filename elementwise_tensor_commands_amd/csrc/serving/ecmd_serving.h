@@ -290,7 +290,7 @@ struct MassArgs {
     int64_t pages_s[2], lens_s, lse_s[2], mass_s[2], out_s[2];
     uint32_t b, hk, group, d, n, cols, page, window;
     uint32_t cols_group, groups;           // columns of a work-group; work-groups of a row
-    float scale_log2, decay;
+    float scale, decay;
     Div31 by_page, by_groups;
 };
 int launch_mass_f16(const MassArgs &A, void *stream);

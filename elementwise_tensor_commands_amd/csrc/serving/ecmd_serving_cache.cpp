@@ -514,8 +514,8 @@ int cmd_page_mass(const cmd_arg args[7], float scale, float decay, int32_t windo
     if (d < 1) return refuse(CMD_E_SHAPE, "heads of width 0");
     if (d > 256) return refuse(CMD_E_LIMIT, "heads wider than 256");
     if (window < 0) return refuse(CMD_E_ARG, "negative window");
-    const float scale_log2 = (float)((double)scale * 1.44269504088896340736);
-    if (!std::isfinite(scale_log2)) return refuse(CMD_E_ARG, "scale is not finite, or too large for binary32 in base 2");
+    if (!std::isfinite((float)((double)scale * 1.44269504088896340736)))   // as attention does
+        return refuse(CMD_E_ARG, "scale is not finite, or too large for binary32 in base 2");
     if (!std::isfinite(decay)) return refuse(CMD_E_ARG, "decay is not finite");
     TRY(check_unit(t[0]));
     TRY(check_unit(t[1]));
@@ -557,7 +557,7 @@ int cmd_page_mass(const cmd_arg args[7], float scale, float decay, int32_t windo
     A.n = (uint32_t)n;
     A.cols = (uint32_t)cols;
     A.window = (uint32_t)window;
-    A.scale_log2 = scale_log2;
+    A.scale = scale;
     A.decay = decay;
     A.by_page = Div31(A.page);
     A.by_groups = Div31(A.groups);
