@@ -19,7 +19,7 @@
 // It serves few queries or positions, where the chain from a row's length to its first key is
 // what counts (one row of 777, 8 tokens of 32 heads over 8, f16: 13 us and 4 for the join),
 // binary32, whose products run at a sixteenth of the 16-bit rate and hide everything else (5
-// rows, 23 tokens of 12 heads of 80 and 64, a window of 1000: 18 us and 6), and rows off
+// rows, 23 tokens of 12 heads of 80 and 64, a window of 1000: 19 us and 6), and rows off
 // 16 bytes.  k_tree_many stages tiles of
 // 32 positions in LDS, once for all queries of a work-group, by loads from memory straight to
 // LDS that are up to two tiles ahead, one barrier a tile; values are read from there transposed.
